@@ -56,7 +56,8 @@ EXPORTS = ("ep_status_str", "ep_rows_capacity", "ep_scale_cols", "ep_scale_words
            "ep_layout_workspace_bytes",
            "ep_layout", "ep_dispatch", "ep_layout_dispatch", "ep_combine", "ep_masked_repack",
            "ep_layout_noalloc", "ep_selftest_bounded_wait", "ep_selftest_cluster_wait",
-           "ep_rank_layout", "ep_rank_expand", "ep_route_topk")
+           "ep_rank_layout", "ep_rank_expand", "ep_route_topk", "ep_rmsnorm", "ep_expert_gemm",
+           "ep_expert_swiglu", "ep_moe_decode", "ep_moe_decode_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 256 * 1024
 
 
@@ -103,6 +104,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ep_selftest_cluster_wait.argtypes = [P, I64, P]
     L.ep_layout_noalloc.restype = ctypes.c_int
     L.ep_layout_noalloc.argtypes = [P, LP, P]
+    Q = ctypes.c_int
+    L.ep_rmsnorm.restype = ctypes.c_int
+    L.ep_rmsnorm.argtypes = [P, P, P, ctypes.c_float, I32, I32, Q, P, P, P, P, P]
+    L.ep_expert_gemm.restype = ctypes.c_int
+    L.ep_expert_gemm.argtypes = [LP, P, P, I32, Q, P, P, I32, P, P]
+    L.ep_expert_swiglu.restype = ctypes.c_int
+    L.ep_expert_swiglu.argtypes = [LP, P, P, I32, Q, P, P, I32, Q, P, P, P]
+    L.ep_moe_decode_workspace_bytes.restype = SZ
+    L.ep_moe_decode_workspace_bytes.argtypes = [I32] * 5
+    L.ep_moe_decode.restype = ctypes.c_int
+    L.ep_moe_decode.argtypes = [P, P, Q, P, P, I32, I32, I32, I32, I32, P, P, P, P, P, P, P, SZ, P]
     if path == LIB_PATH:
         _lib = L
     return L
@@ -472,3 +484,263 @@ def ep_route_topk(logits: torch.Tensor, num_topk: int, mode: str = "softmax",
                                         _stream(stream))
     _check(code, "ep_route_topk")
     return topk_idx, topk_w
+
+
+# ------------------------------------------------------- norm, experts, decode
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _want(t: Optional[torch.Tensor], name: str, dtypes, shape, device) -> None:
+    """Check one tensor argument (None passes): dtype, shape (-1 = any), device, layout."""
+    if t is None:
+        return
+    if t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
+        raise ValueError(f"{name}: dtype {t.dtype} is not accepted")
+    if t.dim() != len(shape) or any(w != -1 and s != w for s, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError("libep needs contiguous tensors")
+
+
+def _cuda(t: torch.Tensor) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError("libep works on CUDA tensors only")
+    return t.device
+
+
+class _On:
+    """The device of a call's tensors and the stream its kernels run on: `stream`,
+    or that device's current one.  Outputs the call allocates belong to that stream."""
+
+    def __init__(self, dev: torch.device, stream):
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+        self.dev, self.given = dev, stream
+        s = stream if stream is not None else torch.cuda.current_stream(dev)
+        self.stream = ctypes.c_void_p(s.cuda_stream)
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        if self.given is None:
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+        with torch.cuda.stream(self.given):
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+
+    def call(self, name: str, *args) -> None:
+        fn = getattr(load_library(), name)
+        if self.dev.index == torch.cuda.current_device():
+            code = fn(*args, self.stream)
+        else:
+            with torch.cuda.device(self.dev):
+                code = fn(*args, self.stream)
+        _check(code, name)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _scale_shape(rows: int, hidden: int, quant: str, slab=None):
+    """(dtype, shape) of the scales of `rows` rows; slab = (E, capacity) of a masked layout."""
+    cols = ep_scale_cols(hidden, quant)
+    if cols < 0:
+        raise EPError(EP_ERR_INVALID_ARG, f"hidden {hidden} for {quant}")
+    if quant == "fp8_ue8m0_mn":
+        if slab is not None:
+            return torch.int32, (slab[0], cols, (slab[1] + 3) // 4 * 4)
+        return torch.int32, (cols, (rows + 3) // 4 * 4)
+    return (torch.float32 if quant == "fp8_f32" else torch.int32), (rows, cols)
+
+
+def ep_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+               residual: Optional[torch.Tensor] = None, quant: str = "none",
+               out: Optional[torch.Tensor] = None, out_rows: Optional[torch.Tensor] = None,
+               out_scales: Optional[torch.Tensor] = None,
+               residual_out: Optional[torch.Tensor] = None, with_out: bool = True, stream=None):
+    """RMS norm of x + residual (bf16 [T, H]), as bf16 and / or 8-bit rows.
+
+    Returns (out, out_rows, out_scales, residual_out): out is None with
+    ``with_out=False`` (8-bit rows only), out_rows and out_scales are None for
+    quant "none", residual_out (the sum; may be ``residual`` or ``x`` itself) is
+    None without a residual unless a tensor is passed for it.
+    """
+    dev = _cuda(x)
+    bf16 = torch.bfloat16
+    _want(x, "x", bf16, (-1, -1), dev)
+    T, H = x.shape
+    _want(weight, "weight", bf16, (H,), dev)
+    _want(residual, "residual", bf16, (T, H), dev)
+    on = _On(dev, stream)
+    if residual is not None and residual_out is None:
+        residual_out = on.empty((T, H), bf16)
+    _want(residual_out, "residual_out", bf16, (T, H), dev)
+    if out is None and with_out:
+        out = on.empty((T, H), bf16)
+    _want(out, "out", bf16, (T, H), dev)
+    if quant != "none":
+        sdt, sshape = _scale_shape(T, H, quant)
+        if out_rows is None:
+            out_rows = on.empty((T, H), torch.uint8)
+        if out_scales is None:
+            out_scales = on.empty(sshape, sdt)
+        _want(out_rows, "out_rows", _E4M3, (T, H), dev)
+        _want(out_scales, "out_scales", sdt, sshape, dev)
+    on.call("ep_rmsnorm", _addr(x), _addr(residual), _addr(weight), eps, T, H, QUANT[quant],
+            _addr(residual_out), _addr(out), _addr(out_rows), _addr(out_scales))
+    return out, out_rows, out_scales, residual_out
+
+
+def _expert_checks(layout: Layout, rows, row_scales, weights, weight_scales, quant: str):
+    """Shared argument checks; returns (device, rows of the row space, slab, E, N, K)."""
+    dev = _cuda(rows)
+    cap = ep_rows_capacity(layout)
+    if cap < 0:
+        raise EPError(EP_ERR_INVALID_ARG, "layout shape")
+    slab = (layout.num_experts, layout.capacity) if layout.kind == "masked" else None
+    if rows.dim() == 3 and slab is not None:  # [E, capacity, K], as ep_masked_repack returns it
+        rows = rows.flatten(0, 1)
+    if row_scales is not None and row_scales.dim() == 3 and slab is not None \
+            and quant != "fp8_ue8m0_mn":
+        row_scales = row_scales.flatten(0, 1)
+    _want(rows, "rows", _E4M3, (max(cap, 1), -1), dev)
+    E, K = layout.num_experts, rows.shape[1]
+    if quant in ("none", "mxfp8"):
+        raise EPError(EP_ERR_UNSUPPORTED, f"expert products of {quant} rows")
+    sdt, sshape = _scale_shape(max(cap, 1), K, quant, slab)
+    if row_scales is None:
+        raise ValueError("row_scales is missing")
+    _want(row_scales, "row_scales", sdt, sshape, dev)
+    _want(weights, "weights", _E4M3, (E, -1, K), dev)
+    N = weights.shape[1]
+    _want(weight_scales, "weight_scales", torch.float32, (E, (N + 127) // 128, K // 128), dev)
+    _want(layout.expert_count, "layout.expert_count", torch.int32, (E,), dev)
+    return dev, cap, slab, N, K
+
+
+def ep_expert_gemm(layout: Layout, rows: torch.Tensor, row_scales: torch.Tensor,
+                   weights: torch.Tensor, weight_scales: torch.Tensor, quant: str = "fp8_f32",
+                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Each expert's block-scaled product on its rows: bf16 [rows, N].
+
+    rows / row_scales as ep_dispatch (or ep_masked_repack) wrote them; weights
+    E4M3 [E, N, K], weight_scales fp32 [E, ceil(N/128), K/128].  Rows of the
+    layout that no entry fills are not written.
+    """
+    dev, cap, _, N, K = _expert_checks(layout, rows, row_scales, weights, weight_scales, quant)
+    on = _On(dev, stream)
+    if out is None:
+        out = on.empty((max(cap, 1), N), torch.bfloat16)
+    _want(out, "out", torch.bfloat16, (max(cap, 1), N), dev)
+    on.call("ep_expert_gemm", ctypes.byref(layout.struct()), _addr(rows), _addr(row_scales), K,
+            QUANT[quant], _addr(weights), _addr(weight_scales), N, _addr(out))
+    return out
+
+
+def ep_expert_swiglu(layout: Layout, rows: torch.Tensor, row_scales: torch.Tensor,
+                     weights: torch.Tensor, weight_scales: torch.Tensor, quant: str = "fp8_f32",
+                     out_quant: str = "fp8_f32", out_rows: Optional[torch.Tensor] = None,
+                     out_scales: Optional[torch.Tensor] = None, stream=None):
+    """Gate and up products (weights E4M3 [E, 2I, K], gate rows first) with the
+    gated SiLU; returns (out_rows, out_scales) of [rows, I] in ``out_quant``, as
+    ep_expert_gemm takes them (bf16 and None for "none")."""
+    dev, cap, slab, N, K = _expert_checks(layout, rows, row_scales, weights, weight_scales, quant)
+    if N % 256:
+        raise EPError(EP_ERR_INVALID_ARG, "weights must have 2*I rows, I a multiple of 128")
+    inter = N // 2
+    if out_quant == "mxfp8":
+        raise EPError(EP_ERR_UNSUPPORTED, "gated SiLU in mxfp8")
+    on = _On(dev, stream)
+    plain = out_quant == "none"
+    if out_rows is None:
+        out_rows = on.empty((max(cap, 1), inter), torch.bfloat16 if plain else torch.uint8)
+    _want(out_rows, "out_rows", torch.bfloat16 if plain else _E4M3, (max(cap, 1), inter), dev)
+    if not plain:
+        sdt, sshape = _scale_shape(max(cap, 1), inter, out_quant, slab)
+        if out_scales is None:
+            out_scales = on.empty(sshape, sdt)
+        _want(out_scales, "out_scales", sdt, sshape, dev)
+    on.call("ep_expert_swiglu", ctypes.byref(layout.struct()), _addr(rows), _addr(row_scales), K,
+            QUANT[quant], _addr(weights), _addr(weight_scales), inter, QUANT[out_quant],
+            _addr(out_rows), _addr(out_scales))
+    return out_rows, out_scales
+
+
+@dataclass
+class MoeWorkspace:
+    """Scratch and status word of ep_moe_decode calls that do not overlap."""
+
+    scratch: torch.Tensor
+    status: torch.Tensor
+
+    def check_status(self) -> None:
+        """Synchronise and raise EPError if the last call recorded a device-side error."""
+        st = int(self.status.item())
+        if st != EP_OK:
+            raise EPError(st, "device status")
+
+
+def ep_moe_decode_workspace_bytes(num_tokens: int, num_topk: int, num_experts: int, hidden: int,
+                                  inter: int) -> int:
+    return int(load_library().ep_moe_decode_workspace_bytes(num_tokens, num_topk, num_experts,
+                                                            hidden, inter))
+
+
+def new_moe_workspace(num_tokens: int, num_topk: int, num_experts: int, hidden: int, inter: int,
+                      device=None) -> MoeWorkspace:
+    """Allocate a workspace for ep_moe_decode calls of up to this shape."""
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    n = ep_moe_decode_workspace_bytes(num_tokens, num_topk, num_experts, hidden, inter)
+    if n == 0 and num_tokens > 0:
+        raise EPError(EP_ERR_INVALID_ARG, "ep_moe_decode shape")
+    return MoeWorkspace(torch.empty(max(n, 16), dtype=torch.uint8, device=dev),
+                        torch.zeros(1, dtype=torch.int32, device=dev))
+
+
+def ep_moe_decode(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                  w13: torch.Tensor, w13_scales: torch.Tensor, w2: torch.Tensor,
+                  w2_scales: torch.Tensor, workspace: Optional[MoeWorkspace] = None,
+                  x_scales: Optional[torch.Tensor] = None, quant: str = "none",
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A whole mixture-of-experts layer for a few tokens: bf16 [T, H].
+
+    x is bf16 [T, H] (quant "none"), or E4M3 rows with x_scales as ep_rmsnorm
+    writes them ("fp8_f32", "fp8_ue8m0").  w13 E4M3 [E, 2I, H] (gate rows
+    first), w2 E4M3 [E, H, I], both with fp32 scales of their 128x128 blocks.
+    A device-side error (a bad expert id) is left in workspace.status.
+    """
+    dev = _cuda(x)
+    _want(x, "x", torch.bfloat16 if quant == "none" else _E4M3, (-1, -1), dev)
+    T, H = x.shape
+    _want(topk_idx, "topk_idx", torch.int32, (T, -1), dev)
+    K = topk_idx.shape[1]
+    _want(topk_w, "topk_w", torch.float32, (T, K), dev)
+    _want(w13, "w13", _E4M3, (-1, -1, H), dev)
+    E, inter = w13.shape[0], w13.shape[1] // 2
+    _want(w2, "w2", _E4M3, (E, H, inter), dev)
+    _want(w13_scales, "w13_scales", torch.float32, (E, w13.shape[1] // 128, H // 128), dev)
+    _want(w2_scales, "w2_scales", torch.float32, (E, H // 128, inter // 128), dev)
+    if w13.shape[1] % 256:
+        raise EPError(EP_ERR_INVALID_ARG, "w13 must have 2*I rows, I a multiple of 128")
+    if quant == "none":
+        if x_scales is not None:
+            raise ValueError("x_scales given for bf16 rows")
+    else:
+        sdt, sshape = _scale_shape(T, H, quant)
+        if x_scales is None:
+            raise ValueError("x_scales is missing")
+        _want(x_scales, "x_scales", sdt, sshape, dev)
+    on = _On(dev, stream)
+    if workspace is None:
+        n = ep_moe_decode_workspace_bytes(T, K, E, H, inter)
+        workspace = MoeWorkspace(on.empty(max(n, 16), torch.uint8), on.empty(1, torch.int32))
+    ws = workspace.scratch
+    _want(ws, "workspace", torch.uint8, (-1,), dev)
+    _want(workspace.status, "workspace.status", torch.int32, (1,), dev)
+    if out is None:
+        out = on.empty((T, H), torch.bfloat16)
+    _want(out, "out", torch.bfloat16, (T, H), dev)
+    on.call("ep_moe_decode", _addr(x), _addr(x_scales), QUANT[quant], _addr(topk_idx),
+            _addr(topk_w), T, K, E, H, inter, _addr(w13), _addr(w13_scales), _addr(w2),
+            _addr(w2_scales), _addr(out), _addr(workspace.status), _addr(ws), ws.numel())
+    return out

@@ -2,11 +2,13 @@
 // argument validation, sizing helpers and the launches.  Every host-detectable
 // error returns before anything is enqueued.
 #include <limits.h>
+#include <math.h>
 #include <stdlib.h>
 
 #include <nvtx3/nvToolsExt.h>
 
 #include "ep_common.cuh"
+#include "expert.cuh"
 
 namespace ep {
 
@@ -89,6 +91,48 @@ ep_status_t check_hidden(int32_t H, ep_quant_t quant) {
         quant == EP_QUANT_FP8_UE8M0_MN)
         return H % 128 == 0 ? EP_OK : EP_ERR_INVALID_ARG;
     return EP_ERR_INVALID_ARG;
+}
+
+// Argument rules shared by ep_expert_gemm and ep_expert_swiglu (N weight rows).
+ep_status_t check_expert(const ep_layout_t *L, const void *rows, const void *row_scales, int32_t K,
+                         ep_quant_t quant, const void *weights, const float *weight_scales) {
+    ep_status_t st = check_layout(L);
+    if (st != EP_OK) return st;
+    st = check_hidden(K, quant);
+    if (st != EP_OK) return st;
+    if (quant == EP_QUANT_NONE || quant == EP_QUANT_MXFP8) return EP_ERR_UNSUPPORTED;
+    if (L->num_tokens == 0) return EP_OK;
+    if (!rows || !row_scales || !weights || !weight_scales || !aligned(rows, 16) ||
+        !aligned(row_scales, 4) || !aligned(weights, 16) || !aligned(weight_scales, 4))
+        return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+
+ExpertArgs expert_args(const ep_layout_t *L, const void *rows, const void *row_scales, int32_t K,
+                       ep_quant_t quant, const void *weights, const float *weight_scales) {
+    ExpertArgs a = {};
+    a.count = L->expert_count;
+    a.offset = L->expert_offset;
+    a.E = L->num_experts;
+    a.cap = L->kind == EP_LAYOUT_MASKED ? L->capacity : 0;
+    a.rows_cap = (int)rows_capacity(*L);
+    a.x = static_cast<const uint8_t *>(rows);
+    a.x_scales = row_scales;
+    a.quant = quant;
+    a.K = K;
+    a.w = static_cast<const uint8_t *>(weights);
+    a.w_scales = weight_scales;
+    a.status = L->status;
+    return a;
+}
+
+// Shape rules of ep_moe_decode.
+ep_status_t check_moe(int32_t T, int32_t K, int32_t E, int32_t H, int32_t I) {
+    if (T < 0 || K < 1 || K > EP_MAX_TOPK || E < 1 || E > EP_MAX_EXPERTS) return EP_ERR_INVALID_ARG;
+    if (H < 128 || H % 128 != 0 || H > EP_MOE_DECODE_MAX_DIM) return EP_ERR_INVALID_ARG;
+    if (I < 128 || I % 128 != 0 || I > EP_MOE_DECODE_MAX_DIM) return EP_ERR_INVALID_ARG;
+    if ((int64_t)T * K > EP_MOE_DECODE_MAX_ENTRIES) return EP_ERR_CAPACITY;
+    return EP_OK;
 }
 
 ep_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? EP_OK : EP_ERR_CUDA; }
@@ -325,6 +369,115 @@ ep_status_t ep_rank_expand(const ep_layout_t *RL, const ep_layout_t *L, const in
     return from_cuda(launch_rank_expand(*RL, *L, topk_idx, row_bytes, scale_bytes, send_rows,
                                         send_scales, out_rows, out_scales,
                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_rmsnorm(const void *x, const void *residual, const void *weight, float eps,
+                       int32_t T, int32_t hidden, ep_quant_t quant, void *residual_out, void *out,
+                       void *out_rows, void *out_scales, ep_stream_t stream) {
+    const TraceRange trace("ep_rmsnorm");
+    const ep_status_t st = check_hidden(hidden, quant);
+    if (st != EP_OK) return st;
+    if (T < 0 || !(eps >= 0.0f) || isinf(eps)) return EP_ERR_INVALID_ARG;
+    if (T == 0) return EP_OK;
+    if (!x || !weight || !aligned(x, 16) || !aligned(weight, 16) || !aligned(residual, 16) ||
+        !aligned(residual_out, 16) || !aligned(out, 16))
+        return EP_ERR_INVALID_ARG;
+    if (quant == EP_QUANT_NONE) {
+        if (!out || out_rows || out_scales) return EP_ERR_INVALID_ARG;
+    } else if (!out_rows || !out_scales || !aligned(out_rows, 16) || !aligned(out_scales, 4)) {
+        return EP_ERR_INVALID_ARG;
+    }
+    return from_cuda(launch_rmsnorm(x, residual, weight, eps, T, hidden, quant, residual_out, out,
+                                    out_rows, out_scales, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_expert_gemm(const ep_layout_t *L, const void *rows, const void *row_scales,
+                           int32_t hidden, ep_quant_t quant, const void *weights,
+                           const float *weight_scales, int32_t n_out, void *y,
+                           ep_stream_t stream) {
+    const TraceRange trace("ep_expert_gemm");
+    const ep_status_t st = check_expert(L, rows, row_scales, hidden, quant, weights, weight_scales);
+    if (st != EP_OK) return st;
+    if (n_out < 8 || n_out % 8 != 0 || n_out > EP_MAX_EXPERT_COLS) return EP_ERR_INVALID_ARG;
+    if (L->num_tokens == 0) return EP_OK;
+    if (!y || !aligned(y, 16)) return EP_ERR_INVALID_ARG;
+    ExpertArgs a = expert_args(L, rows, row_scales, hidden, quant, weights, weight_scales);
+    a.N = n_out;
+    a.out = y;
+    a.out_quant = EP_QUANT_NONE;
+    return from_cuda(launch_expert(a, false, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_expert_swiglu(const ep_layout_t *L, const void *rows, const void *row_scales,
+                             int32_t hidden, ep_quant_t quant, const void *weights,
+                             const float *weight_scales, int32_t inter, ep_quant_t out_quant,
+                             void *out_rows, void *out_scales, ep_stream_t stream) {
+    const TraceRange trace("ep_expert_swiglu");
+    const ep_status_t st = check_expert(L, rows, row_scales, hidden, quant, weights, weight_scales);
+    if (st != EP_OK) return st;
+    if (inter < 128 || inter % 128 != 0 || inter > EP_MAX_EXPERT_COLS / 2) return EP_ERR_INVALID_ARG;
+    if (out_quant == EP_QUANT_MXFP8) return EP_ERR_UNSUPPORTED;
+    if (out_quant != EP_QUANT_NONE && out_quant != EP_QUANT_FP8_F32 &&
+        out_quant != EP_QUANT_FP8_UE8M0 && out_quant != EP_QUANT_FP8_UE8M0_MN)
+        return EP_ERR_INVALID_ARG;
+    if (L->num_tokens == 0) return EP_OK;
+    if (!out_rows || !aligned(out_rows, 16)) return EP_ERR_INVALID_ARG;
+    if (out_quant == EP_QUANT_NONE ? out_scales != nullptr : (!out_scales || !aligned(out_scales, 4)))
+        return EP_ERR_INVALID_ARG;
+    ExpertArgs a = expert_args(L, rows, row_scales, hidden, quant, weights, weight_scales);
+    a.N = inter;
+    a.out = out_rows;
+    a.out_scales = out_scales;
+    a.out_quant = out_quant;
+    return from_cuda(launch_expert(a, true, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t ep_moe_decode_workspace_bytes(int32_t T, int32_t K, int32_t E, int32_t hidden,
+                                     int32_t inter) {
+    if (check_moe(T, K, E, hidden, inter) != EP_OK) return 0;
+    return moe_workspace_bytes(T, K, hidden, inter);
+}
+
+ep_status_t ep_moe_decode(const void *x, const void *x_scales, ep_quant_t quant,
+                          const int32_t *topk_idx, const float *topk_w, int32_t T, int32_t K,
+                          int32_t E, int32_t hidden, int32_t inter, const void *w13,
+                          const float *w13_scales, const void *w2, const float *w2_scales,
+                          void *out, int32_t *status, void *workspace, size_t workspace_bytes,
+                          ep_stream_t stream) {
+    const TraceRange trace("ep_moe_decode");
+    const ep_status_t st = check_moe(T, K, E, hidden, inter);
+    if (st != EP_OK) return st;
+    if (quant == EP_QUANT_MXFP8 || quant == EP_QUANT_FP8_UE8M0_MN) return EP_ERR_UNSUPPORTED;
+    if (quant != EP_QUANT_NONE && quant != EP_QUANT_FP8_F32 && quant != EP_QUANT_FP8_UE8M0)
+        return EP_ERR_INVALID_ARG;
+    if (T == 0) return EP_OK;
+    if (!x || !topk_idx || !topk_w || !w13 || !w13_scales || !w2 || !w2_scales || !out || !status ||
+        !workspace || workspace_bytes < moe_workspace_bytes(T, K, hidden, inter))
+        return EP_ERR_INVALID_ARG;
+    if (quant == EP_QUANT_NONE ? x_scales != nullptr : (!x_scales || !aligned(x_scales, 4)))
+        return EP_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(w13, 16) ||
+        !aligned(w13_scales, 4) || !aligned(w2, 16) || !aligned(w2_scales, 4) || !aligned(out, 16) ||
+        !aligned(status, 4) || !aligned(workspace, 16))
+        return EP_ERR_INVALID_ARG;
+    MoeArgs a = {};
+    a.x = x;
+    a.x_scales = x_scales;
+    a.quant = quant;
+    a.topk_idx = topk_idx;
+    a.topk_w = topk_w;
+    a.T = T;
+    a.K = K;
+    a.E = E;
+    a.H = hidden;
+    a.I = inter;
+    a.w13 = static_cast<const uint8_t *>(w13);
+    a.w13_scales = w13_scales;
+    a.w2 = static_cast<const uint8_t *>(w2);
+    a.w2_scales = w2_scales;
+    a.out = out;
+    a.status = status;
+    return from_cuda(launch_moe_decode(a, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

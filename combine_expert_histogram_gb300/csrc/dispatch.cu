@@ -37,9 +37,8 @@
 // drain itself ran out the CTA would exit with a copy into its shared memory
 // still pending, which is undefined; EP_ERR_TIMEOUT is then the only thing the
 // kernel guarantees, and the caller should treat the context as suspect.
-#include <cuda_fp8.h>
-
 #include "ep_common.cuh"
+#include "fp8.cuh"
 
 namespace ep {
 namespace {
@@ -51,14 +50,6 @@ constexpr int kOutBufs = 4;               // FP8 output rows per CTA, at most
 constexpr int kSmemMax = 227 * 1024;      // dynamic shared memory per CTA
 constexpr int kCopyMaxStages = 8;         // bf16 rows in flight per CTA, at most
 constexpr int kCopyBudget = 144 * 1024;   // bf16: shared memory per CTA aimed for
-
-__device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
-    // __nv_cvt_float2_to_fp8x2: round to nearest even, saturate to +-448;
-    // the first element of the pair lands in the low byte.
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-    return (lo & 0xffffu) | (hi << 16);
-}
 
 // Bulk copy of `bytes` (multiple of 16, both addresses 16-byte aligned) from
 // shared memory to global memory, tracked by the issuing thread's bulk group.
@@ -78,23 +69,6 @@ template <int N>
 __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-// Start the row copy global -> shared: arrive on the barrier, announcing
-// `bytes` of transactions, and issue one bulk copy that completes them.
-__device__ __forceinline__ void load_row(void *sdst, const void *gsrc, uint32_t bytes,
-                                         uint64_t *bar) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
-                 "r"(bytes)
-                 : "memory");
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-            "r"(smem_addr(sdst)),
-        "l"(gsrc), "r"(bytes), "r"(smem_addr(bar))
-        : "memory");
-}
-
 // Quantise one FP8 slot (16 consecutive elements a, b of group j/8, part
 // lane%8 of its 8 lanes).  Returns the 16 E4M3 bytes; `sc` receives the
 // group's fp32 scale bits (FP8_F32), its UE8M0 exponent byte (FP8_UE8M0*), or

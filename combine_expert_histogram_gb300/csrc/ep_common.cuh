@@ -58,6 +58,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const 
     }
 }
 
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// Start the row copy global -> shared: arrive on the barrier, announcing
+// `bytes` of transactions, and issue one bulk copy that completes them.
+__device__ __forceinline__ void load_row(void *sdst, const void *gsrc, uint32_t bytes,
+                                         uint64_t *bar) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
+                 "r"(bytes)
+                 : "memory");
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(smem_addr(sdst)),
+        "l"(gsrc), "r"(bytes), "r"(smem_addr(bar))
+        : "memory");
+}
+
 __device__ __forceinline__ unsigned lanemask_lt() {
     unsigned m;
     asm("mov.u32 %0, %%lanemask_lt;" : "=r"(m));
@@ -272,5 +289,9 @@ cudaError_t launch_rank_expand(const ep_layout_t &rank_layout, const ep_layout_t
                                const int32_t *topk_idx, int row_bytes, int scale_bytes,
                                const void *send_rows, const void *send_scales, void *out_rows,
                                void *out_scales, cudaStream_t stream);
+
+cudaError_t launch_rmsnorm(const void *x, const void *residual, const void *weight, float eps,
+                           int T, int H, ep_quant_t quant, void *residual_out, void *out,
+                           void *rows, void *scales, cudaStream_t stream);
 
 }  // namespace ep

@@ -3,7 +3,7 @@
  *
  * The hot path of expert-parallel MoE layers, on one device whose HBM holds
  * every expert: logical expert-parallel ranks are only partitions of the
- * expert set.  Four operations:
+ * expert set.  Operations:
  *
  *   ep_layout         top-k router output -> per-expert layout: expert
  *                     histogram, padded exclusive scan, stable slots.
@@ -12,6 +12,10 @@
  *   ep_combine        top-k weighted reduction of expert outputs back to
  *                     token order.
  *   ep_masked_repack  contiguous expert segments -> masked [E, cap, H] slab.
+ *   ep_rmsnorm        residual addition and RMS norm, bf16 and 8-bit rows.
+ *   ep_expert_gemm, ep_expert_swiglu  the experts' block-scaled E4M3 products
+ *                     on a layout's rows.
+ *   ep_moe_decode     the whole layer for a few tokens.
  *
  * Sources (the pages describe a library integration, not kernels):
  *   [PR-24443]  SGLang PR "moe: add DeepEP V2 ElasticBuffer support to MoE
@@ -121,6 +125,9 @@ typedef enum ep_route {
 #define EP_MAX_TOPK 32     /* [PR-24443] review: kNumTopk <= 32 */
 #define EP_MAX_EXPERTS 1024
 #define EP_MAX_ALIGN 128
+#define EP_MAX_EXPERT_COLS 65536     /* largest output width of an expert's product */
+#define EP_MOE_DECODE_MAX_ENTRIES 1024 /* ep_moe_decode: largest T*K                 */
+#define EP_MOE_DECODE_MAX_DIM 16384    /* ep_moe_decode: largest hidden and inner    */
 
 /*
  * The layout ("handle"): shape plus caller-owned device arrays.  ep_layout()
@@ -417,6 +424,131 @@ ep_status_t ep_rank_expand(const ep_layout_t *rank_layout, const ep_layout_t *la
 #define EP_NOALLOC_SCRATCH_BYTES (256u * 1024u)
 ep_status_t ep_layout_noalloc(const int32_t *topk_idx, const ep_layout_t *layout,
                               ep_stream_t stream);
+
+/*
+ * ep_rmsnorm -- the norm in front of a mixture-of-experts layer: residual
+ * addition, root-mean-square norm and, optionally, the rows in 8 bits.  Its
+ * bf16 rows are what the router's product, ep_dispatch and ep_moe_decode take;
+ * its 8-bit rows are in ep_dispatch's formats, for ep_moe_decode and, with a
+ * one-expert layout, for ep_expert_gemm / ep_expert_swiglu (a shared expert).
+ *
+ *   x             device bf16 [T, hidden], 16-byte aligned.
+ *   residual      device bf16 [T, hidden] or NULL (no addition).
+ *   weight        device bf16 [hidden], 16-byte aligned.
+ *   eps           finite, >= 0.
+ *   hidden        as for ep_dispatch with `quant`; num_tokens >= 0.
+ *   residual_out  device bf16 [T, hidden] or NULL.
+ *   out           device bf16 [T, hidden]; may be NULL when quant is not
+ *                 EP_QUANT_NONE (the rows are then written in 8 bits only).
+ *   out_rows, out_scales  E4M3 [T, hidden] and the scales of `quant` for T rows
+ *                 (EP_QUANT_FP8_UE8M0_MN: [ceil(H/512)][roundup(T, 4)] words,
+ *                 the padding columns untouched); NULL for EP_QUANT_NONE.
+ *
+ *   s = x + residual (fp32);  residual_out = bf16_rn(s)
+ *   y = (s * (1 / sqrt(mean(s^2) + eps))) * weight  (fp32, from the unrounded s)
+ *   out = bf16_rn(y);  out_rows, out_scales = `quant` of the fp32 y, by the
+ *   rules of ep_dispatch (the 8-bit rows are not rounded to bf16 first).
+ *
+ * residual_out may be residual or x, and out may be x, residual or
+ * residual_out (if the sum is not needed): each row is read before it is
+ * written.  Other overlaps are not allowed.  The kernel does not trigger its
+ * dependents early, so ep_dispatch may follow it directly.  The weight is read
+ * before the kernel waits for its predecessor: it must be complete when that
+ * predecessor started.
+ */
+ep_status_t ep_rmsnorm(const void *x, const void *residual, const void *weight, float eps,
+                       int32_t num_tokens, int32_t hidden, ep_quant_t quant, void *residual_out,
+                       void *out, void *out_rows, void *out_scales, ep_stream_t stream);
+
+/*
+ * ep_expert_gemm -- every expert's product on its rows of a layout, in 8-bit
+ * floating point with one scale per 1x128 group of a row and one per 128x128
+ * block of a weight ([DISC-26563]: 128x128 blockwise FP8 with dynamic
+ * activation scaling).
+ *
+ *   layout         filled by ep_layout(), contiguous or masked.
+ *   rows, row_scales  as ep_dispatch(layout, ..., quant) or ep_masked_repack
+ *                  wrote them; quant EP_QUANT_FP8_F32, EP_QUANT_FP8_UE8M0 or
+ *                  EP_QUANT_FP8_UE8M0_MN (EP_QUANT_NONE and EP_QUANT_MXFP8:
+ *                  EP_ERR_UNSUPPORTED).  rows 16-byte aligned.
+ *   hidden         K, a multiple of 128, at most EP_MAX_HIDDEN.
+ *   weights        device E4M3 [E, n_out, K], 16-byte aligned.
+ *   weight_scales  device fp32 [E, ceil(n_out/128), K/128].
+ *   n_out          a multiple of 8 in [8, EP_MAX_EXPERT_COLS].
+ *   y              device bf16 [rows, n_out], 16-byte aligned.
+ *
+ *   y[r, n] = bf16_rn( sum over blocks b of  sx[r, b] * sw[e, n/128, b] *
+ *                      sum over k in b of  x[r, k] * w[e, n, k] )
+ * with all sums in fp32, for the rows of each expert e: expert_offset[e] + s,
+ * s < expert_count[e] (masked: < min(expert_count[e], capacity)).  Other rows
+ * of y are not written, and their x (which may be anything) does not matter.
+ * A bounded wait that runs out raises EP_ERR_TIMEOUT into the layout's status.
+ */
+ep_status_t ep_expert_gemm(const ep_layout_t *layout, const void *rows, const void *row_scales,
+                           int32_t hidden, ep_quant_t quant, const void *weights,
+                           const float *weight_scales, int32_t n_out, void *y,
+                           ep_stream_t stream);
+
+/*
+ * ep_expert_swiglu -- the experts' gate and up products with the gated SiLU,
+ * and the result in 8 bits for the down product (ep_expert_gemm with K =
+ * inter).  Arguments as for ep_expert_gemm, but
+ *
+ *   weights        device E4M3 [E, 2*inter, hidden]: the gate's rows, then the up's.
+ *   weight_scales  device fp32 [E, 2*inter/128, hidden/128].
+ *   inter          I, a multiple of 128 in [128, EP_MAX_EXPERT_COLS / 2].
+ *   out_quant      EP_QUANT_NONE: out_rows is bf16 [rows, I], out_scales NULL;
+ *                  EP_QUANT_FP8_F32, EP_QUANT_FP8_UE8M0, EP_QUANT_FP8_UE8M0_MN:
+ *                  E4M3 [rows, I] and scales as ep_dispatch writes them for
+ *                  hidden = I (EP_QUANT_MXFP8: EP_ERR_UNSUPPORTED).
+ *
+ *   g, u = the two products (fp32);  h = g / (1 + exp(-g)) * u  (fp32)
+ *   out = bf16_rn(h), or `out_quant` of the fp32 h by ep_dispatch's rules.
+ */
+ep_status_t ep_expert_swiglu(const ep_layout_t *layout, const void *rows, const void *row_scales,
+                             int32_t hidden, ep_quant_t quant, const void *weights,
+                             const float *weight_scales, int32_t inter, ep_quant_t out_quant,
+                             void *out_rows, void *out_scales, ep_stream_t stream);
+
+/*
+ * ep_moe_decode -- a whole mixture-of-experts layer for a few tokens (decode:
+ * single tokens, small batches), without a layout: the experts' weights are
+ * read once and bound the time.
+ *
+ *   x          device, 16-byte aligned.  quant EP_QUANT_NONE: bf16 [T, H],
+ *              quantised inside as EP_QUANT_FP8_F32 does; EP_QUANT_FP8_F32 or
+ *              EP_QUANT_FP8_UE8M0: E4M3 [T, H] with x_scales (as ep_rmsnorm
+ *              writes them).  Others: EP_ERR_UNSUPPORTED.
+ *   topk_idx   device int32 [T, K]; -1 = not routed.  Ids outside [-1, E) count
+ *              as -1 and raise EP_ERR_BAD_EXPERT_ID.  Experts may repeat.
+ *   topk_w     device fp32 [T, K].
+ *   T, K, E    T >= 0, K <= EP_MAX_TOPK, E <= EP_MAX_EXPERTS, and T*K at most
+ *              EP_MOE_DECODE_MAX_ENTRIES (else EP_ERR_CAPACITY: use ep_layout,
+ *              ep_dispatch, ep_expert_swiglu, ep_expert_gemm, ep_combine).
+ *   hidden, inter  H and I, multiples of 128, at most EP_MOE_DECODE_MAX_DIM.
+ *   w13, w13_scales  E4M3 [E, 2I, H], fp32 [E, 2I/128, H/128] (ep_expert_swiglu's).
+ *   w2, w2_scales    E4M3 [E, H, I], fp32 [E, H/128, I/128].
+ *   out        device bf16 [T, H], 16-byte aligned; every element is written.
+ *   status     device int32 [1]: 0, or the largest error code of this call.
+ *   workspace  device scratch of ep_moe_decode_workspace_bytes(), 16-byte
+ *              aligned, clobbered; holds nothing between calls.  Calls that
+ *              share one must not overlap on the GPU.
+ *
+ *   g, u = w13[e] xq (fp32);  h = g / (1 + exp(-g)) * u;  hq = EP_QUANT_FP8_F32 of h
+ *   out[t] = bf16_rn( sum over k of topk_w[t,k] * (w2[e] hq) ),  sums in fp32,
+ * in ascending k; a token with no routed entry gets +0.
+ *
+ * The weights and their scales are read before the kernels wait for their
+ * predecessors: they must be complete when the kernel before this call started.
+ */
+size_t ep_moe_decode_workspace_bytes(int32_t num_tokens, int32_t num_topk, int32_t num_experts,
+                                     int32_t hidden, int32_t inter);
+ep_status_t ep_moe_decode(const void *x, const void *x_scales, ep_quant_t quant,
+                          const int32_t *topk_idx, const float *topk_w, int32_t num_tokens,
+                          int32_t num_topk, int32_t num_experts, int32_t hidden, int32_t inter,
+                          const void *w13, const float *w13_scales, const void *w2,
+                          const float *w2_scales, void *out, int32_t *status, void *workspace,
+                          size_t workspace_bytes, ep_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,218 @@
+"""ep_rmsnorm against the formula in 64 bits.
+
+Tolerances.  s = x + residual is one fp32 rounding of two bf16 numbers; the sum
+of H squares is a tree and chains of positive terms, at most 64 roundings deep
+for the sizes the kernel takes; mean, root, reciprocal and two products add 8.
+So y is within 2^-17 of the formula (72 * 2^-24 < 2^-17), and its bf16 rounding
+adds half a step.
+"""
+import pytest
+import torch
+
+from combine_expert_histogram_gb300 import binding as ep
+from tests import layer_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+REL = 2.0 ** -17
+EPS = 1e-5
+
+
+def make(T, H, seed=0, residual=True):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((T, H), generator=g).bfloat16()
+    r = (3 * torch.randn((T, H), generator=g)).bfloat16() if residual else None
+    w = (1 + 0.3 * torch.randn(H, generator=g)).bfloat16()
+    return x, r, w
+
+
+def formula(x, r, w, eps=EPS):
+    s = x.to(ref.F64) + (r.to(ref.F64) if r is not None else 0)
+    return s, s / torch.sqrt(s.square().mean(1, keepdim=True) + eps) * w.to(ref.F64)
+
+
+def cuda(*ts):
+    return [t.cuda() if t is not None else None for t in ts]
+
+
+def check_scaled(rows, scales, y, quant, T, H):
+    q = ref.decode(rows)
+    noise = y.abs() * REL + 1e-37
+    if quant == "mxfp8":
+        b = ref.word_bytes(scales).to(ref.F64)
+        amax = y.view(T, H // 32, 32).abs().amax(2)
+        lo, hi = (torch.clamp(torch.floor(torch.log2(amax * (1 + k))) - 8, min=-127)
+                  for k in (-REL, REL))
+        assert ((b - 127 >= lo) & (b - 127 <= hi)).all()
+        s = torch.exp2(b - 127).repeat_interleave(32, 1)
+        r = y / s
+        # half a step of E4M3 at the value; up to 512 saturates to 448
+        step = torch.exp2(torch.floor(torch.log2(r.abs().clamp(2.0 ** -6, 448.0))) - 3)
+        over = (r.abs() - 448).clamp(min=0)
+        assert ((q - r).abs() <= step / 2 + over + r.abs() * REL + 1e-30).all()
+        return
+    if quant == "fp8_f32":
+        s = scales.cpu().to(ref.F64)
+    else:
+        words = ref.mn_to_rows(scales, T) if quant == "fp8_ue8m0_mn" else scales
+        s = ref.ue8m0(words, H // 128)
+        b = ref.word_bytes(words)
+        assert (b[:, H // 128:] == 127).all()  # unused bytes of the last word
+    lo, hi, s_lo, s_hi = ref.spread(y, noise, power=quant != "fp8_f32")
+    assert ((s >= s_lo * (1 - ref.U)) & (s <= s_hi * (1 + ref.U))).all()
+    v = q * ref.widen(s)
+    slack = v.abs() * 4 * ref.U
+    assert ((v >= lo - slack) & (v <= hi + slack)).all()
+
+
+SHAPES = [(1, 128), (1, 7168), (3, 640), (17, 2048), (5, 1152), (2, 8192), (2, 8320), (3, 16384),
+          (2, 32768), (257, 512)]
+
+
+@pytest.mark.parametrize("quant", ["none", "fp8_f32", "fp8_ue8m0", "mxfp8", "fp8_ue8m0_mn"])
+@pytest.mark.parametrize("T,H", SHAPES)
+def test_formula(T, H, quant):
+    x, r, w = make(T, H, seed=H + T)
+    s, y = formula(x, r, w)
+    out, rows, scales, res = ep.ep_rmsnorm(*cuda(x, w), EPS, residual=r.cuda(), quant=quant)
+    torch.cuda.synchronize()
+    ref.close_bf16(out, y, y.abs() * REL)
+    ref.close_bf16(res, s, s.abs() * ref.U)
+    if quant != "none":
+        check_scaled(rows, scales, y, quant, T, H)
+
+
+@pytest.mark.parametrize("H", [8, 24, 200, 2056, 4104])
+def test_bf16_rows_of_any_multiple_of_8_without_residual(H):
+    x, _, w = make(9, H, seed=H, residual=False)
+    _, y = formula(x, None, w)
+    out, rows, scales, res = ep.ep_rmsnorm(*cuda(x, w), EPS)
+    assert rows is None and scales is None and res is None
+    ref.close_bf16(out, y, y.abs() * REL)
+
+
+@pytest.mark.parametrize("T", [700, 5000])
+def test_many_rows(T):
+    x, r, w = make(T, 1024, seed=T)
+    s, y = formula(x, r, w)
+    out, rows, scales, res = ep.ep_rmsnorm(*cuda(x, w), EPS, residual=r.cuda(), quant="fp8_f32")
+    ref.close_bf16(out, y, y.abs() * REL)
+    ref.close_bf16(res, s, s.abs() * ref.U)
+    check_scaled(rows, scales, y, "fp8_f32", T, 1024)
+
+
+@pytest.mark.parametrize("quant", ["none", "fp8_f32", "mxfp8"])
+def test_in_place(quant):
+    """residual_out = residual and out = x give what separate buffers give."""
+    x, r, w = make(33, 1280, seed=4)
+    a = ep.ep_rmsnorm(*cuda(x, w), EPS, residual=r.cuda(), quant=quant)
+    xd, rd, wd = cuda(x, r, w)
+    b = ep.ep_rmsnorm(xd, wd, EPS, residual=rd, quant=quant, out=xd, residual_out=rd)
+    for p, q in zip(a, b):
+        assert p is None and q is None or torch.equal(p, q)
+
+
+def test_8_bit_rows_alone():
+    x, r, w = make(33, 1280, seed=5)
+    a = ep.ep_rmsnorm(*cuda(x, w), EPS, residual=r.cuda(), quant="fp8_f32")
+    b = ep.ep_rmsnorm(*cuda(x, w), EPS, residual=r.cuda(), quant="fp8_f32", with_out=False)
+    assert b[0] is None
+    for p, q in zip(a[1:], b[1:]):
+        assert torch.equal(p, q)
+
+
+def test_rows_of_zeros_and_large_values():
+    """A zero row gives zeros (scale 1e-4 / 448, or the smallest of MX); rows near
+    bf16's range square to finite fp32 sums as long as the formula's do."""
+    x = torch.zeros((3, 256), dtype=torch.bfloat16)
+    x[1] = 1e18
+    x[2, 7] = 1e-20
+    w = torch.ones(256, dtype=torch.bfloat16)
+    for quant in ("fp8_f32", "fp8_ue8m0", "mxfp8"):
+        out, rows, scales, _ = ep.ep_rmsnorm(*cuda(x, w), EPS, quant=quant)
+        _, y = formula(x, None, w)
+        ref.close_bf16(out, y, y.abs() * REL)
+        assert (out[0] == 0).all() and (rows[0] == 0).all()
+        if quant == "fp8_f32":
+            want = torch.tensor(1e-4, dtype=torch.float32) / torch.tensor(448.0)
+            assert (scales[0].cpu() == want).all()
+        if quant == "mxfp8":
+            assert (scales[0] == 0).all()
+
+
+def test_a_row_of_nan_stays_in_its_row():
+    x, r, w = make(4, 512, seed=8)
+    x[2, 100] = float("nan")
+    x[3, 5] = float("inf")
+    out, rows, scales, _ = ep.ep_rmsnorm(*cuda(x, w), EPS, residual=r.cuda(), quant="fp8_f32")
+    _, y = formula(x, r, w)
+    ref.close_bf16(out[:2], y[:2], y[:2].abs() * REL)
+    check_scaled(rows[:2], scales[:2], y[:2], "fp8_f32", 2, 512)
+    assert out[2].isnan().all()
+
+
+def test_no_rows_and_refusals():
+    x, r, w = cuda(*make(0, 256))
+    out, rows, scales, res = ep.ep_rmsnorm(x, w, EPS, residual=r, quant="fp8_f32")
+    assert out.shape == (0, 256) and rows.shape == (0, 256)
+    x, r, w = cuda(*make(4, 256))
+    with pytest.raises(ValueError):
+        ep.ep_rmsnorm(x.float(), w)
+    with pytest.raises(ValueError):
+        ep.ep_rmsnorm(x, w[:128])
+    with pytest.raises(ValueError):
+        ep.ep_rmsnorm(x.t(), w)
+    with pytest.raises(ValueError):
+        ep.ep_rmsnorm(x, w, residual=r.cpu())
+    with pytest.raises(ep.EPError):
+        ep.ep_rmsnorm(x, w, eps=-1.0)
+    with pytest.raises(ep.EPError):
+        ep.ep_rmsnorm(x, w, eps=float("nan"))
+    with pytest.raises(ep.EPError):
+        ep.ep_rmsnorm(x, w, with_out=False)
+    with pytest.raises(ep.EPError):  # no multiple of 128
+        ep.ep_rmsnorm(x[:, :136].contiguous(), w[:136].contiguous(), quant="fp8_f32")
+
+
+def test_another_stream_and_a_replayed_graph():
+    x, r, w = make(6, 1024, seed=11)
+    xd, rd, wd = cuda(x, r, w)
+    s = torch.cuda.Stream()
+    out = torch.empty_like(xd)
+    res = torch.empty_like(xd)
+    with torch.cuda.stream(s):
+        ep.ep_rmsnorm(xd, wd, EPS, residual=rd, out=out, residual_out=res)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        ep.ep_rmsnorm(xd, wd, EPS, residual=rd, out=out, residual_out=res, stream=s)
+    for seed in (12, 13):
+        x, r, _ = make(6, 1024, seed=seed)
+        xd.copy_(x)
+        rd.copy_(r)
+        g.replay()
+        torch.cuda.synchronize()
+        _, y = formula(x, r, w)
+        ref.close_bf16(out, y, y.abs() * REL)
+
+
+@pytest.mark.parametrize("T", [3, 600])
+def test_norm_straight_into_dispatch(T):
+    """ep_dispatch directly after the norm (its early reads of x included): the
+    rows it writes are its own quantisation of the norm's bf16 rows."""
+    E, K, H = 16, 4, 512
+    x, r, w = make(T, H, seed=T)
+    xd, rd, wd = cuda(x, r, w)
+    idx = torch.stack([torch.randperm(E)[:K] for _ in range(T)]).to(torch.int32).cuda()
+    L = ep.ep_layout(idx, E)
+    torch.cuda.synchronize()
+    out, _, _, _ = ep.ep_rmsnorm(xd, wd, EPS, residual=rd)
+    rows, scales, _ = ep.ep_dispatch(L, out, "fp8_f32")
+    torch.cuda.synchronize()
+    q, s = ref.quantise_bf16(out.cpu())
+    dst = L.dst_row.cpu().long()[:T * K]
+    assert torch.equal(ref.decode(rows[dst.cuda()]), q.repeat_interleave(K, 0))
+    assert torch.equal(scales.cpu()[dst].to(ref.F64), s.repeat_interleave(K, 0))

@@ -1,0 +1,106 @@
+"""Host-side argument rules of ep_rmsnorm, ep_expert_gemm, ep_expert_swiglu and
+ep_moe_decode: every refusal returns before any CUDA call (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+from tests import layer_ref as ref
+from tests.test_abi_host import _layout, lib  # noqa: F401
+
+OK, INVALID, CAPACITY, UNSUPPORTED = 0, 1, 2, 5
+P = ctypes.c_void_p
+A = P(4096)  # an aligned address that is never read
+
+
+def _filled(**kw):
+    c = _layout(**kw)
+    c.dst_row = c.expert_count = c.expert_offset = c.status = 256
+    return c
+
+
+def test_rmsnorm_arguments(lib):  # noqa: F811
+    def call(x=A, res=None, w=A, eps=1e-6, T=4, H=256, quant=0, res_out=None, out=A, rows=None,
+             scales=None):
+        return lib.ep_rmsnorm(x, res, w, eps, T, H, quant, res_out, out, rows, scales, None)
+
+    assert call(T=0) == OK
+    for bad in (dict(T=-1), dict(H=0), dict(H=132), dict(H=32776), dict(quant=9), dict(quant=-1),
+                dict(x=None), dict(w=None), dict(out=None), dict(x=P(4104)), dict(w=P(4098)),
+                dict(res=P(4100)), dict(res_out=P(4100)), dict(out=P(4100)), dict(eps=-1e-6),
+                dict(eps=float("nan")), dict(eps=float("inf")), dict(rows=A), dict(scales=A),
+                dict(quant=1), dict(quant=1, rows=A), dict(quant=1, scales=A),
+                dict(quant=1, rows=P(4100), scales=A), dict(quant=1, rows=A, scales=P(4098)),
+                dict(quant=1, H=264, rows=A, scales=A)):
+        assert call(**bad) == INVALID, bad
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_expert_arguments(lib, gated):  # noqa: F811
+    def call(L=None, rows=A, rs=A, H=256, quant=1, w=A, ws=A, n=256, out_quant=1, out=A, os=A):
+        L = ctypes.byref(_filled() if L is None else L)
+        if gated:
+            return lib.ep_expert_swiglu(L, rows, rs, H, quant, w, ws, n, out_quant, out, os, None)
+        return lib.ep_expert_gemm(L, rows, rs, H, quant, w, ws, n, out, None)
+
+    assert call(L=_filled(num_tokens=0)) == OK
+    bad = [dict(L=_layout()), dict(L=_filled(num_topk=33)), dict(rows=None), dict(rs=None),
+           dict(w=None), dict(ws=None), dict(out=None), dict(rows=P(4104)), dict(rs=P(4098)),
+           dict(w=P(4104)), dict(ws=P(4098)), dict(out=P(4104)), dict(H=0), dict(H=200),
+           dict(H=32896), dict(n=0), dict(n=-8), dict(n=12), dict(n=1 << 20), dict(quant=7)]
+    if gated:
+        bad += [dict(n=192), dict(os=None), dict(os=P(4098)), dict(out_quant=0),
+                dict(out_quant=8)]
+    for kw in bad:
+        assert call(**kw) == INVALID, kw
+    assert call(quant=0) == UNSUPPORTED and call(quant=3) == UNSUPPORTED
+    if gated:
+        assert call(out_quant=3) == UNSUPPORTED
+    assert call(L=_filled(max_tokens=8)) == CAPACITY
+
+
+def test_moe_decode_arguments(lib):  # noqa: F811
+    big = 1 << 40
+
+    def call(x=A, xs=None, quant=0, idx=A, w=A, T=4, K=2, E=8, H=256, I=128, w13=A, s13=A, w2=A,
+             s2=A, out=A, status=A, ws=A, n=big):
+        return lib.ep_moe_decode(x, xs, quant, idx, w, T, K, E, H, I, w13, s13, w2, s2, out,
+                                 status, ws, n, None)
+
+    assert call(T=0) == OK
+    for p in ("x", "idx", "w", "w13", "s13", "w2", "s2", "out", "status", "ws"):
+        assert call(**{p: None}) == INVALID, p
+        assert call(**{p: P(4097)}) == INVALID, p
+    for bad in (dict(T=-1), dict(K=0), dict(K=33), dict(E=0), dict(E=1025), dict(H=0),
+                dict(H=200), dict(I=64), dict(H=16512), dict(I=16512), dict(quant=9),
+                dict(xs=A), dict(quant=1), dict(quant=2), dict(quant=1, xs=P(4098)),
+                dict(n=lib.ep_moe_decode_workspace_bytes(4, 2, 8, 256, 128) - 1)):
+        assert call(**bad) == INVALID, bad
+    assert call(quant=3, xs=A) == UNSUPPORTED and call(quant=4, xs=A) == UNSUPPORTED
+    assert call(T=513) == CAPACITY
+    assert lib.ep_moe_decode_workspace_bytes(513, 2, 8, 256, 128) == 0
+    assert lib.ep_moe_decode_workspace_bytes(512, 2, 8, 256, 128) > 0
+
+
+def test_python_calls_refuse_cpu_tensors(lib):  # noqa: F811
+    from combine_expert_histogram_gb300 import binding as ep
+    x = torch.zeros(2, 128, dtype=torch.bfloat16)
+    i = torch.zeros(2, 1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        ep.ep_rmsnorm(x, x[0])
+    with pytest.raises(ValueError):
+        ep.ep_moe_decode(x, i, i.float(), x, x, x, x)
+
+
+def test_the_64_bit_e4m3_agrees_with_torch():
+    """The test's own E4M3 decoding and rounding against torch's cast."""
+    b = torch.arange(256, dtype=torch.uint8)
+    v = b.view(torch.float8_e4m3fn).double()
+    got = ref.decode(b)
+    assert torch.equal(got.isnan(), v.isnan())
+    assert torch.equal(got[~v.isnan()], v[~v.isnan()])
+    x = torch.cat([torch.randn(20000) * 60, torch.randn(2000) * 1e-3, torch.tensor([0.0, 448.0])])
+    x = x.clamp(-448, 448)
+    assert torch.equal(ref.e4m3(x.double()), x.to(torch.float8_e4m3fn).double())
+    mids = (v[:126] + v[1:127]) / 2  # ties go to the even mantissa
+    assert torch.equal(ref.e4m3(mids), mids.float().to(torch.float8_e4m3fn).double())
