@@ -5,149 +5,352 @@
 //   y[r, n] = sum over blocks b of sx[r, b] * sw[e, n/128, b]
 //                                  * sum over k in b of x[r, k] * w[e, n, k]
 //
-// 32 x 128 tiles on the fp32 pipes: the block sums stay in registers and are
-// scaled into the running sums after each 128 of K.
-#include <cuda_bf16.h>
-
+// Persistent CTAs, one per SM, take 128 x 256 tiles of (expert, 128 rows,
+// 256 weight rows); the gated form's tile is 128 gate and the same 128 up
+// columns, so that one CTA holds both factors of 128 outputs, which are one
+// scale group of the result.  Three roles:
+//   - one thread keeps a ring of 128-deep K blocks (rows and weights, 48 KB) in
+//     flight by tiled TMA loads with 128-byte swizzle;
+//   - one thread issues the tensor core's E4M3 products of a block, four
+//     instructions of K = 32, into one of two tensor-memory tiles;
+//   - eight warps take each block's sums out of tensor memory and add them,
+//     times sx * sw, to running sums in registers (128 a thread), while the
+//     tensor core fills the other tile.  The scales change every 128 of K, so
+//     the running sum cannot stay in tensor memory.
+// Rows past an expert's segment are loaded (whatever they hold, products of
+// other rows do not see it) and never stored.
 #include "expert.cuh"
+#include "tcgen05.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTM = 32, kTN = 128;
+constexpr int kEpiWarps = 8;                     // warps that scale and store
+constexpr int kThreads = 32 * (kEpiWarps + 2);   // + loader warp, + product warp
+constexpr int kTM = 128, kTN = 256;              // tile: rows, weight rows
+constexpr int kABytes = kTM * 128, kBBytes = kTN * 128;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kStages = 4;
 
-__device__ __forceinline__ float warp_max(float v) {
+struct Shared {
+    uint64_t full[kStages], empty[kStages];  // ring of K blocks
+    uint64_t tfull[2], tempty[2];            // tensor-memory tiles
+    uint64_t xchg;                           // the two halves' group maxima
+    uint64_t drain;
+    uint32_t tmem;
+    int fail;
+    int issued;                              // K blocks requested, for the drain
+    int32_t scan[kThreads / 32];
+    float amax[2][2][kTM];                   // [tile parity][column half][row]
+};
+
+struct Tile {
+    int e, row, rows, n0;  // expert, first row of the tile, valid rows in it, first weight row
+};
+
+// Tile t of the list: experts in order; within one, row tiles run fastest, so
+// that CTAs working at the same time share weights.
+__device__ __forceinline__ Tile find_tile(const ExpertArgs &a, const int32_t *pre, int ntn, int t,
+                                          int cols) {
+    int lo = 0, hi = a.E;  // pre[lo] * ntn <= t < pre[hi] * ntn
+    const int m = t / ntn;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= m) lo = mid; else hi = mid;
+    }
+    const int local = t - pre[lo] * ntn, mt = pre[lo + 1] - pre[lo];
+    const int i = local % mt;
+    Tile r;
+    r.e = lo;
+    r.n0 = local / mt * cols;
+    r.row = expert_first(a, lo) + i * kTM;
+    r.rows = min(expert_rows(a, lo) - i * kTM, kTM);
+    return r;
+}
+
+// acc[2i], acc[2i+1] += v[2i] * s, v[2i+1] * s, two to an instruction.
+__device__ __forceinline__ void fma_scaled16(float *acc, const uint32_t (&v)[16], float s) {
+    uint64_t ss;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
 #pragma unroll
-    for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, d));
-    return v;
+    for (int i = 0; i < 8; ++i) {
+        uint64_t p, c;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(v[2 * i]), "r"(v[2 * i + 1]));
+        asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(acc[2 * i]), "f"(acc[2 * i + 1]));
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(p), "l"(ss));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[2 * i]), "=f"(acc[2 * i + 1]) : "l"(c));
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 template <bool GATED>
-__global__ void __launch_bounds__(kThreads) expert_kernel(const ExpertArgs a) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    float *xs = reinterpret_cast<float *>(smem);             // [128][kTM]: k-major
-    uint32_t *ws = reinterpret_cast<uint32_t *>(smem + 128 * kTM * 4);  // [2][kTN][32 + 1]
-    int32_t *pre = reinterpret_cast<int32_t *>(ws + 2 * kTN * 33);      // [E+1]
-    __shared__ int32_t tmp[kThreads / 32];
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+                  const ExpertArgs a) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    // [kStages] K blocks (the swizzle wants 1024-byte alignment), [E+1] tile prefix
+    uint8_t *smem = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
+    __shared__ Shared sh;
+    int32_t *pre = reinterpret_cast<int32_t *>(smem + kStages * kStageBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const volatile int *fail = &sh.fail;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.tfull[i], 1);
+            mbar_init(&sh.tempty[i], kEpiWarps);
+        }
+        mbar_init(&sh.xchg, kEpiWarps);
+        mbar_init(&sh.drain, 1);
+        sh.fail = 0;
+        sh.issued = 0;
+        mbar_init_fence();
+        tma_prefetch_map(&xmap);
+        tma_prefetch_map(&wmap);
+    }
+    // after the wait: a predecessor's blocks that still have to allocate tensor
+    // memory must find it free
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == kEpiWarps + 1) tmem_alloc_all(&sh.tmem);
+    tc_fence_before();
     block_exclusive_scan<kThreads>(
-        a.E, [&](int e) { return (expert_rows(a, e) + kTM - 1) / kTM; }, pre, tmp);
-    const int ntn = (a.N + kTN - 1) / kTN;
-    const long long total = (long long)pre[a.E] * ntn;
-    const int G = a.K >> 7, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int W = GATED ? 2 * a.N : a.N, NB = (W + 127) / 128;
-    for (long long t = blockIdx.x; t < total; t += gridDim.x) {
-        const int mt = (int)(t / ntn), n0 = (int)(t % ntn) * kTN;
-        int lo = 0, hi = a.E;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (pre[mid] <= mt) lo = mid; else hi = mid;
-        }
-        const int e = lo, first = expert_first(a, e), rows = expert_rows(a, e);
-        const int r0 = (mt - pre[e]) * kTM;
-        float acc[GATED ? 2 : 1][4][4] = {};
-        for (int g = 0; g < G; ++g) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < kTM * 32; i += kThreads) {
-                const int m = i >> 5, k4 = i & 31;
-                float4 f = make_float4(0, 0, 0, 0);
-                if (r0 + m < rows)
-                    f = e4m3x4_to_float4((uint32_t)ld_dep(reinterpret_cast<const int32_t *>(
-                        a.x + (size_t)(first + r0 + m) * a.K + g * 128 + k4 * 4)));
-                xs[(4 * k4) * kTM + m] = f.x;
-                xs[(4 * k4 + 1) * kTM + m] = f.y;
-                xs[(4 * k4 + 2) * kTM + m] = f.z;
-                xs[(4 * k4 + 3) * kTM + m] = f.w;
-            }
-#pragma unroll
-            for (int h = 0; h < (GATED ? 2 : 1); ++h)
-                for (int i = threadIdx.x; i < kTN * 32; i += kThreads) {
-                    const int n = i >> 5, k4 = i & 31;
-                    uint32_t v = 0;
-                    if (n0 + n < a.N)
-                        v = __ldg(reinterpret_cast<const uint32_t *>(
-                            a.w + ((size_t)e * W + h * a.N + n0 + n) * a.K + g * 128 + k4 * 4));
-                    ws[(h * kTN + n) * 33 + k4] = v;
-                }
-            __syncthreads();
-            float blk[GATED ? 2 : 1][4][4] = {};
-            for (int k4 = 0; k4 < 32; ++k4) {
-                float4 xr[4];  // [k][4 rows]
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    xr[q] = *reinterpret_cast<const float4 *>(xs + (4 * k4 + q) * kTM + ty * 4);
-#pragma unroll
-                for (int h = 0; h < (GATED ? 2 : 1); ++h)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 w = e4m3x4_to_float4(ws[(h * kTN + j * 32 + tx) * 33 + k4]);
-                        const float wk[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            blk[h][0][j] = fmaf(xr[q].x, wk[q], blk[h][0][j]);
-                            blk[h][1][j] = fmaf(xr[q].y, wk[q], blk[h][1][j]);
-                            blk[h][2][j] = fmaf(xr[q].z, wk[q], blk[h][2][j]);
-                            blk[h][3][j] = fmaf(xr[q].w, wk[q], blk[h][3][j]);
-                        }
+        a.E, [&](int e) { return (expert_rows(a, e) + kTM - 1) / kTM; }, pre, sh.scan);
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int cols = GATED ? 128 : kTN;  // output columns of a tile
+    const int ntn = (a.N + cols - 1) / cols, total = pre[a.E] * ntn;
+    const int G = a.K >> 7;
+
+    if (warp == kEpiWarps) {
+        // ---- loads ----
+        if (lane == 0) {
+            int it = 0;
+            for (int t = blockIdx.x; t < total && !*fail; t += gridDim.x) {
+                const Tile q = find_tile(a, pre, ntn, t, cols);
+                for (int g = 0; g < G; ++g, ++it) {
+                    const int s = it % kStages;
+                    if (it >= kStages && !mbar_wait_fast(&sh.empty[s], (it / kStages - 1) & 1, fail)) {
+                        sh.fail = 1;
+                        break;
                     }
-            }
-#pragma unroll
-            for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-                const float sw = __ldg(a.w_scales + ((size_t)e * NB + (h * a.N + n0) / 128) * G + g);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = r0 + ty * 4 + i;
-                    if (r >= rows) continue;
-                    const float s = sw * row_scale(a, first + r, e, g);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[h][i][j] = fmaf(blk[h][i][j], s, acc[h][i][j]);
+                    uint8_t *st = smem + s * kStageBytes;
+                    expect_bytes(&sh.full[s], kStageBytes);
+                    tma_load_2d(st, &xmap, g * 128, q.row, &sh.full[s]);
+                    tma_load_3d(st + kABytes, &wmap, g * 128, q.n0, q.e, &sh.full[s]);
+                    tma_load_3d(st + kABytes + kBBytes / 2, &wmap, g * 128,
+                                q.n0 + (GATED ? a.N : 128), q.e, &sh.full[s]);
                 }
             }
+            sh.issued = it;
         }
+    } else if (warp == kEpiWarps + 1) {
+        // ---- products ----
+        if (lane == 0) {
+            constexpr uint32_t instr = e4m3_instr(kTM, kTN);
+            int it = 0;
+            for (int t = blockIdx.x; t < total && !*fail; t += gridDim.x) {
+                for (int g = 0; g < G; ++g, ++it) {
+                    const int s = it % kStages, b = it & 1;
+                    if ((it >= 2 && !mbar_wait_fast(&sh.tempty[b], (it / 2 - 1) & 1, fail)) ||
+                        !mbar_wait_fast(&sh.full[s], (it / kStages) & 1, fail)) {
+                        sh.fail = 1;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t da = tile_desc(smem_addr(smem + s * kStageBytes));
+                    const uint64_t db = tile_desc(smem_addr(smem + s * kStageBytes + kABytes));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = r0 + ty * 4 + i;
-            if (r >= rows) continue;  // the same for the whole warp
-            float v[4], amax = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = acc[0][i][j];
-                if (GATED) v[j] = v[j] / (1.0f + expf(-v[j])) * acc[GATED ? 1 : 0][i][j];
-                amax = fmaxf(amax, fabsf(v[j]));
+                    for (int k = 0; k < 4; ++k)  // 32 bytes of each row further
+                        mma_e4m3(tmem + b * kTN, da + 2 * k, db + 2 * k, instr, k > 0);
+                    mma_commit(&sh.empty[s]);
+                    mma_commit(&sh.tfull[b]);
+                }
             }
-            const size_t at = (size_t)(first + r) * a.N + n0;
-            if (!GATED || a.out_quant == EP_QUANT_NONE) {
+            // tensor memory and the barriers outlive the last product
+            mma_commit(&sh.drain);
+            if (!mbar_wait(&sh.drain, 0, nullptr)) sh.fail = 1;
+        }
+    } else {
+        // ---- scales, running sums, outputs ----
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;  // column half, row of the tile
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        // the gated tile: this half's 64 gate columns, then the same 64 up columns
+        const uint32_t col0 = GATED ? half * 64 : half * 128, col1 = GATED ? 128 + half * 64 : col0 + 64;
+        const int NB = GATED ? a.N / 64 : (a.N + 127) / 128;
+        int it = 0, tiles = 0;
+        for (int t = blockIdx.x; t < total && !__any_sync(kFullMask, *fail); t += gridDim.x, ++tiles) {
+            const Tile q = find_tile(a, pre, ntn, t, cols);
+            const bool valid = r < q.rows;
+            const int b0 = q.n0 / 128 + (GATED ? 0 : min(half, NB - 1 - q.n0 / 128));
+            const float *sw0 = a.w_scales + ((size_t)q.e * NB + b0) * G;
+            const float *sw1 = GATED ? sw0 + (size_t)(a.N / 128) * G : sw0;
+            float acc[128];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (n0 + j * 32 + tx < a.N)
-                        static_cast<__nv_bfloat16 *>(a.out)[at + j * 32 + tx] = __float2bfloat16_rn(v[j]);
+            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+            float sx = valid ? row_scale(a, q.row + r, q.e, 0) : 0.0f;
+            float w0 = __ldg(sw0), w1 = GATED ? __ldg(sw1) : 0.0f;
+            bool ok = true;
+            for (int g = 0; g < G; ++g, ++it) {
+                const int b = it & 1;
+                const float s0 = sx * w0, s1 = GATED ? sx * w1 : s0;
+                if (g + 1 < G) {  // the next block's scales
+                    if (valid) sx = row_scale(a, q.row + r, q.e, g + 1);
+                    w0 = __ldg(sw0 + g + 1);
+                    if (GATED) w1 = __ldg(sw1 + g + 1);
+                }
+                ok = mbar_wait_fast(&sh.tfull[b], (it / 2) & 1, fail);
+                if (!__all_sync(kFullMask, ok)) {
+                    sh.fail = 1;
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t base = tmem + lanes + b * kTN;
+                uint32_t v[2][16];
+                tmem_ld16(base + col0, v[0]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    tmem_ld_wait(v[c & 1]);
+                    if (c < 7) {
+                        tmem_ld16(base + (c + 1 < 4 ? col0 + 16 * (c + 1) : col1 + 16 * (c - 3)),
+                                  v[(c + 1) & 1]);
+                    } else {  // everything is in registers
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.tempty[b]);
+                    }
+                    fma_scaled16(acc + 16 * c, v[c & 1], c < 4 ? s0 : s1);
+                }
+            }
+            if (!ok) break;
+            if constexpr (!GATED) {
+                const int c0 = q.n0 + half * 128;
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) +
+                                                       (size_t)(q.row + r) * a.N + c0);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (valid && c0 + 8 * j < a.N)
+                        st_v4(dst + j, make_uint4(pack_bf16(acc[8 * j], acc[8 * j + 1]),
+                                                  pack_bf16(acc[8 * j + 2], acc[8 * j + 3]),
+                                                  pack_bf16(acc[8 * j + 4], acc[8 * j + 5]),
+                                                  pack_bf16(acc[8 * j + 6], acc[8 * j + 7])));
             } else {
-                amax = warp_max(amax);
+                float amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    const float g = acc[i];
+                    acc[i] = __fdividef(g, 1.0f + __expf(-g)) * acc[64 + i];
+                    amax = fmaxf(amax, fabsf(acc[i]));
+                }
+                const size_t at = (size_t)(q.row + r) * a.N + q.n0 + half * 64;
+                if (a.out_quant == EP_QUANT_NONE) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (valid)
+                            st_v4(dst + j, make_uint4(pack_bf16(acc[8 * j], acc[8 * j + 1]),
+                                                      pack_bf16(acc[8 * j + 2], acc[8 * j + 3]),
+                                                      pack_bf16(acc[8 * j + 4], acc[8 * j + 5]),
+                                                      pack_bf16(acc[8 * j + 6], acc[8 * j + 7])));
+                    continue;
+                }
+                // the row's other 64 columns are with the other half's warp
+                sh.amax[tiles & 1][half][r] = amax;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.xchg);
+                ok = mbar_wait_fast(&sh.xchg, tiles & 1, fail);
+                if (!__all_sync(kFullMask, ok)) {
+                    sh.fail = 1;
+                    break;
+                }
+                amax = fmaxf(amax, sh.amax[tiles & 1][half ^ 1][r]);
                 const float s = group_scale(amax);
                 const int e8 = ue8m0_exponent(s);
+                const float inv = a.out_quant == EP_QUANT_FP8_F32 ? __frcp_rn(s) : exp_reciprocal(e8);
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + at);
+                uint32_t p[16];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float q = a.out_quant == EP_QUANT_FP8_F32
-                                        ? __fdiv_rn(v[j], s)
-                                        : __fmul_rn(v[j], exp_reciprocal(e8));
-                    static_cast<uint8_t *>(a.out)[at + j * 32 + tx] =
-                        __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+                for (int j = 0; j < 16; ++j)
+                    p[j] = fp8x4(acc[4 * j] * inv, acc[4 * j + 1] * inv, acc[4 * j + 2] * inv,
+                                 acc[4 * j + 3] * inv);
+                if (valid) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        st_v4(dst + j, make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]));
+                    if (half == 0) store_out_scale(a, q.row + r, q.e, q.n0 / 128, s, e8);
                 }
-                if (tx == 0) store_out_scale(a, first + r, e, n0 / 128, s, e8);
             }
         }
     }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (sh.fail) {
+        if (threadIdx.x == 0) raise_status(a.status, EP_ERR_TIMEOUT);
+        // let the loads in flight land before the shared memory goes
+        if (threadIdx.x < kStages) {
+            const int last = sh.issued - 1 - (int)threadIdx.x;
+            if (last >= 0) mbar_wait(&sh.full[last % kStages], (last / kStages) & 1, nullptr);
+        }
+        __syncthreads();
+    }
+    if (warp == kEpiWarps + 1) {
+        tc_fence_after();
+        tmem_free_all(tmem);
+    }
+}
+
+// The driver's encoder, looked up once (the library links no libcuda).
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// [d2][d1][d0] bytes in boxes of `box` rows of 128 bytes, 128-byte swizzle.
+bool encode(CUtensorMap *map, const void *p, int64_t d0, int64_t d1, int64_t d2, int box) {
+    const EncodeTiled fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+    const cuuint64_t strides[2] = {(cuuint64_t)d0, (cuuint64_t)(d0 * d1)};
+    const cuuint32_t boxes[3] = {128, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, d2 ? 3 : 2, const_cast<void *>(p), dims, strides,
+              boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
 cudaError_t launch_expert(const ExpertArgs &a, bool gated, cudaStream_t stream) {
-    const size_t smem = 128 * kTM * 4 + 2 * kTN * 33 * 4 + (a.E + 1) * 4;
+    CUtensorMap xmap, wmap;
+    if (!encode(&xmap, a.x, a.K, a.rows_cap, 0, kTM) ||
+        !encode(&wmap, a.w, a.K, gated ? 2 * a.N : a.N, a.E, kTN / 2))
+        return cudaErrorInvalidValue;
+    const size_t smem = 1024 + kStages * kStageBytes + (a.E + 1) * 4;
     auto k = gated ? expert_kernel<true> : expert_kernel<false>;
     const cudaError_t err = allow_dynamic_smem(k, smem);
     if (err != cudaSuccess) return err;
-    return launch_kernel(k, 2 * sm_count(), kThreads, smem, stream, true, a);
+    return launch_kernel(k, sm_count(), kThreads, smem, stream, true, xmap, wmap, a);
 }
 
 }  // namespace ep
