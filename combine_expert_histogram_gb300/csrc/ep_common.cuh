@@ -149,6 +149,14 @@ __device__ __forceinline__ void st_v4(void *p, uint4 v) {
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+// Two fp32 -> packed bf16, round to nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+
 // Exclusive scan over n values produced by value(i), by one CTA of NT threads:
 // out[i] = value(0) + ... + value(i-1) for i in [0, n], out[n] = total.  Thread t
 // owns the contiguous run [t*ipt, (t+1)*ipt), ipt = ceil(n/NT).  `tmp` holds

@@ -17,12 +17,6 @@ namespace {
 
 constexpr int kMaxThreads = 1024;
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 template <int Q, int V>
 __global__ void __launch_bounds__(kMaxThreads)
     rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float eps,

@@ -148,6 +148,34 @@ def test_the_same_bits_every_time():
         assert torch.equal(first, ep.ep_moe_decode(*c.dev))
 
 
+def test_sums_keep_24_bits():
+    """Integers next to cancelling pairs of 448 * 448: any fp32 order of the sums
+    is exact, so the up product, its 8-bit form (values and scales chosen to be
+    representable) and the down product have no error but the last rounding."""
+    T, H, I = 8, 256, 128
+    g = torch.Generator().manual_seed(20)
+    x = torch.zeros((T, H))
+    up, gate = torch.zeros((I, H)), torch.zeros((I, H))
+    for b in (0, 128):
+        at = torch.randperm(126, generator=g)[:8] + 2 + b
+        x[:, at] = 448.0
+        up[:, at[:4]], up[:, at[4:]] = 448.0, -448.0
+    x[:, 0] = 1.0
+    gate[:, 0] = 64.0  # silu(64) = 64 in fp32
+    x[:, 1] = 1.0
+    v = torch.cat([torch.arange(-15, 16), torch.arange(16, 32, 2)]).float()
+    up[:, 1] = v[torch.randint(0, len(v), (I,), generator=g)]
+    up[5, 1] = 448.0  # makes the scale of the gated group 64
+    w2 = torch.randint(-4, 5, (H, I), generator=g).float()
+    f8 = lambda t: t.to(torch.float8_e4m3fn).view(torch.uint8)[None].cuda()  # noqa: E731
+    one = torch.ones
+    out = ep.ep_moe_decode(x.bfloat16().cuda(), torch.zeros((T, 1), dtype=torch.int32).cuda(),
+                           one(T, 1).cuda(), f8(torch.cat([gate, up])), one(1, 2, 2).cuda(),
+                           f8(w2), one(1, 2, 1).cuda())
+    want = 64 * (up[:, 1].double() @ w2.double().T)
+    assert torch.equal(out.cpu(), want.bfloat16().expand(T, H))
+
+
 def test_two_streams_with_a_workspace_each():
     cs = [Case(8, 16, 4, 1024, 512, seed=s) for s in (11, 12)]
     one = [ep.ep_moe_decode(*c.dev) for c in cs]
