@@ -435,7 +435,7 @@ ep_status_t ep_expert_swiglu(const ep_layout_t *L, const void *rows, const void 
 size_t ep_moe_decode_workspace_bytes(int32_t T, int32_t K, int32_t E, int32_t hidden,
                                      int32_t inter) {
     if (check_moe(T, K, E, hidden, inter) != EP_OK) return 0;
-    return moe_workspace_bytes(T, K, hidden, inter);
+    return moe_workspace_bytes(T, K, E, hidden, inter);
 }
 
 ep_status_t ep_moe_decode(const void *x, const void *x_scales, ep_quant_t quant,
@@ -452,7 +452,7 @@ ep_status_t ep_moe_decode(const void *x, const void *x_scales, ep_quant_t quant,
         return EP_ERR_INVALID_ARG;
     if (T == 0) return EP_OK;
     if (!x || !topk_idx || !topk_w || !w13 || !w13_scales || !w2 || !w2_scales || !out || !status ||
-        !workspace || workspace_bytes < moe_workspace_bytes(T, K, hidden, inter))
+        !workspace || workspace_bytes < moe_workspace_bytes(T, K, E, hidden, inter))
         return EP_ERR_INVALID_ARG;
     if (quant == EP_QUANT_NONE ? x_scales != nullptr : (!x_scales || !aligned(x_scales, 4)))
         return EP_ERR_INVALID_ARG;

@@ -210,12 +210,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t base = tmem + lanes + b * kTN;
                 uint32_t v[2][16];
-                tmem_ld16(base + col0, v[0]);
+                tmem_ld(base + col0, v[0]);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     tmem_ld_wait(v[c & 1]);
                     if (c < 7) {
-                        tmem_ld16(base + (c + 1 < 4 ? col0 + 16 * (c + 1) : col1 + 16 * (c - 3)),
+                        tmem_ld(base + (c + 1 < 4 ? col0 + 16 * (c + 1) : col1 + 16 * (c - 3)),
                                   v[(c + 1) & 1]);
                     } else {  // everything is in registers
                         tc_fence_before();
@@ -321,24 +321,33 @@ EncodeTiled encoder() {
     return fn;
 }
 
-// [d2][d1][d0] bytes in boxes of `box` rows of 128 bytes, 128-byte swizzle.
-bool encode(CUtensorMap *map, const void *p, int64_t d0, int64_t d1, int64_t d2, int box) {
+}  // namespace
+
+bool encode_bytes(CUtensorMap *map, const void *p, int rank, const int64_t *dims,
+                  const int64_t *strides, const int *box) {
     const EncodeTiled fn = encoder();
     if (!fn) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
-    const cuuint64_t strides[2] = {(cuuint64_t)d0, (cuuint64_t)(d0 * d1)};
-    const cuuint32_t boxes[3] = {128, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, d2 ? 3 : 2, const_cast<void *>(p), dims, strides,
-              boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5], ones[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = (cuuint64_t)dims[i];
+        b[i] = (cuuint32_t)box[i];
+        ones[i] = 1;
+        if (i + 1 < rank) s[i] = (cuuint64_t)strides[i];
+    }
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(p), d, s, b,
+              ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
-
 cudaError_t launch_expert(const ExpertArgs &a, bool gated, cudaStream_t stream) {
     CUtensorMap xmap, wmap;
-    if (!encode(&xmap, a.x, a.K, a.rows_cap, 0, kTM) ||
-        !encode(&wmap, a.w, a.K, gated ? 2 * a.N : a.N, a.E, kTN / 2))
+    const int64_t xdims[2] = {a.K, a.rows_cap}, xstride[1] = {a.K};
+    const int64_t W = gated ? 2 * a.N : a.N;
+    const int64_t wdims[3] = {a.K, W, a.E}, wstride[2] = {a.K, W * a.K};
+    const int xbox[2] = {128, kTM}, wbox[3] = {128, kTN / 2, 1};
+    if (!encode_bytes(&xmap, a.x, 2, xdims, xstride, xbox) ||
+        !encode_bytes(&wmap, a.w, 3, wdims, wstride, wbox))
         return cudaErrorInvalidValue;
     const size_t smem = 1024 + kStages * kStageBytes + (a.E + 1) * 4;
     auto k = gated ? expert_kernel<true> : expert_kernel<false>;

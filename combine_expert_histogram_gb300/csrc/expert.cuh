@@ -42,7 +42,7 @@ struct MoeArgs {
     void *out;                // bf16 [T, H]
     int32_t *status;
 };
-size_t moe_workspace_bytes(int T, int K, int H, int I);
+size_t moe_workspace_bytes(int T, int K, int E, int H, int I);
 cudaError_t launch_moe_decode(const MoeArgs &a, void *workspace, cudaStream_t stream);
 cudaError_t launch_expert(const ExpertArgs &a, bool gated, cudaStream_t stream);
 

@@ -7,41 +7,47 @@
 // body (rows of W13 against the tokens, rows of W2 against the gated results)
 // and a small one for the weighted sum; all launched as programmatic
 // dependents.  Each CTA groups the T*K entries by expert itself (at most 1024,
-// in shared memory) into chunks of one expert and up to 8 or 16 entries; the
-// (chunk, 16 weight rows) units are split evenly over one persistent CTA per
-// SM, which walks a contiguous run of them:
-//   - a loader warp keeps a ring of (16 rows x 1024 bytes) pieces in flight with
-//     one bulk copy per row.  It never waits for the previous kernel (weights
-//     are not its output), so the second kernel's ring fills while the first
-//     one drains;
-//   - eight warps multiply, each one 128-wide block of the piece, on the
-//     m16n8k32 E4M3 instruction: the weight rows are its 16 rows, the entries
-//     its 8 columns.  Sixteen-row units keep the SMs' shares within a few
-//     percent of each other for single tokens, which 128-row tcgen05 tiles
-//     would not, and the rate of this path is a small part of its peak.  Block
-//     sums are scaled into fp32 registers, and the warps' parts meet in shared
-//     memory at the end of a unit, in a fixed order.
-// The inner order of a product is permuted (each lane takes 16 consecutive
-// bytes of its row), the same for weights and entries, so that shared memory
-// is read 16 bytes a lane; rows are 64 bytes off a multiple of 128 apart, which
-// makes those reads free of bank conflicts.
+// in shared memory) into chunks of one expert and up to `cols` entries.  The
+// units of work, (chunk, 128 weight rows, a part of their length), are split
+// evenly over one persistent CTA per SM, which walks a contiguous run of them:
+//   - a loader thread keeps a ring of 16 KB stages (128 rows x 128 bytes of the
+//     weights) in flight, one tiled TMA copy each.  It never waits for the
+//     previous kernel (weights are not its output), so the second kernel's ring
+//     fills while the first one drains;
+//   - four warps quantise a chunk's entries into shared memory when the run
+//     comes to the next expert;
+//   - one thread issues the tensor core's E4M3 products: the weight rows are the
+//     128 rows of A, the entries the columns of B (at least 16; those past the
+//     chunk are whatever follows in shared memory, and are never read).  With
+//     the entries as A and 64 weight rows as columns, twice as many instructions
+//     of about 165 clocks each held the kernel to 3.6 TB/s; the m16n8k32 E4M3
+//     instruction, which converts its operands on the vector pipes, to 2.8;
+//   - the same four warps take each 128-deep block sum out of tensor memory, one
+//     weight row a thread, and add it, scaled, to fp32 registers.
+// Partial sums over parts of a row's length are added where they are read, in
+// the order of the parts.
 #include "expert.cuh"
+#include "tcgen05.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kWarps = 8;                        // multiplying warps
-constexpr int kThreads = 32 * (kWarps + 1);      // + loader
-constexpr int kRows = 16;                        // weight rows of a unit
-constexpr int kPiece = 128 * kWarps;             // bytes of a row in one piece
-constexpr int kRowStride = kPiece + 64;
-constexpr int kStageBytes = kRows * kRowStride;
+constexpr int kWarps = 4;                        // quantise, scale and store
+constexpr int kThreads = 32 * (kWarps + 2);      // + loader, + products
+constexpr int kRows = 128;                       // weight rows of a unit
+constexpr int kStageBytes = kRows * 128;
 constexpr int kMaxStages = 12;
+constexpr int kMaxCols = 32;                     // entries of a chunk
+constexpr int kTiles = 8;                        // tensor-memory tiles of kMaxCols columns
 constexpr int kMaxEntries = EP_MOE_DECODE_MAX_ENTRIES;
-constexpr int kSmemMax = 227 * 1024 - 2048;      // less the static part
+constexpr int kSmemMax = 227 * 1024 - 1024;      // less the reserve for alignment
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t tfull[kTiles], tempty[kTiles];
+    uint64_t columns;              // a chunk's entries are in shared memory
+    uint64_t drain;
+    uint32_t tmem;
     int fail;
     int issued;
     int32_t scan[kThreads / 32];
@@ -108,34 +114,26 @@ __device__ void group_entries(const MoeArgs &a, int cols, int32_t *tmp, Shared &
     __syncthreads();
 }
 
-__device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                            uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
-        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Unit u of the list: its chunk and its first weight row / 16.
+// Unit u of the list: its chunk, first weight row, and 128-wide blocks [g0, g1).
 struct Unit {
     uint32_t chunk;
-    int rows16;
+    int row, part, g0, g1;
 };
-struct Units {
-    int per_chunk;  // units of one chunk: (2I or H) / 16
-    __device__ __forceinline__ Unit at(const Shared &sh, int u) const {
-        const int c = u / per_chunk;
-        return {sh.chunk[c], u - c * per_chunk};
-    }
-};
+__device__ __forceinline__ Unit unit_at(const Shared &sh, int row_units, int parts, int G, int u) {
+    const int c = u / (row_units * parts), v = u - c * row_units * parts;
+    const int r = v / parts, s = v - r * parts;
+    return {sh.chunk[c], r * kRows, s, G * s / parts, G * (s + 1) / parts};
+}
 
-// The chunk's entries as E4M3 columns in shared memory: xq[col][D + 64] and
-// xs[group][cols].  UP: the tokens' x in any of its formats; else the gated
-// results in fp32.  Half a warp takes a 1x128 group, 8 values a lane.
+// The chunk's entries as E4M3 rows in shared memory: xq[group][cols / 8] atoms of
+// 8 rows x 128 bytes in 128-byte swizzle (16-byte piece j of row r lies at piece
+// j ^ r), and xs[group][cols].  UP: the tokens' x in any of its formats; else
+// silu(gate) * up of the first kernel's sums gu[part][T*K][2D].  Half a warp
+// takes a 1x128 group, 8 values a lane.
 template <bool UP>
-__device__ __forceinline__ void load_columns(const MoeArgs &a, const float *h, uint32_t chunk,
-                                             const Shared &sh, int D, int cols, uint8_t *xq,
-                                             float *xs) {
+__device__ __forceinline__ void load_columns(const MoeArgs &a, const float *gu, int gu_parts,
+                                             uint32_t chunk, const Shared &sh, int D, int cols,
+                                             uint8_t *xq, float *xs) {
     constexpr int kBatch = 4;
     const int first = chunk >> 10 & 1023, n = (int)(chunk >> 20);
     const int G = D >> 7, items = n * G;
@@ -158,10 +156,25 @@ __device__ __forceinline__ void load_columns(const MoeArgs &a, const float *h, u
                 const int entry = sh.entry[first + col], t = UP ? entry / a.K : entry;
                 const size_t at = (size_t)t * D + g * 128 + 8 * l;
                 if (!UP) {
-                    const uint4 lo = ld_dep_v4(h + at), hi = ld_dep_v4(h + at + 4);
-                    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    const float *p = gu + (size_t)entry * 2 * D + g * 128 + 8 * l;
+                    float up[8] = {};
+                    for (int s = 0; s < gu_parts; ++s, p += (size_t)a.T * a.K * 2 * D) {
+                        const uint4 w[4] = {ld_dep_v4(p), ld_dep_v4(p + 4), ld_dep_v4(p + D),
+                                            ld_dep_v4(p + D + 4)};
 #pragma unroll
-                    for (int m = 0; m < 8; ++m) v[b][m] = __uint_as_float(w[m]);
+                        for (int m = 0; m < 2; ++m) {
+                            const uint32_t gw[4] = {w[m].x, w[m].y, w[m].z, w[m].w};
+                            const uint32_t uw[4] = {w[2 + m].x, w[2 + m].y, w[2 + m].z, w[2 + m].w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                v[b][4 * m + j] += __uint_as_float(gw[j]);
+                                up[4 * m + j] += __uint_as_float(uw[j]);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int m = 0; m < 8; ++m)
+                        v[b][m] = __fdividef(v[b][m], 1.0f + __expf(-v[b][m])) * up[m];
                 } else if (a.quant == EP_QUANT_NONE) {
                     const uint4 x = ld_dep_v4(static_cast<const uint16_t *>(a.x) + at);
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -202,184 +215,175 @@ __device__ __forceinline__ void load_columns(const MoeArgs &a, const float *h, u
                                   fp8x4(v[b][4], v[b][5], v[b][6], v[b][7]));
             }
             if (i < items) {
-                *reinterpret_cast<uint2 *>(xq + (size_t)col * (D + 64) + g * 128 + 8 * l) = q[b];
+                *reinterpret_cast<uint2 *>(xq + (g * cols + col) * 128 +
+                                           (((l >> 1) ^ (col & 7)) << 4) + 8 * (l & 1)) = q[b];
                 if (l == 0) xs[g * cols + col] = s[b];
             }
         }
     }
 }
 
-// UP: dst = h [T*K, I] fp32 from x, gate row i and up row i in one unit (8 of
-// each); else dst = y [T*K, H] fp32 from h.  NB: blocks of 8 columns.
-template <bool UP, int NB>
+// dst[part][T*K][R] = rows of W13 (UP: R = 2I, D = H) or of W2 (R = H, D = I)
+// against the entries, fp32.
+template <bool UP>
 __global__ void __launch_bounds__(kThreads, 1)
-    rows_kernel(const MoeArgs a, const float *h, float *dst, int stages) {
-    extern __shared__ __align__(128) uint8_t smem[];
+    rows_kernel(const __grid_constant__ CUtensorMap wmap, const MoeArgs a, const float *gu,
+                int gu_parts, float *dst, int parts, int cols, int stages) {
+    extern __shared__ __align__(16) uint8_t raw[];
     __shared__ Shared sh;
-    constexpr int kCols = 8 * NB;
-    const int D = UP ? a.H : a.I, G = D >> 7;
+    const int D = UP ? a.H : a.I, R = UP ? 2 * a.I : a.H, G = D >> 7;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint8_t *ring = smem;
-    float *red = reinterpret_cast<float *>(ring + stages * kStageBytes);  // [2][kWarps][NB][128]
-    float *xs = red + 2 * kWarps * NB * 128;                              // [G][kCols]
-    uint8_t *xq = reinterpret_cast<uint8_t *>(xs + G * kCols);            // [kCols][D + 64]
+    // entries first: the products' unused columns read on into the ring
+    uint8_t *xq = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
+    uint8_t *ring = xq + G * cols * 128;
+    float *xs = reinterpret_cast<float *>(ring + stages * kStageBytes);  // [G][cols]
     const volatile int *fail = &sh.fail;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], kWarps);
+            mbar_init(&sh.empty[i], 1);
         }
+        for (int i = 0; i < kTiles; ++i) {
+            mbar_init(&sh.tfull[i], 1);
+            mbar_init(&sh.tempty[i], kWarps);
+        }
+        mbar_init(&sh.columns, kWarps);
+        mbar_init(&sh.drain, 1);
         sh.fail = 0;
         sh.issued = 0;
         mbar_init_fence();
+        tma_prefetch_map(&wmap);
     }
     if (UP) {  // the ids may be the previous kernel's; for the second kernel they are complete
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = EP_OK;
-        __syncthreads();
     }
+    // the first kernel lets the second start only once it holds its tensor memory
+    if (warp == kWarps + 1) tmem_alloc_all(&sh.tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    group_entries(a, kCols, reinterpret_cast<int32_t *>(ring), sh);
-    const Units units = {UP ? a.I / 8 : a.H / 16};
-    const long long total = (long long)sh.chunks * units.per_chunk;
+    const uint32_t tmem = sh.tmem;
+    group_entries(a, cols, reinterpret_cast<int32_t *>(ring), sh);
+    const int row_units = R / kRows;
+    const long long total = (long long)sh.chunks * row_units * parts;
     const int u0 = (int)(total * blockIdx.x / gridDim.x), u1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
-    const int pieces = (D + kPiece - 1) / kPiece;
 
     if (warp == kWarps) {
-        // ---- loads: lane r copies row r of each piece ----
-        fence_proxy_async_smem();  // the ring held the grouping's counters
-        int it = 0;
-        for (int u = u0; u < u1 && !__any_sync(kFullMask, *fail); ++u) {
-            const Unit un = units.at(sh, u);
-            const size_t e = un.chunk & 1023;
-            const uint8_t *src;
-            if (UP)  // 8 gate rows, then the same 8 up rows
-                src = a.w13 + (e * 2 * a.I + (size_t)un.rows16 * 8 + (lane & 7) + (lane & 8 ? a.I : 0)) * D;
-            else
-                src = a.w2 + (e * a.H + (size_t)un.rows16 * 16 + (lane & 15)) * D;
-            for (int p = 0; p < pieces; ++p, ++it) {
-                const int s = it % stages;
-                bool ok = it < stages || mbar_wait(&sh.empty[s], (it / stages - 1) & 1, fail);
-                if (!__all_sync(kFullMask, ok)) {
-                    sh.fail = 1;
-                    break;
+        // ---- loads ----
+        if (lane == 0) {
+            fence_proxy_async_smem();  // the ring held the grouping's counters
+            int it = 0;
+            for (int u = u0; u < u1 && !*fail; ++u) {
+                const Unit un = unit_at(sh, row_units, parts, G, u);
+                for (int g = un.g0; g < un.g1; ++g, ++it) {
+                    const int s = it % stages;
+                    if (it >= stages && !mbar_wait_fast(&sh.empty[s], (it / stages - 1) & 1, fail)) {
+                        sh.fail = 1;
+                        break;
+                    }
+                    expect_bytes(&sh.full[s], kStageBytes);
+                    tma_load_3d(ring + s * kStageBytes, &wmap, g * 128, un.row, un.chunk & 1023,
+                                &sh.full[s]);
                 }
-                const uint32_t bytes = min(kPiece, D - p * kPiece);
-                if (lane == 0)
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
-                                     smem_addr(&sh.full[s])),
-                                 "r"(bytes * kRows)
-                                 : "memory");
-                __syncwarp();
-                if (lane < kRows)
-                    asm volatile(
-                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
-                        "[%1], %2, [%3];" ::"r"(smem_addr(ring + s * kStageBytes + lane * kRowStride)),
-                        "l"(src + (size_t)p * kPiece), "r"(bytes), "r"(smem_addr(&sh.full[s]))
-                        : "memory");
             }
+            sh.issued = it;
         }
-        if (lane == 0) sh.issued = it;
+    } else if (warp == kWarps + 1) {
+        // ---- products ----
+        if (lane == 0) {
+            const uint32_t instr = e4m3_instr(kRows, cols < 16 ? 16 : cols);
+            int it = 0, loaded = 0;
+            uint32_t have = 0xffffffffu;
+            for (int u = u0; u < u1 && !*fail; ++u) {
+                const Unit un = unit_at(sh, row_units, parts, G, u);
+                if (un.chunk != have) {
+                    have = un.chunk;
+                    if (!mbar_wait_fast(&sh.columns, loaded & 1, fail)) {
+                        sh.fail = 1;
+                        break;
+                    }
+                    ++loaded;
+                }
+                for (int g = un.g0; g < un.g1; ++g, ++it) {
+                    const int s = it % stages, b = it % kTiles;
+                    if ((it >= kTiles && !mbar_wait_fast(&sh.tempty[b], (it / kTiles - 1) & 1, fail)) ||
+                        !mbar_wait_fast(&sh.full[s], (it / stages) & 1, fail)) {
+                        sh.fail = 1;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t da = tile_desc(smem_addr(ring + s * kStageBytes));
+                    const uint64_t db = tile_desc(smem_addr(xq + g * cols * 128));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_e4m3(tmem + b * kMaxCols, da + 2 * j, db + 2 * j, instr, j > 0);
+                    mma_commit(&sh.empty[s]);
+                    mma_commit(&sh.tfull[b]);
+                }
+            }
+            // tensor memory and the barriers outlive the last product
+            mma_commit(&sh.drain);
+            if (!mbar_wait(&sh.drain, 0, nullptr)) sh.fail = 1;
+        }
     } else {
-        // ---- products.  After a wait that ran out the loops go on (every later
-        // wait returns at once), so that all warps meet at the barriers ----
+        // ---- entries, scales, sums.  After a wait that ran out the loops go on
+        // (every later wait returns at once), so that all warps meet at the barriers ----
         if (!UP) asm volatile("griddepcontrol.wait;" ::: "memory");
-        const int g = lane >> 2, t = lane & 3;
-        const int gb = UP ? a.I / 128 : 0;  // scale rows from a gate block to its up block
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         uint32_t have = 0xffffffffu;  // the chunk whose entries are in xq
         int it = 0;
         for (int u = u0; u < u1; ++u) {
-            const Unit un = units.at(sh, u);
+            const Unit un = unit_at(sh, row_units, parts, G, u);
             const int e = un.chunk & 1023, first = un.chunk >> 10 & 1023, n = (int)(un.chunk >> 20);
-            const int block = un.rows16 / (UP ? 16 : 8);
-            const float *sw = UP ? a.w13_scales + ((size_t)e * 2 * gb + block) * G
-                                 : a.w2_scales + ((size_t)e * (a.H >> 7) + block) * G;
-            float w0 = 0.0f, w1 = 0.0f;
-            if (warp < G) {
-                w0 = __ldg(sw + warp);
-                w1 = UP ? __ldg(sw + (size_t)gb * G + warp) : w0;
-            }
+            const float *sw = (UP ? a.w13_scales : a.w2_scales) +
+                              ((size_t)e * row_units + (un.row >> 7)) * G;
+            float w = __ldg(sw + un.g0);
             if (un.chunk != have) {
-                load_columns<UP>(a, h, un.chunk, sh, D, kCols, xq, xs);
-                have = un.chunk;
+                consumer_sync();  // every warp is done with the old entries
+                load_columns<UP>(a, gu, gu_parts, un.chunk, sh, D, cols, xq, xs);
+                fence_proxy_async_smem();
                 consumer_sync();
+                if (lane == 0) mbar_arrive(&sh.columns);
+                have = un.chunk;
             }
-            float acc[NB][4] = {};
-            for (int p = 0; p < pieces; ++p, ++it) {
-                const int s = it % stages, kb = p * kWarps + warp;
-                const float s0 = w0, s1 = w1;
-                if (kb + kWarps < G) {
-                    w0 = __ldg(sw + kb + kWarps);
-                    w1 = UP ? __ldg(sw + (size_t)gb * G + kb + kWarps) : w0;
+            float acc[kMaxCols];
+#pragma unroll
+            for (int i = 0; i < kMaxCols; ++i) acc[i] = 0.0f;
+            for (int g = un.g0; g < un.g1; ++g, ++it) {
+                const int b = it % kTiles;
+                const float s = w;
+                if (g + 1 < un.g1) w = __ldg(sw + g + 1);
+                const bool ok = mbar_wait_fast(&sh.tfull[b], (it / kTiles) & 1, fail);
+                if (!__all_sync(kFullMask, ok)) sh.fail = 1;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kMaxCols; c += 8) {
+                    if (c >= n) break;
+                    uint32_t v[8];
+                    tmem_ld(tmem + lanes + b * kMaxCols + c, v);
+                    const float4 x0 = *reinterpret_cast<const float4 *>(xs + g * cols + c);
+                    const float4 x1 = *reinterpret_cast<const float4 *>(xs + g * cols + c + 4);
+                    const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+                    tmem_ld_wait(v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        acc[c + i] = fmaf(__uint_as_float(v[i]), s * x[i], acc[c + i]);
                 }
-                if (!mbar_wait(&sh.full[s], (it / stages) & 1, fail)) sh.fail = 1;
-                if (kb < G) {
-                    const uint8_t *ap = ring + s * kStageBytes + g * kRowStride + warp * 128 + t * 16;
-                    uint4 lo[2], hi[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        lo[i] = *reinterpret_cast<const uint4 *>(ap + 64 * i);
-                        hi[i] = *reinterpret_cast<const uint4 *>(ap + 64 * i + 8 * kRowStride);
-                    }
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        if (nb && n <= 8 * nb) break;
-                        const uint8_t *bp = xq + (size_t)(8 * nb + g) * (D + 64) + kb * 128 + t * 16;
-                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint4 b = *reinterpret_cast<const uint4 *>(bp + 64 * i);
-                            mma_16x8x32(d, lo[i].x, hi[i].x, lo[i].y, hi[i].y, b.x, b.y);
-                            mma_16x8x32(d, lo[i].z, hi[i].z, lo[i].w, hi[i].w, b.z, b.w);
-                        }
-                        const float2 x = *reinterpret_cast<const float2 *>(xs + kb * kCols + 8 * nb + 2 * t);
-                        acc[nb][0] = fmaf(d[0], s0 * x.x, acc[nb][0]);
-                        acc[nb][1] = fmaf(d[1], s0 * x.y, acc[nb][1]);
-                        acc[nb][2] = fmaf(d[2], s1 * x.x, acc[nb][2]);
-                        acc[nb][3] = fmaf(d[3], s1 * x.y, acc[nb][3]);
-                    }
-                }
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.empty[s]);
+                if (lane == 0) mbar_arrive(&sh.tempty[b]);
             }
-            // the warps' parts, [row][col] of each block of columns; the buffer of
-            // the unit before last is free, all its readers have met at a barrier since
-            float *mine = red + ((u & 1) * kWarps + warp) * NB * 128;
+            float *out = dst + (size_t)un.part * a.T * a.K * R + un.row + threadIdx.x;
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                *reinterpret_cast<float2 *>(mine + nb * 128 + g * 8 + 2 * t) = make_float2(acc[nb][0], acc[nb][1]);
-                *reinterpret_cast<float2 *>(mine + nb * 128 + (g + 8) * 8 + 2 * t) = make_float2(acc[nb][2], acc[nb][3]);
-            }
-            consumer_sync();
-            const float *part = red + (u & 1) * kWarps * NB * 128;
-            // thread -> (row, column), rows fastest: an entry's outputs are consecutive
-            if (UP) {
-                const int r = threadIdx.x & 7, c = threadIdx.x >> 3;
-                if (c < kCols && c < n) {
-                    const float *q = part + (c >> 3) * 128 + r * 8 + (c & 7);
-                    float gate = 0.0f, up = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) {
-                        gate += q[w * NB * 128];
-                        up += q[w * NB * 128 + 64];
-                    }
-                    dst[(size_t)sh.entry[first + c] * a.I + un.rows16 * 8 + r] =
-                        __fdividef(gate, 1.0f + __expf(-gate)) * up;
-                }
-            } else {
-                const int r = threadIdx.x & 15, c = threadIdx.x >> 4;
-                if (c < kCols && c < n) {
-                    const float *q = part + (c >> 3) * 128 + r * 8 + (c & 7);
-                    float y = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) y += q[w * NB * 128];
-                    dst[(size_t)sh.entry[first + c] * a.H + un.rows16 * 16 + r] = y;
-                }
-            }
+            for (int i = 0; i < kMaxCols; ++i)
+                if (i < n) out[(size_t)sh.entry[first + i] * R] = acc[i];
         }
     }
     __syncwarp();
+    tc_fence_before();
     __syncthreads();
     if (sh.fail) {
         if (threadIdx.x == 0) raise_status(a.status, EP_ERR_TIMEOUT);
@@ -390,10 +394,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncthreads();
     }
+    if (warp == kWarps + 1) {
+        tc_fence_after();
+        tmem_free_all(tmem);
+    }
 }
 
-// out[t] = sum over k of w[t,k] * y[t*K + k], 8 columns a thread.
-__global__ void __launch_bounds__(128) sum_kernel(const MoeArgs a, const float *y) {
+// out[t] = sum over k of w[t,k] * (sum over parts of y[part][t*K + k]), 8 columns a thread.
+__global__ void __launch_bounds__(128) sum_kernel(const MoeArgs a, const float *y, int parts) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int per = a.H / 8, i = blockIdx.x * 128 + threadIdx.x;
     const int t = i / per, c = i - t * per;
@@ -404,51 +412,88 @@ __global__ void __launch_bounds__(128) sum_kernel(const MoeArgs a, const float *
         if (e < 0 || e >= a.E) continue;
         const float w = ld_dep(a.topk_w + entry);
         const float *p = y + (size_t)entry * a.H + 8 * c;
-        const uint4 lo = ld_dep_v4(p), hi = ld_dep_v4(p + 4);
-        const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        float v[8] = {};
+        for (int s = 0; s < parts; ++s, p += (size_t)a.T * a.K * a.H) {
+            const uint4 lo = ld_dep_v4(p), hi = ld_dep_v4(p + 4);
+            const uint32_t b[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-        for (int m = 0; m < 8; ++m) acc[m] = fmaf(w, __uint_as_float(v[m]), acc[m]);
+            for (int m = 0; m < 8; ++m) v[m] += __uint_as_float(b[m]);
+        }
+#pragma unroll
+        for (int m = 0; m < 8; ++m) acc[m] = fmaf(w, v[m], acc[m]);
     }
     st_v4(static_cast<uint16_t *>(a.out) + (size_t)t * a.H + 8 * c,
           make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
                      pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7])));
 }
 
-template <bool UP, int NB>
-cudaError_t launch_rows(const MoeArgs &a, const float *h, float *dst, cudaStream_t stream) {
-    const int D = UP ? a.H : a.I;
-    const size_t fixed = 2 * kWarps * NB * 128 * 4 + (size_t)(D / 128) * 8 * NB * 4 +
-                         (size_t)8 * NB * (D + 64);
-    const int fit = (int)((kSmemMax - sizeof(Shared) - fixed) / kStageBytes);
+// Entries of a chunk: what experts get on average, with room for twice that, as
+// long as the entries leave most of the shared memory to the ring.
+int chunk_cols(const MoeArgs &a, int D) {
+    int cols = 8;
+    while (cols < kMaxCols && cols * a.E < 2 * a.T * a.K && 2 * cols * D <= 128 * 1024) cols *= 2;
+    return cols;
+}
+
+// Parts a row's length is cut into: with few entries there are few 128-row units,
+// and the SM with one more than the others sets the time.  The best share-out of
+// 1, 2 or 4 parts where the units are below 8 an SM; 1 above, where the loss is
+// below an eighth.
+int row_parts(int entries, int E, int R, int D) {
+    const int sms = sm_count();
+    const int64_t units = (int64_t)(entries < E ? entries : E) * (R / kRows);
+    if (units >= 8 * sms) return 1;
+    int best = 1;
+    double most = 0.0;
+    for (int p = 1; p <= 4 && D / 128 >= 2 * p; p *= 2) {
+        const int64_t u = units * p;
+        const double even = (double)u / ((u + sms - 1) / sms * sms);
+        if (even > most + 0.03) {
+            most = even;
+            best = p;
+        }
+    }
+    return best;
+}
+
+template <bool UP>
+cudaError_t launch_rows(const MoeArgs &a, const float *gu, int gu_parts, float *dst, int parts,
+                        cudaStream_t stream) {
+    const int D = UP ? a.H : a.I, G = D / 128, cols = chunk_cols(a, D);
+    const int64_t R = UP ? 2 * a.I : a.H;
+    const int64_t dims[3] = {D, R, a.E}, strides[2] = {D, R * D};
+    const int box[3] = {128, kRows, 1};
+    CUtensorMap wmap;
+    if (!encode_bytes(&wmap, UP ? a.w13 : a.w2, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    const int fixed = G * cols * (128 + 4) + (int)sizeof(Shared);
+    const int fit = (kSmemMax - fixed) / kStageBytes;
     const int stages = fit < kMaxStages ? fit : kMaxStages;
-    const size_t smem = fixed + (size_t)stages * kStageBytes;
-    auto k = rows_kernel<UP, NB>;
+    const size_t smem = 1024 + (size_t)G * cols * (128 + 4) + (size_t)stages * kStageBytes;
+    auto k = rows_kernel<UP>;
     const cudaError_t err = allow_dynamic_smem(k, smem);
     if (err != cudaSuccess) return err;
-    return launch_kernel(k, sm_count(), kThreads, smem, stream, true, a, h, dst, stages);
+    return launch_kernel(k, sm_count(), kThreads, smem, stream, true, wmap, a, gu, gu_parts, dst,
+                         parts, cols, stages);
 }
 
 }  // namespace
 
-size_t moe_workspace_bytes(int T, int K, int H, int I) {
-    return (size_t)T * K * ((size_t)I + H) * 4;
+size_t moe_workspace_bytes(int T, int K, int E, int H, int I) {
+    const int n = T * K;
+    return (size_t)n * 4 * ((size_t)row_parts(n, E, 2 * I, H) * 2 * I + (size_t)row_parts(n, E, H, I) * H);
 }
 
 cudaError_t launch_moe_decode(const MoeArgs &a, void *workspace, cudaStream_t stream) {
-    float *h = static_cast<float *>(workspace), *y = h + (size_t)a.T * a.K * a.I;
-    // 16 columns hold an expert's entries in one chunk where experts have more
-    // than a few on average; 8 leave more shared memory to the ring, and are all
-    // that fits beside it for long rows
-    const bool wide = a.T * a.K > 4 * a.E;
-    cudaError_t err = wide && a.H <= 8192 ? launch_rows<true, 2>(a, nullptr, h, stream)
-                                          : launch_rows<true, 1>(a, nullptr, h, stream);
+    const int n = a.T * a.K;
+    const int p1 = row_parts(n, a.E, 2 * a.I, a.H), p2 = row_parts(n, a.E, a.H, a.I);
+    float *gu = static_cast<float *>(workspace), *y = gu + (size_t)p1 * n * 2 * a.I;
+    cudaError_t err = launch_rows<true>(a, nullptr, 0, gu, p1, stream);
     if (err != cudaSuccess) return err;
-    err = wide && a.I <= 8192 ? launch_rows<false, 2>(a, h, y, stream)
-                              : launch_rows<false, 1>(a, h, y, stream);
+    err = launch_rows<false>(a, gu, p1, y, p2, stream);
     if (err != cudaSuccess) return err;
     const long long threads = (long long)a.T * (a.H / 8);
     return launch_kernel(sum_kernel, (int)((threads + 127) / 128), 128, 0, stream, true, a,
-                         (const float *)y);
+                         (const float *)y, p2);
 }
 
 }  // namespace ep
