@@ -26,7 +26,10 @@ namespace ep {
 namespace {
 
 constexpr int kEpiWarps = 8;                     // warps that scale and store
-constexpr int kThreads = 32 * (kEpiWarps + 2);   // + loader warp, + product warp
+constexpr int kThreads = 32 * (kEpiWarps + 4);   // + loader, + products, + two that fill the group
+// Registers a thread: 168 at launch (384 threads); the last warpgroup gives up
+// what the first two, with 128 sums a thread, take: 2 * 224 + 56 = 3 * 168.
+constexpr int kEpiRegs = 216, kOtherRegs = 72;
 constexpr int kTM = 128, kTN = 256;              // tile: rows, weight rows
 constexpr int kABytes = kTM * 128, kBBytes = kTN * 128;
 constexpr int kStageBytes = kABytes + kBBytes;
@@ -35,7 +38,7 @@ constexpr int kStages = 4;
 struct Shared {
     uint64_t full[kStages], empty[kStages];  // ring of K blocks
     uint64_t tfull[2], tempty[2];            // tensor-memory tiles
-    uint64_t xchg;                           // the two halves' group maxima
+    uint64_t xchg;                           // the column halves' group maxima
     uint64_t drain;
     uint32_t tmem;
     int fail;
@@ -69,17 +72,22 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs &a, const int32_t *pr
 }
 
 // acc[2i], acc[2i+1] += v[2i] * s, v[2i+1] * s, two to an instruction.
-__device__ __forceinline__ void fma_scaled16(float *acc, const uint32_t (&v)[16], float s) {
+__device__ __forceinline__ void fma_scaled(float *acc, const uint32_t (&v)[32], float s) {
     uint64_t ss;
     asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
         uint64_t p, c;
         asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(v[2 * i]), "r"(v[2 * i + 1]));
         asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(acc[2 * i]), "f"(acc[2 * i + 1]));
         asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(p), "l"(ss));
         asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[2 * i]), "=f"(acc[2 * i + 1]) : "l"(c));
     }
+}
+
+__device__ __forceinline__ void store_bf16x8(uint16_t *dst, const float *v) {
+    st_v4(dst, make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                          pack_bf16(v[6], v[7])));
 }
 
 template <bool GATED>
@@ -124,18 +132,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ntn = (a.N + cols - 1) / cols, total = pre[a.E] * ntn;
     const int G = a.K >> 7;
 
+    if (warp >= kEpiWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kEpiWarps) {
         // ---- loads ----
-        if (lane == 0) {
-            int it = 0;
-            for (int t = blockIdx.x; t < total && !*fail; t += gridDim.x) {
-                const Tile q = find_tile(a, pre, ntn, t, cols);
-                for (int g = 0; g < G; ++g, ++it) {
-                    const int s = it % kStages;
-                    if (it >= kStages && !mbar_wait_fast(&sh.empty[s], (it / kStages - 1) & 1, fail)) {
-                        sh.fail = 1;
-                        break;
-                    }
+        int it = 0;
+        for (int t = blockIdx.x; t < total && !__any_sync(kFullMask, *fail); t += gridDim.x) {
+            const Tile q = find_tile(a, pre, ntn, t, cols);
+            for (int g = 0; g < G; ++g, ++it) {
+                const int s = it % kStages;
+                const bool ok = it < kStages || mbar_wait_fast(&sh.empty[s], (it / kStages - 1) & 1, fail);
+                if (!__all_sync(kFullMask, ok)) {
+                    sh.fail = 1;
+                    break;
+                }
+                if (elect_one()) {
                     uint8_t *st = smem + s * kStageBytes;
                     expect_bytes(&sh.full[s], kStageBytes);
                     tma_load_2d(st, &xmap, g * 128, q.row, &sh.full[s]);
@@ -143,42 +154,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d(st + kABytes + kBBytes / 2, &wmap, g * 128,
                                 q.n0 + (GATED ? a.N : 128), q.e, &sh.full[s]);
                 }
+                __syncwarp();
             }
-            sh.issued = it;
         }
+        if (lane == 0) sh.issued = it;
     } else if (warp == kEpiWarps + 1) {
         // ---- products ----
-        if (lane == 0) {
-            constexpr uint32_t instr = e4m3_instr(kTM, kTN);
-            int it = 0;
-            for (int t = blockIdx.x; t < total && !*fail; t += gridDim.x) {
-                for (int g = 0; g < G; ++g, ++it) {
-                    const int s = it % kStages, b = it & 1;
-                    if ((it >= 2 && !mbar_wait_fast(&sh.tempty[b], (it / 2 - 1) & 1, fail)) ||
-                        !mbar_wait_fast(&sh.full[s], (it / kStages) & 1, fail)) {
-                        sh.fail = 1;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t da = tile_desc(smem_addr(smem + s * kStageBytes));
-                    const uint64_t db = tile_desc(smem_addr(smem + s * kStageBytes + kABytes));
+        constexpr uint32_t instr = e4m3_instr(kTM, kTN);
+        int it = 0;
+        for (int t = blockIdx.x; t < total && !__any_sync(kFullMask, *fail); t += gridDim.x) {
+            for (int g = 0; g < G; ++g, ++it) {
+                const int s = it % kStages, b = it & 1;
+                const bool ok = (it < 2 || mbar_wait_fast(&sh.tempty[b], (it / 2 - 1) & 1, fail)) &&
+                                mbar_wait_fast(&sh.full[s], (it / kStages) & 1, fail);
+                if (!__all_sync(kFullMask, ok)) {
+                    sh.fail = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t da = tile_desc(smem_addr(smem + s * kStageBytes));
+                const uint64_t db = tile_desc(smem_addr(smem + s * kStageBytes + kABytes));
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)  // 32 bytes of each row further
                         mma_e4m3(tmem + b * kTN, da + 2 * k, db + 2 * k, instr, k > 0);
                     mma_commit(&sh.empty[s]);
                     mma_commit(&sh.tfull[b]);
                 }
+                __syncwarp();
             }
-            // tensor memory and the barriers outlive the last product
-            mma_commit(&sh.drain);
-            if (!mbar_wait(&sh.drain, 0, nullptr)) sh.fail = 1;
         }
+        // tensor memory and the barriers outlive the last product
+        if (elect_one()) mma_commit(&sh.drain);
+        __syncwarp();
+        if (!mbar_wait(&sh.drain, 0, nullptr)) sh.fail = 1;
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         // ---- scales, running sums, outputs ----
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;  // column half, row of the tile
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         // the gated tile: this half's 64 gate columns, then the same 64 up columns
-        const uint32_t col0 = GATED ? half * 64 : half * 128, col1 = GATED ? 128 + half * 64 : col0 + 64;
+        const uint32_t col0 = half * (GATED ? 64 : 128), col1 = GATED ? 128 + half * 64 : col0 + 64;
         const int NB = GATED ? a.N / 64 : (a.N + 127) / 128;
         int it = 0, tiles = 0;
         for (int t = blockIdx.x; t < total && !__any_sync(kFullMask, *fail); t += gridDim.x, ++tiles) {
@@ -209,34 +226,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t base = tmem + lanes + b * kTN;
-                uint32_t v[2][16];
+                uint32_t v[2][32];
                 tmem_ld(base + col0, v[0]);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    tmem_ld_wait(v[c & 1]);
-                    if (c < 7) {
-                        tmem_ld(base + (c + 1 < 4 ? col0 + 16 * (c + 1) : col1 + 16 * (c - 3)),
-                                  v[(c + 1) & 1]);
-                    } else {  // everything is in registers
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.tempty[b]);
-                    }
-                    fma_scaled16(acc + 16 * c, v[c & 1], c < 4 ? s0 : s1);
-                }
+                tmem_ld_wait(v[0]);
+                tmem_ld(base + col0 + 32, v[1]);
+                fma_scaled(acc, v[0], s0);
+                tmem_ld_wait(v[1]);
+                tmem_ld(base + col1, v[0]);
+                fma_scaled(acc + 32, v[1], s0);
+                tmem_ld_wait(v[0]);
+                tmem_ld(base + col1 + 32, v[1]);
+                fma_scaled(acc + 64, v[0], s1);
+                tmem_ld_wait(v[1]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.tempty[b]);
+                fma_scaled(acc + 96, v[1], s1);
             }
             if (!ok) break;
             if constexpr (!GATED) {
                 const int c0 = q.n0 + half * 128;
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) +
-                                                       (size_t)(q.row + r) * a.N + c0);
+                uint16_t *dst = static_cast<uint16_t *>(a.out) + (size_t)(q.row + r) * a.N + c0;
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    if (valid && c0 + 8 * j < a.N)
-                        st_v4(dst + j, make_uint4(pack_bf16(acc[8 * j], acc[8 * j + 1]),
-                                                  pack_bf16(acc[8 * j + 2], acc[8 * j + 3]),
-                                                  pack_bf16(acc[8 * j + 4], acc[8 * j + 5]),
-                                                  pack_bf16(acc[8 * j + 6], acc[8 * j + 7])));
+                    if (valid && c0 + 8 * j < a.N) store_bf16x8(dst + 8 * j, acc + 8 * j);
             } else {
                 float amax = 0.0f;
 #pragma unroll
@@ -247,14 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const size_t at = (size_t)(q.row + r) * a.N + q.n0 + half * 64;
                 if (a.out_quant == EP_QUANT_NONE) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (valid)
-                            st_v4(dst + j, make_uint4(pack_bf16(acc[8 * j], acc[8 * j + 1]),
-                                                      pack_bf16(acc[8 * j + 2], acc[8 * j + 3]),
-                                                      pack_bf16(acc[8 * j + 4], acc[8 * j + 5]),
-                                                      pack_bf16(acc[8 * j + 6], acc[8 * j + 7])));
+                        if (valid) store_bf16x8(static_cast<uint16_t *>(a.out) + at + 8 * j, acc + 8 * j);
                     continue;
                 }
                 // the row's other 64 columns are with the other half's warp
@@ -270,16 +278,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float s = group_scale(amax);
                 const int e8 = ue8m0_exponent(s);
                 const float inv = a.out_quant == EP_QUANT_FP8_F32 ? __frcp_rn(s) : exp_reciprocal(e8);
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + at);
-                uint32_t p[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    p[j] = fp8x4(acc[4 * j] * inv, acc[4 * j + 1] * inv, acc[4 * j + 2] * inv,
-                                 acc[4 * j + 3] * inv);
+                uint8_t *dst = static_cast<uint8_t *>(a.out) + at;
                 if (valid) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        st_v4(dst + j, make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]));
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t p[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float *v = acc + 16 * j + 4 * i;
+                            p[i] = fp8x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+                        }
+                        st_v4(dst + 16 * j, make_uint4(p[0], p[1], p[2], p[3]));
+                    }
                     if (half == 0) store_out_scale(a, q.row + r, q.e, q.n0 / 128, s, e8);
                 }
             }

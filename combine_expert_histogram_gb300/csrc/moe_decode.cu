@@ -273,61 +273,67 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kWarps) {
         // ---- loads ----
-        if (lane == 0) {
-            fence_proxy_async_smem();  // the ring held the grouping's counters
-            int it = 0;
-            for (int u = u0; u < u1 && !*fail; ++u) {
-                const Unit un = unit_at(sh, row_units, parts, G, u);
-                for (int g = un.g0; g < un.g1; ++g, ++it) {
-                    const int s = it % stages;
-                    if (it >= stages && !mbar_wait_fast(&sh.empty[s], (it / stages - 1) & 1, fail)) {
-                        sh.fail = 1;
-                        break;
-                    }
+        fence_proxy_async_smem();  // the ring held the grouping's counters
+        int it = 0;
+        for (int u = u0; u < u1 && !__any_sync(kFullMask, *fail); ++u) {
+            const Unit un = unit_at(sh, row_units, parts, G, u);
+            for (int g = un.g0; g < un.g1; ++g, ++it) {
+                const int s = it % stages;
+                const bool ok = it < stages || mbar_wait_fast(&sh.empty[s], (it / stages - 1) & 1, fail);
+                if (!__all_sync(kFullMask, ok)) {
+                    sh.fail = 1;
+                    break;
+                }
+                if (elect_one()) {
                     expect_bytes(&sh.full[s], kStageBytes);
                     tma_load_3d(ring + s * kStageBytes, &wmap, g * 128, un.row, un.chunk & 1023,
                                 &sh.full[s]);
                 }
+                __syncwarp();
             }
-            sh.issued = it;
         }
+        if (lane == 0) sh.issued = it;
     } else if (warp == kWarps + 1) {
         // ---- products ----
-        if (lane == 0) {
-            const uint32_t instr = e4m3_instr(kRows, cols < 16 ? 16 : cols);
-            int it = 0, loaded = 0;
-            uint32_t have = 0xffffffffu;
-            for (int u = u0; u < u1 && !*fail; ++u) {
-                const Unit un = unit_at(sh, row_units, parts, G, u);
-                if (un.chunk != have) {
-                    have = un.chunk;
-                    if (!mbar_wait_fast(&sh.columns, loaded & 1, fail)) {
-                        sh.fail = 1;
-                        break;
-                    }
-                    ++loaded;
+        const uint32_t instr = e4m3_instr(kRows, cols < 16 ? 16 : cols);
+        int it = 0, loaded = 0;
+        uint32_t have = 0xffffffffu;
+        for (int u = u0; u < u1 && !__any_sync(kFullMask, *fail); ++u) {
+            const Unit un = unit_at(sh, row_units, parts, G, u);
+            if (un.chunk != have) {
+                have = un.chunk;
+                if (!__all_sync(kFullMask, mbar_wait_fast(&sh.columns, loaded & 1, fail))) {
+                    sh.fail = 1;
+                    break;
                 }
-                for (int g = un.g0; g < un.g1; ++g, ++it) {
-                    const int s = it % stages, b = it % kTiles;
-                    if ((it >= kTiles && !mbar_wait_fast(&sh.tempty[b], (it / kTiles - 1) & 1, fail)) ||
-                        !mbar_wait_fast(&sh.full[s], (it / stages) & 1, fail)) {
-                        sh.fail = 1;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t da = tile_desc(smem_addr(ring + s * kStageBytes));
-                    const uint64_t db = tile_desc(smem_addr(xq + g * cols * 128));
+                ++loaded;
+            }
+            for (int g = un.g0; g < un.g1; ++g, ++it) {
+                const int s = it % stages, b = it % kTiles;
+                const bool ok =
+                    (it < kTiles || mbar_wait_fast(&sh.tempty[b], (it / kTiles - 1) & 1, fail)) &&
+                    mbar_wait_fast(&sh.full[s], (it / stages) & 1, fail);
+                if (!__all_sync(kFullMask, ok)) {
+                    sh.fail = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t da = tile_desc(smem_addr(ring + s * kStageBytes));
+                const uint64_t db = tile_desc(smem_addr(xq + g * cols * 128));
+                if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         mma_e4m3(tmem + b * kMaxCols, da + 2 * j, db + 2 * j, instr, j > 0);
                     mma_commit(&sh.empty[s]);
                     mma_commit(&sh.tfull[b]);
                 }
+                __syncwarp();
             }
-            // tensor memory and the barriers outlive the last product
-            mma_commit(&sh.drain);
-            if (!mbar_wait(&sh.drain, 0, nullptr)) sh.fail = 1;
         }
+        // tensor memory and the barriers outlive the last product
+        if (elect_one()) mma_commit(&sh.drain);
+        __syncwarp();
+        if (!mbar_wait(&sh.drain, 0, nullptr)) sh.fail = 1;
     } else {
         // ---- entries, scales, sums.  After a wait that ran out the loops go on
         // (every later wait returns at once), so that all warps meet at the barriers ----
