@@ -8,11 +8,12 @@
 // Persistent CTAs, one per SM, take 128 x 256 tiles of (expert, 128 rows,
 // 256 weight rows); the gated form's tile is 128 gate and the same 128 up
 // columns, so that one CTA holds both factors of 128 outputs, which are one
-// scale group of the result.  Three roles:
+// scale group of the result.  Four roles:
 //   - one thread keeps a ring of 128-deep K blocks (rows and weights, 48 KB) in
 //     flight by tiled TMA loads with 128-byte swizzle;
 //   - one thread issues the tensor core's E4M3 products of a block, four
 //     instructions of K = 32, into one of two tensor-memory tiles;
+//   - two warps multiply the block's row and weight scales, four blocks ahead;
 //   - eight warps take each block's sums out of tensor memory and add them,
 //     times sx * sw, to running sums in registers (128 a thread), while the
 //     tensor core fills the other tile.  The scales change every 128 of K, so
@@ -26,24 +27,27 @@ namespace ep {
 namespace {
 
 constexpr int kEpiWarps = 8;                     // warps that scale and store
-constexpr int kThreads = 32 * (kEpiWarps + 4);   // + loader, + products, + two that fill the group
+constexpr int kThreads = 32 * (kEpiWarps + 4);   // + loader, + products, + two for the scales
 // Registers a thread: 168 at launch (384 threads); the last warpgroup gives up
-// what the first two, with 128 sums a thread, take: 2 * 224 + 56 = 3 * 168.
+// what the first two, with 128 sums a thread, take: 2 * 216 + 72 = 3 * 168.
 constexpr int kEpiRegs = 216, kOtherRegs = 72;
 constexpr int kTM = 128, kTN = 256;              // tile: rows, weight rows
 constexpr int kABytes = kTM * 128, kBBytes = kTN * 128;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kStages = 4;
+constexpr int kSlots = 4;                        // K blocks of scales ahead of their sums
 
 struct Shared {
     uint64_t full[kStages], empty[kStages];  // ring of K blocks
     uint64_t tfull[2], tempty[2];            // tensor-memory tiles
+    uint64_t sfull[kSlots], sempty[kSlots];  // scales
     uint64_t xchg;                           // the column halves' group maxima
     uint64_t drain;
     uint32_t tmem;
     int fail;
     int issued;                              // K blocks requested, for the drain
     int32_t scan[kThreads / 32];
+    float scale[kSlots][2][kTM];             // sx * sw of each row, for the two weight blocks
     float amax[2][2][kTM];                   // [tile parity][column half][row]
 };
 
@@ -111,6 +115,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.tfull[i], 1);
             mbar_init(&sh.tempty[i], kEpiWarps);
         }
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&sh.sfull[i], 2);
+            mbar_init(&sh.sempty[i], kEpiWarps);
+        }
         mbar_init(&sh.xchg, kEpiWarps);
         mbar_init(&sh.drain, 1);
         sh.fail = 0;
@@ -133,62 +141,106 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int G = a.K >> 7;
 
     if (warp >= kEpiWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kEpiWarps) {
-        // ---- loads ----
-        int it = 0;
-        for (int t = blockIdx.x; t < total && !__any_sync(kFullMask, *fail); t += gridDim.x) {
-            const Tile q = find_tile(a, pre, ntn, t, cols);
-            for (int g = 0; g < G; ++g, ++it) {
-                const int s = it % kStages;
-                const bool ok = it < kStages || mbar_wait_fast(&sh.empty[s], (it / kStages - 1) & 1, fail);
-                if (!__all_sync(kFullMask, ok)) {
-                    sh.fail = 1;
-                    break;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kEpiWarps) {
+            // ---- loads ----
+            int it = 0;
+            for (int t = blockIdx.x; t < total && !__any_sync(kFullMask, *fail); t += gridDim.x) {
+                const Tile q = find_tile(a, pre, ntn, t, cols);
+                for (int g = 0; g < G; ++g, ++it) {
+                    const int s = it % kStages;
+                    const bool ok = it < kStages || mbar_wait_fast(&sh.empty[s], (it / kStages - 1) & 1, fail);
+                    if (!__all_sync(kFullMask, ok)) {
+                        sh.fail = 1;
+                        break;
+                    }
+                    if (elect_one()) {
+                        uint8_t *st = smem + s * kStageBytes;
+                        expect_bytes(&sh.full[s], kStageBytes);
+                        tma_load_2d(st, &xmap, g * 128, q.row, &sh.full[s]);
+                        tma_load_3d(st + kABytes, &wmap, g * 128, q.n0, q.e, &sh.full[s]);
+                        tma_load_3d(st + kABytes + kBBytes / 2, &wmap, g * 128,
+                                    q.n0 + (GATED ? a.N : 128), q.e, &sh.full[s]);
+                    }
+                    __syncwarp();
                 }
-                if (elect_one()) {
-                    uint8_t *st = smem + s * kStageBytes;
-                    expect_bytes(&sh.full[s], kStageBytes);
-                    tma_load_2d(st, &xmap, g * 128, q.row, &sh.full[s]);
-                    tma_load_3d(st + kABytes, &wmap, g * 128, q.n0, q.e, &sh.full[s]);
-                    tma_load_3d(st + kABytes + kBBytes / 2, &wmap, g * 128,
-                                q.n0 + (GATED ? a.N : 128), q.e, &sh.full[s]);
-                }
-                __syncwarp();
             }
-        }
-        if (lane == 0) sh.issued = it;
-    } else if (warp == kEpiWarps + 1) {
-        // ---- products ----
-        constexpr uint32_t instr = e4m3_instr(kTM, kTN);
-        int it = 0;
-        for (int t = blockIdx.x; t < total && !__any_sync(kFullMask, *fail); t += gridDim.x) {
-            for (int g = 0; g < G; ++g, ++it) {
-                const int s = it % kStages, b = it & 1;
-                const bool ok = (it < 2 || mbar_wait_fast(&sh.tempty[b], (it / 2 - 1) & 1, fail)) &&
-                                mbar_wait_fast(&sh.full[s], (it / kStages) & 1, fail);
-                if (!__all_sync(kFullMask, ok)) {
-                    sh.fail = 1;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t da = tile_desc(smem_addr(smem + s * kStageBytes));
-                const uint64_t db = tile_desc(smem_addr(smem + s * kStageBytes + kABytes));
-                if (elect_one()) {
+            if (lane == 0) sh.issued = it;
+        } else if (warp == kEpiWarps + 1) {
+            // ---- products ----
+            constexpr uint32_t instr = e4m3_instr(kTM, kTN);
+            int it = 0;
+            for (int t = blockIdx.x; t < total && !__any_sync(kFullMask, *fail); t += gridDim.x) {
+                for (int g = 0; g < G; ++g, ++it) {
+                    const int s = it % kStages, b = it & 1;
+                    const bool ok = (it < 2 || mbar_wait_fast(&sh.tempty[b], (it / 2 - 1) & 1, fail)) &&
+                                    mbar_wait_fast(&sh.full[s], (it / kStages) & 1, fail);
+                    if (!__all_sync(kFullMask, ok)) {
+                        sh.fail = 1;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t da = tile_desc(smem_addr(smem + s * kStageBytes));
+                    const uint64_t db = tile_desc(smem_addr(smem + s * kStageBytes + kABytes));
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)  // 32 bytes of each row further
-                        mma_e4m3(tmem + b * kTN, da + 2 * k, db + 2 * k, instr, k > 0);
-                    mma_commit(&sh.empty[s]);
-                    mma_commit(&sh.tfull[b]);
+                        for (int k = 0; k < 4; ++k)  // 32 bytes of each row further
+                            mma_e4m3(tmem + b * kTN, da + 2 * k, db + 2 * k, instr, k > 0);
+                        mma_commit(&sh.empty[s]);
+                        mma_commit(&sh.tfull[b]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+            }
+            // tensor memory and the barriers outlive the last product
+            if (elect_one()) mma_commit(&sh.drain);
+            __syncwarp();
+            if (!mbar_wait(&sh.drain, 0, nullptr)) sh.fail = 1;
+        } else {
+            // ---- scales: rows r and r + 64, four K blocks at a time, the next four
+            // in flight.  (Loaded by the adding warps, each from its own row, they cost
+            // a third of the time: 32 lines a load, beside 64 KB of tensor memory.) ----
+            const int r = (warp - kEpiWarps - 2) * 32 + lane;
+            const int NB = GATED ? a.N / 64 : (a.N + 127) / 128;
+            int it = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < total && !__any_sync(kFullMask, *fail); t += gridDim.x) {
+                const Tile q = find_tile(a, pre, ntn, t, cols);
+                const int b0 = q.n0 / 128, b1 = GATED ? b0 + a.N / 128 : min(b0 + 1, NB - 1);
+                const float *sw0 = a.w_scales + ((size_t)q.e * NB + b0) * G;
+                const float *sw1 = a.w_scales + ((size_t)q.e * NB + b1) * G;
+                const bool v0 = r < q.rows, v1 = r + 64 < q.rows;
+                const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float4 n0 = v0 ? row_scales4(a, q.row + r, q.e, 0) : none;
+                float4 n1 = v1 ? row_scales4(a, q.row + r + 64, q.e, 0) : none;
+                for (int g4 = 0; ok && g4 < G; g4 += 4) {
+                    const float x0[4] = {n0.x, n0.y, n0.z, n0.w}, x1[4] = {n1.x, n1.y, n1.z, n1.w};
+                    if (g4 + 4 < G) {
+                        if (v0) n0 = row_scales4(a, q.row + r, q.e, g4 + 4);
+                        if (v1) n1 = row_scales4(a, q.row + r + 64, q.e, g4 + 4);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (g4 + i >= G) break;
+                        const int s = it % kSlots;
+                        const float w0 = __ldg(sw0 + g4 + i), w1 = __ldg(sw1 + g4 + i);
+                        ok = it < kSlots || mbar_wait_fast(&sh.sempty[s], (it / kSlots - 1) & 1, fail);
+                        ok = __all_sync(kFullMask, ok);
+                        if (!ok) {
+                            sh.fail = 1;
+                            break;
+                        }
+                        sh.scale[s][0][r] = x0[i] * w0;
+                        sh.scale[s][0][r + 64] = x1[i] * w0;
+                        sh.scale[s][1][r] = x0[i] * w1;
+                        sh.scale[s][1][r + 64] = x1[i] * w1;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.sfull[s]);
+                        ++it;
+                    }
+                }
             }
         }
-        // tensor memory and the barriers outlive the last product
-        if (elect_one()) mma_commit(&sh.drain);
-        __syncwarp();
-        if (!mbar_wait(&sh.drain, 0, nullptr)) sh.fail = 1;
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         // ---- scales, running sums, outputs ----
@@ -196,29 +248,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         // the gated tile: this half's 64 gate columns, then the same 64 up columns
         const uint32_t col0 = half * (GATED ? 64 : 128), col1 = GATED ? 128 + half * 64 : col0 + 64;
-        const int NB = GATED ? a.N / 64 : (a.N + 127) / 128;
         int it = 0, tiles = 0;
         for (int t = blockIdx.x; t < total && !__any_sync(kFullMask, *fail); t += gridDim.x, ++tiles) {
             const Tile q = find_tile(a, pre, ntn, t, cols);
             const bool valid = r < q.rows;
-            const int b0 = q.n0 / 128 + (GATED ? 0 : min(half, NB - 1 - q.n0 / 128));
-            const float *sw0 = a.w_scales + ((size_t)q.e * NB + b0) * G;
-            const float *sw1 = GATED ? sw0 + (size_t)(a.N / 128) * G : sw0;
             float acc[128];
 #pragma unroll
             for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-            float sx = valid ? row_scale(a, q.row + r, q.e, 0) : 0.0f;
-            float w0 = __ldg(sw0), w1 = GATED ? __ldg(sw1) : 0.0f;
             bool ok = true;
             for (int g = 0; g < G; ++g, ++it) {
-                const int b = it & 1;
-                const float s0 = sx * w0, s1 = GATED ? sx * w1 : s0;
-                if (g + 1 < G) {  // the next block's scales
-                    if (valid) sx = row_scale(a, q.row + r, q.e, g + 1);
-                    w0 = __ldg(sw0 + g + 1);
-                    if (GATED) w1 = __ldg(sw1 + g + 1);
-                }
-                ok = mbar_wait_fast(&sh.tfull[b], (it / 2) & 1, fail);
+                const int b = it & 1, s = it % kSlots;
+                ok = mbar_wait_fast(&sh.sfull[s], (it / kSlots) & 1, fail);
+                const float s0 = sh.scale[s][GATED ? 0 : half][r], s1 = GATED ? sh.scale[s][1][r] : s0;
+                ok = mbar_wait_fast(&sh.tfull[b], (it / 2) & 1, fail) && ok;
                 if (!__all_sync(kFullMask, ok)) {
                     sh.fail = 1;
                     ok = false;
@@ -240,7 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait(v[1]);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.tempty[b]);
+                if (lane == 0) {
+                    mbar_arrive(&sh.tempty[b]);
+                    mbar_arrive(&sh.sempty[s]);
+                }
                 fma_scaled(acc + 96, v[1], s1);
             }
             if (!ok) break;

@@ -56,11 +56,21 @@ __device__ __forceinline__ int expert_rows(const ExpertArgs &a, int e) {
     return a.cap ? min(n, a.cap) : min(n, a.rows_cap - expert_first(a, e));
 }
 
-// Scale of group g of row r (row r belongs to expert e).
-__device__ __forceinline__ float row_scale(const ExpertArgs &a, int r, int e, int g) {
+// Scales of groups g .. g+3 of row r (row r belongs to expert e; g a multiple of
+// 4; groups past the last one get anything).  The packed forms are one word.
+__device__ __forceinline__ float4 row_scales4(const ExpertArgs &a, int r, int e, int g) {
     const int G = a.K >> 7, P = (G + 3) >> 2;
-    if (a.quant == EP_QUANT_FP8_F32)
-        return ld_dep(static_cast<const float *>(a.x_scales) + (size_t)r * G + g);
+    if (a.quant == EP_QUANT_FP8_F32) {
+        const float *p = static_cast<const float *>(a.x_scales) + (size_t)r * G + g;
+        if ((G & 3) == 0 && (reinterpret_cast<uintptr_t>(a.x_scales) & 15) == 0) {
+            const uint4 v = ld_dep_v4(p);
+            return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                               __uint_as_float(v.w));
+        }
+        const int last = G - 1 - g;
+        return make_float4(ld_dep(p), ld_dep(p + min(1, last)), ld_dep(p + min(2, last)),
+                           ld_dep(p + min(3, last)));
+    }
     size_t word;
     if (a.quant == EP_QUANT_FP8_UE8M0) {
         word = (size_t)r * P + (g >> 2);
@@ -71,7 +81,8 @@ __device__ __forceinline__ float row_scale(const ExpertArgs &a, int r, int e, in
         word = (size_t)(g >> 2) * ((a.rows_cap + 3ll) / 4 * 4) + r;
     }
     const uint32_t v = (uint32_t)ld_dep(static_cast<const int32_t *>(a.x_scales) + word);
-    return ue8m0_value(v >> (8 * (g & 3)) & 255u);
+    return make_float4(ue8m0_value(v & 255u), ue8m0_value(v >> 8 & 255u),
+                       ue8m0_value(v >> 16 & 255u), ue8m0_value(v >> 24));
 }
 
 // Store the scale of group g of output row r: fp32, or the biased exponent e8
