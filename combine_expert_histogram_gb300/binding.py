@@ -488,69 +488,80 @@ def ep_route_topk(logits: torch.Tensor, num_topk: int, mode: str = "softmax",
 
 # ------------------------------------------------------- norm, experts, decode
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _want(t: Optional[torch.Tensor], name: str, dtypes, shape, device) -> None:
-    """Check one tensor argument (None passes): dtype, shape (-1 = any), device, layout."""
+def _refuse(t, name: str, dtypes, shape, dev: int):
+    """The error for a tensor that _want did not take."""
     if t is None:
-        return
-    if t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
-        raise ValueError(f"{name}: dtype {t.dtype} is not accepted")
-    if t.dim() != len(shape) or any(w != -1 and s != w for s, w in zip(t.shape, shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError("libep needs contiguous tensors")
-
-
-def _cuda(t: torch.Tensor) -> torch.device:
+        raise ValueError(f"{name} is missing")
     if not t.is_cuda:
         raise ValueError("libep works on CUDA tensors only")
-    return t.device
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype} is not accepted")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+    raise ValueError("libep needs contiguous tensors")
 
 
-class _On:
-    """The device of a call's tensors and the stream its kernels run on: `stream`,
-    or that device's current one.  Outputs the call allocates belong to that stream."""
-
-    def __init__(self, dev: torch.device, stream):
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
-        self.dev, self.given = dev, stream
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
-        self.stream = ctypes.c_void_p(s.cuda_stream)
-
-    def empty(self, shape, dtype) -> torch.Tensor:
-        if self.given is None:
-            return torch.empty(shape, dtype=dtype, device=self.dev)
-        with torch.cuda.stream(self.given):
-            return torch.empty(shape, dtype=dtype, device=self.dev)
-
-    def call(self, name: str, *args) -> None:
-        fn = getattr(load_library(), name)
-        if self.dev.index == torch.cuda.current_device():
-            code = fn(*args, self.stream)
-        else:
-            with torch.cuda.device(self.dev):
-                code = fn(*args, self.stream)
-        _check(code, name)
+def _want(t: torch.Tensor, name: str, dtypes, shape, dev: int) -> int:
+    """Address of a tensor argument of one of `dtypes`, `shape`, contiguous on device `dev`."""
+    if t is None or t.dtype not in dtypes or t.shape != shape or t.get_device() != dev \
+            or not t.is_contiguous():
+        _refuse(t, name, dtypes, shape, dev)
+    return t.data_ptr()
 
 
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _rows_of(t: torch.Tensor, name: str, dims: int = 2) -> int:
+    """Device index of a call's first tensor, a CUDA tensor of `dims` dimensions."""
+    if not t.is_cuda:
+        raise ValueError("libep works on CUDA tensors only")
+    if t.dim() != dims:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected {dims}")
+    return t.get_device()
+
+
+def _on(stream, dev: int) -> int:
+    """The stream a call runs on: `stream`, or device `dev`'s current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
+    """An output that belongs to the call's stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+
+
+def _call(fn, name: str, dev: int, *args) -> None:
+    if dev == torch.cuda.current_device():
+        code = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args)
+    if code != EP_OK:
+        raise EPError(code, name)
 
 
 def _scale_shape(rows: int, hidden: int, quant: str, slab=None):
-    """(dtype, shape) of the scales of `rows` rows; slab = (E, capacity) of a masked layout."""
+    """(dtypes, shape) of the scales of `rows` rows; slab = (E, capacity) of a masked layout."""
+    if quant == "fp8_f32" and hidden % 128 == 0:
+        return (_F32,), (rows, hidden // 128)
     cols = ep_scale_cols(hidden, quant)
     if cols < 0:
         raise EPError(EP_ERR_INVALID_ARG, f"hidden {hidden} for {quant}")
     if quant == "fp8_ue8m0_mn":
         if slab is not None:
-            return torch.int32, (slab[0], cols, (slab[1] + 3) // 4 * 4)
-        return torch.int32, (cols, (rows + 3) // 4 * 4)
-    return (torch.float32 if quant == "fp8_f32" else torch.int32), (rows, cols)
+            return (_I32,), (slab[0], cols, (slab[1] + 3) // 4 * 4)
+        return (_I32,), (cols, (rows + 3) // 4 * 4)
+    return (_I32,), (rows, cols)
 
 
 def ep_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -565,57 +576,78 @@ def ep_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     quant "none", residual_out (the sum; may be ``residual`` or ``x`` itself) is
     None without a residual unless a tensor is passed for it.
     """
-    dev = _cuda(x)
-    bf16 = torch.bfloat16
-    _want(x, "x", bf16, (-1, -1), dev)
-    T, H = x.shape
-    _want(weight, "weight", bf16, (H,), dev)
-    _want(residual, "residual", bf16, (T, H), dev)
-    on = _On(dev, stream)
-    if residual is not None and residual_out is None:
-        residual_out = on.empty((T, H), bf16)
-    _want(residual_out, "residual_out", bf16, (T, H), dev)
+    lib = load_library()
+    dev = _rows_of(x, "x")
+    shape = x.shape
+    T, H = shape
+    px = _want(x, "x", (_BF16,), shape, dev)
+    pw = _want(weight, "weight", (_BF16,), (H,), dev)
+    pr = po = pq = ps = pro = None
+    if residual is not None:
+        pr = _want(residual, "residual", (_BF16,), shape, dev)
+        if residual_out is None:
+            residual_out = _empty(shape, _BF16, dev, stream)
+    if residual_out is not None:
+        pro = _want(residual_out, "residual_out", (_BF16,), shape, dev)
     if out is None and with_out:
-        out = on.empty((T, H), bf16)
-    _want(out, "out", bf16, (T, H), dev)
+        out = _empty(shape, _BF16, dev, stream)
+    if out is not None:
+        po = _want(out, "out", (_BF16,), shape, dev)
     if quant != "none":
         sdt, sshape = _scale_shape(T, H, quant)
         if out_rows is None:
-            out_rows = on.empty((T, H), torch.uint8)
+            out_rows = _empty(shape, torch.uint8, dev, stream)
         if out_scales is None:
-            out_scales = on.empty(sshape, sdt)
-        _want(out_rows, "out_rows", _E4M3, (T, H), dev)
-        _want(out_scales, "out_scales", sdt, sshape, dev)
-    on.call("ep_rmsnorm", _addr(x), _addr(residual), _addr(weight), eps, T, H, QUANT[quant],
-            _addr(residual_out), _addr(out), _addr(out_rows), _addr(out_scales))
+            out_scales = _empty(sshape, sdt[0], dev, stream)
+        pq = _want(out_rows, "out_rows", _E4M3, shape, dev)
+        ps = _want(out_scales, "out_scales", sdt, sshape, dev)
+    elif out_rows is not None or out_scales is not None:
+        raise ValueError('out_rows and out_scales belong to an 8-bit quant, not "none"')
+    _call(lib.ep_rmsnorm, "ep_rmsnorm", dev, px, pr, pw, eps, T, H, QUANT[quant], pro, po, pq, ps,
+          _on(stream, dev))
     return out, out_rows, out_scales, residual_out
 
 
-def _expert_checks(layout: Layout, rows, row_scales, weights, weight_scales, quant: str):
-    """Shared argument checks; returns (device, rows of the row space, slab, E, N, K)."""
-    dev = _cuda(rows)
-    cap = ep_rows_capacity(layout)
+def _layout_arg(layout: Layout, dev: int) -> _Layout:
+    """The C struct of a filled layout on device `dev`."""
+    E = layout.num_experts
+    rr, rs = layout.rank_rows, layout.row_src
+    c = _Layout(layout.num_tokens, layout.num_topk, E, layout.num_ranks, LAYOUT_KIND[layout.kind],
+                layout.align, layout.capacity, layout.max_tokens, layout.dst_row.data_ptr(),
+                rs.data_ptr() if rs is not None else None,
+                _want(layout.expert_count, "layout.expert_count", (_I32,), (E,), dev),
+                _want(layout.expert_offset, "layout.expert_offset", (_I32,), (E + 1,), dev),
+                rr.data_ptr() if rr is not None else None,
+                _want(layout.status, "layout.status", (_I32,), (1,), dev))
+    return c
+
+
+def _expert_args(lib, layout: Layout, rows, row_scales, weights, weight_scales, quant: str):
+    """Shared argument checks of the experts' products: (device index, C layout,
+    rows of the row space, slab, N, K, the four addresses)."""
+    slab = (layout.num_experts, layout.capacity) if layout.kind == "masked" else None
+    if slab is not None:  # [E, capacity, ...], as ep_masked_repack returns it
+        if rows.dim() == 3:
+            rows = rows.flatten(0, 1)
+        if row_scales is not None and row_scales.dim() == 3 and quant != "fp8_ue8m0_mn":
+            row_scales = row_scales.flatten(0, 1)
+    dev = _rows_of(rows, "rows")
+    c = _layout_arg(layout, dev)
+    cap = lib.ep_rows_capacity(ctypes.byref(c))
     if cap < 0:
         raise EPError(EP_ERR_INVALID_ARG, "layout shape")
-    slab = (layout.num_experts, layout.capacity) if layout.kind == "masked" else None
-    if rows.dim() == 3 and slab is not None:  # [E, capacity, K], as ep_masked_repack returns it
-        rows = rows.flatten(0, 1)
-    if row_scales is not None and row_scales.dim() == 3 and slab is not None \
-            and quant != "fp8_ue8m0_mn":
-        row_scales = row_scales.flatten(0, 1)
-    _want(rows, "rows", _E4M3, (max(cap, 1), -1), dev)
+    if cap == 0:
+        cap = 1
     E, K = layout.num_experts, rows.shape[1]
-    if quant in ("none", "mxfp8"):
+    px = _want(rows, "rows", _E4M3, (cap, K), dev)
+    if quant == "none" or quant == "mxfp8":
         raise EPError(EP_ERR_UNSUPPORTED, f"expert products of {quant} rows")
-    sdt, sshape = _scale_shape(max(cap, 1), K, quant, slab)
-    if row_scales is None:
-        raise ValueError("row_scales is missing")
-    _want(row_scales, "row_scales", sdt, sshape, dev)
-    _want(weights, "weights", _E4M3, (E, -1, K), dev)
-    N = weights.shape[1]
-    _want(weight_scales, "weight_scales", torch.float32, (E, (N + 127) // 128, K // 128), dev)
-    _want(layout.expert_count, "layout.expert_count", torch.int32, (E,), dev)
-    return dev, cap, slab, N, K
+    sdt, sshape = _scale_shape(cap, K, quant, slab)
+    ps = _want(row_scales, "row_scales", sdt, sshape, dev)
+    N = weights.shape[1] if weights.dim() == 3 else 0
+    pw = _want(weights, "weights", _E4M3, (E, N, K), dev)
+    pws = _want(weight_scales, "weight_scales", (_F32,), (E, (N + 127) // 128, K // 128), dev)
+    return dev, c, cap, slab, N, K, px, ps, pw, pws
 
 
 def ep_expert_gemm(layout: Layout, rows: torch.Tensor, row_scales: torch.Tensor,
@@ -627,13 +659,14 @@ def ep_expert_gemm(layout: Layout, rows: torch.Tensor, row_scales: torch.Tensor,
     E4M3 [E, N, K], weight_scales fp32 [E, ceil(N/128), K/128].  Rows of the
     layout that no entry fills are not written.
     """
-    dev, cap, _, N, K = _expert_checks(layout, rows, row_scales, weights, weight_scales, quant)
-    on = _On(dev, stream)
+    lib = load_library()
+    dev, c, cap, _, N, K, px, ps, pw, pws = _expert_args(lib, layout, rows, row_scales, weights,
+                                                         weight_scales, quant)
     if out is None:
-        out = on.empty((max(cap, 1), N), torch.bfloat16)
-    _want(out, "out", torch.bfloat16, (max(cap, 1), N), dev)
-    on.call("ep_expert_gemm", ctypes.byref(layout.struct()), _addr(rows), _addr(row_scales), K,
-            QUANT[quant], _addr(weights), _addr(weight_scales), N, _addr(out))
+        out = _empty((cap, N), _BF16, dev, stream)
+    po = _want(out, "out", (_BF16,), (cap, N), dev)
+    _call(lib.ep_expert_gemm, "ep_expert_gemm", dev, ctypes.byref(c), px, ps, K, QUANT[quant], pw,
+          pws, N, po, _on(stream, dev))
     return out
 
 
@@ -644,25 +677,28 @@ def ep_expert_swiglu(layout: Layout, rows: torch.Tensor, row_scales: torch.Tenso
     """Gate and up products (weights E4M3 [E, 2I, K], gate rows first) with the
     gated SiLU; returns (out_rows, out_scales) of [rows, I] in ``out_quant``, as
     ep_expert_gemm takes them (bf16 and None for "none")."""
-    dev, cap, slab, N, K = _expert_checks(layout, rows, row_scales, weights, weight_scales, quant)
+    lib = load_library()
+    dev, c, cap, slab, N, K, px, ps, pw, pws = _expert_args(lib, layout, rows, row_scales, weights,
+                                                            weight_scales, quant)
     if N % 256:
         raise EPError(EP_ERR_INVALID_ARG, "weights must have 2*I rows, I a multiple of 128")
     inter = N // 2
     if out_quant == "mxfp8":
         raise EPError(EP_ERR_UNSUPPORTED, "gated SiLU in mxfp8")
-    on = _On(dev, stream)
     plain = out_quant == "none"
     if out_rows is None:
-        out_rows = on.empty((max(cap, 1), inter), torch.bfloat16 if plain else torch.uint8)
-    _want(out_rows, "out_rows", torch.bfloat16 if plain else _E4M3, (max(cap, 1), inter), dev)
+        out_rows = _empty((cap, inter), _BF16 if plain else torch.uint8, dev, stream)
+    po = _want(out_rows, "out_rows", (_BF16,) if plain else _E4M3, (cap, inter), dev)
+    pos = None
     if not plain:
-        sdt, sshape = _scale_shape(max(cap, 1), inter, out_quant, slab)
+        sdt, sshape = _scale_shape(cap, inter, out_quant, slab)
         if out_scales is None:
-            out_scales = on.empty(sshape, sdt)
-        _want(out_scales, "out_scales", sdt, sshape, dev)
-    on.call("ep_expert_swiglu", ctypes.byref(layout.struct()), _addr(rows), _addr(row_scales), K,
-            QUANT[quant], _addr(weights), _addr(weight_scales), inter, QUANT[out_quant],
-            _addr(out_rows), _addr(out_scales))
+            out_scales = _empty(sshape, sdt[0], dev, stream)
+        pos = _want(out_scales, "out_scales", sdt, sshape, dev)
+    elif out_scales is not None:
+        raise ValueError('out_scales belong to an 8-bit out_quant, not "none"')
+    _call(lib.ep_expert_swiglu, "ep_expert_swiglu", dev, ctypes.byref(c), px, ps, K, QUANT[quant],
+          pw, pws, inter, QUANT[out_quant], po, pos, _on(stream, dev))
     return out_rows, out_scales
 
 
@@ -688,7 +724,7 @@ def ep_moe_decode_workspace_bytes(num_tokens: int, num_topk: int, num_experts: i
 
 def new_moe_workspace(num_tokens: int, num_topk: int, num_experts: int, hidden: int, inter: int,
                       device=None) -> MoeWorkspace:
-    """Allocate a workspace for ep_moe_decode calls of up to this shape."""
+    """Allocate a workspace for ep_moe_decode calls of this shape, or of fewer tokens."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     n = ep_moe_decode_workspace_bytes(num_tokens, num_topk, num_experts, hidden, inter)
     if n == 0 and num_tokens > 0:
@@ -709,38 +745,41 @@ def ep_moe_decode(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
     first), w2 E4M3 [E, H, I], both with fp32 scales of their 128x128 blocks.
     A device-side error (a bad expert id) is left in workspace.status.
     """
-    dev = _cuda(x)
-    _want(x, "x", torch.bfloat16 if quant == "none" else _E4M3, (-1, -1), dev)
-    T, H = x.shape
-    _want(topk_idx, "topk_idx", torch.int32, (T, -1), dev)
+    lib = load_library()
+    dev = _rows_of(x, "x")
+    shape = x.shape
+    T, H = shape
+    px = _want(x, "x", (_BF16,) if quant == "none" else _E4M3, shape, dev)
+    _rows_of(topk_idx, "topk_idx")
     K = topk_idx.shape[1]
-    _want(topk_w, "topk_w", torch.float32, (T, K), dev)
-    _want(w13, "w13", _E4M3, (-1, -1, H), dev)
-    E, inter = w13.shape[0], w13.shape[1] // 2
-    _want(w2, "w2", _E4M3, (E, H, inter), dev)
-    _want(w13_scales, "w13_scales", torch.float32, (E, w13.shape[1] // 128, H // 128), dev)
-    _want(w2_scales, "w2_scales", torch.float32, (E, H // 128, inter // 128), dev)
-    if w13.shape[1] % 256:
+    pi = _want(topk_idx, "topk_idx", (_I32,), (T, K), dev)
+    pw = _want(topk_w, "topk_w", (_F32,), (T, K), dev)
+    _rows_of(w13, "w13", 3)
+    E, R, _ = w13.shape
+    if R % 256:
         raise EPError(EP_ERR_INVALID_ARG, "w13 must have 2*I rows, I a multiple of 128")
-    if quant == "none":
-        if x_scales is not None:
-            raise ValueError("x_scales given for bf16 rows")
-    else:
+    inter = R // 2
+    p13 = _want(w13, "w13", _E4M3, (E, R, H), dev)
+    p2 = _want(w2, "w2", _E4M3, (E, H, inter), dev)
+    ps13 = _want(w13_scales, "w13_scales", (_F32,), (E, R // 128, H // 128), dev)
+    ps2 = _want(w2_scales, "w2_scales", (_F32,), (E, H // 128, inter // 128), dev)
+    psx = None
+    if quant != "none":
         sdt, sshape = _scale_shape(T, H, quant)
-        if x_scales is None:
-            raise ValueError("x_scales is missing")
-        _want(x_scales, "x_scales", sdt, sshape, dev)
-    on = _On(dev, stream)
+        psx = _want(x_scales, "x_scales", sdt, sshape, dev)
+    elif x_scales is not None:
+        raise ValueError("x_scales given for bf16 rows")
     if workspace is None:
         n = ep_moe_decode_workspace_bytes(T, K, E, H, inter)
-        workspace = MoeWorkspace(on.empty(max(n, 16), torch.uint8), on.empty(1, torch.int32))
+        workspace = MoeWorkspace(_empty(max(n, 16), torch.uint8, dev, stream),
+                                 _empty(1, _I32, dev, stream))
     ws = workspace.scratch
-    _want(ws, "workspace", torch.uint8, (-1,), dev)
-    _want(workspace.status, "workspace.status", torch.int32, (1,), dev)
+    nbytes = ws.numel()
+    pws = _want(ws, "workspace.scratch", (torch.uint8,), (nbytes,), dev)
+    pst = _want(workspace.status, "workspace.status", (_I32,), (1,), dev)
     if out is None:
-        out = on.empty((T, H), torch.bfloat16)
-    _want(out, "out", torch.bfloat16, (T, H), dev)
-    on.call("ep_moe_decode", _addr(x), _addr(x_scales), QUANT[quant], _addr(topk_idx),
-            _addr(topk_w), T, K, E, H, inter, _addr(w13), _addr(w13_scales), _addr(w2),
-            _addr(w2_scales), _addr(out), _addr(workspace.status), _addr(ws), ws.numel())
+        out = _empty(shape, _BF16, dev, stream)
+    po = _want(out, "out", (_BF16,), shape, dev)
+    _call(lib.ep_moe_decode, "ep_moe_decode", dev, px, psx, QUANT[quant], pi, pw, T, K, E, H, inter,
+          p13, ps13, p2, ps2, po, pst, pws, nbytes, _on(stream, dev))
     return out

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // after the wait: a predecessor's blocks that still have to allocate tensor
     // memory must find it free
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (warp == kEpiWarps + 1) tmem_alloc_all(&sh.tmem);
+    if (warp == kEpiWarps + 1) tmem_alloc<512>(&sh.tmem);
     tc_fence_before();
     block_exclusive_scan<kThreads>(
         a.E, [&](int e) { return (expert_rows(a, e) + kTM - 1) / kTM; }, pre, sh.scan);
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == kEpiWarps + 1) {
         tc_fence_after();
-        tmem_free_all(tmem);
+        tmem_free<512>(tmem);
     }
 }
 

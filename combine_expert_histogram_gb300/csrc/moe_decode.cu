@@ -40,7 +40,8 @@ constexpr int kMaxStages = 12;
 constexpr int kMaxCols = 32;                     // entries of a chunk
 constexpr int kTiles = 8;                        // tensor-memory tiles of kMaxCols columns
 constexpr int kMaxEntries = EP_MOE_DECODE_MAX_ENTRIES;
-constexpr int kSmemMax = 227 * 1024 - 1024;      // less the reserve for alignment
+constexpr int kSmemMax = 227 * 1024;
+constexpr int kSmemHalf = 113 * 1024;            // two blocks an SM (1 KB of each is reserved)
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
@@ -58,6 +59,36 @@ struct Shared {
 
 __device__ __forceinline__ void consumer_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+}
+
+// Group up to 32 entries, one a lane, by one warp.
+__device__ void group_few(const MoeArgs &a, int cols, Shared &sh) {
+    const int n = a.T * a.K, lane = threadIdx.x & 31;
+    int e = lane < n ? ld_dep(a.topk_idx + lane) : -1;
+    if (e < -1 || e >= a.E) {
+        if (blockIdx.x == 0) raise_status(a.status, EP_ERR_BAD_EXPERT_ID);
+        e = -1;
+    }
+    const int key = e < 0 ? EP_MAX_EXPERTS : e;
+    int before = 0, same = 0, count = 0;  // lower ids; the same id on lower lanes, on all
+    for (int i = 0; i < n; ++i) {
+        const int k = __shfl_sync(kFullMask, key, i);
+        before += k < key;
+        same += k == key && i < lane;
+        count += k == key;
+    }
+    const bool head = e >= 0 && same % cols == 0;  // the first entry of a chunk
+    int chunk = 0;
+    for (int i = 0; i < n; ++i) {
+        const int k = __shfl_sync(kFullMask, key, i), s = __shfl_sync(kFullMask, same, i);
+        chunk += __shfl_sync(kFullMask, (int)head, i) && (k < key || (k == key && s < same));
+    }
+    if (e >= 0) sh.entry[before + same] = (uint16_t)lane;
+    if (head)
+        sh.chunk[chunk] = (uint32_t)e | (uint32_t)(before + same) << 10 |
+                          (uint32_t)min(cols, count - same) << 20;
+    const unsigned heads = __ballot_sync(kFullMask, head);
+    if (lane == 0) sh.chunks = __popc(heads);
 }
 
 // Group the routed entries by expert.  `tmp` holds 3 * E + 2 ints and n 16-bit
@@ -158,17 +189,25 @@ __device__ __forceinline__ void load_columns(const MoeArgs &a, const float *gu, 
                 if (!UP) {
                     const float *p = gu + (size_t)entry * 2 * D + g * 128 + 8 * l;
                     float up[8] = {};
-                    for (int s = 0; s < gu_parts; ++s, p += (size_t)a.T * a.K * 2 * D) {
-                        const uint4 w[4] = {ld_dep_v4(p), ld_dep_v4(p + 4), ld_dep_v4(p + D),
-                                            ld_dep_v4(p + D + 4)};
+                    for (int s = 0; s < gu_parts; s += 2, p += (size_t)2 * a.T * a.K * 2 * D) {
+                        const bool two = s + 1 < gu_parts;  // both parts' loads in flight
+                        const float *o = two ? p + (size_t)a.T * a.K * 2 * D : p;
+                        const uint4 w[8] = {ld_dep_v4(p), ld_dep_v4(p + 4), ld_dep_v4(p + D),
+                                            ld_dep_v4(p + D + 4), ld_dep_v4(o), ld_dep_v4(o + 4),
+                                            ld_dep_v4(o + D), ld_dep_v4(o + D + 4)};
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            const uint32_t gw[4] = {w[m].x, w[m].y, w[m].z, w[m].w};
-                            const uint32_t uw[4] = {w[2 + m].x, w[2 + m].y, w[2 + m].z, w[2 + m].w};
+                        for (int q = 0; q < 2; ++q) {
+                            if (q && !two) break;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                v[b][4 * m + j] += __uint_as_float(gw[j]);
-                                up[4 * m + j] += __uint_as_float(uw[j]);
+                            for (int m = 0; m < 2; ++m) {
+                                const uint4 x = w[4 * q + m], y = w[4 * q + 2 + m];
+                                const uint32_t gw[4] = {x.x, x.y, x.z, x.w};
+                                const uint32_t uw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    v[b][4 * m + j] += __uint_as_float(gw[j]);
+                                    up[4 * m + j] += __uint_as_float(uw[j]);
+                                }
                             }
                         }
                     }
@@ -260,13 +299,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = EP_OK;
     }
     // the first kernel lets the second start only once it holds its tensor memory
-    if (warp == kWarps + 1) tmem_alloc_all(&sh.tmem);
+    if (warp == kWarps + 1) tmem_alloc<kTiles * kMaxCols>(&sh.tmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = sh.tmem;
-    group_entries(a, cols, reinterpret_cast<int32_t *>(ring), sh);
+    if (a.T * a.K <= 32) {
+        if (warp == 0) group_few(a, cols, sh);
+        __syncthreads();
+    } else {
+        group_entries(a, cols, reinterpret_cast<int32_t *>(ring), sh);
+    }
     const int row_units = R / kRows;
     const long long total = (long long)sh.chunks * row_units * parts;
     const int u0 = (int)(total * blockIdx.x / gridDim.x), u1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
@@ -402,35 +446,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == kWarps + 1) {
         tc_fence_after();
-        tmem_free_all(tmem);
+        tmem_free<kTiles * kMaxCols>(tmem);
     }
 }
 
-// out[t] = sum over k of w[t,k] * (sum over parts of y[part][t*K + k]), 8 columns a thread.
+// out[t] = sum over k of w[t,k] * (sum over parts of y[part][t*K + k]), 4 columns
+// a thread.  The loads of 8 entries are in flight together.
 __global__ void __launch_bounds__(128) sum_kernel(const MoeArgs a, const float *y, int parts) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int per = a.H / 8, i = blockIdx.x * 128 + threadIdx.x;
+    constexpr int kBatch = 8;
+    const int per = a.H / 4, i = blockIdx.x * 128 + threadIdx.x;
     const int t = i / per, c = i - t * per;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (t >= a.T) return;
-    float acc[8] = {};
-    for (int k = 0; k < a.K; ++k) {
-        const int entry = t * a.K + k, e = ld_dep(a.topk_idx + entry);
-        if (e < 0 || e >= a.E) continue;
-        const float w = ld_dep(a.topk_w + entry);
-        const float *p = y + (size_t)entry * a.H + 8 * c;
-        float v[8] = {};
-        for (int s = 0; s < parts; ++s, p += (size_t)a.T * a.K * a.H) {
-            const uint4 lo = ld_dep_v4(p), hi = ld_dep_v4(p + 4);
-            const uint32_t b[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    float acc[4] = {};
+    for (int k0 = 0; k0 < a.K; k0 += kBatch) {
+        int e[kBatch];
+        float w[kBatch];
+        uint4 v[kBatch];
 #pragma unroll
-            for (int m = 0; m < 8; ++m) v[m] += __uint_as_float(b[m]);
+        for (int k = 0; k < kBatch; ++k) {
+            const int entry = t * a.K + min(k0 + k, a.K - 1);
+            e[k] = ld_dep(a.topk_idx + entry);
+            w[k] = ld_dep(a.topk_w + entry);
+            // what an entry that is not routed holds is loaded too, and not used
+            v[k] = ld_dep_v4(y + (size_t)entry * a.H + 4 * c);
+        }
+        float s[kBatch][4];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            s[k][0] = __uint_as_float(v[k].x);
+            s[k][1] = __uint_as_float(v[k].y);
+            s[k][2] = __uint_as_float(v[k].z);
+            s[k][3] = __uint_as_float(v[k].w);
+        }
+        for (int p = 1; p < parts; ++p) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                v[k] = ld_dep_v4(y + ((size_t)p * a.T * a.K + t * a.K + min(k0 + k, a.K - 1)) * a.H + 4 * c);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                s[k][0] += __uint_as_float(v[k].x);
+                s[k][1] += __uint_as_float(v[k].y);
+                s[k][2] += __uint_as_float(v[k].z);
+                s[k][3] += __uint_as_float(v[k].w);
+            }
         }
 #pragma unroll
-        for (int m = 0; m < 8; ++m) acc[m] = fmaf(w, v[m], acc[m]);
+        for (int k = 0; k < kBatch; ++k) {
+            if (k0 + k >= a.K || e[k] < 0 || e[k] >= a.E) continue;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) acc[m] = fmaf(w[k], s[k][m], acc[m]);
+        }
     }
-    st_v4(static_cast<uint16_t *>(a.out) + (size_t)t * a.H + 8 * c,
-          make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
-                     pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7])));
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + (size_t)t * a.H + 4 * c) =
+        make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));
 }
 
 // Entries of a chunk: what experts get on average, with room for twice that, as
@@ -471,9 +540,11 @@ cudaError_t launch_rows(const MoeArgs &a, const float *gu, int gu_parts, float *
     const int box[3] = {128, kRows, 1};
     CUtensorMap wmap;
     if (!encode_bytes(&wmap, UP ? a.w13 : a.w2, 3, dims, strides, box)) return cudaErrorInvalidValue;
-    const int fixed = G * cols * (128 + 4) + (int)sizeof(Shared);
-    const int fit = (kSmemMax - fixed) / kStageBytes;
-    const int stages = fit < kMaxStages ? fit : kMaxStages;
+    const int fixed = 1024 + G * cols * (128 + 4) + (int)sizeof(Shared);
+    // Half of an SM's shared memory where that leaves a ring of five stages: the
+    // next kernel's blocks then start beside this one's and load their weights.
+    const int half = (kSmemHalf - fixed) / kStageBytes, fit = (kSmemMax - fixed) / kStageBytes;
+    const int stages = half >= 5 ? half : fit < kMaxStages ? fit : kMaxStages;
     const size_t smem = 1024 + (size_t)G * cols * (128 + 4) + (size_t)stages * kStageBytes;
     auto k = rows_kernel<UP>;
     const cudaError_t err = allow_dynamic_smem(k, smem);
@@ -497,7 +568,7 @@ cudaError_t launch_moe_decode(const MoeArgs &a, void *workspace, cudaStream_t st
     if (err != cudaSuccess) return err;
     err = launch_rows<false>(a, gu, p1, y, p2, stream);
     if (err != cudaSuccess) return err;
-    const long long threads = (long long)a.T * (a.H / 8);
+    const long long threads = (long long)a.T * (a.H / 4);
     return launch_kernel(sum_kernel, (int)((threads + 127) / 128), 128, 0, stream, true, a,
                          (const float *)y, p2);
 }
