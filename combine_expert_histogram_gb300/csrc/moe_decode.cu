@@ -14,7 +14,7 @@
 //     weights) in flight, one tiled TMA copy each.  It never waits for the
 //     previous kernel (weights are not its output), so the second kernel's ring
 //     fills while the first one drains;
-//   - four warps quantise a chunk's entries into shared memory when the run
+//   - eight warps quantise a chunk's entries into shared memory when the run
 //     comes to the next expert;
 //   - one thread issues the tensor core's E4M3 products: the weight rows are the
 //     128 rows of A, the entries the columns of B (at least 16; those past the
@@ -22,7 +22,7 @@
 //     the entries as A and 64 weight rows as columns, twice as many instructions
 //     of about 165 clocks each held the kernel to 3.6 TB/s; the m16n8k32 E4M3
 //     instruction, which converts its operands on the vector pipes, to 2.8;
-//   - the same four warps take each 128-deep block sum out of tensor memory, one
+//   - four of these warps take each 128-deep block sum out of tensor memory, one
 //     weight row a thread, and add it, scaled, to fp32 registers.
 // Partial sums over parts of a row's length are added where they are read, in
 // the order of the parts.
@@ -32,7 +32,7 @@
 namespace ep {
 namespace {
 
-constexpr int kWarps = 4;                        // quantise, scale and store
+constexpr int kWarps = 8;                        // quantise; the first four also scale and store
 constexpr int kThreads = 32 * (kWarps + 2);      // + loader, + products
 constexpr int kRows = 128;                       // weight rows of a unit
 constexpr int kStageBytes = kRows * 128;
@@ -156,116 +156,129 @@ __device__ __forceinline__ Unit unit_at(const Shared &sh, int row_units, int par
     return {sh.chunk[c], r * kRows, s, G * s / parts, G * (s + 1) / parts};
 }
 
+// Eight values of group g of the chunk's entry `col`, for lane l of the half warp
+// that takes the group: E4M3 bytes (q) and scale (s) where x is in 8 bits, else
+// fp32 (v).  UP: the token's x; else silu(gate) * up of the first kernel's sums
+// gu[part][T*K][2D].
+struct Piece {
+    uint4 raw[4];
+    float s;
+};
+template <bool UP>
+__device__ __forceinline__ Piece load_piece(const MoeArgs &a, const float *gu, int entry, int D,
+                                            int g, int l) {
+    Piece r;
+    r.s = 0.0f;
+    const int t = UP ? entry / a.K : entry, G = D >> 7;
+    const size_t at = (size_t)t * D + g * 128 + 8 * l;
+    if (!UP) {
+        const float *p = gu + (size_t)t * 2 * D + g * 128 + 8 * l;
+        r.raw[0] = ld_dep_v4(p);
+        r.raw[1] = ld_dep_v4(p + 4);
+        r.raw[2] = ld_dep_v4(p + D);
+        r.raw[3] = ld_dep_v4(p + D + 4);
+    } else if (a.quant == EP_QUANT_NONE) {
+        r.raw[0] = ld_dep_v4(static_cast<const uint16_t *>(a.x) + at);
+    } else {
+        const int32_t *p = reinterpret_cast<const int32_t *>(static_cast<const uint8_t *>(a.x) + at);
+        r.raw[0].x = (uint32_t)ld_dep(p);
+        r.raw[0].y = (uint32_t)ld_dep(p + 1);
+        if (a.quant == EP_QUANT_FP8_F32) {
+            r.s = ld_dep(static_cast<const float *>(a.x_scales) + (size_t)t * G + g);
+        } else {
+            const uint32_t word = (uint32_t)ld_dep(static_cast<const int32_t *>(a.x_scales) +
+                                                   (size_t)t * ((G + 3) / 4) + (g >> 2));
+            r.s = ue8m0_value(word >> (8 * (g & 3)) & 255u);
+        }
+    }
+    return r;
+}
+__device__ __forceinline__ void add4(uint4 &s, uint4 v) {
+    s.x = __float_as_uint(__uint_as_float(s.x) + __uint_as_float(v.x));
+    s.y = __float_as_uint(__uint_as_float(s.y) + __uint_as_float(v.y));
+    s.z = __float_as_uint(__uint_as_float(s.z) + __uint_as_float(v.z));
+    s.w = __float_as_uint(__uint_as_float(s.w) + __uint_as_float(v.w));
+}
+__device__ __forceinline__ float gate_up(uint32_t g, uint32_t u) {
+    const float x = __uint_as_float(g);
+    return __fdividef(x, 1.0f + __expf(-x)) * __uint_as_float(u);
+}
+
 // The chunk's entries as E4M3 rows in shared memory: xq[group][cols / 8] atoms of
 // 8 rows x 128 bytes in 128-byte swizzle (16-byte piece j of row r lies at piece
-// j ^ r), and xs[group][cols].  UP: the tokens' x in any of its formats; else
-// silu(gate) * up of the first kernel's sums gu[part][T*K][2D].  Half a warp
-// takes a 1x128 group, 8 values a lane.
+// j ^ r), and xs[group][cols].  Half a warp takes a 1x128 group, 8 values a lane,
+// with the next group's loads in flight.
 template <bool UP>
 __device__ __forceinline__ void load_columns(const MoeArgs &a, const float *gu, int gu_parts,
                                              uint32_t chunk, const Shared &sh, int D, int cols,
                                              uint8_t *xq, float *xs) {
-    constexpr int kBatch = 4;
     const int first = chunk >> 10 & 1023, n = (int)(chunk >> 20);
     const int G = D >> 7, items = n * G;
-    const int half = (threadIdx.x >> 4) & 1, l = threadIdx.x & 15;
-    // the bound is the same for both halves of a warp, which shuffle together
-    for (int w0 = 2 * (threadIdx.x >> 5); w0 < items; w0 += 2 * kWarps * kBatch) {
-        const int i0 = w0 + half;
-        float v[kBatch][8];
-        uint2 q[kBatch];
-        float s[kBatch];
+    const int l = threadIdx.x & 15, step = 2 * kWarps;
+    // items w, w + step, ... of this warp's two halves; the bound is the same for
+    // both, which shuffle together
+    int i = threadIdx.x >> 4;
+    int col = min(i, items - 1) / G, g = min(i, items - 1) - col * G;
+    Piece next = load_piece<UP>(a, gu, sh.entry[first + col], D, g, l);
+#pragma unroll 1
+    for (int w0 = i & ~1; w0 < items; w0 += step, i += step) {
+        Piece p = next;
+        const int c = col, gc = g, entry = sh.entry[first + col];
+        if (w0 + step < items) {
+            const int j = min(i + step, items - 1);
+            col = j / G;
+            g = j - col * G;
+            next = load_piece<UP>(a, gu, sh.entry[first + col], D, g, l);
+        }
+        uint2 q = make_uint2(p.raw[0].x, p.raw[0].y);
+        float s = p.s;
+        if (!UP || a.quant == EP_QUANT_NONE) {
+            float v[8];
+            if (UP) {
+                const uint32_t w[4] = {p.raw[0].x, p.raw[0].y, p.raw[0].z, p.raw[0].w};
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * 2 * kWarps;
-            const int col = i / G, g = i - col * G;
+                for (int m = 0; m < 4; ++m) {
+                    v[2 * m] = bf16_lo(w[m]);
+                    v[2 * m + 1] = bf16_hi(w[m]);
+                }
+            } else {
+                for (int k = 1; k < gu_parts; ++k) {  // the sums' other parts, in order
+                    const Piece o = load_piece<UP>(a, gu + (size_t)k * a.T * a.K * 2 * D, entry, D, gc, l);
 #pragma unroll
-            for (int m = 0; m < 8; ++m) v[b][m] = 0.0f;
-            q[b] = make_uint2(0, 0);
-            s[b] = 0.0f;
-            if (i < items) {
-                const int entry = sh.entry[first + col], t = UP ? entry / a.K : entry;
-                const size_t at = (size_t)t * D + g * 128 + 8 * l;
-                if (!UP) {
-                    const float *p = gu + (size_t)entry * 2 * D + g * 128 + 8 * l;
-                    float up[8] = {};
-                    for (int s = 0; s < gu_parts; s += 2, p += (size_t)2 * a.T * a.K * 2 * D) {
-                        const bool two = s + 1 < gu_parts;  // both parts' loads in flight
-                        const float *o = two ? p + (size_t)a.T * a.K * 2 * D : p;
-                        const uint4 w[8] = {ld_dep_v4(p), ld_dep_v4(p + 4), ld_dep_v4(p + D),
-                                            ld_dep_v4(p + D + 4), ld_dep_v4(o), ld_dep_v4(o + 4),
-                                            ld_dep_v4(o + D), ld_dep_v4(o + D + 4)};
+                    for (int m = 0; m < 4; ++m) add4(p.raw[m], o.raw[m]);
+                }
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            if (q && !two) break;
-#pragma unroll
-                            for (int m = 0; m < 2; ++m) {
-                                const uint4 x = w[4 * q + m], y = w[4 * q + 2 + m];
-                                const uint32_t gw[4] = {x.x, x.y, x.z, x.w};
-                                const uint32_t uw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    v[b][4 * m + j] += __uint_as_float(gw[j]);
-                                    up[4 * m + j] += __uint_as_float(uw[j]);
-                                }
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int m = 0; m < 8; ++m)
-                        v[b][m] = __fdividef(v[b][m], 1.0f + __expf(-v[b][m])) * up[m];
-                } else if (a.quant == EP_QUANT_NONE) {
-                    const uint4 x = ld_dep_v4(static_cast<const uint16_t *>(a.x) + at);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        v[b][2 * m] = bf16_lo(w[m]);
-                        v[b][2 * m + 1] = bf16_hi(w[m]);
-                    }
-                } else {
-                    const int32_t *p = reinterpret_cast<const int32_t *>(
-                        static_cast<const uint8_t *>(a.x) + at);
-                    q[b] = make_uint2((uint32_t)ld_dep(p), (uint32_t)ld_dep(p + 1));
-                    if (a.quant == EP_QUANT_FP8_F32) {
-                        s[b] = ld_dep(static_cast<const float *>(a.x_scales) + (size_t)t * G + g);
-                    } else {
-                        const uint32_t word = (uint32_t)ld_dep(
-                            static_cast<const int32_t *>(a.x_scales) + (size_t)t * ((G + 3) / 4) +
-                            (g >> 2));
-                        s[b] = ue8m0_value(word >> (8 * (g & 3)) & 255u);
-                    }
+                for (int m = 0; m < 2; ++m) {
+                    const uint4 x = p.raw[m], y = p.raw[2 + m];
+                    v[4 * m] = gate_up(x.x, y.x);
+                    v[4 * m + 1] = gate_up(x.y, y.y);
+                    v[4 * m + 2] = gate_up(x.z, y.z);
+                    v[4 * m + 3] = gate_up(x.w, y.w);
                 }
             }
+            float amax = 0.0f;
+#pragma unroll
+            for (int m = 0; m < 8; ++m) amax = fmaxf(amax, fabsf(v[m]));
+#pragma unroll
+            for (int d = 8; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, d));
+            s = group_scale(amax);
+#pragma unroll
+            for (int m = 0; m < 8; ++m) v[m] = __fdiv_rn(v[m], s);
+            q = make_uint2(fp8x4(v[0], v[1], v[2], v[3]), fp8x4(v[4], v[5], v[6], v[7]));
         }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * 2 * kWarps;
-            const int col = i / G, g = i - col * G;
-            if (!UP || a.quant == EP_QUANT_NONE) {
-                float amax = 0.0f;
-#pragma unroll
-                for (int m = 0; m < 8; ++m) amax = fmaxf(amax, fabsf(v[b][m]));
-#pragma unroll
-                for (int d = 8; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, d));
-                s[b] = group_scale(amax);
-#pragma unroll
-                for (int m = 0; m < 8; ++m) v[b][m] = __fdiv_rn(v[b][m], s[b]);
-                q[b] = make_uint2(fp8x4(v[b][0], v[b][1], v[b][2], v[b][3]),
-                                  fp8x4(v[b][4], v[b][5], v[b][6], v[b][7]));
-            }
-            if (i < items) {
-                *reinterpret_cast<uint2 *>(xq + (g * cols + col) * 128 +
-                                           (((l >> 1) ^ (col & 7)) << 4) + 8 * (l & 1)) = q[b];
-                if (l == 0) xs[g * cols + col] = s[b];
-            }
+        if (i < items) {
+            *reinterpret_cast<uint2 *>(xq + (gc * cols + c) * 128 + (((l >> 1) ^ (c & 7)) << 4) +
+                                       8 * (l & 1)) = q;
+            if (l == 0) xs[gc * cols + c] = s;
         }
+        __syncwarp();
     }
 }
 
 // dst[part][T*K][R] = rows of W13 (UP: R = 2I, D = H) or of W2 (R = H, D = I)
 // against the entries, fp32.
 template <bool UP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     rows_kernel(const __grid_constant__ CUtensorMap wmap, const MoeArgs a, const float *gu,
                 int gu_parts, float *dst, int parts, int cols, int stages) {
     extern __shared__ __align__(16) uint8_t raw[];
@@ -285,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kTiles; ++i) {
             mbar_init(&sh.tfull[i], 1);
-            mbar_init(&sh.tempty[i], kWarps);
+            mbar_init(&sh.tempty[i], 4);
         }
         mbar_init(&sh.columns, kWarps);
         mbar_init(&sh.drain, 1);
@@ -382,15 +395,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- entries, scales, sums.  After a wait that ran out the loops go on
         // (every later wait returns at once), so that all warps meet at the barriers ----
         if (!UP) asm volatile("griddepcontrol.wait;" ::: "memory");
+        const bool adds = warp < 4;  // one for each 32 lanes of tensor memory
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const float *scales = UP ? a.w13_scales : a.w2_scales;
+        // the weight scales of up to 32 blocks, one a lane; those of the next blocks
+        // or of the next unit are in flight meanwhile
+        auto fetch = [&](const Unit &un, int g0) {
+            return g0 + lane < un.g1
+                       ? __ldg(scales + ((size_t)(un.chunk & 1023) * row_units + (un.row >> 7)) * G + g0 + lane)
+                       : 0.0f;
+        };
         uint32_t have = 0xffffffffu;  // the chunk whose entries are in xq
         int it = 0;
+        Unit un = unit_at(sh, row_units, parts, G, u0 < u1 ? u0 : 0);
+        float wnext = adds && u0 < u1 ? fetch(un, un.g0) : 0.0f;
         for (int u = u0; u < u1; ++u) {
-            const Unit un = unit_at(sh, row_units, parts, G, u);
-            const int e = un.chunk & 1023, first = un.chunk >> 10 & 1023, n = (int)(un.chunk >> 20);
-            const float *sw = (UP ? a.w13_scales : a.w2_scales) +
-                              ((size_t)e * row_units + (un.row >> 7)) * G;
-            float w = __ldg(sw + un.g0);
+            const int first = un.chunk >> 10 & 1023, n = (int)(un.chunk >> 20);
             if (un.chunk != have) {
                 consumer_sync();  // every warp is done with the old entries
                 load_columns<UP>(a, gu, gu_parts, un.chunk, sh, D, cols, xq, xs);
@@ -399,34 +419,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&sh.columns);
                 have = un.chunk;
             }
+            const Unit now = un;
+            if (u + 1 < u1) un = unit_at(sh, row_units, parts, G, u + 1);
+            if (!adds) continue;
             float acc[kMaxCols];
 #pragma unroll
             for (int i = 0; i < kMaxCols; ++i) acc[i] = 0.0f;
-            for (int g = un.g0; g < un.g1; ++g, ++it) {
-                const int b = it % kTiles;
-                const float s = w;
-                if (g + 1 < un.g1) w = __ldg(sw + g + 1);
-                const bool ok = mbar_wait_fast(&sh.tfull[b], (it / kTiles) & 1, fail);
-                if (!__all_sync(kFullMask, ok)) sh.fail = 1;
-                tc_fence_after();
+            for (int g32 = now.g0; g32 < now.g1; g32 += 32) {
+                const float w = wnext;
+                if (g32 + 32 < now.g1) wnext = fetch(now, g32 + 32);
+                else if (u + 1 < u1) wnext = fetch(un, un.g0);
+                for (int g = g32; g < min(g32 + 32, now.g1); ++g, ++it) {
+                    const int b = it % kTiles;
+                    const bool ok = mbar_wait_fast(&sh.tfull[b], (it / kTiles) & 1, fail);
+                    const float s = __shfl_sync(kFullMask, w, g - g32);
+                    if (!__all_sync(kFullMask, ok)) sh.fail = 1;
+                    tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < kMaxCols; c += 8) {
-                    if (c >= n) break;
-                    uint32_t v[8];
-                    tmem_ld(tmem + lanes + b * kMaxCols + c, v);
-                    const float4 x0 = *reinterpret_cast<const float4 *>(xs + g * cols + c);
-                    const float4 x1 = *reinterpret_cast<const float4 *>(xs + g * cols + c + 4);
-                    const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-                    tmem_ld_wait(v);
+                    for (int c = 0; c < kMaxCols; c += 8) {
+                        if (c >= n) break;
+                        uint32_t v[8];
+                        tmem_ld(tmem + lanes + b * kMaxCols + c, v);
+                        const float4 x0 = *reinterpret_cast<const float4 *>(xs + g * cols + c);
+                        const float4 x1 = *reinterpret_cast<const float4 *>(xs + g * cols + c + 4);
+                        const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+                        tmem_ld_wait(v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        acc[c + i] = fmaf(__uint_as_float(v[i]), s * x[i], acc[c + i]);
+                        for (int i = 0; i < 8; ++i)
+                            acc[c + i] = fmaf(__uint_as_float(v[i]), s * x[i], acc[c + i]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.tempty[b]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.tempty[b]);
             }
-            float *out = dst + (size_t)un.part * a.T * a.K * R + un.row + threadIdx.x;
+            float *out = dst + (size_t)now.part * a.T * a.K * R + now.row + threadIdx.x;
 #pragma unroll
             for (int i = 0; i < kMaxCols; ++i)
                 if (i < n) out[(size_t)sh.entry[first + i] * R] = acc[i];
@@ -511,16 +538,17 @@ int chunk_cols(const MoeArgs &a, int D) {
 }
 
 // Parts a row's length is cut into: with few entries there are few 128-row units,
-// and the SM with one more than the others sets the time.  The best share-out of
-// 1, 2 or 4 parts where the units are below 8 an SM; 1 above, where the loss is
-// below an eighth.
+// and the SM with one more than the others sets the time.  1 from 24 units an SM
+// on, 2 from 8 on (how many there will be is not known to a few percent), below
+// that the best share-out of 1, 2 or 4.
 int row_parts(int entries, int E, int R, int D) {
-    const int sms = sm_count();
+    const int sms = sm_count(), G = D / 128;
     const int64_t units = (int64_t)(entries < E ? entries : E) * (R / kRows);
-    if (units >= 8 * sms) return 1;
+    if (units >= 24 * sms) return 1;
+    if (units >= 8 * sms) return G >= 4 ? 2 : 1;
     int best = 1;
     double most = 0.0;
-    for (int p = 1; p <= 4 && D / 128 >= 2 * p; p *= 2) {
+    for (int p = 1; p <= 4 && G >= 2 * p; p *= 2) {
         const int64_t u = units * p;
         const double even = (double)u / ((u + sms - 1) / sms * sms);
         if (even > most + 0.03) {
