@@ -343,8 +343,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 if (elect_one()) {
                     expect_bytes(&sh.full[s], kStageBytes);
-                    tma_load_3d(ring + s * kStageBytes, &wmap, g * 128, un.row, un.chunk & 1023,
-                                &sh.full[s]);
+                    tma_load_3d_once(ring + s * kStageBytes, &wmap, g * 128, un.row,
+                                     un.chunk & 1023, &sh.full[s]);
                 }
                 __syncwarp();
             }
@@ -569,10 +569,15 @@ cudaError_t launch_rows(const MoeArgs &a, const float *gu, int gu_parts, float *
     CUtensorMap wmap;
     if (!encode_bytes(&wmap, UP ? a.w13 : a.w2, 3, dims, strides, box)) return cudaErrorInvalidValue;
     const int fixed = 1024 + G * cols * (128 + 4) + (int)sizeof(Shared);
-    // Half of an SM's shared memory where that leaves a ring of five stages: the
-    // next kernel's blocks then start beside this one's and load their weights.
+    // Up to 1 MB of weights an SM, half of its shared memory where that leaves a
+    // ring of five stages: the next kernel's blocks then start beside this one's
+    // and load their weights (moe_odd's sizes: 28.0 us, 30.5 with all of it).
+    // Above, all of it: five stages hold 64 tokens of H = 7168, I = 2048 to 1.90 ms,
+    // ten to 1.85.
+    const int n = a.T * a.K;
+    const bool small = (int64_t)(n < a.E ? n : a.E) * R * D <= (int64_t)sm_count() << 20;
     const int half = (kSmemHalf - fixed) / kStageBytes, fit = (kSmemMax - fixed) / kStageBytes;
-    const int stages = half >= 5 ? half : fit < kMaxStages ? fit : kMaxStages;
+    const int stages = small && half >= 5 ? half : fit < kMaxStages ? fit : kMaxStages;
     const size_t smem = 1024 + (size_t)G * cols * (128 + 4) + (size_t)stages * kStageBytes;
     auto k = rows_kernel<UP>;
     const cudaError_t err = allow_dynamic_smem(k, smem);
