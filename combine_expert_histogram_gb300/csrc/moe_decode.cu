@@ -38,7 +38,9 @@ constexpr int kRows = 128;                       // weight rows of a unit
 constexpr int kStageBytes = kRows * 128;
 constexpr int kMaxStages = 12;
 constexpr int kMaxCols = 32;                     // entries of a chunk
-constexpr int kTiles = 8;                        // tensor-memory tiles of kMaxCols columns
+constexpr int kGroup = 4;                        // blocks of 128 taken together
+constexpr int kTiles = 2;                        // tensor-memory tiles of kGroup block sums
+constexpr int kTileCols = kGroup * kMaxCols;
 constexpr int kMaxEntries = EP_MOE_DECODE_MAX_ENTRIES;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kSmemHalf = 113 * 1024;            // two blocks an SM (1 KB of each is reserved)
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = EP_OK;
     }
     // the first kernel lets the second start only once it holds its tensor memory
-    if (warp == kWarps + 1) tmem_alloc<kTiles * kMaxCols>(&sh.tmem);
+    if (warp == kWarps + 1) tmem_alloc<kTiles * kTileCols>(&sh.tmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -331,12 +333,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == kWarps) {
         // ---- loads ----
         fence_proxy_async_smem();  // the ring held the grouping's counters
-        int it = 0;
+        int it = 0, s = 0;
+        uint32_t lap = 0;
         for (int u = u0; u < u1 && !__any_sync(kFullMask, *fail); ++u) {
             const Unit un = unit_at(sh, row_units, parts, G, u);
             for (int g = un.g0; g < un.g1; ++g, ++it) {
-                const int s = it % stages;
-                const bool ok = it < stages || mbar_wait_fast(&sh.empty[s], (it / stages - 1) & 1, fail);
+                const bool ok = lap == 0 || mbar_wait_fast(&sh.empty[s], (lap - 1) & 1, fail);
                 if (!__all_sync(kFullMask, ok)) {
                     sh.fail = 1;
                     break;
@@ -347,46 +349,54 @@ __global__ void __launch_bounds__(kThreads, 2)
                                      un.chunk & 1023, &sh.full[s]);
                 }
                 __syncwarp();
+                if (++s == stages) {
+                    s = 0;
+                    ++lap;
+                }
             }
         }
         if (lane == 0) sh.issued = it;
     } else if (warp == kWarps + 1) {
         // ---- products ----
         const uint32_t instr = e4m3_instr(kRows, cols < 16 ? 16 : cols);
-        int it = 0, loaded = 0;
+        int tile = 0, s = 0, loaded = 0;
+        uint32_t lap = 0;
         uint32_t have = 0xffffffffu;
-        for (int u = u0; u < u1 && !__any_sync(kFullMask, *fail); ++u) {
+        bool ok = true;
+        for (int u = u0; ok && u < u1; ++u) {
             const Unit un = unit_at(sh, row_units, parts, G, u);
             if (un.chunk != have) {
                 have = un.chunk;
-                if (!__all_sync(kFullMask, mbar_wait_fast(&sh.columns, loaded & 1, fail))) {
-                    sh.fail = 1;
-                    break;
-                }
+                ok = __all_sync(kFullMask, mbar_wait_fast(&sh.columns, loaded & 1, fail));
                 ++loaded;
             }
-            for (int g = un.g0; g < un.g1; ++g, ++it) {
-                const int s = it % stages, b = it % kTiles;
-                const bool ok =
-                    (it < kTiles || mbar_wait_fast(&sh.tempty[b], (it / kTiles - 1) & 1, fail)) &&
-                    mbar_wait_fast(&sh.full[s], (it / stages) & 1, fail);
-                if (!__all_sync(kFullMask, ok)) {
-                    sh.fail = 1;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t da = tile_desc(smem_addr(ring + s * kStageBytes));
-                const uint64_t db = tile_desc(smem_addr(xq + g * cols * 128));
-                if (elect_one()) {
+            for (int g0 = un.g0; ok && g0 < un.g1; g0 += kGroup, ++tile) {
+                const int b = tile % kTiles, n = min(kGroup, un.g1 - g0);
+                ok = tile < kTiles || mbar_wait_fast(&sh.tempty[b], (tile / kTiles - 1) & 1, fail);
+                for (int k = 0; k < n; ++k) {
+                    ok = mbar_wait_fast(&sh.full[s], lap & 1, fail) && ok;
+                    ok = __all_sync(kFullMask, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t da = tile_desc(smem_addr(ring + s * kStageBytes));
+                    const uint64_t db = tile_desc(smem_addr(xq + (g0 + k) * cols * 128));
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_e4m3(tmem + b * kMaxCols, da + 2 * j, db + 2 * j, instr, j > 0);
-                    mma_commit(&sh.empty[s]);
-                    mma_commit(&sh.tfull[b]);
+                        for (int j = 0; j < 4; ++j)
+                            mma_e4m3(tmem + b * kTileCols + k * kMaxCols, da + 2 * j, db + 2 * j,
+                                     instr, j > 0);
+                        mma_commit(&sh.empty[s]);
+                        if (k == n - 1) mma_commit(&sh.tfull[b]);
+                    }
+                    __syncwarp();
+                    if (++s == stages) {
+                        s = 0;
+                        ++lap;
+                    }
                 }
-                __syncwarp();
             }
         }
+        if (!ok) sh.fail = 1;
         // tensor memory and the barriers outlive the last product
         if (elect_one()) mma_commit(&sh.drain);
         __syncwarp();
@@ -406,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                        : 0.0f;
         };
         uint32_t have = 0xffffffffu;  // the chunk whose entries are in xq
-        int it = 0;
+        int tile = 0;
         Unit un = unit_at(sh, row_units, parts, G, u0 < u1 ? u0 : 0);
         float wnext = adds && u0 < u1 ? fetch(un, un.g0) : 0.0f;
         for (int u = u0; u < u1; ++u) {
@@ -429,24 +439,35 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const float w = wnext;
                 if (g32 + 32 < now.g1) wnext = fetch(now, g32 + 32);
                 else if (u + 1 < u1) wnext = fetch(un, un.g0);
-                for (int g = g32; g < min(g32 + 32, now.g1); ++g, ++it) {
-                    const int b = it % kTiles;
-                    const bool ok = mbar_wait_fast(&sh.tfull[b], (it / kTiles) & 1, fail);
-                    const float s = __shfl_sync(kFullMask, w, g - g32);
+                for (int g0 = g32; g0 < min(g32 + 32, now.g1); g0 += kGroup, ++tile) {
+                    const int b = tile % kTiles, m = min(kGroup, now.g1 - g0);
+                    const bool ok = mbar_wait_fast(&sh.tfull[b], (tile / kTiles) & 1, fail);
                     if (!__all_sync(kFullMask, ok)) sh.fail = 1;
                     tc_fence_after();
+                    // eight entries of all the tile's blocks at a time (what lies past
+                    // the last block is read and not used)
+                    float s[kGroup];
+#pragma unroll
+                    for (int k = 0; k < kGroup; ++k) s[k] = __shfl_sync(kFullMask, w, g0 - g32 + k);
 #pragma unroll
                     for (int c = 0; c < kMaxCols; c += 8) {
                         if (c >= n) break;
-                        uint32_t v[8];
-                        tmem_ld(tmem + lanes + b * kMaxCols + c, v);
-                        const float4 x0 = *reinterpret_cast<const float4 *>(xs + g * cols + c);
-                        const float4 x1 = *reinterpret_cast<const float4 *>(xs + g * cols + c + 4);
-                        const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-                        tmem_ld_wait(v);
+                        uint32_t v[kGroup][8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            acc[c + i] = fmaf(__uint_as_float(v[i]), s * x[i], acc[c + i]);
+                        for (int k = 0; k < kGroup; ++k)
+                            tmem_ld(tmem + lanes + b * kTileCols + k * kMaxCols + c, v[k]);
+#pragma unroll
+                        for (int k = 0; k < kGroup; ++k) tmem_ld_wait(v[k]);
+#pragma unroll
+                        for (int k = 0; k < kGroup; ++k) {
+                            if (k >= m) break;
+                            const float4 x0 = *reinterpret_cast<const float4 *>(xs + (g0 + k) * cols + c);
+                            const float4 x1 = *reinterpret_cast<const float4 *>(xs + (g0 + k) * cols + c + 4);
+                            const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                acc[c + i] = fmaf(__uint_as_float(v[k][i]), s[k] * x[i], acc[c + i]);
+                        }
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -473,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (warp == kWarps + 1) {
         tc_fence_after();
-        tmem_free<kTiles * kMaxCols>(tmem);
+        tmem_free<kTiles * kTileCols>(tmem);
     }
 }
 
