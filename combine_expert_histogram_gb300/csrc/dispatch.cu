@@ -63,12 +63,6 @@ __device__ __forceinline__ void bulk_store(void *gdst, const void *ssrc, uint32_
                  ::"l"(gdst), "r"(smem_addr(ssrc)), "r"(bytes), "l"(policy)
                  : "memory");
 }
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// Wait until at most N of this thread's bulk groups are still reading their source.
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
 // Quantise one FP8 slot (16 consecutive elements a, b of group j/8, part
 // lane%8 of its 8 lanes).  Returns the 16 E4M3 bytes; `sc` receives the
 // group's fp32 scale bits (FP8_F32), its UE8M0 exponent byte (FP8_UE8M0*), or

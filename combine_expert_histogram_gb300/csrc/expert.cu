@@ -34,11 +34,18 @@ constexpr int kEpiRegs = 216, kOtherRegs = 72;
 constexpr int kTM = 128, kTN = 256;              // tile: rows, weight rows
 constexpr int kABytes = kTM * 128, kBBytes = kTN * 128;
 constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 4;
+constexpr int kMaxStages = 4;
+constexpr int kOutStride = 256 + 16;             // staged bf16 half row; the pad spreads the banks
+constexpr int kOutBytes = kEpiWarps * 32 * kOutStride;
+// The plain product stages its output rows in place of a fourth K block.
+template <bool GATED>
+constexpr int stages() { return GATED ? 4 : 3; }
+template <bool GATED>
+constexpr int ring_bytes() { return stages<GATED>() * kStageBytes + (GATED ? 0 : kOutBytes); }
 constexpr int kSlots = 4;                        // K blocks of scales ahead of their sums
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages];  // ring of K blocks
+    uint64_t full[kMaxStages], empty[kMaxStages];  // ring of K blocks
     uint64_t tfull[2], tempty[2];            // tensor-memory tiles
     uint64_t sfull[kSlots], sempty[kSlots];  // scales
     uint64_t xchg;                           // the column halves' group maxima
@@ -89,9 +96,14 @@ __device__ __forceinline__ void fma_scaled(float *acc, const uint32_t (&v)[32], 
     }
 }
 
-__device__ __forceinline__ void store_bf16x8(uint16_t *dst, const float *v) {
-    st_v4(dst, make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                          pack_bf16(v[6], v[7])));
+__device__ __forceinline__ uint4 bf16x8(const float *v) {
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                      pack_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ void bulk_store_row(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                 "r"(smem_addr(src)), "r"(bytes)
+                 : "memory");
 }
 
 template <bool GATED>
@@ -99,10 +111,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     expert_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                   const ExpertArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
-    // [kStages] K blocks (the swizzle wants 1024-byte alignment), [E+1] tile prefix
+    // K blocks (the swizzle wants 1024-byte alignment), output rows, [E+1] tile prefix
     uint8_t *smem = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
     __shared__ Shared sh;
-    int32_t *pre = reinterpret_cast<int32_t *>(smem + kStages * kStageBytes);
+    constexpr int kStages = stages<GATED>();
+    int32_t *pre = reinterpret_cast<int32_t *>(smem + ring_bytes<GATED>());
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const volatile int *fail = &sh.fail;
 
@@ -290,11 +303,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             if constexpr (!GATED) {
+                // Each thread's 256 bytes of its row go through shared memory to one
+                // bulk copy: stored from registers, 32 rows an instruction, a tile took
+                // 4300 clocks.
                 const int c0 = q.n0 + half * 128;
-                uint16_t *dst = static_cast<uint16_t *>(a.out) + (size_t)(q.row + r) * a.N + c0;
+                uint8_t *row = smem + kStages * kStageBytes + threadIdx.x * kOutStride;
+                bulk_wait_read<0>();  // the last tile's copy has read them
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    if (valid && c0 + 8 * j < a.N) store_bf16x8(dst + 8 * j, acc + 8 * j);
+                    *reinterpret_cast<uint4 *>(row + 16 * j) = bf16x8(acc + 8 * j);
+                fence_proxy_async_smem();
+                if (valid && c0 < a.N) {
+                    bulk_store_row(static_cast<uint16_t *>(a.out) + (size_t)(q.row + r) * a.N + c0,
+                                   row, 2u * (uint32_t)min(128, a.N - c0));
+                    bulk_commit();
+                }
+                __syncwarp();
             } else {
                 float amax = 0.0f;
 #pragma unroll
@@ -307,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (a.out_quant == EP_QUANT_NONE) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (valid) store_bf16x8(static_cast<uint16_t *>(a.out) + at + 8 * j, acc + 8 * j);
+                        if (valid) st_v4(static_cast<uint16_t *>(a.out) + at + 8 * j, bf16x8(acc + 8 * j));
                     continue;
                 }
                 // the row's other 64 columns are with the other half's warp
@@ -340,13 +364,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
+    bulk_wait_read<0>();  // shared memory outlives the copies out of it
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (sh.fail) {
         if (threadIdx.x == 0) raise_status(a.status, EP_ERR_TIMEOUT);
         // let the loads in flight land before the shared memory goes
-        if (threadIdx.x < kStages) {
+        if ((int)threadIdx.x < kStages) {
             const int last = sh.issued - 1 - (int)threadIdx.x;
             if (last >= 0) mbar_wait(&sh.full[last % kStages], (last / kStages) & 1, nullptr);
         }
@@ -404,7 +429,7 @@ cudaError_t launch_expert(const ExpertArgs &a, bool gated, cudaStream_t stream) 
     if (!encode_bytes(&xmap, a.x, 2, xdims, xstride, xbox) ||
         !encode_bytes(&wmap, a.w, 3, wdims, wstride, wbox))
         return cudaErrorInvalidValue;
-    const size_t smem = 1024 + kStages * kStageBytes + (a.E + 1) * 4;
+    const size_t smem = 1024 + (gated ? ring_bytes<true>() : ring_bytes<false>()) + (a.E + 1) * 4;
     auto k = gated ? expert_kernel<true> : expert_kernel<false>;
     const cudaError_t err = allow_dynamic_smem(k, smem);
     if (err != cudaSuccess) return err;
