@@ -147,16 +147,41 @@ __device__ void group_entries(const MoeArgs &a, int cols, int32_t *tmp, Shared &
     __syncthreads();
 }
 
-// Unit u of the list: its chunk, first weight row, and 128-wide blocks [g0, g1).
+// A unit of the list: its chunk, first weight row, and 128-wide blocks [g0, g1).
 struct Unit {
     uint32_t chunk;
-    int row, part, g0, g1;
+    int c, row, part, g0, g1;
 };
-__device__ __forceinline__ Unit unit_at(const Shared &sh, int row_units, int parts, int G, int u) {
-    const int c = u / (row_units * parts), v = u - c * row_units * parts;
-    const int r = v / parts, s = v - r * parts;
-    return {sh.chunk[c], r * kRows, s, G * s / parts, G * (s + 1) / parts};
-}
+struct Units {
+    int row_units, parts, G;
+    __device__ __forceinline__ void blocks(Unit &u) const {
+        u.g0 = parts == 1 ? 0 : G * u.part / parts;
+        u.g1 = parts == 1 ? G : G * (u.part + 1) / parts;
+    }
+    // Unit number i (i below their number).
+    __device__ __forceinline__ Unit at(const Shared &sh, int i) const {
+        Unit u;
+        u.c = i / (row_units * parts);
+        const int v = i - u.c * row_units * parts, r = v / parts;
+        u.part = v - r * parts;
+        u.row = r * kRows;
+        u.chunk = sh.chunk[u.c];
+        blocks(u);
+        return u;
+    }
+    // The one after u (there has to be one).
+    __device__ __forceinline__ void next(const Shared &sh, Unit &u) const {
+        if (++u.part == parts) {
+            u.part = 0;
+            u.row += kRows;
+            if (u.row == row_units * kRows) {
+                u.row = 0;
+                u.chunk = sh.chunk[++u.c];
+            }
+        }
+        blocks(u);
+    }
+};
 
 // Eight values of group g of the chunk's entry `col`, for lane l of the half warp
 // that takes the group: E4M3 bytes (q) and scale (s) where x is in 8 bits, else
@@ -327,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         group_entries(a, cols, reinterpret_cast<int32_t *>(ring), sh);
     }
     const int row_units = R / kRows;
+    const Units units = {row_units, parts, G};
     const long long total = (long long)sh.chunks * row_units * parts;
     const int u0 = (int)(total * blockIdx.x / gridDim.x), u1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
 
@@ -335,8 +361,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         fence_proxy_async_smem();  // the ring held the grouping's counters
         int it = 0, s = 0;
         uint32_t lap = 0;
+        Unit un;
         for (int u = u0; u < u1 && !__any_sync(kFullMask, *fail); ++u) {
-            const Unit un = unit_at(sh, row_units, parts, G, u);
+            if (u == u0) un = units.at(sh, u);
+            else units.next(sh, un);
             for (int g = un.g0; g < un.g1; ++g, ++it) {
                 const bool ok = lap == 0 || mbar_wait_fast(&sh.empty[s], (lap - 1) & 1, fail);
                 if (!__all_sync(kFullMask, ok)) {
@@ -363,8 +391,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint32_t lap = 0;
         uint32_t have = 0xffffffffu;
         bool ok = true;
+        Unit un;
         for (int u = u0; ok && u < u1; ++u) {
-            const Unit un = unit_at(sh, row_units, parts, G, u);
+            if (u == u0) un = units.at(sh, u);
+            else units.next(sh, un);
             if (un.chunk != have) {
                 have = un.chunk;
                 ok = __all_sync(kFullMask, mbar_wait_fast(&sh.columns, loaded & 1, fail));
@@ -417,8 +447,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         uint32_t have = 0xffffffffu;  // the chunk whose entries are in xq
         int tile = 0;
-        Unit un = unit_at(sh, row_units, parts, G, u0 < u1 ? u0 : 0);
-        float wnext = adds && u0 < u1 ? fetch(un, un.g0) : 0.0f;
+        Unit un = {};
+        float wnext = 0.0f;
+        if (u0 < u1) {
+            un = units.at(sh, u0);
+            if (adds) wnext = fetch(un, un.g0);
+        }
         for (int u = u0; u < u1; ++u) {
             const int first = un.chunk >> 10 & 1023, n = (int)(un.chunk >> 20);
             if (un.chunk != have) {
@@ -430,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 have = un.chunk;
             }
             const Unit now = un;
-            if (u + 1 < u1) un = unit_at(sh, row_units, parts, G, u + 1);
+            if (u + 1 < u1) units.next(sh, un);
             if (!adds) continue;
             float acc[kMaxCols];
 #pragma unroll
@@ -476,8 +510,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             float *out = dst + (size_t)now.part * a.T * a.K * R + now.row + threadIdx.x;
 #pragma unroll
-            for (int i = 0; i < kMaxCols; ++i)
-                if (i < n) out[(size_t)sh.entry[first + i] * R] = acc[i];
+            for (int i = 0; i < kMaxCols; ++i) {
+                if (i >= n) break;
+                out[(size_t)sh.entry[first + i] * R] = acc[i];
+            }
         }
     }
     __syncwarp();
