@@ -39,15 +39,14 @@ constexpr int kStageBytes = kRows * 128;
 constexpr int kMaxStages = 12;
 constexpr int kMaxCols = 32;                     // entries of a chunk
 constexpr int kGroup = 4;                        // blocks of 128 taken together
-constexpr int kTiles = 2;                        // tensor-memory tiles of kGroup block sums
-constexpr int kTileCols = kGroup * kMaxCols;
+constexpr int kMaxTiles = 4;                     // tensor-memory tiles of kGroup block sums
 constexpr int kMaxEntries = EP_MOE_DECODE_MAX_ENTRIES;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kSmemHalf = 113 * 1024;            // two blocks an SM (1 KB of each is reserved)
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t tfull[kTiles], tempty[kTiles];
+    uint64_t tfull[kMaxTiles], tempty[kMaxTiles];
     uint64_t columns;              // a chunk's entries are in shared memory
     uint64_t drain;
     uint32_t tmem;
@@ -304,12 +303,15 @@ __device__ __forceinline__ void load_columns(const MoeArgs &a, const float *gu, 
 
 // dst[part][T*K][R] = rows of W13 (UP: R = 2I, D = H) or of W2 (R = H, D = I)
 // against the entries, fp32.
-template <bool UP>
+template <bool UP, int COLS>
 __global__ void __launch_bounds__(kThreads, 2)
     rows_kernel(const __grid_constant__ CUtensorMap wmap, const MoeArgs a, const float *gu,
-                int gu_parts, float *dst, int parts, int cols, int stages) {
+                int gu_parts, float *dst, int parts, int stages) {
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ Shared sh;
+    constexpr int cols = COLS;                       // entries of a chunk
+    constexpr int kN = COLS < 16 ? 16 : COLS;        // columns of a product
+    constexpr int kTileCols = kGroup * kN, kTiles = COLS < 32 ? 4 : 2;
     const int D = UP ? a.H : a.I, R = UP ? 2 * a.I : a.H, G = D >> 7;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // entries first: the products' unused columns read on into the ring
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) sh.issued = it;
     } else if (warp == kWarps + 1) {
         // ---- products ----
-        const uint32_t instr = e4m3_instr(kRows, cols < 16 ? 16 : cols);
+        constexpr uint32_t instr = e4m3_instr(kRows, kN);
         int tile = 0, s = 0, loaded = 0;
         uint32_t lap = 0;
         uint32_t have = 0xffffffffu;
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (elect_one()) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            mma_e4m3(tmem + b * kTileCols + k * kMaxCols, da + 2 * j, db + 2 * j,
+                            mma_e4m3(tmem + b * kTileCols + k * kN, da + 2 * j, db + 2 * j,
                                      instr, j > 0);
                         mma_commit(&sh.empty[s]);
                         if (k == n - 1) mma_commit(&sh.tfull[b]);
@@ -466,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             const Unit now = un;
             if (u + 1 < u1) units.next(sh, un);
             if (!adds) continue;
-            float acc[kMaxCols];
+            float acc[COLS];
 #pragma unroll
-            for (int i = 0; i < kMaxCols; ++i) acc[i] = 0.0f;
+            for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
             for (int g32 = now.g0; g32 < now.g1; g32 += 32) {
                 const float w = wnext;
                 if (g32 + 32 < now.g1) wnext = fetch(now, g32 + 32);
@@ -484,12 +486,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                     for (int k = 0; k < kGroup; ++k) s[k] = __shfl_sync(kFullMask, w, g0 - g32 + k);
 #pragma unroll
-                    for (int c = 0; c < kMaxCols; c += 8) {
+                    for (int c = 0; c < COLS; c += 8) {
                         if (c >= n) break;
                         uint32_t v[kGroup][8];
 #pragma unroll
                         for (int k = 0; k < kGroup; ++k)
-                            tmem_ld(tmem + lanes + b * kTileCols + k * kMaxCols + c, v[k]);
+                            tmem_ld(tmem + lanes + b * kTileCols + k * kN + c, v[k]);
 #pragma unroll
                         for (int k = 0; k < kGroup; ++k) tmem_ld_wait(v[k]);
 #pragma unroll
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             float *out = dst + (size_t)now.part * a.T * a.K * R + now.row + threadIdx.x;
 #pragma unroll
-            for (int i = 0; i < kMaxCols; ++i) {
+            for (int i = 0; i < COLS; ++i) {
                 if (i >= n) break;
                 out[(size_t)sh.entry[first + i] * R] = acc[i];
             }
@@ -616,31 +618,41 @@ int row_parts(int entries, int E, int R, int D) {
     return best;
 }
 
-template <bool UP>
-cudaError_t launch_rows(const MoeArgs &a, const float *gu, int gu_parts, float *dst, int parts,
+template <bool UP, int COLS>
+cudaError_t launch_cols(const MoeArgs &a, const float *gu, int gu_parts, float *dst, int parts,
                         cudaStream_t stream) {
-    const int D = UP ? a.H : a.I, G = D / 128, cols = chunk_cols(a, D);
+    const int D = UP ? a.H : a.I, G = D / 128;
     const int64_t R = UP ? 2 * a.I : a.H;
     const int64_t dims[3] = {D, R, a.E}, strides[2] = {D, R * D};
     const int box[3] = {128, kRows, 1};
     CUtensorMap wmap;
     if (!encode_bytes(&wmap, UP ? a.w13 : a.w2, 3, dims, strides, box)) return cudaErrorInvalidValue;
-    const int fixed = 1024 + G * cols * (128 + 4) + (int)sizeof(Shared);
+    const int fixed = 1024 + G * COLS * (128 + 4) + (int)sizeof(Shared);
     // Up to 1 MB of weights an SM, half of its shared memory where that leaves a
     // ring of five stages: the next kernel's blocks then start beside this one's
-    // and load their weights (moe_odd's sizes: 28.0 us, 30.5 with all of it).
-    // Above, all of it: five stages hold 64 tokens of H = 7168, I = 2048 to 1.90 ms,
-    // ten to 1.85.
+    // and load their weights (13 tokens, H = 1152, I = 640: 28.0 us, 30.5 with all
+    // of it).  Above, all of it: five stages hold 64 tokens of H = 7168, I = 2048 to
+    // 1.90 ms where ten took 1.85.
     const int n = a.T * a.K;
     const bool small = (int64_t)(n < a.E ? n : a.E) * R * D <= (int64_t)sm_count() << 20;
     const int half = (kSmemHalf - fixed) / kStageBytes, fit = (kSmemMax - fixed) / kStageBytes;
     const int stages = small && half >= 5 ? half : fit < kMaxStages ? fit : kMaxStages;
-    const size_t smem = 1024 + (size_t)G * cols * (128 + 4) + (size_t)stages * kStageBytes;
-    auto k = rows_kernel<UP>;
+    const size_t smem = 1024 + (size_t)G * COLS * (128 + 4) + (size_t)stages * kStageBytes;
+    auto k = rows_kernel<UP, COLS>;
     const cudaError_t err = allow_dynamic_smem(k, smem);
     if (err != cudaSuccess) return err;
     return launch_kernel(k, sm_count(), kThreads, smem, stream, true, wmap, a, gu, gu_parts, dst,
-                         parts, cols, stages);
+                         parts, stages);
+}
+
+template <bool UP>
+cudaError_t launch_rows(const MoeArgs &a, const float *gu, int gu_parts, float *dst, int parts,
+                        cudaStream_t stream) {
+    switch (chunk_cols(a, UP ? a.H : a.I)) {
+        case 8: return launch_cols<UP, 8>(a, gu, gu_parts, dst, parts, stream);
+        case 16: return launch_cols<UP, 16>(a, gu, gu_parts, dst, parts, stream);
+        default: return launch_cols<UP, 32>(a, gu, gu_parts, dst, parts, stream);
+    }
 }
 
 }  // namespace
