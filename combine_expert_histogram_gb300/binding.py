@@ -726,7 +726,8 @@ def new_moe_workspace(num_tokens: int, num_topk: int, num_experts: int, hidden: 
                       device=None) -> MoeWorkspace:
     """Allocate a workspace for ep_moe_decode calls of this shape, or of fewer tokens."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    n = ep_moe_decode_workspace_bytes(num_tokens, num_topk, num_experts, hidden, inter)
+    with torch.cuda.device(dev):  # the size depends on the device's number of SMs
+        n = ep_moe_decode_workspace_bytes(num_tokens, num_topk, num_experts, hidden, inter)
     if n == 0 and num_tokens > 0:
         raise EPError(EP_ERR_INVALID_ARG, "ep_moe_decode shape")
     return MoeWorkspace(torch.empty(max(n, 16), dtype=torch.uint8, device=dev),

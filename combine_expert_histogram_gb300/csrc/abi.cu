@@ -435,7 +435,7 @@ ep_status_t ep_expert_swiglu(const ep_layout_t *L, const void *rows, const void 
 size_t ep_moe_decode_workspace_bytes(int32_t T, int32_t K, int32_t E, int32_t hidden,
                                      int32_t inter) {
     if (check_moe(T, K, E, hidden, inter) != EP_OK) return 0;
-    return moe_workspace_bytes(T, K, E, hidden, inter);
+    return moe_workspace_bytes_up_to(T, K, E, hidden, inter);
 }
 
 ep_status_t ep_moe_decode(const void *x, const void *x_scales, ep_quant_t quant,

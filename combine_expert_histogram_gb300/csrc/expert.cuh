@@ -42,7 +42,9 @@ struct MoeArgs {
     void *out;                // bf16 [T, H]
     int32_t *status;
 };
+// Bytes of scratch for exactly T tokens, and for any number up to T.
 size_t moe_workspace_bytes(int T, int K, int E, int H, int I);
+size_t moe_workspace_bytes_up_to(int T, int K, int E, int H, int I);
 cudaError_t launch_moe_decode(const MoeArgs &a, void *workspace, cudaStream_t stream);
 cudaError_t launch_expert(const ExpertArgs &a, bool gated, cudaStream_t stream);
 

@@ -662,6 +662,15 @@ size_t moe_workspace_bytes(int T, int K, int E, int H, int I) {
     return (size_t)n * 4 * ((size_t)row_parts(n, E, 2 * I, H) * 2 * I + (size_t)row_parts(n, E, H, I) * H);
 }
 
+size_t moe_workspace_bytes_up_to(int T, int K, int E, int H, int I) {
+    size_t most = 0;  // fewer tokens may be cut into more parts
+    for (int t = 1; t <= T; ++t) {
+        const size_t b = moe_workspace_bytes(t, K, E, H, I);
+        if (b > most) most = b;
+    }
+    return most;
+}
+
 cudaError_t launch_moe_decode(const MoeArgs &a, void *workspace, cudaStream_t stream) {
     const int n = a.T * a.K;
     const int p1 = row_parts(n, a.E, 2 * a.I, a.H), p2 = row_parts(n, a.E, a.H, a.I);

@@ -156,7 +156,7 @@ cudaError_t launch_q(const uint16_t *x, const uint16_t *residual, const uint16_t
     const int threads = ((vecs + V - 1) / V + 31) / 32 * 32;
     auto k = V == 1 ? rmsnorm_kernel<Q, 1> : V == 2 ? rmsnorm_kernel<Q, 2> : rmsnorm_kernel<Q, 4>;
     return launch_kernel(k, T, threads, 0, stream, true, x, residual, weight, eps, H, residual_out,
-                         out, rows, scales, (T + 3) / 4 * 4);
+                         out, rows, scales, (int)((T + 3ll) / 4 * 4));
 }
 
 }  // namespace

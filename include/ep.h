@@ -42,7 +42,9 @@
  *   - All array arguments are DEVICE pointers owned by the caller; the library
  *     allocates no memory and never synchronises the host.  Its only state is
  *     a per-device cache of the SM count (read once with
- *     cudaDeviceGetAttribute) and, for ep_layout_noalloc alone, the fixed
+ *     cudaDeviceGetAttribute), the address of the driver's tensor-map encoder
+ *     (looked up by the first ep_expert_gemm, ep_expert_swiglu or
+ *     ep_moe_decode) and, for ep_layout_noalloc alone, the fixed
  *     device array that call uses as scratch (with its looked-up address);
  *     every other entry point keeps nothing between calls.
  *   - Tracing: with the environment variable EP_NVTX=1 (read once per
@@ -530,16 +532,19 @@ ep_status_t ep_expert_swiglu(const ep_layout_t *layout, const void *rows, const 
  *   w2, w2_scales    E4M3 [E, H, I], fp32 [E, H/128, I/128].
  *   out        device bf16 [T, H], 16-byte aligned; every element is written.
  *   status     device int32 [1]: 0, or the largest error code of this call.
- *   workspace  device scratch of ep_moe_decode_workspace_bytes(), 16-byte
- *              aligned, clobbered; holds nothing between calls.  Calls that
- *              share one must not overlap on the GPU.
+ *   workspace  device scratch, 16-byte aligned, clobbered;
+ *              ep_moe_decode_workspace_bytes() of T tokens, with this device
+ *              current, is enough for T tokens and for fewer.  Holds nothing
+ *              between calls.  Calls (or replayed graphs) that share one must
+ *              not overlap on the GPU.
  *
  *   g, u = w13[e] xq (fp32);  h = g / (1 + exp(-g)) * u;  hq = EP_QUANT_FP8_F32 of h
  *   out[t] = bf16_rn( sum over k of topk_w[t,k] * (w2[e] hq) ),  sums in fp32,
  * in ascending k; a token with no routed entry gets +0.
  *
- * The weights and their scales are read before the kernels wait for their
- * predecessors: they must be complete when the kernel before this call started.
+ * Three kernels, each a programmatic dependent of the one before.  The second
+ * reads w2, its scales and topk_idx while the first still runs (the first has
+ * waited for all earlier work by then).
  */
 size_t ep_moe_decode_workspace_bytes(int32_t num_tokens, int32_t num_topk, int32_t num_experts,
                                      int32_t hidden, int32_t inter);

@@ -187,6 +187,69 @@ def test_no_rows_at_all():
     check_swiglu(c, 128, "fp8_f32")
 
 
+@pytest.mark.parametrize("layout", [dict(kind="contig", align=128), dict(kind="contig", align=1)],
+                         ids=str)
+def test_more_tiles_than_processors(layout):
+    """Several tiles for every SM, of experts with none to several row tiles."""
+    c = Case(900, 40, 4, 256, seed=16, drop=0.05, only=list(range(0, 40, 2)) + [1], **layout)
+    check_gemm(c, 1288)
+    check_swiglu(c, 640, "fp8_f32")
+
+
+@pytest.mark.parametrize("quant", ["fp8_f32", "fp8_ue8m0"])
+def test_longest_rows(quant):
+    c = Case(9, 2, 1, 32768, quant=quant, seed=17, drop=0.0)
+    check_gemm(c, 264)
+
+
+def test_captured_chain_replayed_on_new_inputs():
+    """layout -> dispatch -> swiglu -> product -> combine in one graph."""
+    T, E, K, H, I = 24, 6, 2, 384, 256
+    dev = torch.device("cuda")
+    idx = torch.zeros((T, K), dtype=torch.int32, device=dev)
+    wt = torch.ones((T, K), device=dev)
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device=dev)
+    w13, s13, w2, s2 = (t.cuda() for p in (weights(E, 2 * I, H, 1), weights(E, H, I, 2)) for t in p)
+    L = ep.new_layout(T, K, E, "masked", capacity=T)
+    n = L.rows_capacity
+    rows = torch.empty((n, H), dtype=torch.uint8, device=dev)
+    sc = ep.scale_buffer(L, H, "fp8_f32")
+    h = torch.empty((n, I), dtype=torch.uint8, device=dev)
+    sh = ep.scale_buffer(L, I, "fp8_f32")
+    y = torch.empty((n, H), dtype=torch.bfloat16, device=dev)
+    out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    s = torch.cuda.Stream()
+
+    def chain():
+        ep.ep_layout(idx, E, out=L, stream=s)
+        ep.ep_dispatch(L, x, "fp8_f32", out_rows=rows, out_scales=sc, stream=s)
+        ep.ep_expert_swiglu(L, rows, sc, w13, s13, out_rows=h, out_scales=sh, stream=s)
+        ep.ep_expert_gemm(L, h, sh, w2, s2, out=y, stream=s)
+        ep.ep_combine(L, y, wt, out=out, stream=s)
+
+    torch.cuda.synchronize()
+    chain()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        chain()
+    for seed in (1, 2, 3):
+        gen = torch.Generator().manual_seed(seed)
+        idx.copy_(picks(T, E, K, seed))
+        x.copy_(torch.randn((T, H), generator=gen).bfloat16())
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        chain()
+        torch.cuda.synchronize()
+        assert torch.equal(got, out) and not out.isnan().any()
+        # the few-token layer computes the same without the chain's bf16 rounding
+        # of each expert's output (half a step of each, added up)
+        few = ep.ep_moe_decode(x, idx, wt, w13, s13, w2, s2).double()
+        big = ep.ep_combine(L, y.abs(), wt).double()
+        assert ((few - out.double()).abs() <= 2.1 * ref.BF16 * big + 2 * ref.BF16 * few.abs()).all()
+
+
 def test_sums_keep_24_bits():
     """Integers whose block sums stay below 2^24 in any order: every partial sum
     is an fp32 number, so the result has no error but the final rounding."""

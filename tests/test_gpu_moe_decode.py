@@ -141,6 +141,44 @@ def test_workspace_left_dirty_and_shared_by_calls_in_a_row():
     b.check(ob)
 
 
+def test_one_workspace_for_any_smaller_batch():
+    """Batches from 1 to 40 tokens, on both sides of where rows are cut into parts."""
+    c = Case(40, 64, 8, 256, 640, seed=21)
+    x, idx, w = c.dev[:3]
+    ws = ep.new_moe_workspace(40, 8, 64, 256, 640)
+    want, noise = c.formula()
+    for T in (1, 2, 3, 5, 8, 13, 21, 30, 39, 40):
+        out = ep.ep_moe_decode(x[:T], idx[:T], w[:T], *c.dev[3:], ws)
+        ref.close_bf16(out, want[:T], noise[:T])
+
+
+def test_norm_straight_into_the_layer_and_on():
+    """norm -> layer -> norm without a wait between them, many times over one set
+    of buffers: every kernel waits for what it reads and for what it overwrites."""
+    c = Case(3, 16, 4, 640, 384, seed=22, drop=0.0)
+    res = c.dev[0].clone()
+    wn = torch.ones(640, dtype=torch.bfloat16, device="cuda")
+    ws = ep.new_moe_workspace(3, 4, 16, 640, 384)
+
+    def step(sync):
+        x, h, out = res.clone(), torch.empty_like(res), torch.zeros_like(res)
+        seen = []
+        for _ in range(6):
+            ep.ep_rmsnorm(out, wn, residual=x, out=h, residual_out=x)
+            if sync:
+                torch.cuda.synchronize()
+            ep.ep_moe_decode(h, *c.dev[1:], ws, out=out)
+            if sync:
+                torch.cuda.synchronize()
+            seen.append(out.clone())
+        return seen
+
+    want = step(True)
+    for _ in range(5):
+        for a, b in zip(want, step(False)):
+            assert torch.equal(a, b)
+
+
 def test_the_same_bits_every_time():
     c = Case(24, 12, 4, 512, 384, seed=10)
     first = ep.ep_moe_decode(*c.dev)

@@ -82,6 +82,18 @@ def test_moe_decode_arguments(lib):  # noqa: F811
     assert lib.ep_moe_decode_workspace_bytes(512, 2, 8, 256, 128) > 0
 
 
+@pytest.mark.parametrize("K,E,H,I", [(8, 256, 7168, 2048), (8, 128, 2048, 768), (2, 8, 4096, 14336),
+                                     (1, 1, 128, 128), (4, 60, 2048, 1408)])
+def test_moe_decode_workspace_serves_fewer_tokens(lib, K, E, H, I):  # noqa: F811
+    """Few entries are cut into more parts, so the exact need is not monotone; the
+    size that is handed out is."""
+    sizes = [lib.ep_moe_decode_workspace_bytes(T, K, E, H, I) for T in range(1, 1024 // K + 1)]
+    assert all(a > 0 for a in sizes) and sizes == sorted(sizes)
+    # the partial sums of every entry: 2I and H of fp32, in up to four parts
+    for T, n in enumerate(sizes, 1):
+        assert T * K * 4 * (2 * I + H) <= n <= T * K * 16 * (2 * I + H)
+
+
 def test_python_calls_refuse_cpu_tensors(lib):  # noqa: F811
     from combine_expert_histogram_gb300 import binding as ep
     x = torch.zeros(2, 128, dtype=torch.bfloat16)
