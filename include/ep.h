@@ -468,7 +468,10 @@ ep_status_t ep_rmsnorm(const void *x, const void *residual, const void *weight, 
  * block of a weight ([DISC-26563]: 128x128 blockwise FP8 with dynamic
  * activation scaling).
  *
- *   layout         filled by ep_layout(), contiguous or masked.
+ *   layout         filled by ep_layout(), contiguous or masked.  A masked one may
+ *                  also be made up: only num_experts, capacity, expert_count and
+ *                  status are read, so for ep_masked_repack's slab expert_count
+ *                  may be its masked_m.
  *   rows, row_scales  as ep_dispatch(layout, ..., quant) or ep_masked_repack
  *                  wrote them; quant EP_QUANT_FP8_F32, EP_QUANT_FP8_UE8M0 or
  *                  EP_QUANT_FP8_UE8M0_MN (EP_QUANT_NONE and EP_QUANT_MXFP8:
@@ -531,7 +534,8 @@ ep_status_t ep_expert_swiglu(const ep_layout_t *layout, const void *rows, const 
  *   w13, w13_scales  E4M3 [E, 2I, H], fp32 [E, 2I/128, H/128] (ep_expert_swiglu's).
  *   w2, w2_scales    E4M3 [E, H, I], fp32 [E, H/128, I/128].
  *   out        device bf16 [T, H], 16-byte aligned; every element is written.
- *   status     device int32 [1]: 0, or the largest error code of this call.
+ *   status     device int32 [1]: 0, or the largest error code of this call
+ *              (not written when T is 0).
  *   workspace  device scratch, 16-byte aligned, clobbered;
  *              ep_moe_decode_workspace_bytes() of T tokens, with this device
  *              current, is enough for T tokens and for fewer.  Holds nothing

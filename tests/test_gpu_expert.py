@@ -250,6 +250,53 @@ def test_captured_chain_replayed_on_new_inputs():
         assert ((few - out.double()).abs() <= 2.1 * ref.BF16 * big + 2 * ref.BF16 * few.abs()).all()
 
 
+@pytest.mark.parametrize("quant", ["fp8_f32", "fp8_ue8m0", "fp8_ue8m0_mn"])
+def test_repacked_slab(quant):
+    """A contiguous dispatch repacked into the slab: the product of the slab's rows
+    is the product of the contiguous ones."""
+    c = Case(60, 5, 2, 384, quant=quant, seed=18)
+    cap = 40
+    slab, ss, m = ep.ep_masked_repack(c.L, c.x, c.sx, quant, cap)
+    M = ep.new_layout(60, 2, 5, "masked", capacity=cap)
+    M.expert_count = m
+    w, sw = (t.cuda() for t in weights(5, 136, 384, 3))
+    a = ep.ep_expert_gemm(c.L, c.x, c.sx, w, sw, quant)
+    b = ep.ep_expert_gemm(M, slab, ss, w, sw, quant).view(5, cap, 136)
+    for e, (first, n) in enumerate(c.rows):
+        assert n <= cap and torch.equal(a[first:first + n], b[e, :n])
+
+
+def test_first_call_of_a_process_is_captured():
+    """Nothing of the first call (kernel attributes, the driver's encoder, lazy
+    loading) is forbidden during a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    child = (
+        "import sys; sys.path.insert(0, %r)\n"
+        "import torch\n"
+        "from combine_expert_histogram_gb300 import binding as ep\n"
+        "d = dict(device='cuda')\n"
+        "x = torch.randn(4, 256, **d).bfloat16(); n = torch.ones(256, **d).bfloat16()\n"
+        "idx = torch.tensor([[0, 1]] * 4, dtype=torch.int32, **d); w = torch.ones(4, 2, **d)\n"
+        "w13 = torch.full((2, 512, 256), 0x38, dtype=torch.uint8, **d)\n"
+        "w2 = torch.full((2, 256, 256), 0x38, dtype=torch.uint8, **d)\n"
+        "s13 = torch.full((2, 4, 2), 1e-2, **d); s2 = torch.full((2, 2, 2), 1e-2, **d)\n"
+        "ws = ep.new_moe_workspace(4, 2, 2, 256, 256)\n"
+        "out = torch.zeros_like(x); y = torch.zeros_like(x)\n"
+        "torch.cuda.synchronize(); s = torch.cuda.Stream(); g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g, stream=s):\n"
+        "    ep.ep_rmsnorm(x, n, out=y, stream=s)\n"
+        "    ep.ep_moe_decode(y, idx, w, w13, s13, w2, s2, ws, out=out, stream=s)\n"
+        "g.replay(); torch.cuda.synchronize(); got = out.clone()\n"
+        "want = ep.ep_moe_decode(ep.ep_rmsnorm(x, n)[0], idx, w, w13, s13, w2, s2)\n"
+        "torch.cuda.synchronize(); assert torch.equal(got, want) and got.abs().sum() > 0\n"
+        "print('ok')\n" % root)
+    r = subprocess.run([sys.executable, "-c", child], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
 def test_sums_keep_24_bits():
     """Integers whose block sums stay below 2^24 in any order: every partial sum
     is an fp32 number, so the result has no error but the final rounding."""
