@@ -268,10 +268,17 @@ __device__ __forceinline__ void load_columns(const MoeArgs &a, const float *gu, 
                     v[2 * m + 1] = bf16_hi(w[m]);
                 }
             } else {
-                for (int k = 1; k < gu_parts; ++k) {  // the sums' other parts, in order
-                    const Piece o = load_piece<UP>(a, gu + (size_t)k * a.T * a.K * 2 * D, entry, D, gc, l);
+                // the sums' other parts, in order; two parts' loads in flight
+                const size_t step_k = (size_t)a.T * a.K * 2 * D;
+                for (int k = 1; k < gu_parts; k += 2) {
+                    const Piece o = load_piece<UP>(a, gu + k * step_k, entry, D, gc, l);
+                    const Piece o2 = load_piece<UP>(a, gu + min(k + 1, gu_parts - 1) * step_k, entry, D, gc, l);
 #pragma unroll
                     for (int m = 0; m < 4; ++m) add4(p.raw[m], o.raw[m]);
+                    if (k + 1 < gu_parts) {
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) add4(p.raw[m], o2.raw[m]);
+                    }
                 }
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
@@ -339,23 +346,22 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (UP) {  // the ids may be the previous kernel's; for the second kernel they are complete
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = EP_OK;
+        __syncwarp();  // before this warp's group_few may raise a code
     }
     // the first kernel lets the second start only once it holds its tensor memory
     if (warp == kWarps + 1) tmem_alloc<kTiles * kTileCols>(&sh.tmem);
+    const bool few = a.T * a.K <= 32;
+    if (few && warp == 0) group_few(a, cols, sh);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = sh.tmem;
-    if (a.T * a.K <= 32) {
-        if (warp == 0) group_few(a, cols, sh);
-        __syncthreads();
-    } else {
-        group_entries(a, cols, reinterpret_cast<int32_t *>(ring), sh);
-    }
+    if (!few) group_entries(a, cols, reinterpret_cast<int32_t *>(ring), sh);
     const int row_units = R / kRows;
     const Units units = {row_units, parts, G};
-    const long long total = (long long)sh.chunks * row_units * parts;
+    // at most 1024 chunks of 256 row units in 4 parts: times the grid below 2^32
+    const uint32_t total = (uint32_t)sh.chunks * row_units * parts;
     const int u0 = (int)(total * blockIdx.x / gridDim.x), u1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
 
     if (warp == kWarps) {
@@ -599,7 +605,7 @@ int chunk_cols(const MoeArgs &a, int D) {
 // Parts a row's length is cut into: with few entries there are few 128-row units,
 // and the SM with one more than the others sets the time.  1 from 24 units an SM
 // on, 2 from 8 on (how many there will be is not known to a few percent), below
-// that the best share-out of 1, 2 or 4.
+// that the best share-out of 1 to 4.
 int row_parts(int entries, int E, int R, int D) {
     const int sms = sm_count(), G = D / 128;
     const int64_t units = (int64_t)(entries < E ? entries : E) * (R / kRows);
@@ -607,7 +613,7 @@ int row_parts(int entries, int E, int R, int D) {
     if (units >= 8 * sms) return G >= 4 ? 2 : 1;
     int best = 1;
     double most = 0.0;
-    for (int p = 1; p <= 4 && G >= 2 * p; p *= 2) {
+    for (int p = 1; p <= 4 && G >= 2 * p; ++p) {
         const int64_t u = units * p;
         const double even = (double)u / ((u + sms - 1) / sms * sms);
         if (even > most + 0.03) {
