@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ep.h"
 
 namespace ep {
@@ -252,6 +254,35 @@ cudaError_t launch_kernel(void (*k)(KArgs...), int grid, int threads, size_t sme
     cfg.attrs = attr;
     cfg.numAttrs = programmatic ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, k, static_cast<KArgs>(args)...);
+}
+
+// launch_kernel, as a programmatic dependent, of a kernel that wants more dynamic
+// shared memory than is allowed by default.  The limit is raised to all there is
+// at the first launch on a device (asking for it every time took about 1 us); should
+// it be gone again (cudaDeviceReset), the launch fails and is tried once more.
+template <auto K, typename... Args>
+cudaError_t launch_large(int grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = 1ull << (dev & 63);
+    for (int i = 0; i < 2; ++i) {
+        const bool known = dev < 64 && (raised.load(std::memory_order_relaxed) & bit) && i == 0;
+        if (!known) {
+            cudaFuncAttributes fa;
+            err = cudaFuncGetAttributes(&fa, K);
+            if (err == cudaSuccess)
+                err = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)(227 * 1024 - fa.sharedSizeBytes));
+            if (err != cudaSuccess) return err;
+            raised.fetch_or(bit, std::memory_order_relaxed);
+        }
+        err = launch_kernel(K, grid, threads, smem, stream, true, args...);
+        if (err != cudaErrorInvalidValue || !known) return err;
+        cudaGetLastError();  // not sticky
+    }
+    return err;
 }
 
 // Internal launchers (one translation unit each).  They assume arguments were

@@ -430,10 +430,8 @@ cudaError_t launch_expert(const ExpertArgs &a, bool gated, cudaStream_t stream) 
         !encode_bytes(&wmap, a.w, 3, wdims, wstride, wbox))
         return cudaErrorInvalidValue;
     const size_t smem = 1024 + (gated ? ring_bytes<true>() : ring_bytes<false>()) + (a.E + 1) * 4;
-    auto k = gated ? expert_kernel<true> : expert_kernel<false>;
-    const cudaError_t err = allow_dynamic_smem(k, smem);
-    if (err != cudaSuccess) return err;
-    return launch_kernel(k, sm_count(), kThreads, smem, stream, true, xmap, wmap, a);
+    return gated ? launch_large<expert_kernel<true>>(sm_count(), kThreads, smem, stream, xmap, wmap, a)
+                 : launch_large<expert_kernel<false>>(sm_count(), kThreads, smem, stream, xmap, wmap, a);
 }
 
 }  // namespace ep

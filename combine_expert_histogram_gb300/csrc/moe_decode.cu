@@ -644,11 +644,8 @@ cudaError_t launch_cols(const MoeArgs &a, const float *gu, int gu_parts, float *
     const int half = (kSmemHalf - fixed) / kStageBytes, fit = (kSmemMax - fixed) / kStageBytes;
     const int stages = small && half >= 5 ? half : fit < kMaxStages ? fit : kMaxStages;
     const size_t smem = 1024 + (size_t)G * COLS * (128 + 4) + (size_t)stages * kStageBytes;
-    auto k = rows_kernel<UP, COLS>;
-    const cudaError_t err = allow_dynamic_smem(k, smem);
-    if (err != cudaSuccess) return err;
-    return launch_kernel(k, sm_count(), kThreads, smem, stream, true, wmap, a, gu, gu_parts, dst,
-                         parts, stages);
+    return launch_large<rows_kernel<UP, COLS>>(sm_count(), kThreads, smem, stream, wmap, a, gu,
+                                               gu_parts, dst, parts, stages);
 }
 
 template <bool UP>
