@@ -146,6 +146,17 @@ __device__ void group_entries(const MoeArgs &a, int cols, int32_t *tmp, Shared &
     __syncthreads();
 }
 
+// a / b for a below 2^28 and a quotient below 2^21: the fp32 quotient is off by
+// less than one, which the remainder tells.  A third of the latency of an integer
+// division, of which a block's first unit takes six in a row.
+__device__ __forceinline__ int quotient(uint32_t a, uint32_t b) {
+    int q = (int)__fdividef((float)a, (float)b);
+    const int r = (int)a - q * (int)b;
+    if (r < 0) --q;
+    else if (r >= (int)b) ++q;
+    return q;
+}
+
 // A unit of the list: its chunk, first weight row, and 128-wide blocks [g0, g1).
 struct Unit {
     uint32_t chunk;
@@ -154,14 +165,14 @@ struct Unit {
 struct Units {
     int row_units, parts, G;
     __device__ __forceinline__ void blocks(Unit &u) const {
-        u.g0 = parts == 1 ? 0 : G * u.part / parts;
-        u.g1 = parts == 1 ? G : G * (u.part + 1) / parts;
+        u.g0 = parts == 1 ? 0 : quotient(G * u.part, parts);
+        u.g1 = parts == 1 ? G : quotient(G * (u.part + 1), parts);
     }
     // Unit number i (i below their number).
     __device__ __forceinline__ Unit at(const Shared &sh, int i) const {
         Unit u;
-        u.c = i / (row_units * parts);
-        const int v = i - u.c * row_units * parts, r = v / parts;
+        u.c = quotient(i, row_units * parts);
+        const int v = i - u.c * row_units * parts, r = quotient(v, parts);
         u.part = v - r * parts;
         u.row = r * kRows;
         u.chunk = sh.chunk[u.c];
@@ -244,7 +255,7 @@ __device__ __forceinline__ void load_columns(const MoeArgs &a, const float *gu, 
     // items w, w + step, ... of this warp's two halves; the bound is the same for
     // both, which shuffle together
     int i = threadIdx.x >> 4;
-    int col = min(i, items - 1) / G, g = min(i, items - 1) - col * G;
+    int col = quotient(min(i, items - 1), G), g = min(i, items - 1) - col * G;
     Piece next = load_piece<UP>(a, gu, sh.entry[first + col], D, g, l);
 #pragma unroll 1
     for (int w0 = i & ~1; w0 < items; w0 += step, i += step) {
@@ -252,7 +263,7 @@ __device__ __forceinline__ void load_columns(const MoeArgs &a, const float *gu, 
         const int c = col, gc = g, entry = sh.entry[first + col];
         if (w0 + step < items) {
             const int j = min(i + step, items - 1);
-            col = j / G;
+            col = quotient(j, G);
             g = j - col * G;
             next = load_piece<UP>(a, gu, sh.entry[first + col], D, g, l);
         }
@@ -268,16 +279,18 @@ __device__ __forceinline__ void load_columns(const MoeArgs &a, const float *gu, 
                     v[2 * m + 1] = bf16_hi(w[m]);
                 }
             } else {
-                // the sums' other parts, in order; two parts' loads in flight
-                const size_t step_k = (size_t)a.T * a.K * 2 * D;
-                for (int k = 1; k < gu_parts; k += 2) {
-                    const Piece o = load_piece<UP>(a, gu + k * step_k, entry, D, gc, l);
-                    const Piece o2 = load_piece<UP>(a, gu + min(k + 1, gu_parts - 1) * step_k, entry, D, gc, l);
+                // the sums' other parts, in order, all their loads in flight
+                if (gu_parts > 1) {
+                    const size_t step_k = (size_t)a.T * a.K * 2 * D;
+                    Piece o[3];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) add4(p.raw[m], o.raw[m]);
-                    if (k + 1 < gu_parts) {
+                    for (int k = 0; k < 3; ++k)
+                        o[k] = load_piece<UP>(a, gu + min(k + 1, gu_parts - 1) * step_k, entry, D, gc, l);
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) add4(p.raw[m], o2.raw[m]);
+                    for (int k = 0; k < 3; ++k) {
+                        if (k + 1 >= gu_parts) break;
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) add4(p.raw[m], o[k].raw[m]);
                     }
                 }
 #pragma unroll
@@ -360,9 +373,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!few) group_entries(a, cols, reinterpret_cast<int32_t *>(ring), sh);
     const int row_units = R / kRows;
     const Units units = {row_units, parts, G};
-    // at most 1024 chunks of 256 row units in 4 parts: times the grid below 2^32
+    // at most 1024 chunks of 256 row units in 4 parts, 2^20; the grid is the SMs
     const uint32_t total = (uint32_t)sh.chunks * row_units * parts;
-    const int u0 = (int)(total * blockIdx.x / gridDim.x), u1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
+    const int u0 = quotient(total * blockIdx.x, gridDim.x);
+    const int u1 = quotient(total * (blockIdx.x + 1), gridDim.x);
 
     if (warp == kWarps) {
         // ---- loads ----
@@ -442,7 +456,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else {
         // ---- entries, scales, sums.  After a wait that ran out the loops go on
         // (every later wait returns at once), so that all warps meet at the barriers ----
-        if (!UP) asm volatile("griddepcontrol.wait;" ::: "memory");
         const bool adds = warp < 4;  // one for each 32 lanes of tensor memory
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const float *scales = UP ? a.w13_scales : a.w2_scales;
@@ -461,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             un = units.at(sh, u0);
             if (adds) wnext = fetch(un, un.g0);
         }
+        if (!UP) asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel's sums
         for (int u = u0; u < u1; ++u) {
             const int first = un.chunk >> 10 & 1023, n = (int)(un.chunk >> 20);
             if (un.chunk != have) {
