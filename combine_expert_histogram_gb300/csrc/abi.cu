@@ -116,7 +116,6 @@ ExpertArgs expert_args(const ep_layout_t *L, const void *rows, const void *row_s
     a.E = L->num_experts;
     a.cap = L->kind == EP_LAYOUT_MASKED ? L->capacity : 0;
     a.rows_cap = (int)rows_capacity(*L);
-    a.entries = (int64_t)L->num_tokens * L->num_topk;
     a.x = static_cast<const uint8_t *>(rows);
     a.x_scales = row_scales;
     a.quant = quant;

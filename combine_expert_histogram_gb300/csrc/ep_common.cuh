@@ -240,41 +240,27 @@ cudaError_t allow_dynamic_smem(Kern k, size_t dynamic) {
 // Launch with cudaLaunchKernelEx; `programmatic` lets the kernel start while the
 // previous kernel on the stream still runs (programmatic dependent launch): it
 // must then call griddepcontrol.wait before touching that kernel's results.
-// `cluster`: blocks of a thread-block cluster.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*k)(KArgs...), int grid, int cluster, int threads, size_t smem,
-                            cudaStream_t stream, bool programmatic, Args... args) {
+cudaError_t launch_kernel(void (*k)(KArgs...), int grid, int threads, size_t smem,
+                          cudaStream_t stream, bool programmatic, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 0;
-    if (programmatic) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    if (cluster > 1) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        attr[cfg.numAttrs].val.clusterDim.x = cluster;
-        attr[cfg.numAttrs].val.clusterDim.y = 1;
-        attr[cfg.numAttrs++].val.clusterDim.z = 1;
-    }
+    cfg.numAttrs = programmatic ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, k, static_cast<KArgs>(args)...);
-}
-template <typename... KArgs, typename... Args>
-cudaError_t launch_kernel(void (*k)(KArgs...), int grid, int threads, size_t smem,
-                          cudaStream_t stream, bool programmatic, Args... args) {
-    return launch_clusters(k, grid, 1, threads, smem, stream, programmatic, args...);
 }
 
 // launch_kernel, as a programmatic dependent, of a kernel that wants more dynamic
 // shared memory than is allowed by default.  The limit is raised to all there is
 // at the first launch on a device (asking for it every time took about 1 us); should
 // it be gone again (cudaDeviceReset), the launch fails and is tried once more.
-template <auto K, int CLUSTER = 1, typename... Args>
+template <auto K, typename... Args>
 cudaError_t launch_large(int grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
     static std::atomic<uint64_t> raised{0};
     int dev = 0;
@@ -292,7 +278,7 @@ cudaError_t launch_large(int grid, int threads, size_t smem, cudaStream_t stream
             if (err != cudaSuccess) return err;
             raised.fetch_or(bit, std::memory_order_relaxed);
         }
-        err = launch_clusters(K, grid, CLUSTER, threads, smem, stream, true, args...);
+        err = launch_kernel(K, grid, threads, smem, stream, true, args...);
         if (err != cudaErrorInvalidValue || !known) return err;
         cudaGetLastError();  // not sticky
     }

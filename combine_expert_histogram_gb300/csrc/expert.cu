@@ -18,13 +18,12 @@
 //     times sx * sw, to running sums in registers (128 a thread), while the
 //     tensor core fills the other tile.  The scales change every 128 of K, so
 //     the running sum cannot stay in tensor memory.
-// Where experts have enough rows, clusters of two take two row tiles of the same
-// weights; each block brings one half of the weights' K block to both
-// (multicast), which spares a third of the reads from L2.  These products run
-// under the power cap (1370 W, SM at 1.5 to 1.9 GHz) when repeated: what is not
-// moved makes the clock.
-// Rows past an expert's segment are loaded (whatever they hold, products of
-// other rows do not see it) and never stored.
+// Large products run under the power cap when repeated (1370 W, SM at 1.5 to 1.8
+// GHz).  Clusters of two with the weights by multicast, which spare a third of the
+// reads from L2, took the same time there.
+// Rows past an expert's segment that share 32 of a tile with its last ones are
+// loaded (whatever they hold, products of other rows do not see it) and never
+// stored.
 #include "expert.cuh"
 #include "tcgen05.cuh"
 
@@ -37,6 +36,7 @@ constexpr int kThreads = 32 * (kEpiWarps + 4);   // + loader, + products, + two 
 // what the first two, with 128 sums a thread, take: 2 * 216 + 72 = 3 * 168.
 constexpr int kEpiRegs = 216, kOtherRegs = 72;
 constexpr int kTM = 128, kTN = 256;              // tile: rows, weight rows
+constexpr int kPart = 32;                        // rows of a part of a tile that is not full
 constexpr int kABytes = kTM * 128, kBBytes = kTN * 128;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kMaxStages = 4;
@@ -51,7 +51,6 @@ constexpr int kSlots = 4;                        // K blocks of scales ahead of 
 
 struct Tile {
     int e, row, rows, n0;  // expert, first row of the tile, valid rows in it, first weight row
-    bool both;             // the pair's other tile has the same weights
 };
 
 struct Shared {
@@ -74,49 +73,21 @@ struct Shared {
 __device__ __forceinline__ int row_tiles(const ExpertArgs &a, int e) {
     return (expert_rows(a, e) + kTM - 1) / kTM;
 }
-// Units of an expert: tiles, or pairs of tiles.
-template <bool PAIR>
-__device__ __forceinline__ int expert_units(const ExpertArgs &a, int e, int ntn) {
-    const int mt = row_tiles(a, e);
-    return PAIR ? (mt >> 1) * ntn + (mt & 1) * ((ntn + 1) >> 1) : mt * ntn;
-}
 
-// This block's tile of unit t.  Experts in order; within one, row tiles run
-// fastest, so that blocks working at the same time share weights.  A pair takes
-// two row tiles of the same weights; an odd last row tile is taken with two
-// neighbouring weight tiles instead (the second block of the last such pair may
-// get none: rows = 0).
-template <bool PAIR>
-__device__ __forceinline__ Tile find_tile(const ExpertArgs &a, const int32_t *pre, int ntn, int t,
-                                          int cols, int rank) {
+// Tile t of the list: experts in order; within one, row tiles run fastest, so
+// that CTAs working at the same time share weights.
+__device__ __forceinline__ Tile find_tile(const ExpertArgs &a, const int32_t *pre, int t, int cols) {
     int lo = 0, hi = a.E;  // pre[lo] <= t < pre[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (pre[mid] <= t) lo = mid; else hi = mid;
     }
-    const int mt = row_tiles(a, lo);
-    int local = t - pre[lo], i, n;
+    const int mt = row_tiles(a, lo), local = t - pre[lo], n = local / mt, i = local - n * mt;
     Tile r;
-    r.both = false;
-    bool none = false;
-    if (!PAIR) {
-        n = local / mt;
-        i = local - n * mt;
-    } else if (local < (mt >> 1) * ntn) {
-        n = local / (mt >> 1);
-        i = 2 * (local - n * (mt >> 1)) + rank;
-        r.both = true;
-    } else {
-        local -= (mt >> 1) * ntn;
-        i = mt - 1;
-        n = 2 * local + rank;
-        none = n >= ntn;
-        if (none) n = ntn - 1;
-    }
     r.e = lo;
     r.n0 = n * cols;
     r.row = expert_first(a, lo) + i * kTM;
-    r.rows = none ? 0 : min(expert_rows(a, lo) - i * kTM, kTM);
+    r.rows = min(expert_rows(a, lo) - i * kTM, kTM);
     return r;
 }
 
@@ -144,10 +115,10 @@ __device__ __forceinline__ void bulk_store_row(void *dst, const void *src, uint3
                  : "memory");
 }
 
-template <bool GATED, bool PAIR>
+template <bool GATED>
 __global__ void __launch_bounds__(kThreads, 1)
-    expert_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-                  const ExpertArgs a) {
+    expert_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap pmap,
+                  const __grid_constant__ CUtensorMap wmap, const ExpertArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
     // K blocks (the swizzle wants 1024-byte alignment), output rows, [E+1] tile prefix
     uint8_t *smem = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
@@ -160,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], PAIR ? 2 : 1);
+            mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.tfull[i], 1);
@@ -186,14 +157,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cols = GATED ? 128 : kTN;  // output columns of a tile
     const int ntn = (a.N + cols - 1) / cols;
     block_exclusive_scan<kThreads>(
-        a.E, [&](int e) { return expert_units<PAIR>(a, e, ntn); }, pre, sh.scan);
-    if (PAIR) cluster_sync();  // the other block's barriers are ready
+        a.E, [&](int e) { return row_tiles(a, e) * ntn; }, pre, sh.scan);
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     const int total = pre[a.E];
-    // a pair's blocks walk the same units, each one taking its own tile of them
-    const int rank = PAIR ? blockIdx.x & 1 : 0;
-    const int t0 = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
     const int G = a.K >> 7;
 
     if (warp >= kEpiWarps) {
@@ -201,8 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kEpiWarps) {
             // ---- loads ----
             int it = 0;
-            for (int t = t0; t < total && !__any_sync(kFullMask, *fail); t += step) {
-                const Tile q = find_tile<PAIR>(a, pre, ntn, t, cols, rank);
+            for (int t = blockIdx.x; t < total && !__any_sync(kFullMask, *fail); t += gridDim.x) {
+                const Tile q = find_tile(a, pre, t, cols);
                 for (int g = 0; g < G; ++g, ++it) {
                     const int s = it % kStages;
                     const bool ok = it < kStages || mbar_wait_fast(&sh.empty[s], (it / kStages - 1) & 1, fail);
@@ -213,30 +180,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (elect_one()) {
                         uint8_t *st = smem + s * kStageBytes;
                         expect_bytes(&sh.full[s], kStageBytes);
-                        tma_load_2d(st, &xmap, g * 128, q.row, &sh.full[s]);
-                        const int n1 = q.n0 + (GATED ? a.N : 128);
-                        if (PAIR && q.both) {  // each block brings one half to both
-                            tma_load_3d_pair(st + kABytes + rank * (kBBytes / 2), &wmap, g * 128,
-                                             rank ? n1 : q.n0, q.e, &sh.full[s]);
+                        if (q.rows > kTM - kPart) {
+                            tma_load_2d(st, &xmap, g * 128, q.row, &sh.full[s]);
                         } else {
-                            tma_load_3d(st + kABytes, &wmap, g * 128, q.n0, q.e, &sh.full[s]);
-                            tma_load_3d(st + kABytes + kBBytes / 2, &wmap, g * 128, n1, q.e,
-                                        &sh.full[s]);
+                            // parts without a row start past the row space: zeros, and no
+                            // reads (a decode batch of 16 rows an expert: 73.7 us, 76.2
+                            // with whole tiles)
+#pragma unroll
+                            for (int i = 0; i < kTM; i += kPart)
+                                tma_load_2d(st + i * 128, &pmap, g * 128,
+                                            i < q.rows ? q.row + i : a.rows_cap, &sh.full[s]);
                         }
+                        tma_load_3d(st + kABytes, &wmap, g * 128, q.n0, q.e, &sh.full[s]);
+                        tma_load_3d(st + kABytes + kBBytes / 2, &wmap, g * 128,
+                                    q.n0 + (GATED ? a.N : 128), q.e, &sh.full[s]);
                     }
                     __syncwarp();
                 }
             }
             if (lane == 0) sh.issued = it;
-            // the other block's last arrivals are here before this one may leave
-            if (PAIR && !__any_sync(kFullMask, *fail))
-                for (int i = max(0, it - kStages); i < it; ++i)
-                    if (!mbar_wait_fast(&sh.empty[i % kStages], (i / kStages) & 1, fail)) sh.fail = 1;
         } else if (warp == kEpiWarps + 1) {
             // ---- products ----
             constexpr uint32_t instr = e4m3_instr(kTM, kTN);
             int it = 0;
-            for (int t = t0; t < total && !__any_sync(kFullMask, *fail); t += step) {
+            for (int t = blockIdx.x; t < total && !__any_sync(kFullMask, *fail); t += gridDim.x) {
                 for (int g = 0; g < G; ++g, ++it) {
                     const int s = it % kStages, b = it & 1;
                     const bool ok = (it < 2 || mbar_wait_fast(&sh.tempty[b], (it / 2 - 1) & 1, fail)) &&
@@ -252,9 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)  // 32 bytes of each row further
                             mma_e4m3(tmem + b * kTN, da + 2 * k, db + 2 * k, instr, k > 0);
-                        // a pair's stage is free when both blocks are done with theirs
-                        if (PAIR) mma_commit_pair(&sh.empty[s]);
-                        else mma_commit(&sh.empty[s]);
+                        mma_commit(&sh.empty[s]);
                         mma_commit(&sh.tfull[b]);
                     }
                     __syncwarp();
@@ -272,8 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int NB = GATED ? a.N / 64 : (a.N + 127) / 128;
             int it = 0, tiles = 0;
             bool ok = true;
-            for (int t = t0; ok && t < total && !__any_sync(kFullMask, *fail); t += step, ++tiles) {
-                const Tile q = find_tile<PAIR>(a, pre, ntn, t, cols, rank);
+            for (int t = blockIdx.x; ok && t < total && !__any_sync(kFullMask, *fail); t += gridDim.x, ++tiles) {
+                const Tile q = find_tile(a, pre, t, cols);
                 if (warp == kEpiWarps + 2 && lane == 0) sh.tile[tiles & 7] = q;
                 const int b0 = q.n0 / 128, b1 = GATED ? b0 + a.N / 128 : min(b0 + 1, NB - 1);
                 const float *sw0 = a.w_scales + ((size_t)q.e * NB + b0) * G;
@@ -318,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the gated tile: this half's 64 gate columns, then the same 64 up columns
         const uint32_t col0 = half * (GATED ? 64 : 128), col1 = GATED ? 128 + half * 64 : col0 + 64;
         int it = 0, tiles = 0;
-        for (int t = t0; t < total && !__any_sync(kFullMask, *fail); t += step, ++tiles) {
+        for (int t = blockIdx.x; t < total && !__any_sync(kFullMask, *fail); t += gridDim.x, ++tiles) {
             float acc[128];
 #pragma unroll
             for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
@@ -424,7 +389,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_sync();  // nothing of the other block's is on its way here any more
     if (sh.fail) {
         if (threadIdx.x == 0) raise_status(a.status, EP_ERR_TIMEOUT);
         // let the loads in flight land before the shared memory goes
@@ -478,26 +442,20 @@ bool encode_bytes(CUtensorMap *map, const void *p, int rank, const int64_t *dims
 }
 
 cudaError_t launch_expert(const ExpertArgs &a, bool gated, cudaStream_t stream) {
-    CUtensorMap xmap, wmap;
+    CUtensorMap xmap, pmap, wmap;
     const int64_t xdims[2] = {a.K, a.rows_cap}, xstride[1] = {a.K};
     const int64_t W = gated ? 2 * a.N : a.N;
     const int64_t wdims[3] = {a.K, W, a.E}, wstride[2] = {a.K, W * a.K};
-    const int xbox[2] = {128, kTM}, wbox[3] = {128, kTN / 2, 1};
+    const int xbox[2] = {128, kTM}, pbox[2] = {128, kPart}, wbox[3] = {128, kTN / 2, 1};
     if (!encode_bytes(&xmap, a.x, 2, xdims, xstride, xbox) ||
+        !encode_bytes(&pmap, a.x, 2, xdims, xstride, pbox) ||
         !encode_bytes(&wmap, a.w, 3, wdims, wstride, wbox))
         return cudaErrorInvalidValue;
     const size_t smem = 1024 + (gated ? ring_bytes<true>() : ring_bytes<false>()) + (a.E + 1) * 4;
-    // Pairs where experts have two row tiles and more on average.  131072 entries of
-    // 256 experts, K = 7168, I = 2048: 3.28 ms, 3.39 without; 65536, K = 2048,
-    // N = 7168: 1.07 and 1.10 ms.  At 16384 to 49152 entries of the same experts
-    // the two are within 2 % of each other, mostly for the single blocks.
-    const bool pair = a.entries >= 256ll * a.E;
-    const int sms = sm_count(), pairs = sms / 2 * 2;
-    if (pair && pairs)
-        return gated ? launch_large<expert_kernel<true, true>, 2>(pairs, kThreads, smem, stream, xmap, wmap, a)
-                     : launch_large<expert_kernel<false, true>, 2>(pairs, kThreads, smem, stream, xmap, wmap, a);
-    return gated ? launch_large<expert_kernel<true, false>>(sms, kThreads, smem, stream, xmap, wmap, a)
-                 : launch_large<expert_kernel<false, false>>(sms, kThreads, smem, stream, xmap, wmap, a);
+    return gated ? launch_large<expert_kernel<true>>(sm_count(), kThreads, smem, stream, xmap, pmap,
+                                                     wmap, a)
+                 : launch_large<expert_kernel<false>>(sm_count(), kThreads, smem, stream, xmap, pmap,
+                                                      wmap, a);
 }
 
 }  // namespace ep

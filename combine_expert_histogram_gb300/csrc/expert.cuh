@@ -14,7 +14,6 @@ struct ExpertArgs {
     int E;
     int cap;                // masked: slots per expert; 0: contiguous layout
     int rows_cap;           // rows of the row space
-    int64_t entries;        // T*K: as many rows at most
     const uint8_t *x;       // [rows_cap, K] E4M3
     const void *x_scales;   // by `quant`
     int quant;              // EP_QUANT_FP8_F32, _UE8M0 or _UE8M0_MN

@@ -116,15 +116,6 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
                  : "memory");
 }
 
-// The same on the barriers at this place in both blocks of a cluster of two.
-__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-        "[%0], %1;" ::"r"(smem_addr(bar)),
-        "h"((uint16_t)3)
-        : "memory");
-}
-
 // ---- tiled TMA loads ----
 __device__ __forceinline__ void expect_bytes(uint64_t *bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
@@ -147,16 +138,6 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
         : "memory");
 }
-// tma_load_3d into both blocks of a cluster of two, at the same place, with the
-// bytes counted on each one's own barrier.
-__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, int x, int y,
-                                                 int z, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "h"((uint16_t)3)
-        : "memory");
-}
 // tma_load_3d of bytes that are read once: their L2 lines go first.
 __device__ __forceinline__ void tma_load_3d_once(void *dst, const CUtensorMap *map, int x, int y,
                                                  int z, uint64_t *bar) {
@@ -170,12 +151,6 @@ __device__ __forceinline__ void tma_load_3d_once(void *dst, const CUtensorMap *m
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
-
-// All threads of a cluster meet; what each wrote before is visible after.
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // mbar_wait that looks at the clock only once the first try has failed.
