@@ -206,7 +206,7 @@ __device__ __forceinline__ Piece load_piece(const MoeArgs &a, const float *gu, i
                                             int g, int l) {
     Piece r;
     r.s = 0.0f;
-    const int t = UP ? entry / a.K : entry, G = D >> 7;
+    const int t = UP ? quotient(entry, a.K) : entry, G = D >> 7;
     const size_t at = (size_t)t * D + g * 128 + 8 * l;
     if (!UP) {
         const float *p = gu + (size_t)t * 2 * D + g * 128 + 8 * l;
