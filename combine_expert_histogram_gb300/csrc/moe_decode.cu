@@ -92,56 +92,55 @@ __device__ void group_few(const MoeArgs &a, int cols, Shared &sh) {
     if (lane == 0) sh.chunks = __popc(heads);
 }
 
-// Group the routed entries by expert.  `tmp` holds 3 * E + 2 ints and n 16-bit
+// Group the routed entries by expert.  `tmp` holds 2 * E + 1 ints and n 16-bit
 // ids; every thread of the CTA calls it.  Every CTA must put the same entries
 // into the same chunk.  Within a chunk their order is free (no entry's result
 // depends on which column it takes), so only the entries of an expert with
 // several chunks are ranked by counting the same ids before them.
 __device__ void group_entries(const MoeArgs &a, int cols, int32_t *tmp, Shared &sh) {
-    int32_t *cnt = tmp, *start = cnt + a.E, *first = start + a.E + 1;  // [E], [E+1], [E+1]
-    uint16_t *ids = reinterpret_cast<uint16_t *>(first + a.E + 1);     // [n]
+    constexpr int kEach = (kMaxEntries + kThreads - 1) / kThreads;
+    int32_t *cnt = tmp, *at = cnt + a.E;  // [E]; [E+1] first entry | first chunk << 16
+    uint16_t *ids = reinterpret_cast<uint16_t *>(at + a.E + 1);  // [n]
     const int n = a.T * a.K;
-    for (int e = threadIdx.x; e < a.E; e += kThreads) cnt[e] = 0;
-    __syncthreads();
-    int mine[(kMaxEntries + kThreads - 1) / kThreads];
+    int mine[kEach];
 #pragma unroll
-    for (int i = 0; i < (kMaxEntries + kThreads - 1) / kThreads; ++i) {
+    for (int i = 0; i < kEach; ++i) {
         const int j = i * kThreads + threadIdx.x;
-        mine[i] = -1;
-        if (j < n) {
-            const int e = ld_dep(a.topk_idx + j);
-            ids[j] = (uint16_t)(e >= 0 && e < a.E ? e : a.E);
-            if (e >= 0 && e < a.E) {
-                mine[i] = e;
-                atomicAdd(cnt + e, 1);
-            } else if (e != -1 && blockIdx.x == 0) {
-                raise_status(a.status, EP_ERR_BAD_EXPERT_ID);
-            }
-        }
+        mine[i] = j < n ? ld_dep(a.topk_idx + j) : -1;
     }
-    __syncthreads();
-    block_exclusive_scan<kThreads>(a.E, [&](int e) { return cnt[e]; }, start, sh.scan);
-    block_exclusive_scan<kThreads>(
-        a.E, [&](int e) { return (cnt[e] + cols - 1) / cols; }, first, sh.scan);
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
-        for (int c = 0, at = 0; at < cnt[e]; ++c, at += cols)
-            sh.chunk[first[e] + c] = (uint32_t)e | (uint32_t)(start[e] + at) << 10 |
-                                     (uint32_t)min(cols, cnt[e] - at) << 20;
-    }
-    if (threadIdx.x == 0) sh.chunks = first[a.E];
-    __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += kThreads) cnt[e] = 0;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < (kMaxEntries + kThreads - 1) / kThreads; ++i) {
+    for (int i = 0; i < kEach; ++i) {
+        const int j = i * kThreads + threadIdx.x;
+        if (mine[i] < -1 || mine[i] >= a.E) {
+            if (blockIdx.x == 0) raise_status(a.status, EP_ERR_BAD_EXPERT_ID);
+            mine[i] = -1;
+        }
+        if (j < n) ids[j] = (uint16_t)(mine[i] >= 0 ? mine[i] : a.E);
+        if (mine[i] >= 0) atomicAdd(cnt + mine[i], 1);
+    }
+    __syncthreads();
+    // both counts in one scan: neither total is above 1024
+    block_exclusive_scan<kThreads>(
+        a.E, [&](int e) { return cnt[e] | (cnt[e] + cols - 1) / cols << 16; }, at, sh.scan);
+    if (threadIdx.x == 0) sh.chunks = at[a.E] >> 16;
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+        const int first = at[e] & 0xffff, end = at[e + 1] & 0xffff;
+        for (int c = at[e] >> 16, f = first; f < end; ++c, f += cols)
+            sh.chunk[c] = (uint32_t)e | (uint32_t)f << 10 | (uint32_t)min(cols, end - f) << 20;
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
         const int e = mine[i], j = i * kThreads + threadIdx.x;
         if (e < 0) continue;
+        const int first = at[e] & 0xffff;
         int rank = 0;
-        if (start[e + 1] - start[e] <= cols)
-            rank = atomicAdd(cnt + e, 1);
+        if ((at[e + 1] & 0xffff) - first <= cols)
+            rank = atomicSub(cnt + e, 1) - 1;
         else
             for (int k = 0; k < j; ++k) rank += ids[k] == e;
-        sh.entry[start[e] + rank] = (uint16_t)j;
+        sh.entry[first + rank] = (uint16_t)j;
     }
     __syncthreads();
 }
