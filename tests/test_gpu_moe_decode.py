@@ -229,6 +229,37 @@ def test_two_streams_with_a_workspace_each():
         assert torch.equal(a, b)
 
 
+def test_all_operators_at_once_on_four_streams():
+    """Blocks of the few-token layer (half an SM's shared memory, half its tensor
+    memory), of the experts' products (all of both) and of the norm wait for one
+    another's resources, never for each other."""
+    from tests.test_gpu_expert import Case as Rows
+    small, other = Case(5, 12, 4, 512, 384, seed=23), Case(40, 6, 4, 512, 384, seed=24)
+    r = Rows(300, 8, 2, 768, seed=25)
+    w, sw = (t.cuda() for t in weights(8, 512, 768, 26))
+    x = torch.randn((700, 1024), device="cuda").bfloat16()
+    g = torch.ones(1024, dtype=torch.bfloat16, device="cuda")
+    ws = [ep.new_moe_workspace(5, 4, 12, 512, 384), ep.new_moe_workspace(40, 4, 6, 512, 384)]
+    used = (~r.unused()).cuda()
+    calls = [lambda s: ep.ep_moe_decode(*small.dev, ws[0], stream=s),
+             lambda s: ep.ep_moe_decode(*other.dev, ws[1], stream=s),
+             lambda s: ep.ep_expert_swiglu(r.L, r.x, r.sx, w, sw, out_quant="none", stream=s)[0][used],
+             lambda s: ep.ep_rmsnorm(x, g, quant="fp8_f32", with_out=False, stream=s)[1]]
+    want = [c(None) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(20):
+        got = []
+        for c, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                got.append(c(s))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+    for q in ws:
+        q.check_status()
+
+
 def test_captured_and_replayed_on_new_inputs():
     c = Case(5, 8, 3, 384, 256, seed=13)
     ws = ep.new_moe_workspace(5, 3, 8, 384, 256)
