@@ -644,7 +644,7 @@ def _expert_args(lib, layout: Layout, rows, row_scales, weights, weight_scales, 
         raise EPError(EP_ERR_UNSUPPORTED, f"expert products of {quant} rows")
     sdt, sshape = _scale_shape(cap, K, quant, slab)
     ps = _want(row_scales, "row_scales", sdt, sshape, dev)
-    N = weights.shape[1] if weights.dim() == 3 else 0
+    N = weights.shape[1] if weights is not None and weights.dim() == 3 else 0
     pw = _want(weights, "weights", _E4M3, (E, N, K), dev)
     pws = _want(weight_scales, "weight_scales", (_F32,), (E, (N + 127) // 128, K // 128), dev)
     return dev, c, cap, slab, N, K, px, ps, pw, pws

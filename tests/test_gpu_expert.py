@@ -157,6 +157,11 @@ def test_gemm_widths(N):
     check_gemm(Case(33, 3, 2, 256, seed=N), N)
 
 
+def test_widest_outputs():
+    check_gemm(Case(5, 2, 1, 128, seed=19, drop=0.0), 65536)
+    check_swiglu(Case(5, 2, 1, 128, seed=20, drop=0.0), 32768, "fp8_ue8m0")
+
+
 @pytest.mark.parametrize("H", [128, 256, 384, 512, 896, 1408, 2048])
 def test_gemm_inner_lengths(H):
     check_gemm(Case(20, 4, 2, H, seed=H), 136)
