@@ -454,9 +454,7 @@ ep_status_t ep_layout_noalloc(const int32_t *topk_idx, const ep_layout_t *layout
  * residual_out may be residual or x, and out may be x, residual or
  * residual_out (if the sum is not needed): each row is read before it is
  * written.  Other overlaps are not allowed.  The kernel does not trigger its
- * dependents early, so ep_dispatch may follow it directly.  The weight is read
- * before the kernel waits for its predecessor: it must be complete when that
- * predecessor started.
+ * dependents early, so ep_dispatch may follow it directly.
  */
 ep_status_t ep_rmsnorm(const void *x, const void *residual, const void *weight, float eps,
                        int32_t num_tokens, int32_t hidden, ep_quant_t quant, void *residual_out,

@@ -216,3 +216,31 @@ def test_norm_straight_into_dispatch(T):
     dst = L.dst_row.cpu().long()[:T * K]
     assert torch.equal(ref.decode(rows[dst.cuda()]), q.repeat_interleave(K, 0))
     assert torch.equal(scales.cpu()[dst].to(ref.F64), s.repeat_interleave(K, 0))
+
+
+def test_weight_that_the_kernel_before_writes():
+    """combine lets the norm start early, and its last row is the norm's weight: the
+    norm has to wait for it.  The stream is held, so that the launches queue."""
+    T, K, E, H = 1024, 32, 64, 1024
+    g = torch.Generator().manual_seed(12)
+    idx = torch.rand((T, E), generator=g).topk(K).indices.int().cuda()
+    w = torch.rand((T, K), generator=g).cuda()
+    L = ep.ep_layout(idx, E)
+    ys = [torch.randn((ep.ep_rows_capacity(L), H), generator=g).bfloat16().cuda() for _ in range(2)]
+    x = torch.randn((8, H), generator=g).bfloat16().cuda()
+    want = []
+    for y in ys:
+        weight = ep.ep_combine(L, y, w)[-1].clone()
+        torch.cuda.synchronize()
+        want.append(ep.ep_rmsnorm(x, weight, EPS)[0])
+    out = ep.ep_combine(L, ys[1], w)
+    big = torch.empty(1 << 29, dtype=torch.uint8, device="cuda")
+    for _ in range(6):
+        big.fill_(1)
+    got = []
+    for i in range(20):
+        ep.ep_combine(L, ys[i % 2], w, out=out)
+        got.append(ep.ep_rmsnorm(x, out[-1], EPS)[0])
+    torch.cuda.synchronize()
+    for i, h in enumerate(got):
+        assert torch.equal(h, want[i % 2]), i
