@@ -622,15 +622,23 @@ def _layout_arg(layout: Layout, dev: int) -> _Layout:
     return c
 
 
+def _slab_rows(t: torch.Tensor) -> torch.Tensor:
+    """A slab [E, capacity, n] as its rows [E * capacity, n], in the same memory
+    (flatten would copy another one, into a tensor that is gone before the launch)."""
+    if not t.is_contiguous():
+        raise ValueError("libep needs contiguous tensors")
+    return t.flatten(0, 1)
+
+
 def _expert_args(lib, layout: Layout, rows, row_scales, weights, weight_scales, quant: str):
     """Shared argument checks of the experts' products: (device index, C layout,
     rows of the row space, slab, N, K, the four addresses)."""
     slab = (layout.num_experts, layout.capacity) if layout.kind == "masked" else None
     if slab is not None:  # [E, capacity, ...], as ep_masked_repack returns it
         if rows.dim() == 3:
-            rows = rows.flatten(0, 1)
+            rows = _slab_rows(rows)
         if row_scales is not None and row_scales.dim() == 3 and quant != "fp8_ue8m0_mn":
-            row_scales = row_scales.flatten(0, 1)
+            row_scales = _slab_rows(row_scales)
     dev = _rows_of(rows, "rows")
     c = _layout_arg(layout, dev)
     cap = lib.ep_rows_capacity(ctypes.byref(c))

@@ -104,6 +104,40 @@ def test_python_calls_refuse_cpu_tensors(lib):  # noqa: F811
         ep.ep_moe_decode(x, i, i.float(), x, x, x, x)
 
 
+def _cpu_slab(E=3, cap=4):
+    from combine_expert_histogram_gb300 import binding as ep
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    return ep.Layout(6, 2, E, 1, "masked", 1, cap, 0, dst_row=i32(12), row_src=None,
+                     expert_count=i32(E), expert_offset=i32(E + 1), rank_rows=None,
+                     status=i32(1))
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("which", ["rows", "scales"])
+def test_a_slab_cut_out_of_a_larger_one_is_refused(lib, gated, which):  # noqa: F811
+    """[E, capacity, ...] views of a larger slab are no contiguous rows: a copy of
+    them would be freed before the launch."""
+    from combine_expert_histogram_gb300 import binding as ep
+    E, cap, K = 3, 4, 256
+    rows = torch.zeros((E, cap + 2, K), dtype=torch.uint8)
+    sc = torch.zeros((E, cap + 2, K // 128))
+    w, ws = torch.zeros((E, 256, K), dtype=torch.uint8), torch.zeros((E, 2, K // 128))
+    if which == "rows":
+        rows, sc = rows[:, :cap], sc[:, :cap].contiguous()
+    else:
+        rows, sc = rows[:, :cap].contiguous(), sc[:, :cap]
+    with pytest.raises(ValueError, match="contiguous"):
+        (ep.ep_expert_swiglu if gated else ep.ep_expert_gemm)(_cpu_slab(E, cap), rows, sc, w, ws)
+
+
+def test_the_rows_of_a_slab_share_its_memory():
+    from combine_expert_histogram_gb300 import binding as ep
+    for shape in ((3, 4, 256), (1, 1, 128), (2, 0, 128)):
+        t = torch.zeros(shape)
+        r = ep._slab_rows(t)
+        assert r.shape == (shape[0] * shape[1], shape[2]) and r.data_ptr() == t.data_ptr()
+
+
 def test_the_64_bit_e4m3_agrees_with_torch():
     """The test's own E4M3 decoding and rounding against torch's cast."""
     b = torch.arange(256, dtype=torch.uint8)
