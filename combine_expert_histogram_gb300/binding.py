@@ -609,17 +609,20 @@ def ep_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
 
 
 def _layout_arg(layout: Layout, dev: int) -> _Layout:
-    """The C struct of a filled layout on device `dev`."""
+    """The C struct of a layout on device `dev` for the experts' products.  Of a
+    masked one, which may be made up, they read only the counts and the status."""
     E = layout.num_experts
+    count = _want(layout.expert_count, "layout.expert_count", (_I32,), (E,), dev)
+    status = _want(layout.status, "layout.status", (_I32,), (1,), dev)
+    if layout.kind == "masked":
+        return _Layout(num_experts=E, kind=LAYOUT_KIND["masked"], capacity=layout.capacity,
+                       expert_count=count, status=status)
     rr, rs = layout.rank_rows, layout.row_src
-    c = _Layout(layout.num_tokens, layout.num_topk, E, layout.num_ranks, LAYOUT_KIND[layout.kind],
-                layout.align, layout.capacity, layout.max_tokens, layout.dst_row.data_ptr(),
-                rs.data_ptr() if rs is not None else None,
-                _want(layout.expert_count, "layout.expert_count", (_I32,), (E,), dev),
-                _want(layout.expert_offset, "layout.expert_offset", (_I32,), (E + 1,), dev),
-                rr.data_ptr() if rr is not None else None,
-                _want(layout.status, "layout.status", (_I32,), (1,), dev))
-    return c
+    return _Layout(layout.num_tokens, layout.num_topk, E, layout.num_ranks,
+                   LAYOUT_KIND[layout.kind], layout.align, layout.capacity, layout.max_tokens,
+                   layout.dst_row.data_ptr(), rs.data_ptr() if rs is not None else None, count,
+                   _want(layout.expert_offset, "layout.expert_offset", (_I32,), (E + 1,), dev),
+                   rr.data_ptr() if rr is not None else None, status)
 
 
 def _slab_rows(t: torch.Tensor) -> torch.Tensor:
@@ -641,7 +644,7 @@ def _expert_args(lib, layout: Layout, rows, row_scales, weights, weight_scales, 
             row_scales = _slab_rows(row_scales)
     dev = _rows_of(rows, "rows")
     c = _layout_arg(layout, dev)
-    cap = lib.ep_rows_capacity(ctypes.byref(c))
+    cap = slab[0] * slab[1] if slab is not None else lib.ep_rows_capacity(ctypes.byref(c))
     if cap < 0:
         raise EPError(EP_ERR_INVALID_ARG, "layout shape")
     if cap == 0:

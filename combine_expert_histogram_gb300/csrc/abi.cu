@@ -93,15 +93,32 @@ ep_status_t check_hidden(int32_t H, ep_quant_t quant) {
     return EP_ERR_INVALID_ARG;
 }
 
+// The layout of the experts' products.  Of a masked one, which a caller may make up,
+// only what they read is looked at.
+ep_status_t check_product_layout(const ep_layout_t *L) {
+    if (!L || L->kind != EP_LAYOUT_MASKED) return check_layout(L);
+    if (L->num_experts < 1 || L->num_experts > EP_MAX_EXPERTS || L->capacity < 1 ||
+        rows_capacity(*L) > INT_MAX)
+        return EP_ERR_INVALID_ARG;
+    if (!L->expert_count || !L->status || !aligned(L->expert_count, 4) || !aligned(L->status, 4))
+        return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+
+// True if the layout has no rows, whatever its counts hold (a slab has its slots).
+bool no_rows(const ep_layout_t *L) {
+    return L->kind == EP_LAYOUT_CONTIG && L->num_tokens == 0;
+}
+
 // Argument rules shared by ep_expert_gemm and ep_expert_swiglu (N weight rows).
 ep_status_t check_expert(const ep_layout_t *L, const void *rows, const void *row_scales, int32_t K,
                          ep_quant_t quant, const void *weights, const float *weight_scales) {
-    ep_status_t st = check_layout(L);
+    ep_status_t st = check_product_layout(L);
     if (st != EP_OK) return st;
     st = check_hidden(K, quant);
     if (st != EP_OK) return st;
     if (quant == EP_QUANT_NONE || quant == EP_QUANT_MXFP8) return EP_ERR_UNSUPPORTED;
-    if (L->num_tokens == 0) return EP_OK;
+    if (no_rows(L)) return EP_OK;
     if (!rows || !row_scales || !weights || !weight_scales || !aligned(rows, 16) ||
         !aligned(row_scales, 4) || !aligned(weights, 16) || !aligned(weight_scales, 4))
         return EP_ERR_INVALID_ARG;
@@ -399,7 +416,7 @@ ep_status_t ep_expert_gemm(const ep_layout_t *L, const void *rows, const void *r
     const ep_status_t st = check_expert(L, rows, row_scales, hidden, quant, weights, weight_scales);
     if (st != EP_OK) return st;
     if (n_out < 8 || n_out % 8 != 0 || n_out > EP_MAX_EXPERT_COLS) return EP_ERR_INVALID_ARG;
-    if (L->num_tokens == 0) return EP_OK;
+    if (no_rows(L)) return EP_OK;
     if (!y || !aligned(y, 16)) return EP_ERR_INVALID_ARG;
     ExpertArgs a = expert_args(L, rows, row_scales, hidden, quant, weights, weight_scales);
     a.N = n_out;
@@ -420,7 +437,7 @@ ep_status_t ep_expert_swiglu(const ep_layout_t *L, const void *rows, const void 
     if (out_quant != EP_QUANT_NONE && out_quant != EP_QUANT_FP8_F32 &&
         out_quant != EP_QUANT_FP8_UE8M0 && out_quant != EP_QUANT_FP8_UE8M0_MN)
         return EP_ERR_INVALID_ARG;
-    if (L->num_tokens == 0) return EP_OK;
+    if (no_rows(L)) return EP_OK;
     if (!out_rows || !aligned(out_rows, 16)) return EP_ERR_INVALID_ARG;
     if (out_quant == EP_QUANT_NONE ? out_scales != nullptr : (!out_scales || !aligned(out_scales, 4)))
         return EP_ERR_INVALID_ARG;

@@ -467,9 +467,9 @@ ep_status_t ep_rmsnorm(const void *x, const void *residual, const void *weight, 
  * activation scaling).
  *
  *   layout         filled by ep_layout(), contiguous or masked.  A masked one may
- *                  also be made up: only num_experts, capacity, expert_count and
- *                  status are read, so for ep_masked_repack's slab expert_count
- *                  may be its masked_m.
+ *                  also be made up: only kind, num_experts, capacity, expert_count
+ *                  and status are read (the other fields may hold anything), so for
+ *                  ep_masked_repack's slab expert_count may be its masked_m.
  *   rows, row_scales  as ep_dispatch(layout, ..., quant) or ep_masked_repack
  *                  wrote them; quant EP_QUANT_FP8_F32, EP_QUANT_FP8_UE8M0 or
  *                  EP_QUANT_FP8_UE8M0_MN (EP_QUANT_NONE and EP_QUANT_MXFP8:

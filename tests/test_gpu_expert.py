@@ -287,6 +287,35 @@ def test_repacked_slab(quant):
         assert n <= cap and torch.equal(a[first:first + n], b[e, :n])
 
 
+def test_a_made_up_slab_of_a_batch_without_tokens():
+    """Only the counts, the status and the slab's shape describe a made-up masked
+    layout: its product is there although no token of this process is."""
+    E, cap, K, N, I = 3, 20, 256, 136, 128
+    c = Case(30, E, 2, K, kind="masked", cap=cap, seed=21)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    made = ep.Layout(0, 0, E, 0, "masked", 0, cap, 0, dst_row=None, row_src=None,
+                     expert_count=c.L.expert_count, expert_offset=None, rank_rows=None,
+                     status=torch.zeros(1, **i32))
+    empty = ep.new_layout(0, 2, E, "masked", capacity=cap)
+    empty.expert_count = c.L.expert_count
+    (w, sw), (wg, sg) = ([t.cuda() for t in weights(E, n, K, 3)] for n in (N, 2 * I))
+    used = (~c.unused()).cuda()
+    want = ep.ep_expert_gemm(c.L, c.x, c.sx, w, sw)[used]
+    want_g = [t[used] for t in ep.ep_expert_swiglu(c.L, c.x, c.sx, wg, sg)]
+    assert want.shape[0] > 20
+    for L in (made, empty):
+        assert torch.equal(ep.ep_expert_gemm(L, c.x, c.sx, w, sw)[used], want)
+        got = ep.ep_expert_swiglu(L, c.x, c.sx, wg, sg)
+        assert torch.equal(got[0][used], want_g[0]) and torch.equal(got[1][used], want_g[1])
+        assert int(L.status.item()) == 0
+
+
+def test_a_slab_of_no_tokens_writes_nothing():
+    c = Case(0, 4, 2, 128, kind="masked", cap=6, seed=22)
+    check_gemm(c, 64)
+    check_swiglu(c, 128, "fp8_f32")
+
+
 def test_first_call_of_a_process_is_captured():
     """Nothing of the first call (kernel attributes, the driver's encoder, lazy
     loading) is forbidden during a capture."""

@@ -59,6 +59,35 @@ def test_expert_arguments(lib, gated):  # noqa: F811
     assert call(L=_filled(max_tokens=8)) == CAPACITY
 
 
+@pytest.mark.parametrize("gated", [False, True])
+def test_a_made_up_masked_layout_needs_only_what_is_read(lib, gated):  # noqa: F811
+    """kind, num_experts, capacity, expert_count and status; all else is zero.  No
+    call gets as far as a launch: an mxfp8 call that is not refused for its layout
+    answers EP_ERR_UNSUPPORTED, and one without rows EP_ERR_INVALID_ARG, so the
+    layout's num_tokens = 0 did not end it."""
+    from combine_expert_histogram_gb300.binding import _Layout
+
+    def call(rows=A, quant=1, **kw):
+        c = _Layout(num_experts=8, kind=1, capacity=4, expert_count=256, status=256)
+        for k, v in kw.items():
+            setattr(c, k, v)
+        if gated:
+            return lib.ep_expert_swiglu(ctypes.byref(c), rows, A, 256, quant, A, A, 256, 1, A, A,
+                                        None)
+        return lib.ep_expert_gemm(ctypes.byref(c), rows, A, 256, quant, A, A, 256, A, None)
+
+    assert call(quant=3) == UNSUPPORTED
+    for other in (dict(num_tokens=-3), dict(num_topk=99), dict(num_ranks=7), dict(align=5),
+                  dict(num_tokens=9, max_tokens=8), dict(dst_row=3), dict(expert_offset=3),
+                  dict(row_src=1), dict(rank_rows=1)):
+        assert call(quant=3, **other) == UNSUPPORTED, other
+    assert call(rows=None) == INVALID and call(rows=P(4104)) == INVALID
+    for bad in (dict(num_experts=0), dict(num_experts=1025), dict(capacity=0), dict(capacity=-4),
+                dict(expert_count=None), dict(expert_count=258), dict(status=None),
+                dict(status=257), dict(capacity=1 << 30), dict(kind=2)):
+        assert call(quant=3, **bad) == INVALID, bad
+
+
 def test_moe_decode_arguments(lib):  # noqa: F811
     big = 1 << 40
 
