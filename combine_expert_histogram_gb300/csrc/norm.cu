@@ -110,11 +110,11 @@ __global__ void __launch_bounds__(kMaxThreads)
                 amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 8));
             }
             if (Q == EP_QUANT_FP8_F32) {
-                // times the reciprocal: y itself is a few roundings from the formula's,
-                // and eight IEEE divisions a lane made the kernel 4 % slower
+                // 16384 x 7168: 156.2 us; 161.4 with eight divisions a lane, 155.5 with
+                // the product by inv alone, which falls to the other side of some ties
                 const float s = group_scale(amax), inv = __frcp_rn(s);
 #pragma unroll
-                for (int m = 0; m < 8; ++m) y[m] *= inv;
+                for (int m = 0; m < 8; ++m) y[m] = group_quotient(y[m], s, inv);
                 if (j < vecs && (lane & 15) == 0)
                     reinterpret_cast<float *>(scales)[row * (H >> 7) + (j >> 4)] = s;
             } else {

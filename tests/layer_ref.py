@@ -58,6 +58,25 @@ def quantise_bf16(x: torch.Tensor):
     return e4m3((x.to(F64) / widen(s)).float().to(F64)), s
 
 
+def tie_groups(n: int, g: torch.Generator) -> torch.Tensor:
+    """n groups of 128 bf16 values (in fp32): the largest of each is an 8-bit whole
+    number, and among the others are all whose E4M3 value of the binary32 quotient
+    x / s differs from that of x times the binary32 reciprocal of s."""
+    out = torch.empty((n, 128))
+    for i in range(n):
+        a = 128 + i % 128
+        m = torch.arange(128, 256)[:, None] * torch.exp2(-torch.arange(9.0))
+        v = m.flatten()[m.flatten() <= a]
+        s = torch.tensor(float(a)) / torch.tensor(448.0)
+        inv = (1 / s.to(F64)).float()
+        moved = v[e4m3((v / s).to(F64)) != e4m3((v * inv).to(F64))][:100]
+        rest = v[torch.randint(0, len(v), (127 - len(moved),), generator=g)]
+        sign = torch.randint(0, 2, (127,), generator=g) * 2 - 1
+        out[i, 0] = a
+        out[i, 1:] = torch.cat([moved, rest]) * sign
+    return out
+
+
 def word_bytes(words: torch.Tensor) -> torch.Tensor:
     """The bytes of int32 rows, little-endian: [rows, 4 * columns]."""
     w = words.cpu().long()

@@ -85,6 +85,41 @@ def test_formula(T, H, quant):
         check_scaled(rows, scales, y, quant, T, H)
 
 
+def bytes_of(t):
+    return t.cpu().view(torch.uint8)
+
+
+@pytest.mark.parametrize("T", [3, 2500])
+@pytest.mark.parametrize("quant", ["fp8_f32", "fp8_ue8m0", "mxfp8", "fp8_ue8m0_mn"])
+def test_quantised_by_the_rule_of_dispatch(T, quant):
+    """Rows of +-1 without eps have a mean square of 1, so y is +-weight, a bf16
+    number: the 8-bit rows and scales are ep_dispatch's of the bf16 rows, bit for
+    bit.  Among the weights are the groups whose quotient x / s is a tie of E4M3
+    (or next to one) that a product by the rounded 1 / s moves."""
+    H = 16384
+    g = torch.Generator().manual_seed(T)
+    w = ref.tie_groups(H // 128, g)
+    w[40, 3], w[41, 5], w[42] = float("inf"), float("nan"), 0.0
+    w[43, :3] = torch.tensor([3e38, -1e-39, 1e-30])
+    w[44] *= 2.0 ** -130
+    w[45] *= 2.0 ** 110
+    w[46, 64:] = 0.0
+    w = w.flatten().bfloat16().cuda()
+    x = (torch.randint(0, 2, (T, H), generator=g) * 2 - 1).bfloat16().cuda()
+    out, rows, scales, _ = ep.ep_rmsnorm(x, w, 0.0, quant=quant)
+    assert torch.equal((x * w).view(torch.int16)[:, :40 * 128], out.view(torch.int16)[:, :40 * 128])
+    L = ep.ep_layout(torch.zeros((T, 1), dtype=torch.int32, device="cuda"), 1, align=1)
+    want, want_s, _ = ep.ep_dispatch(L, out, quant)
+    assert torch.equal(bytes_of(rows), bytes_of(want))
+    if quant == "fp8_ue8m0_mn":
+        scales, want_s = scales[:, :T].contiguous(), want_s[:, :T].contiguous()
+    assert torch.equal(bytes_of(scales), bytes_of(want_s))
+    if quant == "fp8_f32":
+        q, s = ref.quantise_bf16(out.cpu()[:8, :40 * 128])
+        assert torch.equal(ref.decode(rows[:8, :40 * 128]), q)
+        assert torch.equal(scales.cpu()[:8, :40].to(ref.F64), s)
+
+
 @pytest.mark.parametrize("H", [8, 24, 200, 2056, 4104])
 def test_bf16_rows_of_any_multiple_of_8_without_residual(H):
     x, _, w = make(9, H, seed=H, residual=False)

@@ -167,6 +167,19 @@ def test_the_rows_of_a_slab_share_its_memory():
         assert r.shape == (shape[0] * shape[1], shape[2]) and r.data_ptr() == t.data_ptr()
 
 
+def test_some_quotients_are_moved_by_a_reciprocal():
+    """tie_groups has what it promises: values that the quotient and the product by
+    the reciprocal quantise differently, so that a kernel with the other rule fails."""
+    v = ref.tie_groups(128, torch.Generator().manual_seed(1))
+    assert torch.equal(v.bfloat16().float(), v)
+    assert torch.equal(v.abs().amax(1), torch.arange(128.0, 256.0))
+    s = v[:, :1].abs() / torch.full((128, 1), 448.0)
+    inv = (1 / s.double()).float()
+    moved = ref.e4m3((v / s).double()) != ref.e4m3((v * inv).double())
+    assert moved.sum() >= 60 and moved.any(1).sum() >= 7
+    assert torch.equal(ref.quantise_bf16(v)[0], ref.e4m3((v / s).double()))
+
+
 def test_the_64_bit_e4m3_agrees_with_torch():
     """The test's own E4M3 decoding and rounding against torch's cast."""
     b = torch.arange(256, dtype=torch.uint8)
