@@ -316,6 +316,45 @@ def test_a_slab_of_no_tokens_writes_nothing():
     check_swiglu(c, 128, "fp8_f32")
 
 
+@pytest.mark.parametrize("quant", ["fp8_f32", "fp8_ue8m0", "fp8_ue8m0_mn"])
+def test_gated_rows_are_quantised_by_the_rule_of_dispatch(quant):
+    """Gates of 64 (silu(64) is 64 in fp32) and whole up sums of 8 bits: h is a
+    bf16 number, so the 8-bit rows and scales are ep_dispatch's of the bf16 output,
+    bit for bit.  The up values hold the quotients that ref.tie_groups picks."""
+    groups, K, T = 128, 256, 5
+    I = groups * 128
+    g = torch.Generator().manual_seed(23)
+    u = ref.tie_groups(groups, g).flatten()
+    u[7 * 128:8 * 128] = 0.0
+    # an 8-bit number is two E4M3 numbers of four bits
+    unit = torch.exp2(torch.floor(torch.log2(u.abs().clamp(min=0.5))) - 3)
+    hi = torch.trunc(u / unit) * unit
+    w = torch.zeros((1, 2 * I, K))
+    w[0, :I, 2] = 64.0
+    w[0, I:, 0], w[0, I:, 1] = hi, u - hi
+    f8 = w.to(torch.float8_e4m3fn)
+    assert torch.equal(f8.float(), w)
+    x = torch.zeros((T, K))
+    x[:, 0], x[:, 2] = torch.tensor([1.0, -1, 1, 2, -0.5]), 1.0
+    x[:, 1] = x[:, 0]
+    L = ep.ep_layout(torch.zeros((T, 1), dtype=torch.int32, device="cuda"), 1, align=1)
+    one = torch.ones
+    args = (L, x.to(torch.float8_e4m3fn).view(torch.uint8).cuda(), one(T, K // 128).cuda(),
+            f8.view(torch.uint8).cuda(), one(1, 2 * I // 128, K // 128).cuda())
+    out, _ = ep.ep_expert_swiglu(*args, out_quant="none")
+    assert torch.equal(out.cpu().float(), 64 * x[:, :1] * u)
+    rows, scales = ep.ep_expert_swiglu(*args, out_quant=quant)
+    want, want_s, _ = ep.ep_dispatch(L, out, quant)
+    # h of a zero up sum may have either sign
+    as_bytes = lambda t: t.cpu().view(torch.uint8)  # noqa: E731
+    zero = out.cpu() == 0
+    assert torch.equal(as_bytes(rows)[~zero], as_bytes(want)[~zero])
+    assert (as_bytes(rows)[zero] & 127 == 0).all()
+    if quant == "fp8_ue8m0_mn":
+        scales, want_s = scales[:, :T].contiguous(), want_s[:, :T].contiguous()
+    assert torch.equal(as_bytes(scales), as_bytes(want_s))
+
+
 def test_first_call_of_a_process_is_captured():
     """Nothing of the first call (kernel attributes, the driver's encoder, lazy
     loading) is forbidden during a capture."""
