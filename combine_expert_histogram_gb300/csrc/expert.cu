@@ -349,8 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float amax = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 64; ++i) {
-                    const float g = acc[i];
-                    acc[i] = __fdividef(g, 1.0f + __expf(-g)) * acc[64 + i];
+                    acc[i] = gated_silu(acc[i], acc[64 + i]);
                     amax = fmaxf(amax, fabsf(acc[i]));
                 }
                 const size_t at = (size_t)(q.row + r) * a.N + q.n0 + half * 64;

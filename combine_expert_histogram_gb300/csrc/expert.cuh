@@ -48,6 +48,17 @@ size_t moe_workspace_bytes_up_to(int T, int K, int E, int H, int I);
 cudaError_t launch_moe_decode(const MoeArgs &a, void *workspace, cudaStream_t stream);
 cudaError_t launch_expert(const ExpertArgs &a, bool gated, cudaStream_t stream);
 
+// silu(g) * u = g / (1 + exp(-g)) * u by the fast exponential and division.  The
+// first is off by at most 2 + 1.173 |g| units in the last place, the second by 2, so
+// the result is within (11 + 2.4 |g|) 2^-24 of the formula: below half a step of
+// bf16 and E4M3 for any |g| whose exponential is finite.  Where 1 + exp(-g) is above
+// 2^126 (g < -87.3) the division gives 0; there |silu(g)| < 2^-119.  (expf and the
+// rounded division, whose slow path is a call across 128 live sums, took the prompt
+// case of ep_expert_swiglu from 3.6 to 4.7 ms, the few-token layer from 16.6 to 17.2 us.)
+__device__ __forceinline__ float gated_silu(float g, float u) {
+    return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+
 // Rows of expert e: [first, first + n).  Clamped into the row space, so a
 // layout whose arrays were never filled addresses nothing outside it.
 __device__ __forceinline__ int expert_first(const ExpertArgs &a, int e) {

@@ -240,8 +240,7 @@ __device__ __forceinline__ void add4(uint4 &s, uint4 v) {
     s.w = __float_as_uint(__uint_as_float(s.w) + __uint_as_float(v.w));
 }
 __device__ __forceinline__ float gate_up(uint32_t g, uint32_t u) {
-    const float x = __uint_as_float(g);
-    return __fdividef(x, 1.0f + __expf(-x)) * __uint_as_float(u);
+    return gated_silu(__uint_as_float(g), __uint_as_float(u));
 }
 
 // The chunk's entries as E4M3 rows in shared memory: xq[group][cols / 8] atoms of

@@ -505,7 +505,8 @@ ep_status_t ep_expert_gemm(const ep_layout_t *layout, const void *rows, const vo
  *                  E4M3 [rows, I] and scales as ep_dispatch writes them for
  *                  hidden = I (EP_QUANT_MXFP8: EP_ERR_UNSUPPORTED).
  *
- *   g, u = the two products (fp32);  h = g / (1 + exp(-g)) * u  (fp32)
+ *   g, u = the two products (fp32);  h = g / (1 + exp(-g)) * u, within
+ *   (16 + 4 |g|) 2^-24 |h| + 2^-119 |u| of the formula (fast exponential and division)
  *   out = bf16_rn(h), or `out_quant` of the fp32 h by ep_dispatch's rules.
  */
 ep_status_t ep_expert_swiglu(const ep_layout_t *layout, const void *rows, const void *row_scales,
@@ -540,7 +541,8 @@ ep_status_t ep_expert_swiglu(const ep_layout_t *layout, const void *rows, const 
  *              between calls.  Calls (or replayed graphs) that share one must
  *              not overlap on the GPU.
  *
- *   g, u = w13[e] xq (fp32);  h = g / (1 + exp(-g)) * u;  hq = EP_QUANT_FP8_F32 of h
+ *   g, u = w13[e] xq (fp32);  h = g / (1 + exp(-g)) * u (as in ep_expert_swiglu);
+ *   hq = EP_QUANT_FP8_F32 of h
  *   out[t] = bf16_rn( sum over k of topk_w[t,k] * (w2[e] hq) ),  sums in fp32,
  * in ascending k; a token with no routed entry gets +0.
  *

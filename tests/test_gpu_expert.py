@@ -355,6 +355,43 @@ def test_gated_rows_are_quantised_by_the_rule_of_dispatch(quant):
     assert torch.equal(as_bytes(scales), as_bytes(want_s))
 
 
+def test_gate_within_its_stated_bound():
+    """Exact gates from -448 to 448, close around where exp(-g) leaves fp32, and
+    exact up sums from 2^-20 to 2^120: |h - formula| <= (16 + 4 |g|) 2^-24 |h| +
+    2^-119 |u|, and half a step of bf16."""
+    groups, K = 16, 128
+    I = groups * 128
+    gen = torch.Generator().manual_seed(24)
+    v = ref.e4m3_values()
+    v = v[~v.isnan()]
+    near = -torch.tensor([80.0, 88, 88, 88, 96, 104]).to(ref.F64)
+    a = torch.cat([near.repeat(64), v[torch.randint(0, len(v), (I - 384,), generator=gen)]])
+    b = v[torch.randint(0, len(v), (I,), generator=gen)]
+    b[:384] = torch.arange(384).remainder(65) / 16 - 2  # steps of 1/16 of four bits and a sign
+    b = ref.e4m3(b)
+    up = v[torch.randint(0, len(v), (I,), generator=gen)]
+    up[::7] = 1.0
+    w = torch.zeros((1, 2 * I, K))
+    w[0, :I, 0], w[0, :I, 1], w[0, I:, 2] = a.float(), b.float(), up.float()
+    power = torch.tensor([0, 100, 120, -20])[torch.arange(groups) % 4].to(ref.F64)
+    scales = torch.cat([torch.ones(groups, dtype=ref.F64), torch.exp2(power)])
+    x = torch.zeros((1, K))
+    x[0, :3] = 1.0
+    f8 = lambda t: t.to(torch.float8_e4m3fn).view(torch.uint8).cuda()  # noqa: E731
+    L = ep.ep_layout(torch.zeros((1, 1), dtype=torch.int32, device="cuda"), 1, align=1)
+    out, _ = ep.ep_expert_swiglu(L, f8(x), torch.ones((1, 1), device="cuda"), f8(w),
+                                 scales.float().view(1, -1, 1).cuda(), out_quant="none")
+    g, u = a + b, up * torch.exp2(power).repeat_interleave(128)
+    h = g / (1 + torch.exp(-g)) * u
+    noise = (16 + 4 * g.abs()) * ref.U * h.abs() + 2.0 ** -119 * u.abs()
+    assert ((g < -86) & (g > -89) & (u.abs() > 2.0 ** 90)).sum() > 20
+    # the bound is on fp32 numbers: 448 * 2^120 is none (2^128.8), nor are some of h;
+    # there fp32 arithmetic gives an infinity, or NaN of one times zero
+    fits = (u.abs() <= torch.finfo(torch.float32).max) & (h.abs() <= torch.finfo(torch.bfloat16).max)
+    assert fits.sum() > 1800 and not out[0].cpu()[~fits].isfinite().any()
+    ref.close_bf16(out[0].cpu()[fits], h[fits], noise[fits])
+
+
 def test_first_call_of_a_process_is_captured():
     """Nothing of the first call (kernel attributes, the driver's encoder, lazy
     loading) is forbidden during a capture."""
