@@ -22,16 +22,15 @@ __device__ __forceinline__ float group_scale(float amax) {
     return __fdiv_rn(fmaxf(amax, 1e-4f), 448.0f);
 }
 // x / s to the nearest fp32, ep_dispatch's rule, without a division for each x:
-// inv is 1 / s to the nearest, q the quotient's estimate, x - q * s its remainder,
-// which one fused product-and-sum gives exactly, and q + remainder * inv rounds to
-// the quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000", IBM J. Res. Dev. 34, 1990).  The remainder is inexact only where the
-// quotient is far below E4M3's smallest value.  A zero keeps its sign; an infinite
-// scale (of an infinite amax) leaves 0 of finite x and NaN of the others, as a
-// division does.
+// inv is 1 / s to the nearest, q the quotient's estimate, q * s - x its error, which
+// one fused product-and-sum gives exactly, and q - error * inv rounds to the quotient
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000",
+// IBM J. Res. Dev. 34, 1990).  The error is inexact only where the quotient is far
+// below E4M3's smallest value.  Zeros keep their sign.  An infinite scale (of an
+// infinite amax) leaves 0 of finite x and NaN of the others, as a division does.
 __device__ __forceinline__ float group_quotient(float x, float s, float inv) {
-    const float q = x * inv, r = fmaf(-q, fminf(s, 3.402823466e38f), x);
-    return copysignf(fmaf(r, inv, q), x);
+    const float q = x * inv, err = fmaf(q, fminf(s, 3.402823466e38f), -x);
+    return fmaf(-err, inv, q);
 }
 // s rounded up to a power of two 2^(e-127): the biased exponent e.
 __device__ __forceinline__ int ue8m0_exponent(float s) {
