@@ -139,6 +139,49 @@ def test_many_rows(T):
     check_scaled(rows, scales, y, "fp8_f32", T, 1024)
 
 
+def check_some_rows(T, H, quant, seed):
+    """All bf16 rows against the formula on the device, 8-bit rows of some."""
+    x, r, w = cuda(*make(T, H, seed=seed))
+    out, rows, scales, res = ep.ep_rmsnorm(x, w, EPS, residual=r, quant=quant)
+    s = x.to(ref.F64) + r.to(ref.F64)
+    y = s / torch.sqrt(s.square().mean(1, keepdim=True) + EPS) * w.to(ref.F64)
+    assert ((res.to(ref.F64) - s).abs() <= s.abs() * (ref.BF16 + ref.U)).all()
+    assert ((out.to(ref.F64) - y).abs() <= y.abs() * (ref.BF16 + 1.01 * REL) + 2.0 ** -133).all()
+    if quant != "none":
+        g = torch.Generator().manual_seed(seed)
+        some = torch.cat([torch.tensor([0, T // 2, T - 1]), torch.randint(0, T, (20,), generator=g)])
+        at = some.cuda()
+        sc = scales[:, at] if quant == "fp8_ue8m0_mn" else scales[at]
+        check_scaled(rows[at], sc, y[at].cpu(), quant, len(some), H)
+
+
+@pytest.mark.parametrize("quant", ["none", "fp8_f32", "fp8_ue8m0", "mxfp8", "fp8_ue8m0_mn"])
+@pytest.mark.parametrize("H", [2048, 2176, 4096, 4224, 7168, 8320, 32768])
+def test_many_rows_of_two_and_four_vectors_a_lane(H, quant):
+    """Blocks of many rows: lanes with one, two or four vectors, the last vectors of
+    a row in all of them, in some warps, or in part of a warp."""
+    check_some_rows(2500, H, quant, seed=H)
+
+
+@pytest.mark.parametrize("quant", ["none", "fp8_f32", "fp8_ue8m0", "mxfp8", "fp8_ue8m0_mn"])
+@pytest.mark.parametrize("H", [8320, 12416, 16512, 20608, 24704, 32640])
+def test_few_long_rows(H, quant):
+    """Few rows of two and four vectors a lane that end inside a vector's round."""
+    check_some_rows(3, H, quant, seed=H)
+
+
+@pytest.mark.parametrize("over", [-1, 0, 1])
+@pytest.mark.parametrize("rows_per_sm", [1, 2, 3, 16])
+def test_rows_around_multiples_of_the_processors(rows_per_sm, over):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    check_some_rows(rows_per_sm * sms + over, 4224, "fp8_f32", seed=rows_per_sm)
+
+
+@pytest.mark.parametrize("H", [2056, 4104, 8200, 16392])
+def test_many_bf16_rows_of_any_multiple_of_8(H):
+    check_some_rows(2500, H, "none", seed=H)
+
+
 @pytest.mark.parametrize("quant", ["none", "fp8_f32", "mxfp8"])
 def test_in_place(quant):
     """residual_out = residual and out = x give what separate buffers give."""
