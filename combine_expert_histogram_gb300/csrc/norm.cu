@@ -149,11 +149,13 @@ cudaError_t launch_q(const uint16_t *x, const uint16_t *residual, const uint16_t
                      int T, int H, uint16_t *residual_out, uint16_t *out, uint8_t *rows,
                      uint8_t *scales, cudaStream_t stream) {
     const int vecs = H / 8;
-    // Few rows: a vector a lane, the shortest way through one row (1021 x 2056:
-    // 6.8 us, 8.4 with two).  Many: blocks of up to 256 threads with up to four, so
-    // that more rows share an SM and some load while others reduce (16384 x 7168
-    // with 8-bit rows: 157 us, 173 with blocks of 448, 194 with blocks of 896).
-    const int want = T > 16 * sm_count() ? 256 : kMaxThreads;
+    // Up to two rows an SM: a vector a lane, the shortest way through one row.  Above:
+    // blocks of up to 256 threads with up to four, so that more rows share an SM and
+    // some load while others reduce.  On the GPU, 8-bit rows of 7168: 1 row 2.3 us
+    // (2.8 in blocks of 256), 304 rows 3.8 (4.0); 305 rows 4.8 (5.1 with a vector a
+    // lane), 456 rows 5.2 (5.6), 16384 rows 154 (185).  bf16 rows of 2056: 1.7 either
+    // way at 304, 2.3 (2.6) at 1021.
+    const int want = T > 2 * sm_count() ? 256 : kMaxThreads;
     int V = 1;
     while (V < 4 && vecs > V * want) V *= 2;
     const int threads = ((vecs + V - 1) / V + 31) / 32 * 32;
