@@ -650,15 +650,15 @@ cudaError_t launch_cols(const MoeArgs &a, const float *gu, int gu_parts, float *
     CUtensorMap wmap;
     if (!encode_bytes(&wmap, UP ? a.w13 : a.w2, 3, dims, strides, box)) return cudaErrorInvalidValue;
     const int fixed = 1024 + G * COLS * (128 + 4) + (int)sizeof(Shared);
-    // Up to 1 MB of weights an SM, half of its shared memory where that leaves a
-    // ring of five stages: the next kernel's blocks then start beside this one's
-    // and load their weights (13 tokens, H = 1152, I = 640: 28.0 us, 30.5 with all
-    // of it).  Above, all of it: five stages hold 64 tokens of H = 7168, I = 2048 to
-    // 1.90 ms where ten took 1.85.
-    const int n = a.T * a.K;
-    const bool small = (int64_t)(n < a.E ? n : a.E) * R * D <= (int64_t)sm_count() << 20;
+    // Half of an SM's shared memory where that leaves a ring of five stages: the next
+    // kernel's blocks then start beside this one's and load their weights.  H = 7168,
+    // I = 2048, E = 256 (the second kernel's; the first has room for two stages): 64
+    // tokens 1.49 ms (1.54 with all of the memory), 8 tokens 371 us (375), 1 token
+    // 65.6 (64.5).  H = 2048, I = 768, E = 128: 1, 2, 4, 16, 64 tokens 15.7, 26.0,
+    // 36.8, 77.4, 119 us (16.4, 25.1, 38.5, 78.0, 121).  13 tokens of 20 experts, H =
+    // 1152, I = 640: 21.1 us either way.
     const int half = (kSmemHalf - fixed) / kStageBytes, fit = (kSmemMax - fixed) / kStageBytes;
-    const int stages = small && half >= 5 ? half : fit < kMaxStages ? fit : kMaxStages;
+    const int stages = half >= 5 ? half : fit < kMaxStages ? fit : kMaxStages;
     const size_t smem = 1024 + (size_t)G * COLS * (128 + 4) + (size_t)stages * kStageBytes;
     return launch_large<rows_kernel<UP, COLS>>(sm_count(), kThreads, smem, stream, wmap, a, gu,
                                                gu_parts, dst, parts, stages);
