@@ -733,12 +733,17 @@ def ep_moe_decode_workspace_bytes(num_tokens: int, num_topk: int, num_experts: i
                                                             hidden, inter))
 
 
+def _moe_scratch_bytes(dev, *shape) -> int:
+    """ep_moe_decode_workspace_bytes for device `dev`: it depends on the number of SMs."""
+    with torch.cuda.device(dev):
+        return ep_moe_decode_workspace_bytes(*shape)
+
+
 def new_moe_workspace(num_tokens: int, num_topk: int, num_experts: int, hidden: int, inter: int,
                       device=None) -> MoeWorkspace:
     """Allocate a workspace for ep_moe_decode calls of this shape, or of fewer tokens."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    with torch.cuda.device(dev):  # the size depends on the device's number of SMs
-        n = ep_moe_decode_workspace_bytes(num_tokens, num_topk, num_experts, hidden, inter)
+    n = _moe_scratch_bytes(dev, num_tokens, num_topk, num_experts, hidden, inter)
     if n == 0 and num_tokens > 0:
         raise EPError(EP_ERR_INVALID_ARG, "ep_moe_decode shape")
     return MoeWorkspace(torch.empty(max(n, 16), dtype=torch.uint8, device=dev),
@@ -782,7 +787,7 @@ def ep_moe_decode(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
     elif x_scales is not None:
         raise ValueError("x_scales given for bf16 rows")
     if workspace is None:
-        n = ep_moe_decode_workspace_bytes(T, K, E, H, inter)
+        n = _moe_scratch_bytes(dev, T, K, E, H, inter)
         workspace = MoeWorkspace(_empty(max(n, 16), torch.uint8, dev, stream),
                                  _empty(1, _I32, dev, stream))
     ws = workspace.scratch

@@ -167,6 +167,36 @@ def test_the_rows_of_a_slab_share_its_memory():
         assert r.shape == (shape[0] * shape[1], shape[2]) and r.data_ptr() == t.data_ptr()
 
 
+def test_the_layers_own_workspace_is_sized_on_its_device(lib, monkeypatch):  # noqa: F811
+    """Tensors on device 3 while another one is current (a stand-in for both: the
+    argument checks pass, the call is recorded): the size is asked for with device
+    3 current, as new_moe_workspace does."""
+    import contextlib
+    from combine_expert_histogram_gb300 import binding as ep
+    current, asked = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        old, current[0] = current[0], d if isinstance(d, int) else d.index
+        yield
+        current[0] = old
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(ep, "_rows_of", lambda t, name, dims=2: 3)
+    monkeypatch.setattr(ep, "_want", lambda *a: 256)
+    monkeypatch.setattr(ep, "_empty", lambda shape, dtype, dev, stream: torch.empty(shape, dtype=dtype))
+    monkeypatch.setattr(ep, "_on", lambda stream, dev: 0)
+    monkeypatch.setattr(ep, "_call", lambda *a: asked.append("call"))
+    monkeypatch.setattr(ep, "ep_moe_decode_workspace_bytes",
+                        lambda *a: asked.append((current[0], a)) or 64)
+    u8 = lambda *n: torch.zeros(n, dtype=torch.uint8)  # noqa: E731
+    idx = torch.zeros((2, 1), dtype=torch.int32)
+    ep.ep_moe_decode(torch.zeros((2, 128), dtype=torch.bfloat16), idx, idx.float(),
+                     u8(4, 256, 128), torch.zeros(4, 2, 1), u8(4, 128, 128), torch.zeros(4, 1, 1))
+    assert asked == [(3, (2, 1, 4, 128, 128)), "call"] and current == [0]
+
+
 def test_some_quotients_are_moved_by_a_reciprocal():
     """tie_groups has what it promises: values that the quotient and the product by
     the reciprocal quantise differently, so that a kernel with the other rule fails."""
