@@ -80,16 +80,23 @@ __device__ __forceinline__ int row_tiles(const ExpertArgs &a, int e) {
 }
 
 // Tile t of the list: experts in order; within one, row tiles run fastest, so
-// that CTAs working at the same time share weights.
-__device__ __forceinline__ Tile find_tile(const ExpertArgs &a, const int32_t *pre, int t, int cols) {
+// that CTAs working at the same time share weights.  Where the counts are no
+// layout's and their tiles' sum wrapped, a tile that is none has no rows.
+__device__ __forceinline__ Tile find_tile(const ExpertArgs &a, const int32_t *pre, int t, int cols,
+                                          int ntn) {
     int lo = 0, hi = a.E;  // pre[lo] <= t < pre[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (pre[mid] <= t) lo = mid; else hi = mid;
     }
-    const int mt = row_tiles(a, lo), local = t - pre[lo], n = local / mt, i = local - n * mt;
+    const int mt = row_tiles(a, lo), local = t - pre[lo];
+    const int n = local / max(mt, 1), i = local - n * mt;
     Tile r;
     r.e = lo;
+    if (local < 0 || n >= ntn || mt == 0) {
+        r.row = r.rows = r.n0 = 0;
+        return r;
+    }
     r.n0 = n * cols;
     r.row = expert_first(a, lo) + i * kTM;
     r.rows = min(expert_rows(a, lo) - i * kTM, kTM);
@@ -165,7 +172,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         a.E, [&](int e) { return row_tiles(a, e) * ntn; }, pre, sh.scan);
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    const int total = pre[a.E];
+    // at most this many tiles where the experts' rows are disjoint: more are no layout's
+    const int64_t most = ((int64_t)a.rows_cap / kTM + a.E) * ntn;
+    const int total = pre[a.E] <= most ? min(pre[a.E], 0x7fffffff - (int)gridDim.x) : 0;
     const int G = a.K >> 7;
 
     if (warp >= kEpiWarps) {
@@ -174,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- loads ----
             int it = 0;
             for (int t = blockIdx.x; t < total && !__any_sync(kFullMask, *fail); t += gridDim.x) {
-                const Tile q = find_tile(a, pre, t, cols);
+                const Tile q = find_tile(a, pre, t, cols, ntn);
                 for (int g = 0; g < G; ++g, ++it) {
                     const int s = it % kStages;
                     const bool ok = it < kStages || mbar_wait_fast(&sh.empty[s], (it / kStages - 1) & 1, fail);
@@ -243,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int it = 0, tiles = 0;
             bool ok = true;
             for (int t = blockIdx.x; ok && t < total && !__any_sync(kFullMask, *fail); t += gridDim.x, ++tiles) {
-                const Tile q = find_tile(a, pre, t, cols);
+                const Tile q = find_tile(a, pre, t, cols, ntn);
                 if (warp == kEpiWarps + 2 && lane == 0) sh.tile[tiles & 7] = q;
                 const int b0 = q.n0 / 128, b1 = GATED ? b0 + a.N / 128 : min(b0 + 1, NB - 1);
                 const float *sw0 = a.w_scales + ((size_t)q.e * NB + b0) * G;

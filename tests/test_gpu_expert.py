@@ -474,6 +474,23 @@ def test_a_layout_that_was_never_filled_reads_and_writes_inside_its_rows():
     assert (guard[c.n:] == 7.0).all()
 
 
+@pytest.mark.parametrize("first", [-5, 0, "end - 3", 2 ** 30])
+def test_one_expert_that_claims_more_rows_than_there_are(first):
+    """One count of 2^30 is cut off at the end of the row space; the other experts
+    have none."""
+    c = Case(10, 4, 2, 128, seed=11)
+    w, sw = weights(4, 264, 128, 3)
+    first = c.n - 3 if first == "end - 3" else first
+    guard = torch.full((c.n + 64, 264), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.L.expert_count.copy_(torch.tensor([0, 0, 2 ** 30, 0], dtype=torch.int32))
+    c.L.expert_offset.copy_(torch.tensor([0, 0, first, 0, 0], dtype=torch.int32))
+    ep.ep_expert_gemm(c.L, c.x, c.sx, w.cuda(), sw.cuda(), out=guard[:c.n])
+    torch.cuda.synchronize()
+    a = min(max(first, 0), c.n)
+    assert (guard[c.n:] == 7.0).all() and (guard[:a] == 7.0).all()
+    assert (guard[a:c.n] != 7.0).any(1).all()
+
+
 def test_the_same_call_twice_and_on_another_stream():
     c = Case(90, 5, 2, 512, seed=12)
     w, sw = (t.cuda() for t in weights(5, 512, 512, 3))
