@@ -431,8 +431,10 @@ ep_status_t ep_layout_noalloc(const int32_t *topk_idx, const ep_layout_t *layout
  * ep_rmsnorm -- the norm in front of a mixture-of-experts layer: residual
  * addition, root-mean-square norm and, optionally, the rows in 8 bits.  Its
  * bf16 rows are what the router's product, ep_dispatch and ep_moe_decode take;
- * its 8-bit rows are in ep_dispatch's formats, for ep_moe_decode and, with a
- * one-expert layout, for ep_expert_gemm / ep_expert_swiglu (a shared expert).
+ * its 8-bit rows are in ep_dispatch's formats, for ep_moe_decode and (but those of
+ * EP_QUANT_MXFP8) for ep_expert_gemm / ep_expert_swiglu as a shared expert: with a
+ * contiguous layout of one expert, align 1, that has every token once, whose row t
+ * is token t.
  *
  *   x             device bf16 [T, hidden], 16-byte aligned.
  *   residual      device bf16 [T, hidden] or NULL (no addition).

@@ -311,6 +311,31 @@ def test_a_layer_from_norm_to_combine(T, kind):
         ref.close_bf16(ep.ep_moe_decode(x, idx, w, *c.dev[3:]), want, noise)
 
 
+@pytest.mark.parametrize("quant", ["fp8_f32", "fp8_ue8m0", "fp8_ue8m0_mn"])
+@pytest.mark.parametrize("T", [1, 6, 131])
+def test_a_shared_expert_on_the_norms_rows(T, quant):
+    """norm -> swiglu -> product of a one-expert layout: the norm's 8-bit rows as they
+    are (token t is row t), in every scale format, with gated rows of the same; for
+    the formats ep_moe_decode takes, it gives the same layer."""
+    H, I = 640, 384
+    c = Case(T, 1, 1, H, I, seed=T, idx=torch.zeros((T, 1), dtype=torch.int32))
+    wn = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    _, q, s, _ = ep.ep_rmsnorm(c.dev[0], wn, quant=quant, with_out=False)
+    L = ep.ep_layout(c.dev[1], 1, align=1)
+    assert L.rows_capacity == T
+    w13, s13, w2, s2 = c.dev[3:]
+    h, sh = ep.ep_expert_swiglu(L, q, s, w13, s13, quant, out_quant="fp8_f32")
+    y = ep.ep_expert_gemm(L, h, sh, w2, s2)
+    c.w = torch.ones((T, 1))
+    words = ref.mn_to_rows(s, T) if quant == "fp8_ue8m0_mn" else s
+    sv = s.cpu().to(ref.F64) if quant == "fp8_f32" else ref.ue8m0(words, H // 128)
+    c.check(y, q=ref.decode(q), s=sv)
+    if quant != "fp8_ue8m0_mn":
+        few = ep.ep_moe_decode(q, c.dev[1], torch.ones((T, 1), device="cuda"), *c.dev[3:],
+                               x_scales=s, quant=quant)
+        c.check(few, q=ref.decode(q), s=sv)
+
+
 def test_refusals():
     c = Case(4, 4, 2, 256, 256, seed=16)
     x, idx, w, w13, s13, w2, s2 = c.dev
