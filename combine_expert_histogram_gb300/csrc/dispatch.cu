@@ -63,6 +63,20 @@ __device__ __forceinline__ void bulk_store(void *gdst, const void *ssrc, uint32_
                  ::"l"(gdst), "r"(smem_addr(ssrc)), "r"(bytes), "l"(policy)
                  : "memory");
 }
+// Start the row copy global -> shared: arrive on the barrier, announcing
+// `bytes` of transactions, and issue one bulk copy that completes them.
+__device__ __forceinline__ void load_row(void *sdst, const void *gsrc, uint32_t bytes,
+                                         uint64_t *bar) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
+                 "r"(bytes)
+                 : "memory");
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(smem_addr(sdst)),
+        "l"(gsrc), "r"(bytes), "r"(smem_addr(bar))
+        : "memory");
+}
+
 // Quantise one FP8 slot (16 consecutive elements a, b of group j/8, part
 // lane%8 of its 8 lanes).  Returns the 16 E4M3 bytes; `sc` receives the
 // group's fp32 scale bits (FP8_F32), its UE8M0 exponent byte (FP8_UE8M0*), or

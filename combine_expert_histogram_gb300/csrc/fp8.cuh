@@ -51,12 +51,5 @@ __device__ __forceinline__ float exp_reciprocal(int e) {
 __device__ __forceinline__ float ue8m0_value(uint32_t e) {
     return e ? __uint_as_float(e << 23) : __uint_as_float(0x00400000u);
 }
-// Four E4M3 bytes -> fp32 (exact: E4M3 is a subset of fp16).
-__device__ __forceinline__ float4 e4m3x4_to_float4(uint32_t v) {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xffffu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v >> 16), __NV_E4M3);
-    const float2 fa = __half22float2(__half2(a)), fb = __half22float2(__half2(b));
-    return make_float4(fa.x, fa.y, fb.x, fb.y);
-}
 
 }  // namespace ep
