@@ -3,7 +3,8 @@
 //   xq = 1x128 E4M3 of x,  g = W13[e][:I] xq,  u = W13[e][I:] xq,
 //   hq = 1x128 E4M3 of silu(g) * u,  out[t] = sum over k of w[t,k] * W2[e] hq
 //
-// Bound by reading the picked experts' weights once.  Two kernels of the same
+// Bound by reading the picked experts' weights, once for each chunk of an expert's
+// entries: once in all where experts get few.  Two kernels of the same
 // body (rows of W13 against the tokens, rows of W2 against the gated results)
 // and a small one for the weighted sum; all launched as programmatic
 // dependents.  Each CTA groups the T*K entries by expert itself (at most 1024,

@@ -518,8 +518,14 @@ ep_status_t ep_expert_swiglu(const ep_layout_t *layout, const void *rows, const 
 
 /*
  * ep_moe_decode -- a whole mixture-of-experts layer for a few tokens (decode:
- * single tokens, small batches), without a layout: the experts' weights are
- * read once and bound the time.
+ * single tokens, small batches), without a layout.  The time goes to reading the
+ * picked experts' weights: once for every chunk of an expert's entries, a chunk
+ * being up to 8 to 32 of them (twice what experts get on average; at most 16 for
+ * rows longer than 4096, 8 for rows longer than 8192).  With more entries an expert
+ * than a chunk holds, the chain of ep_layout, ep_dispatch, ep_expert_swiglu,
+ * ep_expert_gemm and ep_combine is faster: 8 experts, top-2, H = 4096, I = 14336:
+ * 67 us against 109 for 1 token, 162 and 160 for 4, 449 and 227 for 64, 2125 and
+ * 293 for 512.
  *
  *   x          device, 16-byte aligned.  quant EP_QUANT_NONE: bf16 [T, H],
  *              quantised inside as EP_QUANT_FP8_F32 does; EP_QUANT_FP8_F32 or
