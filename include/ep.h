@@ -40,13 +40,16 @@
  *
  * Conventions for every call:
  *   - All array arguments are DEVICE pointers owned by the caller; the library
- *     allocates no memory and never synchronises the host.  Its only state is
- *     a per-device cache of the SM count (read once with
- *     cudaDeviceGetAttribute), the address of the driver's tensor-map encoder
- *     (looked up by the first ep_expert_gemm, ep_expert_swiglu or
- *     ep_moe_decode) and, for ep_layout_noalloc alone, the fixed
- *     device array that call uses as scratch (with its looked-up address);
- *     every other entry point keeps nothing between calls.
+ *     allocates no memory and never synchronises the host.  Its only state, none
+ *     of it from a caller's arrays:
+ *       - the SM count of each device (read once with cudaDeviceGetAttribute);
+ *       - for ep_layout and ep_layout_dispatch, the cluster size that each device
+ *         can place, and its cap (EP_MAX_CLUSTER_CTAS, read once);
+ *       - for ep_expert_gemm, ep_expert_swiglu and ep_moe_decode, the address of
+ *         the driver's tensor-map encoder, and on which devices their kernels'
+ *         shared-memory limits have been raised;
+ *       - for ep_layout_noalloc alone, the fixed device array that call uses as
+ *         scratch, with its looked-up address.
  *   - Tracing: with the environment variable EP_NVTX=1 (read once per
  *     process) every entry point wraps its work in an NVTX range of its own
  *     name, for nsys / ncu timelines; off by default, and the ranges do
