@@ -19,13 +19,14 @@
 //     tensor core fills the other tile.  The scales change every 128 of K, so
 //     the running sum cannot stay in tensor memory.
 // Few rows an expert are bound by reading the weights (16384 entries of 256 experts,
-// K = 7168, I = 2048: 1.14 ms, 6.7 TB/s; 256 tokens in slabs, K = 2048, I = 768: 72 us,
-// 768 tiles in 6 rounds).  Many (131072 entries of the 256 experts: 3.2 ms, 2.4
-// PFLOP/s) by the chain of a block's product and its scaling over two tensor-memory
-// tiles, about 850 clocks a block where the product alone takes 512.
-// Large products run under the power cap when repeated (1370 W, SM at 1.5 to 1.8
-// GHz).  Clusters of two with the weights by multicast, which spare a third of the
-// reads from L2, took the same time there.
+// K = 7168, I = 2048: 1.13 ms, 6.8 TB/s; 256 tokens in slabs, K = 2048, I = 768: 72 us,
+// 768 tiles in 6 rounds).  Many (131072 entries of the 256 experts: 3.1 ms the first
+// pass after a pause, 3.66 ms or 2.1 PFLOP/s repeated) by the power cap when repeated
+// (1370 W, SM at 1.5 to 1.8 GHz), else by the chain of a block's product and its
+// scaling over two tensor-memory tiles, about 850 clocks a block where the product
+// alone takes 512.  Every expert's rows are rounded up to 128, which is about 12 % more
+// products at 512 rows an expert, 25 % at 256.  Clusters of two with the weights by
+// multicast, which spare a third of the reads from L2, took the same time.
 // Rows past an expert's segment that share 32 of a tile with its last ones are
 // loaded (whatever they hold, products of other rows do not see it) and never
 // stored.

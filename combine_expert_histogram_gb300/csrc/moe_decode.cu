@@ -25,10 +25,10 @@
 //     instruction, which converts its operands on the vector pipes, to 2.8;
 //   - four of these warps take each 128-deep block sum out of tensor memory, one
 //     weight row a thread, and add it, scaled, to fp32 registers.
-// 64 tokens to 8 of 256 experts, H = 7168, I = 2048 (9.76 GB): 1.51 ms, 6.4 TB/s; 8
-// tokens (2.5 GB): 0.375 ms, 6.6 TB/s.  One token to 8 experts, H = 2048, I = 768
-// (38 MB): 15 us, of which 2 pass before the first weights are asked for and 1 at
-// each of the two waits between the kernels.
+// 64 tokens to 8 of 256 experts, H = 7168, I = 2048 (9.76 GB): 1.48 ms, 6.6 TB/s; 8
+// tokens (2.5 GB): 0.37 ms in a graph, 0.385 call by call, 6.5 to 6.7 TB/s.  One
+// token to 8 experts, H = 2048, I = 768 (38 MB): 16 us, of which 2 pass before the
+// first weights are asked for and 1 at each of the two waits between the kernels.
 // Partial sums over parts of a row's length are added where they are read, in
 // the order of the parts.
 #include "expert.cuh"

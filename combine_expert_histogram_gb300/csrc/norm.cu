@@ -9,8 +9,8 @@
 // through shared memory), scaled, and written from the same registers; the
 // 8-bit output takes the group maxima by xor-shuffles over the 16 lanes that
 // hold a 1x128 group (4 lanes for 1x32), so nothing is read twice.  HBM-bound:
-// 16384 rows of 7168 with the residual, bf16 and 8-bit rows (1.06 GB) take 155 us,
-// 6.8 TB/s; one such row 2.3 us.
+// 16384 rows of 7168 with the residual, bf16 and 8-bit rows (1.06 GB) take 154 to
+// 155 us, 6.8 TB/s; one such row 2.4 us.
 #include "ep_common.cuh"
 #include "fp8.cuh"
 
