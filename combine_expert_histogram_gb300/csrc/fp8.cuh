@@ -25,9 +25,10 @@ __device__ __forceinline__ float group_scale(float amax) {
 // inv is 1 / s to the nearest, q the quotient's estimate, q * s - x its error, which
 // one fused product-and-sum gives exactly, and q - error * inv rounds to the quotient
 // (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000",
-// IBM J. Res. Dev. 34, 1990).  The error is inexact only where the quotient is far
-// below E4M3's smallest value.  Zeros keep their sign.  An infinite scale (of an
-// infinite amax) leaves 0 of finite x and NaN of the others, as a division does.
+// IBM J. Res. Dev. 34, 1990); compared with the division for every significand of s
+// at every tie of E4M3.  The error is inexact only where the quotient is far below
+// E4M3's smallest value.  Zeros keep their sign.  An infinite scale (of an infinite
+// amax) leaves 0 of finite x and NaN of the others, as a division does.
 __device__ __forceinline__ float group_quotient(float x, float s, float inv) {
     const float q = x * inv, err = fmaf(q, fminf(s, 3.402823466e38f), -x);
     return fmaf(-err, inv, q);
