@@ -5,13 +5,20 @@ package is its Python binding.  Build the library with
 ``python -m combine_expert_histogram_gb300.build``.
 """
 from .binding import (  # noqa: F401
+    AttnWorkspace,
     EPError,
+    KvCache,
+    KvSeqs,
     Layout,
     MoeWorkspace,
+    ep_attn_decode,
+    ep_attn_decode_workspace_bytes,
+    ep_attn_prefill,
     ep_combine,
     ep_dispatch,
     ep_expert_gemm,
     ep_expert_swiglu,
+    ep_kv_append,
     ep_layout,
     ep_layout_workspace_bytes,
     ep_masked_repack,
@@ -21,6 +28,9 @@ from .binding import (  # noqa: F401
     ep_rows_capacity,
     ep_scale_cols,
     load_library,
+    new_attn_workspace,
+    new_kv_cache,
+    new_kv_seqs,
     new_layout,
     new_moe_workspace,
     status_str,

@@ -19,7 +19,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libep.so")
 
 (EP_OK, EP_ERR_INVALID_ARG, EP_ERR_CAPACITY, EP_ERR_BAD_EXPERT_ID, EP_ERR_CUDA, EP_ERR_UNSUPPORTED,
- EP_ERR_TIMEOUT) = range(7)
+ EP_ERR_TIMEOUT, EP_ERR_BAD_PAGE) = range(8)
 LAYOUT_KIND = {"contig": 0, "masked": 1}
 QUANT = {"none": 0, "fp8_f32": 1, "fp8_ue8m0": 2, "mxfp8": 3, "fp8_ue8m0_mn": 4}
 MAX_TOPK, MAX_EXPERTS, MAX_ALIGN = 32, 1024, 128
@@ -50,6 +50,35 @@ class _Layout(ctypes.Structure):
     ]
 
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("quant", ctypes.c_int32),
+        ("page_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+    ]
+
+
+class _KvSeqs(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int32),
+        ("num_tokens", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("block_table", ctypes.c_void_p),
+        ("kv_len", ctypes.c_void_p),
+        ("q_start", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 EXPORTS = ("ep_status_str", "ep_rows_capacity", "ep_scale_cols", "ep_scale_words",
@@ -57,7 +86,8 @@ EXPORTS = ("ep_status_str", "ep_rows_capacity", "ep_scale_cols", "ep_scale_words
            "ep_layout", "ep_dispatch", "ep_layout_dispatch", "ep_combine", "ep_masked_repack",
            "ep_layout_noalloc", "ep_selftest_bounded_wait", "ep_selftest_cluster_wait",
            "ep_rank_layout", "ep_rank_expand", "ep_route_topk", "ep_rmsnorm", "ep_expert_gemm",
-           "ep_expert_swiglu", "ep_moe_decode", "ep_moe_decode_workspace_bytes")
+           "ep_expert_swiglu", "ep_moe_decode", "ep_moe_decode_workspace_bytes", "ep_kv_append",
+           "ep_attn_decode", "ep_attn_decode_workspace_bytes", "ep_attn_prefill")
 NOALLOC_SCRATCH_BYTES = 256 * 1024
 
 
@@ -115,6 +145,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ep_moe_decode_workspace_bytes.argtypes = [I32] * 5
     L.ep_moe_decode.restype = ctypes.c_int
     L.ep_moe_decode.argtypes = [P, P, Q, P, P, I32, I32, I32, I32, I32, P, P, P, P, P, P, P, SZ, P]
+    F, CP, SP = ctypes.c_float, ctypes.POINTER(_KvCache), ctypes.POINTER(_KvSeqs)
+    L.ep_kv_append.restype = ctypes.c_int
+    L.ep_kv_append.argtypes = [CP, SP, P, I64, I32, P, I64, P, I64, P, I32, I32, I32, P, I64, P]
+    L.ep_attn_decode_workspace_bytes.restype = SZ
+    L.ep_attn_decode_workspace_bytes.argtypes = [I32] * 4
+    L.ep_attn_decode.restype = ctypes.c_int
+    L.ep_attn_decode.argtypes = [CP, SP, P, I64, I32, F, I32, I32, P, P, P, SZ, P]
+    L.ep_attn_prefill.restype = ctypes.c_int
+    L.ep_attn_prefill.argtypes = [CP, SP, P, I64, I32, F, I32, I32, P, P, P]
     if path == LIB_PATH:
         _lib = L
     return L
@@ -799,4 +838,244 @@ def ep_moe_decode(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
     po = _want(out, "out", (_BF16,), shape, dev)
     _call(lib.ep_moe_decode, "ep_moe_decode", dev, px, psx, QUANT[quant], pi, pw, T, K, E, H, inter,
           p13, ps13, p2, ps2, po, pst, pws, nbytes, _on(stream, dev))
+    return out
+
+
+# ------------------------------------------------------ paged cache, attention
+@dataclass(frozen=True)
+class KvCache:
+    """The paged cache of keys and values of one attention layer.
+
+    k and v are [num_pages, page_size, num_kv_heads, head_dim], bf16 (quant "none") or
+    E4M3 ("fp8_ue8m0", with k_scales and v_scales uint8 [num_pages, num_kv_heads,
+    page_size]); both may be strided alike (pages stored by head, a slice of a larger
+    pool), with contiguous rows of head_dim.  The handle keeps its tensors' addresses: make
+    another one for other tensors.
+    """
+
+    k: torch.Tensor
+    v: torch.Tensor
+    quant: str = "none"
+    k_scales: Optional[torch.Tensor] = None
+    v_scales: Optional[torch.Tensor] = None
+    _c: _KvCache = field(default=None, init=False, repr=False, compare=False)
+
+    def __post_init__(self):
+        k, v = self.k, self.v
+        dev = _rows_of(k, "k", 4)
+        if self.quant not in ("none", "fp8_ue8m0"):
+            raise EPError(EP_ERR_UNSUPPORTED if self.quant in QUANT else EP_ERR_INVALID_ARG,
+                          f"a cache of {self.quant} rows")
+        plain = self.quant == "none"
+        for t, name in ((k, "k"), (v, "v")):
+            if t.dtype not in ((_BF16,) if plain else _E4M3) or t.shape != k.shape \
+                    or t.get_device() != dev:
+                _refuse(t, name, (_BF16,) if plain else _E4M3, k.shape, dev)
+        pages, rows, heads, D = k.shape
+        if any(n > 1 and a != b for n, a, b in zip(k.shape, k.stride(), v.stride())) \
+                or (D > 1 and k.stride(3) != 1):
+            raise ValueError("k and v need the same strides, and contiguous rows of head_dim")
+        # a dimension of one has no stride of its own
+        sp, sr, sh = (st if n > 1 else D for n, st in zip(k.shape[:3], k.stride()))
+        pks = pvs = None
+        if not plain:
+            pks, pvs = (_want(t, name, (torch.uint8,), (pages, heads, rows), dev) for t, name in
+                        ((self.k_scales, "k_scales"), (self.v_scales, "v_scales")))
+        elif self.k_scales is not None or self.v_scales is not None:
+            raise ValueError('scales belong to "fp8_ue8m0", not to bf16 rows')
+        object.__setattr__(self, "_c", _KvCache(pages, rows, heads, D, QUANT[self.quant], sp, sr, sh,
+                                                k.data_ptr(), v.data_ptr(), pks, pvs))
+
+
+def new_kv_cache(num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
+                 quant: str = "none", device=None) -> KvCache:
+    """Allocate a cache (zeros), stored by head: the rows of a head in a page are contiguous."""
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    shape = (num_pages, num_kv_heads, page_size, head_dim)
+    kind = _BF16 if quant == "none" else torch.uint8
+    k, v = (torch.zeros(shape, dtype=kind, device=dev).transpose(1, 2) for _ in range(2))
+    if quant == "none":
+        return KvCache(k, v)
+    ks, vs = (torch.zeros(shape[:3], dtype=torch.uint8, device=dev) for _ in range(2))
+    return KvCache(k, v, quant, ks, vs)
+
+
+@dataclass(frozen=True)
+class KvSeqs:
+    """The sequences of a call: block_table int32 [B, max_pages], kv_len int32 [B] (tokens in
+    the cache, the call's own included), q_start int32 [B+1] (first row of each sequence) or None
+    (one row a sequence).  Calls read the arrays on the device, and raise errors into status,
+    which none resets.  The handle keeps its tensors' addresses: write new lengths into them,
+    or make another one."""
+
+    block_table: torch.Tensor
+    kv_len: torch.Tensor
+    q_start: Optional[torch.Tensor]
+    status: torch.Tensor
+    _c: _KvSeqs = field(default=None, init=False, repr=False, compare=False)
+
+    def __post_init__(self):
+        dev = _rows_of(self.block_table, "block_table")
+        B, P = self.block_table.shape
+        table = _want(self.block_table, "block_table", (_I32,), (B, P), dev)
+        lens = _want(self.kv_len, "kv_len", (_I32,), (B,), dev)
+        start = None
+        if self.q_start is not None:
+            start = _want(self.q_start, "q_start", (_I32,), (B + 1,), dev)
+        status = _want(self.status, "status", (_I32,), (1,), dev)
+        object.__setattr__(self, "_c", _KvSeqs(B, B, P, table, lens, start, status))
+
+    def check_status(self) -> None:
+        """Synchronise and raise EPError if a call recorded a device-side error."""
+        st = int(self.status.item())
+        if st != EP_OK:
+            raise EPError(st, "device status")
+
+    def _struct(self, tokens: int) -> _KvSeqs:
+        """The C struct of a call of `tokens` rows."""
+        c = self._c
+        return _KvSeqs(c.num_seqs, tokens, c.max_pages, c.block_table, c.kv_len, c.q_start, c.status)
+
+
+def new_kv_seqs(block_table: torch.Tensor, kv_len: torch.Tensor,
+                q_start: Optional[torch.Tensor] = None) -> KvSeqs:
+    """The sequences' handle, with a status word of its own."""
+    return KvSeqs(block_table, kv_len, q_start,
+                  torch.zeros(1, dtype=torch.int32, device=block_table.device))
+
+
+def _head_rows(t: torch.Tensor, name: str, shape, dev: int):
+    """(address, elements between tokens) of bf16 head rows [T, heads, D], each token's contiguous."""
+    if t is None or t.dtype != _BF16 or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, (_BF16,), shape, dev)
+    T, heads, D = shape
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (heads > 1 and st[1] != D):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.data_ptr(), st[0] if T > 1 else heads * D
+
+
+def _cache_and_seqs(cache: KvCache, seqs: KvSeqs, t: torch.Tensor, name: str):
+    """(device index, C cache, C sequences, T, heads of t) of a call with the rows t."""
+    dev = _rows_of(t, name, 3)
+    if cache.k.get_device() != dev or seqs.kv_len.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, the cache on {cache.k.device}, the sequences on "
+                         f"{seqs.kv_len.device}")
+    return dev, cache._c, seqs._struct(t.shape[0]), t.shape[0], t.shape[1]
+
+
+def ep_kv_append(cache: KvCache, seqs: KvSeqs, k: torch.Tensor, v: torch.Tensor,
+                 cos_sin: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                 q_out: Optional[torch.Tensor] = None, interleaved: bool = False,
+                 stream=None) -> Optional[torch.Tensor]:
+    """Rotate and append the new tokens' keys and values (bf16 [T, num_kv_heads, head_dim], tokens
+    may be strided) to the cache; returns q (bf16 [T, num_q_heads, head_dim]) rotated, None without.
+
+    cos_sin is fp32 [positions, rotary_dim]: a position's cosines, then its sines; None: no
+    rotation.  q_out may be q itself.  Rows of q_out that belong to no sequence are not written.
+    """
+    lib = load_library()
+    dev, c, s, T, Hkv = _cache_and_seqs(cache, seqs, k, "k")
+    D = c.head_dim
+    pk, sk = _head_rows(k, "k", (T, c.num_kv_heads, D), dev)
+    pv, sv = _head_rows(v, "v", (T, c.num_kv_heads, D), dev)
+    pq = po = pc = None
+    sq = so = Hq = R = positions = 0
+    if q is not None:
+        _rows_of(q, "q", 3)
+        Hq = q.shape[1]
+        pq, sq = _head_rows(q, "q", (T, Hq, D), dev)
+        if q_out is None:
+            q_out = _empty((T, Hq, D), _BF16, dev, stream)
+        po, so = _head_rows(q_out, "q_out", (T, Hq, D), dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if cos_sin is not None:
+        _rows_of(cos_sin, "cos_sin")
+        positions, R = cos_sin.shape
+        pc = _want(cos_sin, "cos_sin", (_F32,), (positions, R), dev)
+        if R == 0:
+            pc = None
+    _call(lib.ep_kv_append, "ep_kv_append", dev, ctypes.byref(c), ctypes.byref(s), pq, sq, Hq, pk,
+          sk, pv, sv, pc, R, positions, interleaved, po, so, _on(stream, dev))
+    return q_out
+
+
+@dataclass
+class AttnWorkspace:
+    """Scratch of ep_attn_decode calls that do not overlap."""
+
+    scratch: torch.Tensor
+
+
+def ep_attn_decode_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                                   head_dim: int) -> int:
+    return int(load_library().ep_attn_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads,
+                                                             head_dim))
+
+
+def _attn_scratch_bytes(dev, *shape) -> int:
+    """ep_attn_decode_workspace_bytes for device `dev`: it depends on the number of SMs."""
+    with torch.cuda.device(dev):
+        n = ep_attn_decode_workspace_bytes(*shape)
+    if n == 0:
+        raise EPError(EP_ERR_INVALID_ARG, "ep_attn_decode shape")
+    return n
+
+
+def new_attn_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                       device=None) -> AttnWorkspace:
+    """Allocate a workspace for ep_attn_decode calls of this shape, or of fewer sequences."""
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    n = _attn_scratch_bytes(dev, num_seqs, num_q_heads, num_kv_heads, head_dim)
+    return AttnWorkspace(torch.empty(n, dtype=torch.uint8, device=dev))
+
+
+def _attn_args(cache, seqs, q, scale, out, lse, stream):
+    """Shared arguments of the attention: (device index, C cache, C sequences, q's address, its
+    stride, heads, scale, out, out's address, lse's address)."""
+    dev, c, s, T, Hq = _cache_and_seqs(cache, seqs, q, "q")
+    D = c.head_dim
+    pq, sq = _head_rows(q, "q", (T, Hq, D), dev)
+    if out is None:
+        out = _empty((T, Hq, D), _BF16, dev, stream)
+    po = _want(out, "out", (_BF16,), (T, Hq, D), dev)
+    pl = _want(lse, "lse", (_F32,), (T, Hq), dev) if lse is not None else None
+    return dev, c, s, pq, sq, Hq, D ** -0.5 if scale is None else scale, out, po, pl
+
+
+def ep_attn_decode(cache: KvCache, seqs: KvSeqs, q: torch.Tensor, scale: Optional[float] = None,
+                   window: int = 0, sinks: int = 0, workspace: Optional[AttnWorkspace] = None,
+                   out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """Attention of one new token a sequence over the cache: q and the result bf16
+    [B, num_q_heads, head_dim].
+
+    scale defaults to head_dim ** -0.5.  With a window a query sees its last ``window`` keys (its
+    own included) and the first ``sinks``.  lse, if given, takes the logarithm of each row's sum
+    of exponentials.  seqs has no q_start: row b is sequence b's.
+    """
+    lib = load_library()
+    dev, c, s, pq, sq, Hq, scale, out, po, pl = _attn_args(cache, seqs, q, scale, out, lse, stream)
+    if workspace is None:
+        n = _attn_scratch_bytes(dev, s.num_seqs, Hq, c.num_kv_heads, c.head_dim)
+        workspace = AttnWorkspace(_empty(n, torch.uint8, dev, stream))
+    ws = workspace.scratch
+    nbytes = ws.numel()
+    pws = _want(ws, "workspace.scratch", (torch.uint8,), (nbytes,), dev)
+    _call(lib.ep_attn_decode, "ep_attn_decode", dev, ctypes.byref(c), ctypes.byref(s), pq, sq, Hq,
+          scale, window, sinks, po, pl, pws, nbytes, _on(stream, dev))
+    return out
+
+
+def ep_attn_prefill(cache: KvCache, seqs: KvSeqs, q: torch.Tensor, scale: Optional[float] = None,
+                    window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention of prompts, or of their next chunks, over the cache that already holds
+    their keys and values: q and the result bf16 [T, num_q_heads, head_dim].  Arguments as for
+    ep_attn_decode.  Rows of the result that belong to no sequence are not written."""
+    lib = load_library()
+    dev, c, s, pq, sq, Hq, scale, out, po, pl = _attn_args(cache, seqs, q, scale, out, lse, stream)
+    _call(lib.ep_attn_prefill, "ep_attn_prefill", dev, ctypes.byref(c), ctypes.byref(s), pq, sq, Hq,
+          scale, window, sinks, po, pl, _on(stream, dev))
     return out

@@ -179,6 +179,7 @@ const char *ep_status_str(ep_status_t s) {
         case EP_ERR_CUDA: return "EP_ERR_CUDA: a CUDA launch failed";
         case EP_ERR_UNSUPPORTED: return "EP_ERR_UNSUPPORTED";
         case EP_ERR_TIMEOUT: return "EP_ERR_TIMEOUT: a device-side copy did not complete in time";
+        case EP_ERR_BAD_PAGE: return "EP_ERR_BAD_PAGE: a page id outside [0, num_pages) or a position past a table";
     }
     return "unknown ep_status_t";
 }

@@ -1,0 +1,96 @@
+// What the paged cache's kernels share: their arguments, the visible keys of a
+// query, the cache's addresses.
+#pragma once
+
+#include "ep_common.cuh"
+#include "fp8.cuh"
+
+namespace ep {
+
+// The cache, checked by the C ABI.  Strides in bytes.
+struct KvArgs {
+    uint8_t *k, *v;              // bf16 or E4M3
+    uint8_t *k_scales, *v_scales;  // E8M0 [pages, Hkv, page_size]; nullptr: bf16 rows
+    int64_t page_stride, row_stride, head_stride;
+    int pages, page_size, Hkv, D;
+};
+
+// The sequences.
+struct SeqArgs {
+    const int32_t *table;    // [B, max_pages]
+    const int32_t *kv_len;   // [B]
+    const int32_t *q_start;  // [B+1], or nullptr: token b is sequence b's
+    int32_t *status;
+    int B, T, max_pages;
+};
+
+struct AttnArgs {
+    KvArgs kv;
+    SeqArgs seq;
+    const uint16_t *q;  // bf16 [T, Hq, D], tokens q_stride elements apart
+    int64_t q_stride;
+    int Hq;
+    float scale;
+    int window, sinks;  // window 0: none
+    uint16_t *out;      // bf16 [T, Hq, D]
+    float *lse;         // [T, Hq] or nullptr
+};
+
+// Tokens of sequence b among the call's rows, and its length; both are whatever the
+// device arrays hold, brought into range (a length past the table raises
+// EP_ERR_BAD_PAGE).
+struct Span {
+    int first, n, len;
+};
+__device__ __forceinline__ Span seq_span(const SeqArgs &s, int page_size, int b) {
+    Span r;
+    r.len = max(ld_dep(s.kv_len + b), 0);
+    const int most = s.max_pages * page_size;
+    if (r.len > most) {
+        raise_status(s.status, EP_ERR_BAD_PAGE);
+        r.len = most;
+    }
+    if (s.q_start) {
+        r.first = min(max(ld_dep(s.q_start + b), 0), s.T);
+        r.n = min(max(ld_dep(s.q_start + b + 1), r.first), s.T) - r.first;
+    } else {
+        r.first = b;
+        r.n = 1;
+    }
+    return r;
+}
+
+// Sequence of token t, or -1: the last b with q_start[b] <= t, if t is its.
+__device__ __forceinline__ int seq_of(const SeqArgs &s, int t) {
+    if (!s.q_start) return t < s.B ? t : -1;
+    int lo = 0, hi = s.B;  // q_start[lo] <= t < q_start[hi], if t is any sequence's
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (ld_dep(s.q_start + mid) <= t) lo = mid; else hi = mid;
+    }
+    return s.B > 0 && ld_dep(s.q_start + lo) <= t && t < ld_dep(s.q_start + lo + 1) ? lo : -1;
+}
+
+// The page of a table's entry, -1 (and EP_ERR_BAD_PAGE) if the cache has no such page.
+__device__ __forceinline__ int page_of(const KvArgs &kv, const SeqArgs &s, int b, int entry) {
+    const int p = ld_dep(s.table + (int64_t)b * s.max_pages + entry);
+    if ((unsigned)p < (unsigned)kv.pages) return p;
+    raise_status(s.status, EP_ERR_BAD_PAGE);
+    return -1;
+}
+
+// The value of an E8M0 scale (255: NaN).
+__device__ __forceinline__ float scale_value(uint32_t e) {
+    return e == 255 ? __uint_as_float(0x7fffffffu) : ue8m0_value(e);
+}
+
+cudaError_t launch_kv_append(const KvArgs &kv, const SeqArgs &seq, const uint16_t *q,
+                             int64_t q_stride, int Hq, const uint16_t *k, int64_t k_stride,
+                             const uint16_t *v, int64_t v_stride, const float *cos_sin, int R,
+                             int positions, bool interleaved, uint16_t *q_out,
+                             int64_t q_out_stride, cudaStream_t stream);
+cudaError_t launch_attn_decode(const AttnArgs &a, void *workspace, cudaStream_t stream);
+size_t attn_decode_workspace(int B, int Hq, int Hkv, int D);
+cudaError_t launch_attn_prefill(const AttnArgs &a, cudaStream_t stream);
+
+}  // namespace ep

@@ -16,6 +16,8 @@
  *   ep_expert_gemm, ep_expert_swiglu  the experts' block-scaled E4M3 products
  *                     on a layout's rows.
  *   ep_moe_decode     the whole layer for a few tokens.
+ *   ep_kv_append, ep_attn_decode, ep_attn_prefill  the attention before it: a paged
+ *                     cache of keys and values, and what writes and reads it.
  *
  * Sources (the pages describe a library integration, not kernels):
  *   [PR-24443]  SGLang PR "moe: add DeepEP V2 ElasticBuffer support to MoE
@@ -74,7 +76,9 @@
  *     the copies it issued and returns; if even that drain runs out, a copy
  *     may still be landing in a CTA that has exited, and the context should
  *     be treated as suspect).
- *     Read it back after the stream completes.
+ *     Read it back after the stream completes.  The attention's calls raise
+ *     EP_ERR_BAD_PAGE and EP_ERR_TIMEOUT into the word of their ep_kv_seqs_t,
+ *     which the caller sets to 0 and no call resets.
  *   - bf16 means IEEE binary32's upper 16 bits; FP8 means E4M3FN (OCP OFP8).
  */
 #ifndef EP_H_
@@ -96,8 +100,10 @@ typedef enum ep_status {
     EP_ERR_BAD_EXPERT_ID = 3, /* device-side only: id outside [-1, E)          */
     EP_ERR_CUDA = 4,          /* a CUDA launch failed                           */
     EP_ERR_UNSUPPORTED = 5,   /* valid request this build does not implement    */
-    EP_ERR_TIMEOUT = 6        /* device-side only: a bulk copy a kernel waited
+    EP_ERR_TIMEOUT = 6,       /* device-side only: a bulk copy a kernel waited
                                  for did not complete within about a second    */
+    EP_ERR_BAD_PAGE = 7       /* device-side only: a page id outside [0, num_pages), or
+                                 a position past a block table or a rotation table */
 } ep_status_t;
 
 typedef enum ep_layout_kind {
@@ -569,6 +575,134 @@ ep_status_t ep_moe_decode(const void *x, const void *x_scales, ep_quant_t quant,
                           const void *w13, const float *w13_scales, const void *w2,
                           const float *w2_scales, void *out, int32_t *status, void *workspace,
                           size_t workspace_bytes, ep_stream_t stream);
+
+/*
+ * The paged cache of keys and values of one attention layer.  Row (p, r, h), the
+ * head_dim values of head h in row r of page p, starts at element
+ * p*page_stride + r*row_stride + h*head_stride of k, and at the same of v, so pages
+ * may be stored by row or by head.  Position j of a sequence is row j % page_size of
+ * the page that its block table names at j / page_size; several sequences may
+ * share pages that no call writes.
+ */
+typedef struct ep_kv_cache {
+    int32_t num_pages;     /* >= 1                                                  */
+    int32_t page_size;     /* rows a page, a multiple of 8 in [8, EP_KV_MAX_PAGE]    */
+    int32_t num_kv_heads;  /* in [1, EP_ATTN_MAX_HEADS]                             */
+    int32_t head_dim;      /* 64 or 128 (others: EP_ERR_UNSUPPORTED)                 */
+    int32_t quant;         /* EP_QUANT_NONE: bf16 rows; EP_QUANT_FP8_UE8M0: E4M3 rows
+                              with one power-of-two scale each (others:
+                              EP_ERR_UNSUPPORTED)                                   */
+    int64_t page_stride, row_stride, head_stride; /* in elements; bytes that are
+                              multiples of 16, > 0 and < 2^40                       */
+    void *k, *v;           /* device, 16-byte aligned                               */
+    uint8_t *k_scales, *v_scales; /* EP_QUANT_FP8_UE8M0: device E8M0
+                              [num_pages, num_kv_heads, page_size], 8-byte aligned, a
+                              row's values being q * 2^(byte - 127), or NaN where the
+                              byte is 255; EP_QUANT_NONE: NULL                       */
+} ep_kv_cache_t;
+
+/*
+ * The sequences of a call.  kv_len[b] counts the tokens of sequence b in the cache,
+ * the call's own included: its n_b tokens have the positions kv_len[b] - n_b ..
+ * kv_len[b] - 1.  Their rows in the call's q, k, v and outputs are
+ * q_start[b] .. q_start[b+1] - 1; without q_start sequence b has the one row b.
+ * Rows that no sequence owns (before q_start[0], from q_start[num_seqs] on) are
+ * neither read nor written.  All of it is read on the device when the kernels run,
+ * so a captured call follows the arrays.  Arrays that are no such lists (negative or
+ * falling numbers) give results without meaning, but no access outside the arrays;
+ * negative lengths count as 0, rows at negative positions (n_b > kv_len[b]) are skipped by
+ * ep_kv_append and see no key in the attention.
+ */
+typedef struct ep_kv_seqs {
+    int32_t num_seqs;    /* B >= 0                                                   */
+    int32_t num_tokens;  /* T >= 0, rows of q, k, v; B without q_start                */
+    int32_t max_pages;   /* columns of block_table, >= 1; times page_size < 2^31      */
+    const int32_t *block_table; /* device [B, max_pages]; entries that no token of the
+                              call needs (past a sequence's end, before its window)
+                              are not read                                         */
+    const int32_t *kv_len;   /* device [B]; more than max_pages * page_size raises
+                                EP_ERR_BAD_PAGE and counts as that                   */
+    const int32_t *q_start;  /* device [B+1], rising, or NULL                       */
+    int32_t *status;         /* device [1], see above                               */
+} ep_kv_seqs_t;
+
+#define EP_KV_MAX_PAGE 4096
+#define EP_ATTN_MAX_HEADS 1024
+
+/*
+ * ep_kv_append -- the new tokens' keys and values into the cache, with the rotation
+ * of queries and keys by position on the way.
+ *
+ *   k, v       device bf16 [T, num_kv_heads, head_dim], 16-byte aligned, a token's heads
+ *              contiguous, tokens k_stride / v_stride elements apart (multiples
+ *              of 8; a fused projection's columns).
+ *   q          device bf16 [T, num_q_heads, head_dim], tokens q_stride apart, rotated into
+ *              q_out (tokens q_out_stride apart; may be q itself with the same
+ *              stride); NULL with num_q_heads 0: keys and values only.
+ *   cos_sin    device fp32 [positions, rotary_dim], 16-byte aligned: the cosines, then the
+ *              sines, of a position's rotary_dim / 2 angles; NULL with rotary_dim 0: no
+ *              rotation.
+ *   rotary_dim R: the first R channels of a head are rotated, a multiple of 16 in
+ *              [0, head_dim]; channel pairs (i, i + R/2), or (2i, 2i+1) if interleaved.
+ *
+ *   a' = a cos - b sin,  b' = b cos + a sin   for the pair i of a row, by angle i, in
+ * fp32 with each product and sum rounded (no fused multiply-add).  q_out and bf16 rows
+ * of the cache are bf16_rn of the result.  EP_QUANT_FP8_UE8M0: each row of k and of v
+ * by ep_dispatch's rule for that mode, with the row as the group, from the fp32 values;
+ * a row with an infinity or a NaN is stored as NaN (scale byte 255).
+ *
+ * A token whose position is past the rotation table or the block table, or whose page
+ * is not the cache's, is skipped and raises EP_ERR_BAD_PAGE.  Two tokens of a call
+ * must not share a place in the cache (one of the two is then stored, or parts of both).
+ */
+ep_status_t ep_kv_append(const ep_kv_cache_t *cache, const ep_kv_seqs_t *seqs, const void *q,
+                         int64_t q_stride, int32_t num_q_heads, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, const float *cos_sin,
+                         int32_t rotary_dim, int32_t positions, int32_t interleaved, void *q_out,
+                         int64_t q_out_stride, ep_stream_t stream);
+
+/*
+ * ep_attn_decode -- attention of one new token a sequence over the cache.
+ *
+ *   seqs       without q_start: row b of q, out and lse is sequence b's.
+ *   q          device bf16 [B, num_q_heads, head_dim], 16-byte aligned, tokens q_stride
+ *              elements apart (a multiple of 8).
+ *   num_q_heads  a multiple of num_kv_heads, at most EP_ATTN_MAX_HEADS; heads
+ *              [g*G, (g+1)*G), G = num_q_heads / num_kv_heads, share key head g.
+ *   scale      of the products q.k, finite and > 0.
+ *   window     > 0: a query at position i sees the keys i - window < j <= i and the
+ *              first `sinks` keys; 0: all keys j <= i (sinks is then ignored).
+ *   sinks      >= 0.
+ *   out        device bf16 [B, num_q_heads, head_dim], 16-byte aligned.
+ *   lse        device fp32 [B, num_q_heads] or NULL.
+ *   workspace  device scratch, 16-byte aligned, of at least
+ *              ep_attn_decode_workspace_bytes() with this device current, clobbered.
+ *              Holds nothing between calls.  Calls (or replayed graphs) that share one
+ *              must not overlap on the GPU.
+ *
+ *   out = bf16_rn( sum over visible j of p_j v_j / sum of p_j ),  p_j = exp(scale * q.k_j)
+ *   lse = log( sum of p_j )
+ * with the sums in fp32.  A query that sees no key (kv_len[b] = 0) gets +0, and -infinity
+ * in lse.  Cache rows that a query does not see, whatever they hold, do not matter to it.  A
+ * page that is needed and not the cache's raises EP_ERR_BAD_PAGE; its rows count as zeros.
+ */
+size_t ep_attn_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim);
+ep_status_t ep_attn_decode(const ep_kv_cache_t *cache, const ep_kv_seqs_t *seqs, const void *q,
+                           int64_t q_stride, int32_t num_q_heads, float scale, int32_t window,
+                           int32_t sinks, void *out, float *lse, void *workspace,
+                           size_t workspace_bytes, ep_stream_t stream);
+
+/*
+ * ep_attn_prefill -- attention of prompts, or of their next chunks, over the cache, to
+ * which ep_kv_append has added the chunk: every token sees the keys up to its own
+ * position, within the window and the first keys if one is given.  Arguments and
+ * results as for ep_attn_decode with q_start given (or not: one token a sequence), and
+ * no workspace.  lse is [T, num_q_heads].
+ */
+ep_status_t ep_attn_prefill(const ep_kv_cache_t *cache, const ep_kv_seqs_t *seqs, const void *q,
+                            int64_t q_stride, int32_t num_q_heads, float scale, int32_t window,
+                            int32_t sinks, void *out, float *lse, ep_stream_t stream);
 
 #ifdef __cplusplus
 }
