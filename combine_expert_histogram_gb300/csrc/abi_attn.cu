@@ -1,7 +1,6 @@
 // C ABI of the paged cache and its attention (declared in include/ep.h): argument
 // validation and the launches.  Every host-detectable error returns before anything is
 // enqueued.
-#include <limits.h>
 #include <math.h>
 
 #include "attn.cuh"
@@ -37,7 +36,7 @@ ep_status_t check_cache(const ep_kv_cache_t *c) {
 
 ep_status_t check_seqs(const ep_kv_seqs_t *s, const ep_kv_cache_t *c) {
     if (!s || s->num_seqs < 0 || s->num_tokens < 0 || s->max_pages < 1 ||
-        (int64_t)s->max_pages * c->page_size > INT_MAX)
+        (int64_t)s->max_pages * c->page_size > EP_KV_MAX_LEN)
         return EP_ERR_INVALID_ARG;
     if (!s->q_start && s->num_tokens != s->num_seqs) return EP_ERR_INVALID_ARG;
     if (!s->status || !aligned(s->status, 4)) return EP_ERR_INVALID_ARG;
@@ -85,7 +84,7 @@ ep_status_t check_attn(const ep_kv_cache_t *c, const ep_kv_seqs_t *s, const void
     st = check_heads(Hq, c->num_kv_heads);
     if (st != EP_OK) return st;
     if (!(scale > 0.0f) || isinf(scale) || window < 0 || sinks < 0) return EP_ERR_INVALID_ARG;
-    if ((int64_t)s->num_tokens * Hq > INT_MAX) return EP_ERR_INVALID_ARG;
+    if ((int64_t)s->num_tokens * Hq > EP_ATTN_MAX_ROWS) return EP_ERR_INVALID_ARG;
     if (no_rows(s)) return EP_OK;
     if (check_rows(q, q_stride, Hq, c->head_dim) != EP_OK || !out || !aligned(out, 16) ||
         !aligned(lse, 4))
@@ -96,8 +95,8 @@ ep_status_t check_attn(const ep_kv_cache_t *c, const ep_kv_seqs_t *s, const void
     a->q_stride = q_stride;
     a->Hq = Hq;
     a->scale = scale;
-    a->window = window;
-    a->sinks = window ? sinks : 0;
+    a->window = window > EP_KV_MAX_LEN ? 0 : window;  // all keys
+    a->sinks = a->window ? (sinks < EP_KV_MAX_LEN ? sinks : EP_KV_MAX_LEN) : 0;
     a->out = static_cast<uint16_t *>(out);
     a->lse = lse;
     return EP_OK;
@@ -124,7 +123,7 @@ ep_status_t ep_kv_append(const ep_kv_cache_t *c, const ep_kv_seqs_t *s, const vo
     if (st != EP_OK) return st;
     if (Hq < 0 || Hq > EP_ATTN_MAX_HEADS || positions < 0) return EP_ERR_INVALID_ARG;
     if (rotary_dim < 0 || rotary_dim % 16 != 0 || rotary_dim > c->head_dim) return EP_ERR_INVALID_ARG;
-    if ((int64_t)s->num_tokens * (Hq + 2 * c->num_kv_heads) > INT_MAX) return EP_ERR_INVALID_ARG;
+    if ((int64_t)s->num_tokens * (Hq + 2 * c->num_kv_heads) > EP_ATTN_MAX_ROWS) return EP_ERR_INVALID_ARG;
     if (no_rows(s)) return EP_OK;
     if (check_rows(k, k_stride, c->num_kv_heads, c->head_dim) != EP_OK ||
         check_rows(v, v_stride, c->num_kv_heads, c->head_dim) != EP_OK)

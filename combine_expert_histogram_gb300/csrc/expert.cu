@@ -447,7 +447,7 @@ EncodeTiled encoder() {
 }  // namespace
 
 bool encode_bytes(CUtensorMap *map, const void *p, int rank, const int64_t *dims,
-                  const int64_t *strides, const int *box) {
+                  const int64_t *strides, const int *box, CUtensorMapSwizzle swizzle) {
     const EncodeTiled fn = encoder();
     if (!fn) return false;
     cuuint64_t d[5], s[4];
@@ -459,7 +459,7 @@ bool encode_bytes(CUtensorMap *map, const void *p, int rank, const int64_t *dims
         if (i + 1 < rank) s[i] = (cuuint64_t)strides[i];
     }
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(p), d, s, b,
-              ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

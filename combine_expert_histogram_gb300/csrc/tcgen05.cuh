@@ -168,9 +168,10 @@ __device__ __forceinline__ bool mbar_wait_fast(uint64_t *bar, uint32_t parity,
 }
 
 // Tensor map of `rank` dimensions of bytes (strides of all but the first, in
-// bytes) in 128-byte swizzle; out-of-range bytes of a box read as zero.  False
-// if the driver refuses it.
+// bytes) in 128-byte swizzle (or the given one); out-of-range bytes of a box read as
+// zero.  False if the driver refuses it.
 bool encode_bytes(CUtensorMap *map, const void *p, int rank, const int64_t *dims,
-                  const int64_t *strides, const int *box);
+                  const int64_t *strides, const int *box,
+                  CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 }  // namespace ep

@@ -139,6 +139,10 @@ typedef enum ep_route {
 #define EP_MAX_EXPERT_COLS 65536     /* largest output width of an expert's product */
 #define EP_MOE_DECODE_MAX_ENTRIES 1024 /* ep_moe_decode: largest T*K                 */
 #define EP_MOE_DECODE_MAX_DIM 16384    /* ep_moe_decode: largest hidden and inner    */
+#define EP_KV_MAX_PAGE 4096          /* largest page of a cache, in rows             */
+#define EP_KV_MAX_LEN (1 << 30)      /* longest sequence of a block table            */
+#define EP_ATTN_MAX_HEADS 1024       /* most query heads, and key heads              */
+#define EP_ATTN_MAX_ROWS (1 << 30)   /* most tokens times heads of a call            */
 
 /*
  * The layout ("handle"): shape plus caller-owned device arrays.  ep_layout()
@@ -615,8 +619,11 @@ typedef struct ep_kv_cache {
  */
 typedef struct ep_kv_seqs {
     int32_t num_seqs;    /* B >= 0                                                   */
-    int32_t num_tokens;  /* T >= 0, rows of q, k, v; B without q_start                */
-    int32_t max_pages;   /* columns of block_table, >= 1; times page_size < 2^31      */
+    int32_t num_tokens;  /* T >= 0, rows of q, k, v; B without q_start; T times the heads
+                            of a call (ep_kv_append: q, k and v) at most
+                            EP_ATTN_MAX_ROWS                                       */
+    int32_t max_pages;   /* columns of block_table, >= 1; times page_size at most
+                            EP_KV_MAX_LEN                                          */
     const int32_t *block_table; /* device [B, max_pages]; entries that no token of the
                               call needs (past a sequence's end, before its window)
                               are not read                                         */
@@ -626,8 +633,6 @@ typedef struct ep_kv_seqs {
     int32_t *status;         /* device [1], see above                               */
 } ep_kv_seqs_t;
 
-#define EP_KV_MAX_PAGE 4096
-#define EP_ATTN_MAX_HEADS 1024
 
 /*
  * ep_kv_append -- the new tokens' keys and values into the cache, with the rotation
