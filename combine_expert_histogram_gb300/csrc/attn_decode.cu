@@ -3,42 +3,54 @@
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - m),  m the largest so far
 //
 // in one pass over the visible keys.  HBM-bound: a cache row is read once for all query
-// heads that share it, up to 16 of them, which are the rows of a 16 x 8 x 16 matrix
-// instruction (few rows: the 128-row instructions of tensor memory would be idle for
-// 7/8; the memory's rate leaves these 1/4 used).
+// heads that share it, up to 16 of them, which are the columns of 16 x 8 x 16 matrix
+// instructions with 16 keys, then 16 channels of the values, as the rows (so few columns
+// would leave 7/8 of a product in tensor memory unused).
 //
-// The work, 16 keys of one key head being a unit, is one list over sequences and heads, of
-// which every block takes an equal run, wherever sequences begin and end.  In it each of
-// eight warps has every eighth unit, a ring of its own in shared memory that
-// asynchronous copies fill ahead, across the ends of heads and sequences, and sums of its own
+// The work, a unit being 8 KB of one key head's keys and values, is one list over sequences
+// and heads, of which every block takes an equal run, wherever sequences begin and end.  In
+// it each of eight warps has every eighth unit, a ring of its own in shared memory that tiled
+// TMA loads fill ahead, across the ends of heads and sequences, and sums of its own
 // (m, l, o), which the warps add at the end of a head.  A head that several blocks share
 // leaves its sums in the workspace, and a second kernel adds them in order.
 #include "attn.cuh"
+#include "tcgen05.cuh"
 
 namespace ep {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kUnit = 16;            // keys of a unit
-constexpr int kHeads = 16;           // query heads of an item
-constexpr int kLeast = 2 * kWarps;   // units a block takes at least
+constexpr int kHeads = 16;           // query heads of an item at most
+constexpr int kLeast = kWarps;       // units a block takes at least
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, bool FP8>
 struct Cfg {
     static constexpr int kRow = FP8 ? D : 2 * D;             // bytes of a cache row
+    static constexpr int kUnit = 4096 / kRow;                // keys of a unit
+    static constexpr int kGroups = kUnit / 8;                // of 8 rows, which a page holds together
+    static constexpr int kPitch = kRow < 128 ? kRow : 128;   // a panel's row
+    static constexpr int kPanels = kRow / kPitch;
+    static constexpr int kPanel = kUnit * kPitch;
     static constexpr int kTile = kUnit * kRow;               // keys, then values
-    static constexpr int kStage = 2 * kTile + (FP8 ? 32 : 0);  // and their scales
-    static constexpr int kStages = (FP8 ? 20480 : 24576) / (2 * kTile);
-    static constexpr int kRing = kWarps * kStages * kStage;
-    static constexpr int kMerge = kWarps * 8 * D * 4;  // eight rows of every warp's o
-    static constexpr int kSmem = kRing + kMerge;
+    static constexpr int kStages = 3;
+    static constexpr int kRing = kWarps * kStages * 2 * kTile;
+    static constexpr int kScales = FP8 ? kWarps * kStages * 2 * kUnit : 0;
+    static constexpr int kMerge = kWarps * 8 * D * 4;  // eight heads of every warp's o
+    static constexpr int kSmem = kRing + kMerge + kScales + 1024;  // and Shared
 };
 
 // What a block leaves of a head that others share: [block][first or last][row].
 struct Part {
     float m, l;  // in log2 units
 };
+struct Shared {
+    uint64_t full[kWarps][3];
+    int64_t sums[kWarps], found_at;
+    int found_b, fail;
+    Part part[kWarps][8];
+};
+static_assert(sizeof(Shared) <= 1024, "what Cfg::kSmem has for it");
 __host__ __device__ constexpr size_t ws_parts(int blocks) { return (size_t)blocks * 16; }
 __host__ __device__ constexpr size_t ws_sums(int blocks) {
     return ws_parts(blocks) + (size_t)blocks * 2 * kHeads * sizeof(Part);
@@ -49,15 +61,18 @@ __host__ __device__ constexpr size_t ws_bytes(int blocks, int D) {
 
 struct DecodeArgs {
     AttnArgs a;
-    int G, groups, items;  // query heads a key head, groups of 16 of them, items a sequence
+    int G, groups, heads, items;  // query heads a key head, in `groups` of up to `heads`; items a sequence
+    int box;                      // cache rows of a TMA box
     uint8_t *ws;
 };
 
-// The visible keys of a sequence's newest token: [lo, L) and [0, S), S <= lo, as n units.
+// The visible keys of a sequence's newest token: [lo, L) and [0, S), S <= lo, as n units of
+// U keys: ns of the first keys, then those from unit `first` on.
 struct Keys {
-    int L, lo, S, n, first;  // units [0, n - ...) of the first keys, then from unit `first` on
-    int ns;
+    int L, lo, S, n, ns, first;
+    __device__ __forceinline__ bool sees(int j) const { return j < L && (j >= lo || j < S); }
 };
+template <int U>
 __device__ __forceinline__ Keys visible(const AttnArgs &a, int b) {
     Keys k;
     k.L = max(ld_dep(a.seq.kv_len + b), 0);
@@ -69,14 +84,15 @@ __device__ __forceinline__ Keys visible(const AttnArgs &a, int b) {
     k.lo = a.window ? max(k.L - a.window, 0) : 0;
     k.S = a.sinks;
     if (k.S >= k.lo) k.lo = k.S = 0;
-    k.first = k.lo / kUnit;
-    k.ns = min((k.S + kUnit - 1) / kUnit, k.first);
+    k.first = k.lo / U;
+    k.ns = min((k.S + U - 1) / U, k.first);
     // a sequence without a key has one unit that sees none
-    k.n = max(k.ns + (k.L + kUnit - 1) / kUnit - k.first, 1);
+    k.n = max(k.ns + (k.L + U - 1) / U - k.first, 1);
     return k;
 }
 
 // A place in the list of work: an item (sequence, key head, group of query heads).
+template <int U>
 struct Place {
     int b, item;
     int64_t at;  // the item's first unit in the list
@@ -85,29 +101,14 @@ struct Place {
         at += k.n;
         if (++item == d.items) {
             item = 0;
-            if (++b < d.a.seq.B) k = visible(d.a, b);
+            if (++b < d.a.seq.B) k = visible<U>(d.a, b);
         }
     }
     __device__ __forceinline__ int key(int unit) const {
-        return (unit < k.ns ? unit : unit - k.ns + k.first) * kUnit;
+        return (unit < k.ns ? unit : unit - k.ns + k.first) * U;
     }
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(live ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool live) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
-                 "r"(live ? 8 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 template <bool T>
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     if constexpr (T)
@@ -120,6 +121,12 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                      : "r"(addr)
                      : "memory");
+}
+// The transpose of an 8 x 8 matrix of 16-bit values, two of a row a lane.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     uint4 v;
@@ -145,6 +152,13 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+        : "memory");
+}
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -155,23 +169,25 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Two E4M3 values (the low and the high half's bytes) -> two fp16, exactly.
-__device__ __forceinline__ uint32_t half_pair(uint32_t two) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
-    return r;
+// Four E4M3 values -> two pairs of fp16, exactly.
+__device__ __forceinline__ void half_pairs(uint32_t four, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
 }
 
 // A warp's stream of units: what is to be loaded next.
 template <int D, bool FP8>
 struct Loader {
     using C = Cfg<D, FP8>;
-    Place p;
+    Place<C::kUnit> p;
     int64_t x0, x1;       // the block's run
     int u, end;           // the warp's next unit in the item, the piece's end in it
-    int left;             // units whose pages the lanes hold
-    int64_t off, scale;   // lane: the row of half lane & 1 of unit u + 8 (lane / 2), or -1
-    int slot;
+    int left, held;       // units of which the lanes (still) hold the pages
+    int page, row;        // lane: of box lane % (boxes a unit); the page past the last: none
+    int slot, behind;     // slot whose scales are not yet in shared memory, or -1
+    uint2 scales;         // lane: eight of those
     bool more;
 
     __device__ __forceinline__ void piece(int warp) {
@@ -179,110 +195,112 @@ struct Loader {
         end = (int)min((int64_t)p.k.n, x1 - p.at);
         left = 0;
     }
-    __device__ __forceinline__ void pages(const DecodeArgs &d, int lane) {
+    __device__ __forceinline__ void pages(const DecodeArgs &d, int boxes, int lane) {
         const AttnArgs &a = d.a;
-        const int unit = u + kWarps * (lane / 2);
-        off = -1;
-        scale = 0;
+        const int at = lane / boxes, unit = u + kWarps * at;
+        page = a.kv.pages;
+        row = 0;
         if (unit < end) {
-            const int key = p.key(unit) + 8 * (lane & 1);
-            if (key < p.k.L && (key + 8 > p.k.lo || key < p.k.S)) {
-                const int entry = key / a.kv.page_size, row = key - entry * a.kv.page_size;
-                const int page = page_of(a.kv, a.seq, p.b, entry);
-                if (page >= 0) {
-                    off = page * a.kv.page_stride + row * a.kv.row_stride;
-                    scale = (int64_t)page * a.kv.Hkv * a.kv.page_size + row;
-                }
+            const int key = p.key(unit) + d.box * (lane - at * boxes);
+            if (key < p.k.L && (key + d.box > p.k.lo || key < p.k.S)) {
+                const int entry = key / a.kv.page_size;
+                const int q = page_of(a.kv, a.seq, p.b, entry);
+                if (q >= 0) page = q;
+                row = key - entry * a.kv.page_size;
             }
         }
-        left = 16;
+        left = held;
     }
-    // Ask for the next unit, if there is one; one group of copies either way.
-    __device__ __forceinline__ void issue(const DecodeArgs &d, uint32_t ring, int warp, int lane) {
+    __device__ __forceinline__ void store_scales(uint32_t to, int lane) {
+        if (FP8 && behind >= 0) {
+            if (lane < 2 * C::kGroups)
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to + behind * 2 * C::kUnit + 8 * lane),
+                             "r"(scales.x), "r"(scales.y)
+                             : "memory");
+            behind = -1;
+        }
+    }
+    // Ask for the next unit, if there is one.
+    __device__ __forceinline__ void issue(const DecodeArgs &d, const CUtensorMap *kmap, const CUtensorMap *vmap,
+                                          uint32_t ring, uint32_t scale_ring, uint64_t *full, int warp, int lane) {
         const AttnArgs &a = d.a;
+        store_scales(scale_ring, lane);
         while (more && u >= end) {
             p.next(d);
             more = p.at < x1;
             if (more) piece(warp);
         }
-        if (more) {
-            if (left == 0) pages(d, lane);
-            constexpr int CH = C::kRow / 16, RP = 32 / CH;  // chunks a row, rows a pass
-            const int h = p.item / d.groups, key = p.key(u), from = 2 * (16 - left);
-            const int64_t head = h * a.kv.head_stride;
-            const uint32_t st = ring + slot * C::kStage;
-            const int c = lane % CH;
-            int64_t at[2];
+        if (!more) return;
+        const int boxes = C::kUnit / d.box;
+        if (left == 0) pages(d, boxes, lane);
+        const int h = p.item / d.groups, from = boxes * (held - left);
+        const uint32_t st = ring + slot * 2 * C::kTile;
+        const bool leader = elect_one();
+        if (leader) expect_bytes(full + slot, 2 * C::kTile);
+        for (int x = 0; x < boxes; ++x) {
+            const int px = __shfl_sync(kFullMask, page, from + x), rx = __shfl_sync(kFullMask, row, from + x);
+            if (leader) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) at[i] = __shfl_sync(kFullMask, off, from + i);
-#pragma unroll
-            for (int i = 0; i < kUnit / RP; ++i) {
-                const int r = i * RP + lane / CH, j = key + r, half = i * RP / 8;
-                const bool live = at[half] >= 0 && j < p.k.L && (j >= p.k.lo || j < p.k.S);
-                const int64_t o = live ? at[half] + head + (r & 7) * a.kv.row_stride + 16 * c : 0;
-                // the swizzles that make this unit's reads free of bank conflicts
-                const int ck = FP8 ? (D == 128 ? c ^ ((r & 1) << 2) : c) : c ^ (r & 7);
-                const int cv = FP8 ? (D == 128 ? c ^ (r & 6) : c) : c ^ (r & 7);
-                copy16(st + r * C::kRow + 16 * ck, a.kv.k + o, live);
-                copy16(st + C::kTile + r * C::kRow + 16 * cv, a.kv.v + o, live);
+                for (int n = 0; n < C::kPanels; ++n) {
+                    const uint32_t to = st + n * C::kPanel + x * d.box * C::kPitch;
+                    tma_load_4d(to, kmap, 128 * n, h, rx, px, full + slot);
+                    tma_load_4d(to + C::kTile, vmap, 128 * n, h, rx, px, full + slot);
+                }
             }
-            if constexpr (FP8) {
-                const int64_t s = __shfl_sync(kFullMask, scale, from + (lane & 1));
-                const bool live = (lane & 1 ? at[1] : at[0]) >= 0;
-                if (lane < 4)
-                    copy8(st + 2 * C::kTile + 8 * lane,
-                          (lane < 2 ? a.kv.k_scales : a.kv.v_scales) +
-                              (live ? s + (int64_t)h * a.kv.page_size : 0),
-                          live);
-            }
-            u += kWarps;
-            --left;
         }
+        if constexpr (FP8) {
+            const int r = 8 * (lane % C::kGroups), x = r / d.box;
+            const int px = __shfl_sync(kFullMask, page, from + x), rx = __shfl_sync(kFullMask, row, from + x);
+            scales = make_uint2(0, 0);
+            if (lane < 2 * C::kGroups && px < a.kv.pages) {
+                const uint8_t *src = lane < C::kGroups ? a.kv.k_scales : a.kv.v_scales;
+                const int64_t at = ((int64_t)px * a.kv.Hkv + h) * a.kv.page_size + rx + (r - x * d.box);
+                asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(scales.x), "=r"(scales.y) : "l"(src + at) : "memory");
+            }
+            behind = slot;
+        }
+        u += kWarps;
+        --left;
         slot = slot + 1 == C::kStages ? 0 : slot + 1;
-        copy_commit();
     }
 };
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs d) {
+// NH: tiles of eight query heads.
+template <int D, bool FP8, int NH>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const __grid_constant__ DecodeArgs d) {
     using C = Cfg<D, FP8>;
+    // all of the block's shared memory: the ring (the swizzle wants 1024-byte alignment; static
+    // arrays would push it off), eight heads' sums, the scales
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int64_t sums[kWarps];
-    __shared__ int64_t found_at;
-    __shared__ int found_b;
-    __shared__ Part part[kWarps][kHeads];
+    Shared &sh = *reinterpret_cast<Shared *>(smem + C::kRing + C::kMerge + C::kScales);
     const AttnArgs &a = d.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t ring = smem_addr(smem) + warp * C::kStages * C::kStage;
+    const uint32_t ring = smem_addr(smem) + warp * C::kStages * 2 * C::kTile;
     float *merge = reinterpret_cast<float *>(smem + C::kRing);
+    const uint32_t scale_ring = smem_addr(smem) + C::kRing + C::kMerge + warp * C::kStages * 2 * C::kUnit;
+    uint64_t *full = sh.full[warp];
     int4 *record = reinterpret_cast<int4 *>(d.ws);
     Part *parts = reinterpret_cast<Part *>(d.ws + ws_parts(gridDim.x));
     float *out_sums = reinterpret_cast<float *>(d.ws + ws_sums(gridDim.x));
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWarps * C::kStages; ++i) mbar_init(&sh.full[0][i], 1);
+        sh.fail = 0;
+        mbar_init_fence();
+        tma_prefetch_map(&kmap);
+        tma_prefetch_map(&vmap);
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the kernel that joins may take its place beside this one
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the block's run of the list ----
-    int64_t total = 0;
-    for (int b0 = 0; b0 < a.seq.B; b0 += kThreads) {
+    // Exclusive sums of the sequences' units, kThreads at a time; the first ones are kept.
+    int64_t total = 0, excl0 = 0, n0 = 0;
+    auto scan = [&](int b0, int64_t &n, int64_t &excl) {
         const int b = b0 + threadIdx.x;
-        int64_t n = b < a.seq.B ? visible(a, b).n : 0;
-#pragma unroll
-        for (int s = 16; s; s >>= 1) n += __shfl_xor_sync(kFullMask, n, s);
-        total += n;
-    }
-    if (lane == 0) sums[warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) total += sums[i];
-    total *= d.items;
-    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kLeast);
-    const int64_t x0 = blockIdx.x * per, x1 = min(x0 + per, total);
-    if (threadIdx.x == 0) record[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (x0 >= x1) return;
-    int64_t before = 0;
-    for (int b0 = 0;; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        const int64_t n = b < a.seq.B ? (int64_t)visible(a, b).n * d.items : 0;
+        n = b < a.seq.B ? (int64_t)visible<C::kUnit>(a, b).n * d.items : 0;
         int64_t incl = n;
 #pragma unroll
         for (int s = 1; s < 32; s <<= 1) {
@@ -290,330 +308,395 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs d)
             if (lane >= s) incl += o;
         }
         __syncthreads();
-        if (lane == 31) sums[warp] = incl;
+        if (lane == 31) sh.sums[warp] = incl;
         __syncthreads();
         int64_t all = 0, below = 0;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
             if (i == warp) below = all;
-            all += sums[i];
+            all += sh.sums[i];
         }
-        incl += before + below;
-        if (x0 >= incl - n && x0 < incl) {
-            found_b = b;
-            found_at = incl - n;
+        excl = incl - n + below;
+        return all;
+    };
+    for (int b0 = 0; b0 < a.seq.B; b0 += kThreads) {
+        int64_t n, excl;
+        total += scan(b0, n, excl);
+        if (b0 == 0) n0 = n, excl0 = excl;
+    }
+    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kLeast);
+    const int64_t x0 = blockIdx.x * per, x1 = min(x0 + per, total);
+    if (threadIdx.x == 0) record[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (x0 >= x1) return;
+    int64_t before = 0;
+    for (int b0 = 0;; b0 += kThreads) {
+        int64_t n = n0, excl = excl0, all = total;
+        if (a.seq.B > kThreads) all = scan(b0, n, excl);
+        if (x0 >= before + excl && x0 < before + excl + n) {
+            sh.found_b = b0 + threadIdx.x;
+            sh.found_at = before + excl;
         }
         before += all;
         if (before > x0 || b0 + kThreads >= a.seq.B) break;
     }
     __syncthreads();
-    Place p;
-    p.b = found_b;
-    p.k = visible(a, p.b);
-    p.item = (int)((x0 - found_at) / p.k.n);
-    p.at = found_at + (int64_t)p.item * p.k.n;
+    Place<C::kUnit> p;
+    p.b = sh.found_b;
+    p.k = visible<C::kUnit>(a, p.b);
+    p.item = (int)((x0 - sh.found_at) / p.k.n);
+    p.at = sh.found_at + (int64_t)p.item * p.k.n;
 
     Loader<D, FP8> load;
     load.p = p;
     load.x0 = x0;
     load.x1 = x1;
+    load.held = 32 / (C::kUnit / d.box);
     load.slot = 0;
+    load.behind = -1;
     load.more = true;
     load.piece(warp);
 #pragma unroll 1
-    for (int i = 0; i < C::kStages - 1; ++i) load.issue(d, ring, warp, lane);
+    for (int i = 0; i < C::kStages - 1; ++i) load.issue(d, &kmap, &vmap, ring, scale_ring, full, warp, lane);
 
     const int row = lane >> 2, c = lane & 3;  // of the matrix fragments
     int slot = 0;
+    uint32_t phase = 0;
     for (; p.at < x1; p.next(d)) {
         const int h = p.item / d.groups, g = p.item - h * d.groups;
-        const int q0 = h * d.G + g * kHeads, heads = min(kHeads, d.G - g * kHeads);
-        // ---- queries: the rows `row` and `row + 8` of the first factor ----
-        uint32_t q[D / 16][4];
-        float to_log2[2];  // logits in log2 units, of these rows
+        const int q0 = h * d.G + g * d.heads, heads = min(d.heads, d.G - g * d.heads);
+        // ---- queries: head `row` of each tile as the second factor's column ----
+        uint32_t q[NH][D / 16][2];
+        float to_log2[NH][2];  // logits in log2 units, of the heads 2 c and 2 c + 1
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int r = row + 8 * half;
+        for (int n = 0; n < NH; ++n) {
+            const int r = row + 8 * n;
             const uint16_t *src = a.q + p.b * a.q_stride + (int64_t)(q0 + r) * D;
-            to_log2[half] = a.scale * kLog2e;
+            to_log2[n][0] = to_log2[n][1] = a.scale * kLog2e;
             if constexpr (!FP8) {
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        q[s][half + 2 * i] =
-                            r < heads ? (uint32_t)ld_dep(reinterpret_cast<const int32_t *>(src + 16 * s + 8 * i + 2 * c)) : 0u;
+                        q[n][s][i] = r < heads ? (uint32_t)ld_dep(reinterpret_cast<const int32_t *>(src + 16 * s + 8 * i + 2 * c)) : 0u;
             } else {
-                // a lane's E4M3 key bytes are 16 neighbours, so the channels that a step
-                // takes are 4 s .. 4 s + 3 of each lane's 16; as fp16 next to 2^8 at
-                // most, which is exact down to 2^-32 of the row's largest
-                uint32_t w[D / 64][8];
+                // a lane's E4M3 key bytes are D / 4 neighbours, and a step takes four of each
+                // lane's; as fp16 next to 2^8 at most, which is exact down to 2^-32 of the
+                // head's largest
+                uint32_t w[D / 8];
                 float amax = 0.0f;
 #pragma unroll
-                for (int j = 0; j < D / 64; ++j)
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint4 v = r < heads ? ld_dep_v4(src + D / 4 * c + 8 * i) : make_uint4(0, 0, 0, 0);
+                    w[4 * i] = v.x;
+                    w[4 * i + 1] = v.y;
+                    w[4 * i + 2] = v.z;
+                    w[4 * i + 3] = v.w;
+                }
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 v = r < heads ? ld_dep_v4(src + 64 * j + 16 * c + 8 * i)
-                                                  : make_uint4(0, 0, 0, 0);
-                        w[j][4 * i] = v.x;
-                        w[j][4 * i + 1] = v.y;
-                        w[j][4 * i + 2] = v.z;
-                        w[j][4 * i + 3] = v.w;
-                    }
-#pragma unroll
-                for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[j][i])), fabsf(bf16_hi(w[j][i]))));
+                for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
                 amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
                 // up = 2^k with amax * up in [2^7, 2^8), within what fp32 has of both
                 const int e = min(max((int)(__float_as_uint(amax) >> 23), 8), 254);
-                const float up = __uint_as_float((uint32_t)min(254 - e + 7, 254) << 23);
-                to_log2[half] *= __uint_as_float((uint32_t)max(e - 7, 0) << 23);
+                const float up = __uint_as_float((uint32_t)(261 - e) << 23);
+                const float down = __uint_as_float((uint32_t)max(e - 7, 0) << 23);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) to_log2[n][i] *= __shfl_sync(kFullMask, down, 4 * (2 * c + i));
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t v = w[s / 4][2 * (s % 4) + i];
-                        q[s][half + 2 * i] = pack_half(bf16_lo(v) * up, bf16_hi(v) * up);
-                    }
+                    for (int i = 0; i < 2; ++i) q[n][s][i] = pack_half(bf16_lo(w[2 * s + i]) * up, bf16_hi(w[2 * s + i]) * up);
             }
         }
-        float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-        float mv[2] = {-INFINITY, -INFINITY};  // FP8: largest logit with its value's scale
+        // of the heads 2 c and 2 c + 1: largest logit, sum of probabilities (this lane's keys'),
+        // FP8: largest logit with its value's scale
+        float o[NH][D / 16][4], m[NH][2], l[NH][2], mv[NH][2];
 #pragma unroll
-        for (int t = 0; t < D / 8; ++t)
+        for (int n = 0; n < NH; ++n) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[t][i] = 0.0f;
+            for (int i = 0; i < 2; ++i) m[n][i] = mv[n][i] = -INFINITY, l[n][i] = 0.0f;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][t][i] = 0.0f;
+        }
 
         const int piece0 = (int)(max(x0, p.at) - p.at), piece1 = (int)min((int64_t)p.k.n, x1 - p.at);
         for (int u = piece0 + warp; u < piece1; u += kWarps) {
-            copy_wait<C::kStages - 2>();
+            if (!__all_sync(kFullMask, mbar_wait_fast(full + slot, (phase >> slot) & 1, &sh.fail))) {
+                sh.fail = 1;
+                load.more = false;
+            }
+            phase ^= 1u << slot;
             __syncwarp();
-            load.issue(d, ring, warp, lane);
-            const uint32_t st = ring + slot * C::kStage, sv = st + C::kTile;
+            load.issue(d, &kmap, &vmap, ring, scale_ring, full, warp, lane);
+            const uint32_t st = ring + slot * 2 * C::kTile, sv = st + C::kTile;
+            const uint32_t sc = scale_ring + slot * 2 * C::kUnit;
             slot = slot + 1 == C::kStages ? 0 : slot + 1;
+            const int key = p.key(u);
+            const bool whole = key + C::kUnit <= p.k.L && key >= p.k.lo;
+            if (!whole) {  // values that are not seen may be anything, and 0 * NaN is NaN
+                for (int x = lane; x < C::kTile / 16; x += 32) {
+                    const int r = x * 16 % C::kPanel / C::kPitch;
+                    if (!p.k.sees(key + r))
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(sv + 16 * x), "r"(0) : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
 
-            // ---- logits of 16 rows and 16 keys ----
-            float s[2][4];
+            // ---- logits, 16 keys a tile ----
+            constexpr int KT = C::kUnit / 16;
+            float s[KT][NH][4];  // keys row, row + 8; heads 2 c, 2 c + 1
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < KT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[t][i] = 0.0f;
-            float ev[2][2];  // FP8: log2 of the values' scales, of the lane's four keys
+                for (int n = 0; n < NH; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[t][n][i] = 0.0f;
+            float ev[KT][2];  // FP8: log2 of the values' scales
             if constexpr (!FP8) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const int r = (lane & 7) + ((lane >> 4) << 3), ch = 2 * k + ((lane >> 3) & 1);
-                    uint32_t b[4];
-                    ldmatrix4<false>(b, st + r * C::kRow + 16 * (ch ^ (r & 7)));
-                    mma<false>(s[0], q[k], b[0], b[1]);
-                    mma<false>(s[1], q[k], b[2], b[3]);
-                }
+                for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) {
+                        const int r = 16 * t + (lane & 15), ch = 2 * k + (lane >> 4);
+                        uint32_t f[4];
+                        ldmatrix4<false>(f, st + (ch >> 3) * C::kPanel + r * 128 + 16 * ((ch & 7) ^ (r & 7)));
+#pragma unroll
+                        for (int n = 0; n < NH; ++n) mma<false>(s[t][n], f, q[n][k][0], q[n][k][1]);
+                    }
             } else {
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-                    for (int j = 0; j < D / 64; ++j) {
-                        const int r = 8 * t + row, ch = 4 * j + c;
-                        const uint4 v = lds16(st + r * C::kRow + 16 * (D == 128 ? ch ^ ((r & 1) << 2) : ch));
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    for (int t = 0; t < KT; ++t) {
+                        const int r = 16 * t + row, ch = D / 64 * c + j;
+                        uint32_t at = st + r * C::kPitch + 16 * ch;
+                        at ^= (at >> 3) & (D == 128 ? 0x70 : 0x30);  // the TMA's swizzle, by the address
+                        const uint4 x = lds16(at), y = lds16(at + 8 * C::kPitch);
+                        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma<true>(s[t], q[4 * j + i], half_pair(w[i]), half_pair(w[i] >> 16));
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t f[4];
+                            half_pairs(xw[i], f[0], f[2]);
+                            half_pairs(yw[i], f[1], f[3]);
+#pragma unroll
+                            for (int n = 0; n < NH; ++n) mma<true>(s[t][n], f, q[n][4 * j + i][0], q[n][4 * j + i][1]);
+                        }
                     }
-                const uint32_t sc = st + 2 * C::kTile;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    uint32_t ek, evb;  // two keys' bytes
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(ek) : "r"(sc + 8 * t + 2 * c) : "memory");
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(evb) : "r"(sc + 16 + 8 * t + 2 * c) : "memory");
+                for (int t = 0; t < KT; ++t)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float f = scale_value((ek >> 8 * i) & 255);
-                        s[t][i] *= f;
-                        s[t][2 + i] *= f;
-                        const uint32_t e = (evb >> 8 * i) & 255;
+                        uint32_t ek, e;
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(ek) : "r"(sc + 16 * t + 8 * i + row) : "memory");
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(sc + C::kUnit + 16 * t + 8 * i + row) : "memory");
+                        const float f = scale_value(ek);
+#pragma unroll
+                        for (int n = 0; n < NH; ++n) {
+                            s[t][n][2 * i] *= f;
+                            s[t][n][2 * i + 1] *= f;
+                        }
                         ev[t][i] = e == 255 ? __uint_as_float(0x7fffffffu) : (float)((int)e - 127);
                     }
-                }
             }
-            const int key = p.key(u);
-            const bool whole = key + kUnit <= p.k.L && key >= p.k.lo;
-            float top[2] = {m[0], m[1]}, topv[2] = {mv[0], mv[1]};
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < KT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = key + 8 * t + 2 * c + (i & 1);
-                    s[t][i] *= to_log2[i >> 1];
-                    if (!whole && !(j < p.k.L && (j >= p.k.lo || j < p.k.S))) s[t][i] = -INFINITY;
-                    top[i >> 1] = fmaxf(top[i >> 1], s[t][i]);
-                    if constexpr (FP8)
-                        topv[i >> 1] = fmaxf(topv[i >> 1], s[t][i] == -INFINITY ? -INFINITY : s[t][i] + ev[t][i & 1]);
-                }
+                for (int n = 0; n < NH; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[t][n][i] *= to_log2[n][i & 1];
+            if (!whole) {
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (!p.k.sees(key + 16 * t + 8 * i + row)) {
+                            ev[t][i] = 0.0f;  // the scale may be anything too
+#pragma unroll
+                            for (int n = 0; n < NH; ++n) s[t][n][2 * i] = s[t][n][2 * i + 1] = -INFINITY;
+                        }
+            }
+            float base[NH][2], basev[NH][2];
             bool grown = false;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int n = 0; n < NH; ++n)
 #pragma unroll
-                for (int x = 1; x < 4; x <<= 1) {
-                    top[r] = fmaxf(top[r], __shfl_xor_sync(kFullMask, top[r], x));
-                    if constexpr (FP8) topv[r] = fmaxf(topv[r], __shfl_xor_sync(kFullMask, topv[r], x));
+                for (int i = 0; i < 2; ++i) {
+                    float top = m[n][i], topv = mv[n][i];
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) {
+                        top = fmaxf(top, fmaxf(s[t][n][i], s[t][n][2 + i]));
+                        if constexpr (FP8) topv = fmaxf(topv, fmaxf(s[t][n][i] + ev[t][0], s[t][n][2 + i] + ev[t][1]));
+                    }
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) {
+                        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
+                        if constexpr (FP8) topv = fmaxf(topv, __shfl_xor_sync(kFullMask, topv, x));
+                    }
+                    grown |= top > m[n][i] || (FP8 && topv > mv[n][i]);
+                    base[n][i] = top;
+                    basev[n][i] = topv;
                 }
-                grown |= top[r] > m[r] || (FP8 && topv[r] > mv[r]);
-            }
-            // a row that has seen no key yet subtracts 0 from its -infinities
-            float base[2], basev[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                base[r] = top[r] == -INFINITY ? 0.0f : top[r];
-                basev[r] = topv[r] == -INFINITY ? 0.0f : topv[r];
-            }
             if (__any_sync(kFullMask, grown)) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float f = exp2_fast(m[r] - base[r]);
-                    const float fo = FP8 ? exp2_fast(mv[r] - basev[r]) : f;
-                    l[r] *= f;
+                for (int n = 0; n < NH; ++n)
 #pragma unroll
-                    for (int t = 0; t < D / 8; ++t) {
-                        o[t][2 * r] *= fo;
-                        o[t][2 * r + 1] *= fo;
+                    for (int i = 0; i < 2; ++i) {
+                        // a head that has seen no key yet subtracts 0 from its -infinities
+                        const float f = base[n][i] == -INFINITY ? 1.0f : exp2_fast(m[n][i] - base[n][i]);
+                        const float fo = !FP8 ? f : basev[n][i] == -INFINITY ? 1.0f : exp2_fast(mv[n][i] - basev[n][i]);
+                        l[n][i] *= f;
+#pragma unroll
+                        for (int t = 0; t < D / 16; ++t) {
+                            o[n][t][i] *= fo;
+                            o[n][t][2 + i] *= fo;
+                        }
+                        m[n][i] = base[n][i];
+                        mv[n][i] = basev[n][i];
                     }
-                    m[r] = top[r];
-                    mv[r] = topv[r];
-                }
             }
-            // ---- probabilities, and o += p v ----
-            float w[2][4];
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int n = 0; n < NH; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = exp2_fast(s[t][i] - base[i >> 1]);
-                    l[i >> 1] += e;
+                for (int i = 0; i < 2; ++i) {
+                    if (base[n][i] == -INFINITY) base[n][i] = 0.0f;
                     // the value's scale belongs to the weight: next to 2^10 at most, fp16
-                    w[t][i] = !FP8 ? e
-                              : s[t][i] == -INFINITY ? 0.0f
-                                                     : exp2_fast(s[t][i] + ev[t][i & 1] - basev[i >> 1] + 10.0f);
+                    basev[n][i] = 10.0f - (basev[n][i] == -INFINITY ? 0.0f : basev[n][i]);
                 }
-            if constexpr (!FP8) {
-                // p as two bf16, its own and what that leaves: one would be off by 2^-9 in
-                // every probability, and the products are not what bounds the kernel
-                uint32_t hi[4], lo[4];
+            // ---- probabilities, and o += v p, sixteen keys at a time ----
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x = w[i >> 1][2 * (i & 1)], y = w[i >> 1][2 * (i & 1) + 1];
-                    hi[i] = pack_bf16(x, y);
-                    lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
-                }
+            for (int t = 0; t < KT; ++t) {
+                uint32_t hi[NH][2], lo[NH][2];  // keys 2 c, 2 c + 1 (and + 8) of head `row`
 #pragma unroll
-                for (int t = 0; t < D / 16; ++t) {
-                    const int r = lane & 15, ch = 2 * t + (lane >> 4);
-                    uint32_t b[4];
-                    ldmatrix4<true>(b, sv + r * C::kRow + 16 * (ch ^ (r & 7)));
-                    mma<false>(o[2 * t], hi, b[0], b[1]);
-                    mma<false>(o[2 * t + 1], hi, b[2], b[3]);
-                    mma<false>(o[2 * t], lo, b[0], b[1]);
-                    mma<false>(o[2 * t + 1], lo, b[2], b[3]);
-                }
-            } else {
-                uint32_t pw[4];
+                for (int n = 0; n < NH; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) pw[i] = pack_half(w[i >> 1][2 * (i & 1)], w[i >> 1][2 * (i & 1) + 1]);
-                // the lane's four keys, D / 8 channels from D / 8 * row on: column `row` of
-                // the product's tile t is channel D / 8 * row + t
-                uint32_t v[4][D / 32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 2 * c + (i & 1) + 8 * (i >> 1);
-                    if constexpr (D == 128) {
-                        const uint4 x = lds16(sv + r * C::kRow + 16 * (row ^ (r & 6)));
-                        v[i][0] = x.x;
-                        v[i][1] = x.y;
-                        v[i][2] = x.z;
-                        v[i][3] = x.w;
-                    } else {
-                        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                                     : "=r"(v[i][0]), "=r"(v[i][1])
-                                     : "r"(sv + r * C::kRow + 8 * row)
-                                     : "memory");
+                    for (int i = 0; i < 2; ++i) {
+                        const float x = s[t][n][2 * i], y = s[t][n][2 * i + 1];
+                        const float ex = exp2_fast(x - base[n][0]), ey = exp2_fast(y - base[n][1]);
+                        l[n][0] += ex;
+                        l[n][1] += ey;
+                        if constexpr (FP8) {
+                            hi[n][i] = transposed(pack_half(exp2_fast(x + (ev[t][i] + basev[n][0])),
+                                                            exp2_fast(y + (ev[t][i] + basev[n][1]))));
+                        } else {
+                            // p as two bf16, its own and what that leaves: one would be off by
+                            // 2^-9 in every probability, and the products are not what bounds
+                            // the kernel
+                            const uint32_t w = pack_bf16(ex, ey);
+                            hi[n][i] = transposed(w);
+                            lo[n][i] = transposed(pack_bf16(ex - bf16_lo(w), ey - bf16_hi(w)));
+                        }
                     }
-                }
+                if constexpr (!FP8) {
 #pragma unroll
-                for (int x = 0; x < D / 32; ++x) {
-                    const uint32_t a0 = __byte_perm(v[0][x], v[1][x], 0x5140), a1 = __byte_perm(v[0][x], v[1][x], 0x7362);
-                    const uint32_t b0 = __byte_perm(v[2][x], v[3][x], 0x5140), b1 = __byte_perm(v[2][x], v[3][x], 0x7362);
-                    mma<true>(o[4 * x], pw, half_pair(a0), half_pair(b0));
-                    mma<true>(o[4 * x + 1], pw, half_pair(a0 >> 16), half_pair(b0 >> 16));
-                    mma<true>(o[4 * x + 2], pw, half_pair(a1), half_pair(b1));
-                    mma<true>(o[4 * x + 3], pw, half_pair(a1 >> 16), half_pair(b1 >> 16));
+                    for (int x = 0; x < D / 16; ++x) {
+                        const int r = 16 * t + (lane & 7) + ((lane >> 4) << 3), ch = 2 * x + ((lane >> 3) & 1);
+                        uint32_t f[4];
+                        ldmatrix4<true>(f, sv + (ch >> 3) * C::kPanel + r * 128 + 16 * ((ch & 7) ^ (r & 7)));
+#pragma unroll
+                        for (int n = 0; n < NH; ++n) {
+                            mma<false>(o[n][x], f, hi[n][0], hi[n][1]);
+                            mma<false>(o[n][x], f, lo[n][0], lo[n][1]);
+                        }
+                    }
+                } else {
+                    // the lane's four keys, D / 8 channels from D / 8 * row on: rows `row` and
+                    // `row` + 8 of the product's tile x are channels D / 8 * row + 2 x and + 1
+                    uint32_t v[4][D / 32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 16 * t + 2 * c + (i & 1) + 8 * (i >> 1);
+                        uint32_t at = sv + r * C::kPitch + D / 8 * row;
+                        at ^= (at >> 3) & (D == 128 ? 0x70 : 0x30);
+                        if constexpr (D == 128) {
+                            const uint4 x = lds16(at);
+                            v[i][0] = x.x;
+                            v[i][1] = x.y;
+                            v[i][2] = x.z;
+                            v[i][3] = x.w;
+                        } else {
+                            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                                         : "=r"(v[i][0]), "=r"(v[i][1])
+                                         : "r"(at)
+                                         : "memory");
+                        }
+                    }
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x) {
+                        uint32_t f[4];
+                        half_pairs(__byte_perm(v[0][x], v[1][x], 0x5140), f[0], f[1]);
+                        half_pairs(__byte_perm(v[2][x], v[3][x], 0x5140), f[2], f[3]);
+#pragma unroll
+                        for (int n = 0; n < NH; ++n) mma<true>(o[n][2 * x], f, hi[n][0], hi[n][1]);
+                        half_pairs(__byte_perm(v[0][x], v[1][x], 0x7362), f[0], f[1]);
+                        half_pairs(__byte_perm(v[2][x], v[3][x], 0x7362), f[2], f[3]);
+#pragma unroll
+                        for (int n = 0; n < NH; ++n) mma<true>(o[n][2 * x + 1], f, hi[n][0], hi[n][1]);
+                    }
                 }
             }
         }
 
-        // ---- the warps' sums together, eight rows at a time ----
+        // ---- the warps' sums together, eight heads at a time ----
         const bool starts = p.at >= x0, ends = p.at + p.k.n <= x1;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(kFullMask, l[r], 1);
-            l[r] += __shfl_xor_sync(kFullMask, l[r], 2);
-            if (c == 0) part[warp][row + 8 * r] = {m[r], l[r]};
-            if constexpr (FP8) {  // from the scaled weights' unit to the probabilities'
-                const float f = m[r] == -INFINITY ? 0.0f : exp2_fast(mv[r] - m[r] - 10.0f);
+        for (int n = 0; n < NH; ++n) {
+            if (8 * n >= heads) break;
 #pragma unroll
-                for (int t = 0; t < D / 8; ++t) {
-                    o[t][2 * r] *= f;
-                    o[t][2 * r + 1] *= f;
-                }
-            }
-        }
+            for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (8 * half >= heads) break;
+                for (int x = 4; x < 32; x <<= 1) l[n][i] += __shfl_xor_sync(kFullMask, l[n][i], x);
+                const int r = 2 * c + i;
+                if (row == 0) sh.part[warp][r] = {m[n][i], l[n][i]};
+                // FP8: from the scaled weights' unit to the probabilities'
+                const float f = !FP8 ? 1.0f : m[n][i] == -INFINITY ? 0.0f : exp2_fast(mv[n][i] - m[n][i] - 10.0f);
+                float *to = merge + (warp * 8 + r) * D;
 #pragma unroll
-            for (int t = 0; t < D / 8; ++t) {
-                // FP8: the fragment's column 2 c + i of tile t is channel D/8 (2 c + i) + t
-                float *at = merge + (warp * 8 + row) * D;
-                if constexpr (!FP8) {
-                    *reinterpret_cast<float2 *>(at + ((8 * t + 2 * c) ^ (8 * row & (D - 1)))) =
-                        make_float2(o[t][2 * half], o[t][2 * half + 1]);
-                } else {
-                    at[((D / 8 * 2 * c + t) ^ (8 * row & (D - 1)))] = o[t][2 * half];
-                    at[((D / 8 * (2 * c + 1) + t) ^ (8 * row & (D - 1)))] = o[t][2 * half + 1];
-                }
+                for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        // channel 16 t + row + 8 x, FP8: D/8 row + 2 t + x, whose place is
+                        // 8 (2 t + x) + row there
+                        const int at = 16 * t + row + 8 * x;
+                        to[at ^ (8 * c)] = FP8 ? o[n][t][2 * x + i] * f : o[n][t][2 * x + i];
+                    }
             }
             __syncthreads();
-            const int r = 8 * half + warp;  // this warp's row
+            const int r = 8 * n + warp;  // this warp's head
             if (r < heads) {
+                constexpr int N = D / 32;
                 float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kWarps; ++i) top = fmaxf(top, part[i][r].m);
+                for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sh.part[i][warp].m);
                 const float base = top == -INFINITY ? 0.0f : top;
-                float acc[D / 32];
+                float acc[N];
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
+                for (int x = 0; x < N; ++x) acc[x] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) {
-                    const float f = exp2_fast(part[i][r].m - base);
-                    sum += part[i][r].l * f;
-                    const float *at = merge + (i * 8 + warp) * D + ((D / 32 * lane) ^ (8 * warp & (D - 1)));
+                    const float f = exp2_fast(sh.part[i][warp].m - base);
+                    sum += sh.part[i][warp].l * f;
+                    const float *from = merge + (i * 8 + warp) * D;
 #pragma unroll
-                    for (int x = 0; x < D / 32; ++x) acc[x] += at[x] * f;
+                    for (int x = 0; x < N; ++x) {
+                        const int ch = N * lane + x, at = FP8 ? ch % (D / 8) * 8 + ch / (D / 8) : ch;
+                        acc[x] += from[at ^ (8 * (warp >> 1))] * f;
+                    }
                 }
                 if (starts && ends) {
                     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                     const int64_t to = (int64_t)p.b * a.Hq + q0 + r;
-                    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + to * D + D / 32 * lane);
+                    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + to * D + N * lane);
 #pragma unroll
-                    for (int x = 0; x < D / 32; x += 2) dst[x / 2] = pack_bf16(acc[x] * inv, acc[x + 1] * inv);
+                    for (int x = 0; x < N; x += 2) dst[x / 2] = pack_bf16(acc[x] * inv, acc[x + 1] * inv);
                     if (a.lse && lane == 0) a.lse[to] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
                 } else {
                     const size_t to = (size_t)(2 * blockIdx.x + starts) * kHeads + r;
-                    float *dst = out_sums + to * D + D / 32 * lane;
+                    float *dst = out_sums + to * D + N * lane;
 #pragma unroll
-                    for (int x = 0; x < D / 32; ++x) dst[x] = acc[x];
+                    for (int x = 0; x < N; ++x) dst[x] = acc[x];
                     if (lane == 0) parts[to] = {top, sum};
                 }
             }
@@ -622,13 +705,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs d)
         if (starts && !ends && threadIdx.x == 0)  // the block where a shared head begins
             record[blockIdx.x] = make_int4(p.b, q0, heads, (int)((p.at + p.k.n - 1) / per) - (int)blockIdx.x);
     }
-    copy_wait<0>();
+    __syncwarp();
+    if (sh.fail) {
+        if (threadIdx.x == 0) raise_status(a.seq.status, EP_ERR_TIMEOUT);
+        // a load that was given up may still be landing: wait, again with a limit
+        for (int i = 0; i < C::kStages; ++i) mbar_wait(full + i, ((phase >> i) & 1) ^ 1, nullptr);
+    }
 }
 
-// A shared head's sums, from the block where it begins on: one warp a row.
+// A shared head's sums, from the block where it begins on: two warps a row, each of which
+// takes every second block's.
 template <int D>
-__global__ void __launch_bounds__(kThreads) join_kernel(const DecodeArgs d, int blocks) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(2 * kThreads) join_kernel(const DecodeArgs d, int blocks) {
+    constexpr int N = D / 32, kAhead = 8;  // channels a lane, sums in flight
+    __shared__ float other[8][D + 1];
+    const int warp = (threadIdx.x >> 5) & 7, second = threadIdx.x >> 8, lane = threadIdx.x & 31;
     const int4 *record = reinterpret_cast<const int4 *>(d.ws);
     const Part *parts = reinterpret_cast<const Part *>(d.ws + ws_parts(blocks));
     const float *sums = reinterpret_cast<const float *>(d.ws + ws_sums(blocks));
@@ -636,37 +727,92 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const DecodeArgs d, int 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint4 rec = ld_dep_v4(record + c0);
     const int n = (int)rec.w;  // blocks after the first
-    if (n == 0 || r >= (int)rec.z) return;
+    if (n == 0 || 8 * (int)(blockIdx.x & 1) >= (int)rec.z) return;
+    const bool live = r < (int)rec.z;
     auto at = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0)) * kHeads + r; };
     float top = -INFINITY;
-    for (int i = lane; i <= n; i += 32) top = fmaxf(top, ld_dep(&parts[at(i)].m));
+    if (live)
+        for (int i = lane; i <= n; i += 32) top = fmaxf(top, ld_dep(&parts[at(i)].m));
 #pragma unroll
     for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
     const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, acc[D / 32];
+    float sum = 0.0f, acc[N];
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) acc[x] = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i <= n; ++i) {
-        const float f = exp2_fast(ld_dep(&parts[at(i)].m) - base);
-        sum += ld_dep(&parts[at(i)].l) * f;
+    for (int x = 0; x < N; ++x) acc[x] = 0.0f;
+    if (live) {
+        for (int i0 = second; i0 <= n; i0 += 2 * kAhead) {
+            float v[kAhead][N], m[kAhead], l[kAhead];
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) acc[x] += ld_dep(sums + at(i) * D + D / 32 * lane + x) * f;
+            for (int i = 0; i < kAhead; ++i) {
+                const int j = i0 + 2 * i;
+                m[i] = -INFINITY;
+                l[i] = 0.0f;
+#pragma unroll
+                for (int x = 0; x < N; ++x) v[i][x] = 0.0f;
+                if (j <= n) {
+                    m[i] = ld_dep(&parts[at(j)].m);
+                    l[i] = ld_dep(&parts[at(j)].l);
+                    const float *src = sums + at(j) * D + N * lane;
+                    if constexpr (N == 4) {
+                        const uint4 w = ld_dep_v4(src);
+                        v[i][0] = __uint_as_float(w.x);
+                        v[i][1] = __uint_as_float(w.y);
+                        v[i][2] = __uint_as_float(w.z);
+                        v[i][3] = __uint_as_float(w.w);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < N; ++x) v[i][x] = ld_dep(src + x);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const float f = exp2_fast(m[i] - base);
+                sum += l[i] * f;
+#pragma unroll
+                for (int x = 0; x < N; ++x) acc[x] += v[i][x] * f;
+            }
+        }
+        if (second) {
+#pragma unroll
+            for (int x = 0; x < N; ++x) other[warp][N * lane + x] = acc[x];
+            if (lane == 0) other[warp][D] = sum;
+        }
     }
+    __syncthreads();
+    if (!live || second) return;
+    sum += other[warp][D];
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int64_t to = (int64_t)rec.x * d.a.Hq + rec.y + r;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(d.a.out + to * D + D / 32 * lane);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(d.a.out + to * D + N * lane);
 #pragma unroll
-    for (int x = 0; x < D / 32; x += 2) dst[x / 2] = pack_bf16(acc[x] * inv, acc[x + 1] * inv);
+    for (int x = 0; x < N; ++x) acc[x] = (acc[x] + other[warp][N * lane + x]) * inv;
+#pragma unroll
+    for (int x = 0; x < N; x += 2) dst[x / 2] = pack_bf16(acc[x], acc[x + 1]);
     if (d.a.lse && lane == 0) d.a.lse[to] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
 }
 
 template <int D, bool FP8>
-cudaError_t launch(const DecodeArgs &d, cudaStream_t stream) {
+cudaError_t launch(DecodeArgs d, cudaStream_t stream) {
+    using C = Cfg<D, FP8>;
+    const KvArgs &kv = d.a.kv;
+    d.box = kv.page_size & -kv.page_size;  // a box lies within a page
+    if (d.box > C::kUnit) d.box = C::kUnit;
+    CUtensorMap kmap, vmap;
+    const int64_t dims[4] = {C::kRow, kv.Hkv, kv.page_size, kv.pages};
+    const int64_t strides[3] = {kv.head_stride, kv.row_stride, kv.page_stride};
+    const int box[4] = {C::kPitch, 1, d.box, 1};
+    const auto swizzle = C::kPitch < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!encode_bytes(&kmap, kv.k, 4, dims, strides, box, swizzle) ||
+        !encode_bytes(&vmap, kv.v, 4, dims, strides, box, swizzle))
+        return cudaErrorInvalidValue;
     const int blocks = sm_count();
-    const cudaError_t err = launch_large<decode_kernel<D, FP8>>(blocks, kThreads, Cfg<D, FP8>::kSmem, stream, d);
+    const cudaError_t err =
+        d.heads <= 8
+            ? launch_large<decode_kernel<D, FP8, 1>>(blocks, kThreads, C::kSmem, stream, kmap, vmap, d)
+            : launch_large<decode_kernel<D, FP8, 2>>(blocks, kThreads, C::kSmem, stream, kmap, vmap, d);
     if (err != cudaSuccess) return err;
-    return launch_kernel(join_kernel<D>, 2 * blocks, kThreads, 0, stream, true, d, blocks);
+    return launch_kernel(join_kernel<D>, 2 * blocks, 2 * kThreads, 0, stream, true, d, blocks);
 }
 
 }  // namespace
@@ -678,6 +824,7 @@ cudaError_t launch_attn_decode(const AttnArgs &a, void *workspace, cudaStream_t 
     d.a = a;
     d.G = a.Hq / a.kv.Hkv;
     d.groups = (d.G + kHeads - 1) / kHeads;
+    d.heads = (d.G + d.groups - 1) / d.groups;
     d.items = a.kv.Hkv * d.groups;
     d.ws = static_cast<uint8_t *>(workspace);
     const bool fp8 = a.kv.k_scales != nullptr;
