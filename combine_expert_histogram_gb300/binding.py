@@ -579,6 +579,14 @@ def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
 
 
+def _zeros(shape, dtype, dev: int, stream) -> torch.Tensor:
+    """Scratch of zeros that belongs to the call's stream."""
+    if stream is None:
+        return torch.zeros(shape, dtype=dtype, device=torch.device("cuda", dev))
+    with torch.cuda.stream(stream):
+        return torch.zeros(shape, dtype=dtype, device=torch.device("cuda", dev))
+
+
 def _call(fn, name: str, dev: int, *args) -> None:
     if dev == torch.cuda.current_device():
         code = fn(*args)
@@ -1003,7 +1011,7 @@ def ep_kv_append(cache: KvCache, seqs: KvSeqs, k: torch.Tensor, v: torch.Tensor,
 
 @dataclass
 class AttnWorkspace:
-    """Scratch of ep_attn_decode calls that do not overlap."""
+    """Scratch of ep_attn_decode calls that do not overlap: zeros before the first of them."""
 
     scratch: torch.Tensor
 
@@ -1028,7 +1036,7 @@ def new_attn_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_
     """Allocate a workspace for ep_attn_decode calls of this shape, or of fewer sequences."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     n = _attn_scratch_bytes(dev, num_seqs, num_q_heads, num_kv_heads, head_dim)
-    return AttnWorkspace(torch.empty(n, dtype=torch.uint8, device=dev))
+    return AttnWorkspace(torch.zeros(n, dtype=torch.uint8, device=dev))
 
 
 def _attn_args(cache, seqs, q, scale, out, lse, stream):
@@ -1059,7 +1067,7 @@ def ep_attn_decode(cache: KvCache, seqs: KvSeqs, q: torch.Tensor, scale: Optiona
     dev, c, s, pq, sq, Hq, scale, out, po, pl = _attn_args(cache, seqs, q, scale, out, lse, stream)
     if workspace is None:
         n = _attn_scratch_bytes(dev, s.num_seqs, Hq, c.num_kv_heads, c.head_dim)
-        workspace = AttnWorkspace(_empty(n, torch.uint8, dev, stream))
+        workspace = AttnWorkspace(_zeros(n, torch.uint8, dev, stream))
     ws = workspace.scratch
     nbytes = ws.numel()
     pws = _want(ws, "workspace.scratch", (torch.uint8,), (nbytes,), dev)

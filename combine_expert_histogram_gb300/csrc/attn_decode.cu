@@ -12,7 +12,8 @@
 // it each of eight warps has every eighth unit, a ring of its own in shared memory that tiled
 // TMA loads fill ahead, across the ends of heads and sequences, and sums of its own
 // (m, l, o), which the warps add at the end of a head.  A head that several blocks share
-// leaves its sums in the workspace, and a second kernel adds them in order.
+// leaves its sums in the workspace, and the block that arrives last adds them (a second kernel
+// for that took 5 us more: 3 from the last block's end to its first instruction).
 #include "attn.cuh"
 #include "tcgen05.cuh"
 
@@ -21,24 +22,9 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kHeads = 16;           // query heads of an item at most
-constexpr int kLeast = kWarps;       // units a block takes at least
+constexpr int kLeast = 2 * kWarps;   // units a block takes at least
+constexpr int kItem = 8;             // units of time that an item costs beside its own
 constexpr float kLog2e = 1.4426950408889634f;
-
-template <int D, bool FP8>
-struct Cfg {
-    static constexpr int kRow = FP8 ? D : 2 * D;             // bytes of a cache row
-    static constexpr int kUnit = 4096 / kRow;                // keys of a unit
-    static constexpr int kGroups = kUnit / 8;                // of 8 rows, which a page holds together
-    static constexpr int kPitch = kRow < 128 ? kRow : 128;   // a panel's row
-    static constexpr int kPanels = kRow / kPitch;
-    static constexpr int kPanel = kUnit * kPitch;
-    static constexpr int kTile = kUnit * kRow;               // keys, then values
-    static constexpr int kStages = 3;
-    static constexpr int kRing = kWarps * kStages * 2 * kTile;
-    static constexpr int kScales = FP8 ? kWarps * kStages * 2 * kUnit : 0;
-    static constexpr int kMerge = kWarps * 8 * D * 4;  // eight heads of every warp's o
-    static constexpr int kSmem = kRing + kMerge + kScales + 1024;  // and Shared
-};
 
 // What a block leaves of a head that others share: [block][first or last][row].
 struct Part {
@@ -50,8 +36,25 @@ struct Shared {
     int found_b, fail;
     Part part[kWarps][8];
 };
-static_assert(sizeof(Shared) <= 1024, "what Cfg::kSmem has for it");
-__host__ __device__ constexpr size_t ws_parts(int blocks) { return (size_t)blocks * 16; }
+template <int D, bool FP8>
+struct Cfg {
+    static constexpr int kRow = FP8 ? D : 2 * D;             // bytes of a cache row
+    static constexpr int kUnit = 4096 / kRow;                // keys of a unit
+    static constexpr int kGroups = kUnit / 8;                // of 8 rows, which a page holds together
+    static constexpr int kPitch = kRow < 128 ? kRow : 128;   // a panel's row
+    static constexpr int kPanels = kRow / kPitch;
+    static constexpr int kPanel = kUnit * kPitch;
+    static constexpr int kTile = kUnit * kRow;               // keys, then values
+    static constexpr int kStages = 3;
+    static constexpr int kRing = kWarps * kStages * 2 * kTile;
+    static constexpr int kScales = FP8 ? kWarps * 2 * 2 * kUnit : 0;  // of two units
+    static constexpr int kMerge = kWarps * 8 * D * 4;  // eight heads of every warp's o
+    static constexpr int kSmem = kRing + kMerge + kScales + (int)sizeof(Shared);
+};
+
+// The workspace: counts of arrivals [block][row] (of the heads that begin in a block), 0
+// between calls; parts; sums.
+__host__ __device__ constexpr size_t ws_parts(int blocks) { return (size_t)blocks * kHeads * 4; }
 __host__ __device__ constexpr size_t ws_sums(int blocks) {
     return ws_parts(blocks) + (size_t)blocks * 2 * kHeads * sizeof(Part);
 }
@@ -91,14 +94,24 @@ __device__ __forceinline__ Keys visible(const AttnArgs &a, int b) {
     return k;
 }
 
+// x / y of numbers >= 0, in 32 bits where that does.
+__device__ __forceinline__ int64_t divided(int64_t x, int64_t y) {
+    if ((x | y) >> 32 == 0) return (uint32_t)x / (uint32_t)y;
+    return x / y;
+}
+
 // A place in the list of work: an item (sequence, key head, group of query heads).
 template <int U>
 struct Place {
     int b, item;
-    int64_t at;  // the item's first unit in the list
+    int64_t at;  // the item's first place in the list
     Keys k;
+    int64_t pad;  // > 0: an item's places are its units, rounded up to a multiple of this
+    __device__ __forceinline__ int64_t places() const {
+        return pad == 0 ? k.n + kItem : divided(k.n + pad - 1, pad) * pad;
+    }
     __device__ __forceinline__ void next(const DecodeArgs &d) {
-        at += k.n;
+        at += places();
         if (++item == d.items) {
             item = 0;
             if (++b < d.a.seq.B) k = visible<U>(d.a, b);
@@ -177,6 +190,86 @@ __device__ __forceinline__ void half_pairs(uint32_t four, uint32_t &lo, uint32_t
         : "r"(four));
 }
 
+// A load that does not look into L1: another block's words.
+template <int N>
+__device__ __forceinline__ auto ld_l2(const void *p) {
+    if constexpr (N == 2) {
+        uint2 v;
+        asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+        return v;
+    } else {
+        uint4 v;
+        asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(p)
+                     : "memory");
+        return v;
+    }
+}
+// A query head's result, by one warp; `top` in log2 units.
+template <int D>
+__device__ __forceinline__ void store_head(const AttnArgs &a, int64_t to, int lane, float top, float sum,
+                                           const float (&acc)[D / 32]) {
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + to * D + D / 32 * lane);
+#pragma unroll
+    for (int x = 0; x < D / 32; x += 2) dst[x / 2] = pack_bf16(acc[x] * inv, acc[x + 1] * inv);
+    if (a.lse && lane == 0) a.lse[to] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
+}
+
+// Heads of which this block has a part: the block where they begin, how many follow that one,
+// row of the output.
+struct Share {
+    int c0, n, heads;
+    int64_t row0;
+};
+// The sum of all blocks' parts of a head, by one warp.
+template <int D>
+__device__ __forceinline__ void join_head(const AttnArgs &a, const Share &t, int r, const Part *parts,
+                                          const float *sums, int lane) {
+    constexpr int N = D / 32, kAhead = 20;  // channels a lane, sums in flight
+    auto at = [&](int i) { return (size_t)(2 * (t.c0 + i) + (i == 0)) * kHeads + r; };
+    auto part = [&](int i) {
+        const uint2 q = ld_l2<2>(&parts[at(min(i, t.n))]);
+        return i <= t.n ? Part{__uint_as_float(q.x), __uint_as_float(q.y)} : Part{-INFINITY, 0.0f};
+    };
+    const float *from = sums + N * lane;
+    Part mine = part(lane);
+    float top = mine.m, base = 0.0f, sum = 0.0f, acc[N];
+#pragma unroll
+    for (int x = 0; x < N; ++x) acc[x] = 0.0f;
+    for (int w0 = 0; w0 <= t.n; w0 += 32) {  // the blocks of whose m and l the lanes hold
+        const int end = min(t.n + 1 - w0, 32);
+        for (int i0 = 0; i0 < end; i0 += kAhead) {
+            decltype(ld_l2<N>(from)) v[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) v[i] = ld_l2<N>(from + at(min(w0 + i0 + i, t.n)) * D);
+            if (w0 + i0 == 0) {  // after the first loads are on their way
+                for (int i = lane + 32; i <= t.n; i += 32) top = fmaxf(top, part(i).m);
+#pragma unroll
+                for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
+                base = top == -INFINITY ? 0.0f : top;
+            } else if (i0 == 0) {
+                mine = part(w0 + lane);
+            }
+            const float f = exp2_fast(mine.m - base), fl = mine.l * f;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const float y = __shfl_sync(kFullMask, f, i0 + i), yl = __shfl_sync(kFullMask, fl, i0 + i);
+                if (i0 + i >= end) break;
+                sum += yl;
+                acc[0] += __uint_as_float(v[i].x) * y;
+                acc[1] += __uint_as_float(v[i].y) * y;
+                if constexpr (N == 4) {
+                    acc[2] += __uint_as_float(v[i].z) * y;
+                    acc[3] += __uint_as_float(v[i].w) * y;
+                }
+            }
+        }
+    }
+    store_head<D>(a, t.row0 + r, lane, top, sum, acc);
+}
+
 // A warp's stream of units: what is to be loaded next.
 template <int D, bool FP8>
 struct Loader {
@@ -186,7 +279,7 @@ struct Loader {
     int u, end;           // the warp's next unit in the item, the piece's end in it
     int left, held;       // units of which the lanes (still) hold the pages
     int page, row;        // lane: of box lane % (boxes a unit); the page past the last: none
-    int slot, behind;     // slot whose scales are not yet in shared memory, or -1
+    int slot, scale_slot, behind;  // behind: whose scales are not yet in shared memory, or -1
     uint2 scales;         // lane: eight of those
     bool more;
 
@@ -257,7 +350,8 @@ struct Loader {
                 const int64_t at = ((int64_t)px * a.kv.Hkv + h) * a.kv.page_size + rx + (r - x * d.box);
                 asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(scales.x), "=r"(scales.y) : "l"(src + at) : "memory");
             }
-            behind = slot;
+            behind = scale_slot;
+            scale_slot ^= 1;
         }
         u += kWarps;
         --left;
@@ -279,9 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = smem_addr(smem) + warp * C::kStages * 2 * C::kTile;
     float *merge = reinterpret_cast<float *>(smem + C::kRing);
-    const uint32_t scale_ring = smem_addr(smem) + C::kRing + C::kMerge + warp * C::kStages * 2 * C::kUnit;
+    const uint32_t scale_ring = smem_addr(smem) + C::kRing + C::kMerge + warp * 2 * 2 * C::kUnit;
     uint64_t *full = sh.full[warp];
-    int4 *record = reinterpret_cast<int4 *>(d.ws);
+    int *arrivals = reinterpret_cast<int *>(d.ws);
     Part *parts = reinterpret_cast<Part *>(d.ws + ws_parts(gridDim.x));
     float *out_sums = reinterpret_cast<float *>(d.ws + ws_sums(gridDim.x));
     if (threadIdx.x == 0) {
@@ -292,66 +386,110 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_map(&vmap);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // the kernel that joins may take its place beside this one
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    // ---- the block's run of the list ----
-    // Exclusive sums of the sequences' units, kThreads at a time; the first ones are kept.
-    int64_t total = 0, excl0 = 0, n0 = 0;
-    auto scan = [&](int b0, int64_t &n, int64_t &excl) {
-        const int b = b0 + threadIdx.x;
-        n = b < a.seq.B ? (int64_t)visible<C::kUnit>(a, b).n * d.items : 0;
-        int64_t incl = n;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const int64_t o = __shfl_up_sync(kFullMask, incl, s);
-            if (lane >= s) incl += o;
-        }
-        __syncthreads();
-        if (lane == 31) sh.sums[warp] = incl;
-        __syncthreads();
-        int64_t all = 0, below = 0;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            if (i == warp) below = all;
-            all += sh.sums[i];
-        }
-        excl = incl - n + below;
-        return all;
-    };
-    for (int b0 = 0; b0 < a.seq.B; b0 += kThreads) {
-        int64_t n, excl;
-        total += scan(b0, n, excl);
-        if (b0 == 0) n0 = n, excl0 = excl;
-    }
-    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kLeast);
-    const int64_t x0 = blockIdx.x * per, x1 = min(x0 + per, total);
-    if (threadIdx.x == 0) record[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (x0 >= x1) return;
-    int64_t before = 0;
-    for (int b0 = 0;; b0 += kThreads) {
-        int64_t n = n0, excl = excl0, all = total;
-        if (a.seq.B > kThreads) all = scan(b0, n, excl);
-        if (x0 >= before + excl && x0 < before + excl + n) {
-            sh.found_b = b0 + threadIdx.x;
-            sh.found_at = before + excl;
-        }
-        before += all;
-        if (before > x0 || b0 + kThreads >= a.seq.B) break;
-    }
-    __syncthreads();
+    // ---- the block's run of the list, and its first item ----
+    const int64_t blocks = gridDim.x;
+    int64_t total = 0, per, x0, x1;
     Place<C::kUnit> p;
-    p.b = sh.found_b;
-    p.k = visible<C::kUnit>(a, p.b);
-    p.item = (int)((x0 - sh.found_at) / p.k.n);
-    p.at = sh.found_at + (int64_t)p.item * p.k.n;
+    p.pad = 0;
+    if (a.seq.B <= 32) {
+        // few sequences, where latency counts: every warp by itself (and in 32 bits where
+        // that does)
+        Keys k = {};
+        int64_t n = 0;
+        if (lane < a.seq.B) {
+            k = visible<C::kUnit>(a, lane);
+            n = (int64_t)(k.n + kItem) * d.items;
+        }
+        auto scan = [&](int64_t incl) {
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const int64_t o = __shfl_up_sync(kFullMask, incl, s);
+                if (lane >= s) incl += o;
+            }
+            return incl;
+        };
+        int64_t incl = scan(n);
+        total = __shfl_sync(kFullMask, incl, 31);
+        per = max(divided(total + blocks - 1, blocks), (int64_t)kLeast);
+        // Runs that end with their item, where that makes them at most 12 units (2 us)
+        // longer: a block with two items' parts comes 3 us later than the others.
+        const int64_t spare = blocks - (int64_t)a.seq.B * d.items;
+        if (spare > 0) {
+            const int64_t units = total - (int64_t)a.seq.B * d.items * kItem;
+            const int64_t longer = max(divided(units + spare - 1, spare), (int64_t)kLeast);
+            if (longer <= per + 12) {
+                per = p.pad = longer;
+                if (lane < a.seq.B) n = divided(k.n + per - 1, per) * per * d.items;
+                incl = scan(n);
+                total = __shfl_sync(kFullMask, incl, 31);
+            }
+        }
+        x0 = blockIdx.x * per;
+        x1 = min(x0 + per, total);
+        __syncthreads();  // the barriers are initialised
+        if (x0 >= x1) return;
+        p.b = __ffs(__ballot_sync(kFullMask, x0 < incl)) - 1;
+        p.at = __shfl_sync(kFullMask, incl - n, p.b);
+        p.k = {__shfl_sync(kFullMask, k.L, p.b),  __shfl_sync(kFullMask, k.lo, p.b), __shfl_sync(kFullMask, k.S, p.b),
+               __shfl_sync(kFullMask, k.n, p.b),  __shfl_sync(kFullMask, k.ns, p.b), __shfl_sync(kFullMask, k.first, p.b)};
+    } else {
+        // exclusive sums of the sequences' units, kThreads at a time; the first ones are kept
+        int64_t excl0 = 0, n0 = 0;
+        auto scan = [&](int b0, int64_t &n, int64_t &excl) {
+            const int b = b0 + threadIdx.x;
+            n = b < a.seq.B ? (int64_t)(visible<C::kUnit>(a, b).n + kItem) * d.items : 0;
+            int64_t incl = n;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const int64_t o = __shfl_up_sync(kFullMask, incl, s);
+                if (lane >= s) incl += o;
+            }
+            __syncthreads();
+            if (lane == 31) sh.sums[warp] = incl;
+            __syncthreads();
+            int64_t all = 0, below = 0;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                if (i == warp) below = all;
+                all += sh.sums[i];
+            }
+            excl = incl - n + below;
+            return all;
+        };
+        for (int b0 = 0; b0 < a.seq.B; b0 += kThreads) {
+            int64_t n, excl;
+            total += scan(b0, n, excl);
+            if (b0 == 0) n0 = n, excl0 = excl;
+        }
+        per = max(divided(total + blocks - 1, blocks), (int64_t)kLeast);
+        x0 = blockIdx.x * per;
+        x1 = min(x0 + per, total);
+        if (x0 >= x1) return;
+        int64_t before = 0;
+        for (int b0 = 0;; b0 += kThreads) {
+            int64_t n = n0, excl = excl0, all = total;
+            if (a.seq.B > kThreads) all = scan(b0, n, excl);
+            if (x0 >= before + excl && x0 < before + excl + n) {
+                sh.found_b = b0 + threadIdx.x;
+                sh.found_at = before + excl;
+            }
+            before += all;
+            if (before > x0 || b0 + kThreads >= a.seq.B) break;
+        }
+        __syncthreads();
+        p.b = sh.found_b;
+        p.at = sh.found_at;
+        p.k = visible<C::kUnit>(a, p.b);
+    }
+    p.item = (int)divided(x0 - p.at, p.places());
+    p.at += p.item * p.places();
 
     Loader<D, FP8> load;
     load.p = p;
     load.x0 = x0;
     load.x1 = x1;
     load.held = 32 / (C::kUnit / d.box);
-    load.slot = 0;
+    load.slot = load.scale_slot = 0;
     load.behind = -1;
     load.more = true;
     load.piece(warp);
@@ -359,41 +497,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < C::kStages - 1; ++i) load.issue(d, &kmap, &vmap, ring, scale_ring, full, warp, lane);
 
     const int row = lane >> 2, c = lane & 3;  // of the matrix fragments
-    int slot = 0;
+    int slot = 0, scale_slot = 0;
     uint32_t phase = 0;
-    for (; p.at < x1; p.next(d)) {
+    // The queries of an item: head `row` of each tile is the second factor's column.  FP8: a
+    // lane's E4M3 key bytes are D / 4 neighbours, of which a step takes four.
+    uint32_t word[NH][D / 8];
+    auto fetch = [&](const Place<C::kUnit> &at) {
+        const int h = at.item / d.groups, g = at.item - h * d.groups;
+        const int heads = min(d.heads, d.G - g * d.heads);
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            const int r = row + 8 * n;
+            const uint16_t *src = a.q + at.b * a.q_stride + (int64_t)(h * d.G + g * d.heads + r) * D;
+            if constexpr (!FP8) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    word[n][i] = r < heads ? (uint32_t)ld_dep(reinterpret_cast<const int32_t *>(src + 8 * i + 2 * c)) : 0u;
+            } else {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint4 v = r < heads ? ld_dep_v4(src + D / 4 * c + 8 * i) : make_uint4(0, 0, 0, 0);
+                    word[n][4 * i] = v.x;
+                    word[n][4 * i + 1] = v.y;
+                    word[n][4 * i + 2] = v.z;
+                    word[n][4 * i + 3] = v.w;
+                }
+            }
+        }
+    };
+    Share first = {}, last = {};  // heads that begin before the run, that end behind it
+    int first_before[NH];
+    if (x0 >= p.at + p.k.n) p.next(d);  // the run begins behind the item's units
+    if (p.at < x1) fetch(p);
+    while (p.at < x1) {
         const int h = p.item / d.groups, g = p.item - h * d.groups;
         const int q0 = h * d.G + g * d.heads, heads = min(d.heads, d.G - g * d.heads);
-        // ---- queries: head `row` of each tile as the second factor's column ----
         uint32_t q[NH][D / 16][2];
         float to_log2[NH][2];  // logits in log2 units, of the heads 2 c and 2 c + 1
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
-            const int r = row + 8 * n;
-            const uint16_t *src = a.q + p.b * a.q_stride + (int64_t)(q0 + r) * D;
             to_log2[n][0] = to_log2[n][1] = a.scale * kLog2e;
             if constexpr (!FP8) {
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        q[n][s][i] = r < heads ? (uint32_t)ld_dep(reinterpret_cast<const int32_t *>(src + 16 * s + 8 * i + 2 * c)) : 0u;
+                for (int i = 0; i < D / 8; ++i) q[n][i / 2][i & 1] = word[n][i];
             } else {
-                // a lane's E4M3 key bytes are D / 4 neighbours, and a step takes four of each
-                // lane's; as fp16 next to 2^8 at most, which is exact down to 2^-32 of the
-                // head's largest
-                uint32_t w[D / 8];
+                // as fp16 next to 2^8 at most, exact down to 2^-32 of the head's largest
                 float amax = 0.0f;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const uint4 v = r < heads ? ld_dep_v4(src + D / 4 * c + 8 * i) : make_uint4(0, 0, 0, 0);
-                    w[4 * i] = v.x;
-                    w[4 * i + 1] = v.y;
-                    w[4 * i + 2] = v.z;
-                    w[4 * i + 3] = v.w;
-                }
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+                for (int i = 0; i < D / 8; ++i)
+                    amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(word[n][i])), fabsf(bf16_hi(word[n][i]))));
                 amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
                 // up = 2^k with amax * up in [2^7, 2^8), within what fp32 has of both
@@ -403,9 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) to_log2[n][i] *= __shfl_sync(kFullMask, down, 4 * (2 * c + i));
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) q[n][s][i] = pack_half(bf16_lo(w[2 * s + i]) * up, bf16_hi(w[2 * s + i]) * up);
+                for (int i = 0; i < D / 8; ++i)
+                    q[n][i / 2][i & 1] = pack_half(bf16_lo(word[n][i]) * up, bf16_hi(word[n][i]) * up);
             }
         }
         // of the heads 2 c and 2 c + 1: largest logit, sum of probabilities (this lane's keys'),
@@ -431,7 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             load.issue(d, &kmap, &vmap, ring, scale_ring, full, warp, lane);
             const uint32_t st = ring + slot * 2 * C::kTile, sv = st + C::kTile;
-            const uint32_t sc = scale_ring + slot * 2 * C::kUnit;
+            const uint32_t sc = scale_ring + scale_slot * 2 * C::kUnit;
+            scale_slot ^= 1;
             slot = slot + 1 == C::kStages ? 0 : slot + 1;
             const int key = p.key(u);
             const bool whole = key + C::kUnit <= p.k.L && key >= p.k.lo;
@@ -639,6 +791,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
 
+        Place<C::kUnit> after = p;
+        after.next(d);
+        if (NH == 1 && after.at < x1) fetch(after);  // its latency passes under the merge
+
         // ---- the warps' sums together, eight heads at a time ----
         const bool starts = p.at >= x0, ends = p.at + p.k.n <= x1;
 #pragma unroll
@@ -686,12 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (starts && ends) {
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                    const int64_t to = (int64_t)p.b * a.Hq + q0 + r;
-                    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + to * D + N * lane);
-#pragma unroll
-                    for (int x = 0; x < N; x += 2) dst[x / 2] = pack_bf16(acc[x] * inv, acc[x + 1] * inv);
-                    if (a.lse && lane == 0) a.lse[to] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
+                    store_head<D>(a, (int64_t)p.b * a.Hq + q0 + r, lane, top, sum, acc);
                 } else {
                     const size_t to = (size_t)(2 * blockIdx.x + starts) * kHeads + r;
                     float *dst = out_sums + to * D + N * lane;
@@ -702,8 +853,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncthreads();
         }
-        if (starts && !ends && threadIdx.x == 0)  // the block where a shared head begins
-            record[blockIdx.x] = make_int4(p.b, q0, heads, (int)((p.at + p.k.n - 1) / per) - (int)blockIdx.x);
+        if (!(starts && ends)) {
+            Share &t = starts ? last : first;
+            t.c0 = starts ? (int)blockIdx.x : (int)divided(p.at, per);
+            t.n = (int)divided(p.at + p.k.n - 1, per) - t.c0;
+            t.row0 = (int64_t)p.b * a.Hq + q0;
+            t.heads = heads;
+            if (!starts) {
+                __threadfence();
+#pragma unroll
+                for (int n = 0; n < NH; ++n)
+                    if (8 * n + warp < heads && lane == 0) first_before[n] = atomicAdd(arrivals + t.c0 * kHeads + 8 * n + warp, 1);
+            }
+        }
+        if (NH > 1 && after.at < x1) fetch(after);
+        p = after;
+    }
+
+    // ---- heads that several blocks share: the warp that comes last to one adds their sums, in
+    // the blocks' order.  At the end of the run: nothing of the block's waits for it ----
+    if (last.heads) __threadfence();
+#pragma unroll
+    for (int n = 0; n < NH; ++n) {
+        const int r = 8 * n + warp;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const Share t = which ? last : first;
+            if (r >= t.heads) continue;
+            int before = 0;
+            if (lane == 0) {
+                int *count = arrivals + t.c0 * kHeads + r;
+                before = which ? atomicAdd(count, 1) : first_before[n];
+                if (before == t.n) *count = 0;
+                // a workspace that was not zeros
+                if (before < 0 || before > t.n) raise_status(a.seq.status, EP_ERR_INVALID_ARG);
+            }
+            before = __shfl_sync(kFullMask, before, 0);
+            if (before != t.n) continue;
+            __threadfence();
+            join_head<D>(a, t, r, parts, out_sums, lane);
+        }
     }
     __syncwarp();
     if (sh.fail) {
@@ -711,85 +900,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a load that was given up may still be landing: wait, again with a limit
         for (int i = 0; i < C::kStages; ++i) mbar_wait(full + i, ((phase >> i) & 1) ^ 1, nullptr);
     }
-}
-
-// A shared head's sums, from the block where it begins on: two warps a row, each of which
-// takes every second block's.
-template <int D>
-__global__ void __launch_bounds__(2 * kThreads) join_kernel(const DecodeArgs d, int blocks) {
-    constexpr int N = D / 32, kAhead = 8;  // channels a lane, sums in flight
-    __shared__ float other[8][D + 1];
-    const int warp = (threadIdx.x >> 5) & 7, second = threadIdx.x >> 8, lane = threadIdx.x & 31;
-    const int4 *record = reinterpret_cast<const int4 *>(d.ws);
-    const Part *parts = reinterpret_cast<const Part *>(d.ws + ws_parts(blocks));
-    const float *sums = reinterpret_cast<const float *>(d.ws + ws_sums(blocks));
-    const int c0 = blockIdx.x >> 1, r = warp + 8 * (blockIdx.x & 1);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const uint4 rec = ld_dep_v4(record + c0);
-    const int n = (int)rec.w;  // blocks after the first
-    if (n == 0 || 8 * (int)(blockIdx.x & 1) >= (int)rec.z) return;
-    const bool live = r < (int)rec.z;
-    auto at = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0)) * kHeads + r; };
-    float top = -INFINITY;
-    if (live)
-        for (int i = lane; i <= n; i += 32) top = fmaxf(top, ld_dep(&parts[at(i)].m));
-#pragma unroll
-    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
-    const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, acc[N];
-#pragma unroll
-    for (int x = 0; x < N; ++x) acc[x] = 0.0f;
-    if (live) {
-        for (int i0 = second; i0 <= n; i0 += 2 * kAhead) {
-            float v[kAhead][N], m[kAhead], l[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int j = i0 + 2 * i;
-                m[i] = -INFINITY;
-                l[i] = 0.0f;
-#pragma unroll
-                for (int x = 0; x < N; ++x) v[i][x] = 0.0f;
-                if (j <= n) {
-                    m[i] = ld_dep(&parts[at(j)].m);
-                    l[i] = ld_dep(&parts[at(j)].l);
-                    const float *src = sums + at(j) * D + N * lane;
-                    if constexpr (N == 4) {
-                        const uint4 w = ld_dep_v4(src);
-                        v[i][0] = __uint_as_float(w.x);
-                        v[i][1] = __uint_as_float(w.y);
-                        v[i][2] = __uint_as_float(w.z);
-                        v[i][3] = __uint_as_float(w.w);
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < N; ++x) v[i][x] = ld_dep(src + x);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const float f = exp2_fast(m[i] - base);
-                sum += l[i] * f;
-#pragma unroll
-                for (int x = 0; x < N; ++x) acc[x] += v[i][x] * f;
-            }
-        }
-        if (second) {
-#pragma unroll
-            for (int x = 0; x < N; ++x) other[warp][N * lane + x] = acc[x];
-            if (lane == 0) other[warp][D] = sum;
-        }
-    }
-    __syncthreads();
-    if (!live || second) return;
-    sum += other[warp][D];
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t to = (int64_t)rec.x * d.a.Hq + rec.y + r;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(d.a.out + to * D + N * lane);
-#pragma unroll
-    for (int x = 0; x < N; ++x) acc[x] = (acc[x] + other[warp][N * lane + x]) * inv;
-#pragma unroll
-    for (int x = 0; x < N; x += 2) dst[x / 2] = pack_bf16(acc[x], acc[x + 1]);
-    if (d.a.lse && lane == 0) d.a.lse[to] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
 }
 
 template <int D, bool FP8>
@@ -807,12 +917,8 @@ cudaError_t launch(DecodeArgs d, cudaStream_t stream) {
         !encode_bytes(&vmap, kv.v, 4, dims, strides, box, swizzle))
         return cudaErrorInvalidValue;
     const int blocks = sm_count();
-    const cudaError_t err =
-        d.heads <= 8
-            ? launch_large<decode_kernel<D, FP8, 1>>(blocks, kThreads, C::kSmem, stream, kmap, vmap, d)
-            : launch_large<decode_kernel<D, FP8, 2>>(blocks, kThreads, C::kSmem, stream, kmap, vmap, d);
-    if (err != cudaSuccess) return err;
-    return launch_kernel(join_kernel<D>, 2 * blocks, 2 * kThreads, 0, stream, true, d, blocks);
+    return d.heads <= 8 ? launch_large<decode_kernel<D, FP8, 1>>(blocks, kThreads, C::kSmem, stream, kmap, vmap, d)
+                        : launch_large<decode_kernel<D, FP8, 2>>(blocks, kThreads, C::kSmem, stream, kmap, vmap, d);
 }
 
 }  // namespace

@@ -681,9 +681,12 @@ ep_status_t ep_kv_append(const ep_kv_cache_t *cache, const ep_kv_seqs_t *seqs, c
  *   out        device bf16 [B, num_q_heads, head_dim], 16-byte aligned.
  *   lse        device fp32 [B, num_q_heads] or NULL.
  *   workspace  device scratch, 16-byte aligned, of at least
- *              ep_attn_decode_workspace_bytes() with this device current, clobbered.
- *              Holds nothing between calls.  Calls (or replayed graphs) that share one
- *              must not overlap on the GPU.
+ *              ep_attn_decode_workspace_bytes() with this device current; enough for
+ *              that many sequences and for fewer.  All zeros before the first call; its
+ *              counters are zero again after each call, the rest is clobbered.  Calls (or
+ *              replayed graphs) that share one must not overlap on the GPU, and nothing
+ *              else may write it between them (counters that are not zero raise
+ *              EP_ERR_INVALID_ARG, and results are missing).
  *
  *   out = bf16_rn( sum over visible j of p_j v_j / sum of p_j ),  p_j = exp(scale * q.k_j)
  *   lse = log( sum of p_j )

@@ -426,8 +426,9 @@ def test_same_call_same_bits(quant):
     ws = ep.new_attn_workspace(4, 16, 2, 128)
     first = ep.ep_attn_decode(cache, seqs, q, workspace=ws)
     for _ in range(20):
-        ws.scratch.fill_(0xFF)  # nothing is kept in it
         assert torch.equal(ep.ep_attn_decode(cache, seqs, q, workspace=ws), first)
+    for _ in range(3):
+        assert torch.equal(ep.ep_attn_decode(cache, seqs, q), first)
     p = Seqs([900, 300], [500, 300], quant=quant)
     cache, seqs, q = p.cuda()
     first = ep.ep_attn_prefill(cache, seqs, q)
@@ -443,6 +444,17 @@ def test_one_workspace_for_smaller_batches():
         out = ep.ep_attn_decode(cache, seqs, q, workspace=ws)
         seqs.check_status()
         close(s, out)
+
+
+def test_workspace_that_was_not_zeros():
+    s = Seqs([5000], Hq=2, Hkv=1)
+    cache, seqs, q = s.cuda()
+    ws = ep.new_attn_workspace(1, 2, 1, 128)
+    ws.scratch.fill_(0xFF)
+    ep.ep_attn_decode(cache, seqs, q, workspace=ws)
+    with pytest.raises(ep.EPError) as e:
+        seqs.check_status()
+    assert e.value.code == ep.EP_ERR_INVALID_ARG
 
 
 def test_workspace_too_small():
