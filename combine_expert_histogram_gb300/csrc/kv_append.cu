@@ -3,10 +3,9 @@
 //
 //   a' = a cos - b sin,  b' = b cos + a sin   for the pairs of the first R channels
 //
-// A warp takes one token and some of its head rows, D/8 lanes a row with eight
-// channels each, so that a lane's eight cosines and sines serve all rows the warp
-// goes through.  A pair's other half is another lane's vector (one shuffle) or the
-// neighbouring channel.  HBM-bound: every row is read once and written once.
+// A warp takes one token and some of its head rows, D/16 lanes a row, each with the
+// eight channels and their pairs' other halves of eight angles, whose cosines and sines serve
+// all rows the warp goes through.  HBM-bound: every row is read once and written once.
 #include "attn.cuh"
 
 namespace ep {
@@ -26,15 +25,54 @@ struct AppendArgs {
     int rows;  // head rows a warp takes
 };
 
+// A pair of channels turned, each product and sum rounded by itself, so that the bits do not
+// hang on a choice of fused operations (the assembler fuses packed ones, mul.rn.f32x2 and
+// add.rn.f32x2, although their rounding is given).
+__device__ __forceinline__ void turn(float &x, float &y, float c, float s) {
+    const float u = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+    y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+    x = u;
+}
+__device__ __forceinline__ uint4 bf16x8(const float (&y)[8]) {
+    return make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+}
+__device__ __forceinline__ void floats(const uint4 &x, float (&y)[8]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[2 * i] = bf16_lo(w[i]), y[2 * i + 1] = bf16_hi(w[i]);
+}
+
 template <int D, bool FP8, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a) {
-    constexpr int L = D / 8, P = 32 / L;  // lanes a row, rows at a time
+    constexpr int L = D / 16, P = 32 / L, U = 2;  // lanes a row, rows at a time, of which in flight
     const int lane = threadIdx.x & 31, c = lane % L, sub = lane / L;
     const int heads = a.Hq + 2 * a.kv.Hkv, parts = (heads + a.rows - 1) / a.rows;
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int t = (int)(unit / parts), h0 = (int)(unit % parts) * a.rows, h1 = min(h0 + a.rows, heads);
+    // the lane's two vectors of eight channels
+    const bool turned = 16 * c < a.R;
+    const int v0 = INTER ? 2 * c : turned ? c : 2 * c, v1 = !INTER && turned ? c + a.R / 16 : v0 + 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int t = (int)(unit / parts), h0 = (int)(unit % parts) * a.rows;
     if (t >= a.seq.T) return;
+    // The rows first: where they go is a chain of small loads.
+    auto load = [&](int h, uint4 (&x)[U][2]) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int r = h + i * P + sub;
+            x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+            if (r >= h1) continue;
+            const bool is_q = r < a.Hq, is_k = r < a.Hq + a.kv.Hkv;
+            const int kh = r - a.Hq - (is_k ? 0 : a.kv.Hkv);
+            const uint16_t *src = is_q   ? a.q + t * a.q_stride + (int64_t)r * D
+                                  : is_k ? a.k + t * a.k_stride + (int64_t)kh * D
+                                         : a.v + t * a.v_stride + (int64_t)kh * D;
+            x[i][0] = ld_dep_stream(src + 8 * v0);
+            x[i][1] = ld_dep_stream(src + 8 * v1);
+        }
+    };
+    uint4 now[U][2], next[U][2];
+    load(h0, now);
+
     const int b = seq_of(a.seq, t);
     if (b < 0) return;
     const Span sp = seq_span(a.seq, a.kv.page_size, b);
@@ -47,101 +85,93 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a)
     const int page = page_of(a.kv, a.seq, b, pos / a.kv.page_size);
     if (page < 0) return;
     const int row = pos % a.kv.page_size;
+    const int64_t place = page * a.kv.page_stride + row * a.kv.row_stride;
 
-    float cs[8], sn[8];
-    const bool turned = 8 * c < a.R, low = 16 * c < a.R;
+    float cs[8], sn[8];  // of the angles 8 c .. 8 c + 7
     if (turned) {
-        // half of a row's angles fall on each lane's eight channels (INTER: four)
-        const float *p = a.cos_sin + (int64_t)pos * a.R;
-        const int at = INTER ? 4 * c : 8 * c - (low ? 0 : a.R / 2);
+        const float *p = a.cos_sin + (int64_t)pos * a.R + 8 * c;
 #pragma unroll
-        for (int i = 0; i < (INTER ? 4 : 8); ++i) {
-            cs[i] = ld_dep(p + at + i);
-            sn[i] = ld_dep(p + a.R / 2 + at + i);
+        for (int i = 0; i < 8; i += 4) {
+            const uint4 u = ld_dep_v4(p + i), w = ld_dep_v4(p + a.R / 2 + i);
+            cs[i] = __uint_as_float(u.x), cs[i + 1] = __uint_as_float(u.y);
+            cs[i + 2] = __uint_as_float(u.z), cs[i + 3] = __uint_as_float(u.w);
+            sn[i] = __uint_as_float(w.x), sn[i + 1] = __uint_as_float(w.y);
+            sn[i + 2] = __uint_as_float(w.z), sn[i + 3] = __uint_as_float(w.w);
         }
     }
-    for (int h = h0 + sub; h - sub < min(h0 + a.rows, heads); h += P) {
-        const bool live = h < min(h0 + a.rows, heads);
-        const bool is_q = h < a.Hq, is_k = h < a.Hq + a.kv.Hkv;
-        const int kh = h - a.Hq - (is_k ? 0 : a.kv.Hkv);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (live) {
-            const uint16_t *src = is_q   ? a.q + t * a.q_stride + (int64_t)h * D
-                                  : is_k ? a.k + t * a.k_stride + (int64_t)kh * D
-                                         : a.v + t * a.v_stride + (int64_t)kh * D;
-            x = ld_dep_stream(src + 8 * c);
-        }
-        float y[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
-                      bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
-        if (a.R) {
-            // each product and sum rounded by itself, so that the bits do not hang on
-            // the compiler's choice of fused operations
-            const bool turn = turned && is_k;
-            if constexpr (INTER) {
+    for (int h = h0; h < h1; h += U * P) {
+        if (h + U * P < h1) load(h + U * P, next);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float u = y[2 * i], w = y[2 * i + 1];
-                    if (turn) {
-                        y[2 * i] = __fsub_rn(__fmul_rn(u, cs[i]), __fmul_rn(w, sn[i]));
-                        y[2 * i + 1] = __fadd_rn(__fmul_rn(w, cs[i]), __fmul_rn(u, sn[i]));
+        for (int i = 0; i < U; ++i) {
+            if (h + i * P >= h1) break;
+            const int r = h + i * P + sub;
+            const bool live = r < h1, is_q = r < a.Hq, is_k = r < a.Hq + a.kv.Hkv;
+            const int kh = r - a.Hq - (is_k ? 0 : a.kv.Hkv);
+            uint4 w0 = now[i][0], w1 = now[i][1];
+            float y0[8], y1[8];
+            floats(w0, y0);
+            floats(w1, y1);
+            if (turned && is_k) {
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    if constexpr (INTER) {
+                        float *y = m < 4 ? y0 + 2 * m : y1 + 2 * (m - 4);
+                        turn(y[0], y[1], cs[m], sn[m]);
+                    } else {
+                        turn(y0[m], y1[m], cs[m], sn[m]);
                     }
                 }
-            } else {
-                const int other = turned ? lane + (low ? a.R / 16 : -(a.R / 16)) : lane;
-                uint4 o;
-                o.x = __shfl_sync(kFullMask, x.x, other);
-                o.y = __shfl_sync(kFullMask, x.y, other);
-                o.z = __shfl_sync(kFullMask, x.z, other);
-                o.w = __shfl_sync(kFullMask, x.w, other);
-                const float z[8] = {bf16_lo(o.x), bf16_hi(o.x), bf16_lo(o.y), bf16_hi(o.y),
-                                    bf16_lo(o.z), bf16_hi(o.z), bf16_lo(o.w), bf16_hi(o.w)};
+                w0 = bf16x8(y0);
+                w1 = bf16x8(y1);
+            }
+            if (is_q) {
+                uint16_t *dst = a.q_out + t * a.q_out_stride + (int64_t)r * D;
+                if (live) {
+                    st_v4(dst + 8 * v0, w0);
+                    st_v4(dst + 8 * v1, w1);
+                }
+            }
+            uint8_t *dst = (is_k ? a.kv.k : a.kv.v) + place + kh * a.kv.head_stride;
+            if constexpr (!FP8) {
+                if (live && !is_q) {
+                    st_v4(dst + 16 * v0, w0);
+                    st_v4(dst + 16 * v1, w1);
+                }
+            } else if (__any_sync(kFullMask, !is_q)) {
+                float amax = 0.0f;
+                bool odd = false;  // an infinity or NaN: the row has no scale
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float p = __fmul_rn(y[i], cs[i]), r = __fmul_rn(z[i], sn[i]);
-                    if (turn) y[i] = low ? __fsub_rn(p, r) : __fadd_rn(p, r);
+                for (int m = 0; m < 8; ++m) {
+                    amax = fmaxf(amax, fmaxf(fabsf(y0[m]), fabsf(y1[m])));
+                    odd |= !(fabsf(y0[m]) <= 3.402823466e38f) || !(fabsf(y1[m]) <= 3.402823466e38f);
+                }
+                if (odd) amax = __uint_as_float(0x7f800000u);
+#pragma unroll
+                for (int m = 1; m < L; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, m));
+                if (live && !is_q) {
+                    int e = ue8m0_exponent(group_scale(amax));
+                    odd = amax > 3.402823466e38f;
+                    if (odd) e = 255;
+                    const float inv = odd ? 0.0f : exp_reciprocal(e);
+                    auto store = [&](int v, const float (&y)[8]) {
+                        uint32_t w[2];
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+                            w[m] = odd ? 0x7f7f7f7fu
+                                       : fp8x4(__fmul_rn(y[4 * m], inv), __fmul_rn(y[4 * m + 1], inv),
+                                               __fmul_rn(y[4 * m + 2], inv), __fmul_rn(y[4 * m + 3], inv));
+                        *reinterpret_cast<uint2 *>(dst + 8 * v) = make_uint2(w[0], w[1]);
+                    };
+                    store(v0, y0);
+                    store(v1, y1);
+                    if (c == 0)
+                        (is_k ? a.kv.k_scales : a.kv.v_scales)[((int64_t)page * a.kv.Hkv + kh) *
+                                                                   a.kv.page_size + row] = (uint8_t)e;
                 }
             }
         }
-        if (is_q) {
-            if (live)
-                st_v4(a.q_out + t * a.q_out_stride + (int64_t)h * D + 8 * c,
-                      make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
-                                 pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])));
-        }
-        uint8_t *dst = (is_k ? a.kv.k : a.kv.v) + page * a.kv.page_stride +
-                       row * a.kv.row_stride + kh * a.kv.head_stride;
-        if constexpr (!FP8) {
-            if (live && !is_q)
-                st_v4(dst + 16 * c, make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
-                                               pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])));
-        } else {
-            float amax = 0.0f;
-            bool odd = false;  // an infinity or NaN: the row has no scale
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                amax = fmaxf(amax, fabsf(y[i]));
-                odd |= !(fabsf(y[i]) <= 3.402823466e38f);
-            }
-            if (odd) amax = __uint_as_float(0x7f800000u);
-#pragma unroll
-            for (int d = 1; d < L; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, d));
-            if (live && !is_q) {
-                int e = ue8m0_exponent(group_scale(amax));
-                odd = amax > 3.402823466e38f;
-                if (odd) e = 255;
-                const float inv = odd ? 0.0f : exp_reciprocal(e);
-                uint32_t w[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    w[i] = odd ? 0x7f7f7f7fu
-                               : fp8x4(__fmul_rn(y[4 * i], inv), __fmul_rn(y[4 * i + 1], inv),
-                                       __fmul_rn(y[4 * i + 2], inv), __fmul_rn(y[4 * i + 3], inv));
-                *reinterpret_cast<uint2 *>(dst + 8 * c) = make_uint2(w[0], w[1]);
-                if (c == 0)
-                    (is_k ? a.kv.k_scales : a.kv.v_scales)[((int64_t)page * a.kv.Hkv + kh) *
-                                                               a.kv.page_size + row] = (uint8_t)e;
-            }
-        }
+        for (int i = 0; i < U; ++i) now[i][0] = next[i][0], now[i][1] = next[i][1];
     }
 }
 
@@ -155,7 +185,13 @@ cudaError_t launch_kv_append(const KvArgs &kv, const SeqArgs &seq, const uint16_
     AppendArgs a = {kv, seq, q, k, v, q_stride, k_stride, v_stride, q_out_stride, Hq, cos_sin,
                     R, positions, q_out, 0};
     const int heads = Hq + 2 * kv.Hkv;
-    a.rows = 8;
+    // Whole tokens where that leaves every SM 32 warps and more, else fewer rows a warp, in whole
+    // passes.
+    const int pass = 512 / kv.D;
+    auto passes = [&](int rows) { return (rows + pass - 1) / pass * pass; };
+    const int64_t warps = 32ll * sm_count();
+    a.rows = passes(heads);
+    while (a.rows > pass && (int64_t)seq.T * ((heads + a.rows - 1) / a.rows) < warps) a.rows = passes(a.rows / 2);
     const int64_t units = (int64_t)seq.T * ((heads + a.rows - 1) / a.rows);
     const int grid = (int)((units + kWarps - 1) / kWarps);
     const bool fp8 = kv.k_scales != nullptr;

@@ -100,6 +100,7 @@ def test_append_rotations(D, R, inter, quant):
     ([3, 20], [5, 20], {}),                            # more rows than tokens: skipped
     ([33, 64, 100], [33, 1, 99], dict(gap=3, tail=4)),  # rows that no sequence owns
     ([600, 500], [600, 400], dict(page=128, Hq=7, Hkv=1)),
+    ([900], [900], dict(page=128, Hq=16, Hkv=8)),      # 3 million values: a fused product shows
     ([17, 9], [17, 2], dict(layout="rows")),
     ([17, 9], [17, 2], dict(layout="slice", D=64)),
 ])
