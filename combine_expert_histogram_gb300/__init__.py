@@ -14,6 +14,7 @@ from .binding import (  # noqa: F401
     ep_attn_decode,
     ep_attn_decode_workspace_bytes,
     ep_attn_prefill,
+    ep_attn_prefill_workspace_bytes,
     ep_combine,
     ep_dispatch,
     ep_expert_gemm,

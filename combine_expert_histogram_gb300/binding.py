@@ -87,7 +87,8 @@ EXPORTS = ("ep_status_str", "ep_rows_capacity", "ep_scale_cols", "ep_scale_words
            "ep_layout_noalloc", "ep_selftest_bounded_wait", "ep_selftest_cluster_wait",
            "ep_rank_layout", "ep_rank_expand", "ep_route_topk", "ep_rmsnorm", "ep_expert_gemm",
            "ep_expert_swiglu", "ep_moe_decode", "ep_moe_decode_workspace_bytes", "ep_kv_append",
-           "ep_attn_decode", "ep_attn_decode_workspace_bytes", "ep_attn_prefill")
+           "ep_attn_decode", "ep_attn_decode_workspace_bytes", "ep_attn_prefill",
+           "ep_attn_prefill_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 256 * 1024
 
 
@@ -153,7 +154,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ep_attn_decode.restype = ctypes.c_int
     L.ep_attn_decode.argtypes = [CP, SP, P, I64, I32, F, I32, I32, P, P, P, SZ, P]
     L.ep_attn_prefill.restype = ctypes.c_int
-    L.ep_attn_prefill.argtypes = [CP, SP, P, I64, I32, F, I32, I32, P, P, P]
+    L.ep_attn_prefill.argtypes = [CP, SP, P, I64, I32, F, I32, I32, P, P, P, SZ, P]
+    L.ep_attn_prefill_workspace_bytes.restype = SZ
+    L.ep_attn_prefill_workspace_bytes.argtypes = [I32] * 5
     if path == LIB_PATH:
         _lib = L
     return L
@@ -1076,14 +1079,33 @@ def ep_attn_decode(cache: KvCache, seqs: KvSeqs, q: torch.Tensor, scale: Optiona
     return out
 
 
+def ep_attn_prefill_workspace_bytes(num_tokens: int, num_seqs: int, num_q_heads: int,
+                                    num_kv_heads: int, head_dim: int) -> int:
+    return int(load_library().ep_attn_prefill_workspace_bytes(num_tokens, num_seqs, num_q_heads,
+                                                              num_kv_heads, head_dim))
+
+
 def ep_attn_prefill(cache: KvCache, seqs: KvSeqs, q: torch.Tensor, scale: Optional[float] = None,
                     window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None,
-                    lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                    lse: Optional[torch.Tensor] = None, scratch: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
     """Causal attention of prompts, or of their next chunks, over the cache that already holds
     their keys and values: q and the result bf16 [T, num_q_heads, head_dim].  Arguments as for
-    ep_attn_decode.  Rows of the result that belong to no sequence are not written."""
+    ep_attn_decode, but scratch is any uint8 tensor of ep_attn_prefill_workspace_bytes() (one of
+    the call's own by default).  Rows of the result that belong to no sequence are not written."""
     lib = load_library()
     dev, c, s, pq, sq, Hq, scale, out, po, pl = _attn_args(cache, seqs, q, scale, out, lse, stream)
+    shape = s.num_tokens, s.num_seqs, Hq, c.num_kv_heads, c.head_dim
+    if scratch is None:
+        if dev == torch.cuda.current_device():
+            n = lib.ep_attn_prefill_workspace_bytes(*shape)
+        else:
+            with torch.cuda.device(dev):
+                n = lib.ep_attn_prefill_workspace_bytes(*shape)
+        if n:
+            scratch = _empty(n, torch.uint8, dev, stream)
+    nbytes = scratch.numel() if scratch is not None else 0
+    pw = _want(scratch, "scratch", (torch.uint8,), (nbytes,), dev) if nbytes else None
     _call(lib.ep_attn_prefill, "ep_attn_prefill", dev, ctypes.byref(c), ctypes.byref(s), pq, sq, Hq,
-          scale, window, sinks, po, pl, _on(stream, dev))
+          scale, window, sinks, po, pl, pw, nbytes, _on(stream, dev))
     return out

@@ -162,14 +162,26 @@ ep_status_t ep_attn_decode(const ep_kv_cache_t *c, const ep_kv_seqs_t *s, const 
     return from_cuda(launch_attn_decode(a, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t ep_attn_prefill_workspace_bytes(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
+    if (T < 0 || B < 0 || check_heads(Hq, Hkv) != EP_OK || check_head_dim(D) != EP_OK ||
+        (int64_t)T * Hq > EP_ATTN_MAX_ROWS)
+        return 0;
+    return attn_prefill_workspace(T, B, Hq, Hkv, D);
+}
+
 ep_status_t ep_attn_prefill(const ep_kv_cache_t *c, const ep_kv_seqs_t *s, const void *q,
                             int64_t q_stride, int32_t Hq, float scale, int32_t window,
-                            int32_t sinks, void *out, float *lse, ep_stream_t stream) {
+                            int32_t sinks, void *out, float *lse, void *workspace,
+                            size_t workspace_bytes, ep_stream_t stream) {
     const TraceRange trace("ep_attn_prefill");
     AttnArgs a = {};
     const ep_status_t st = check_attn(c, s, q, q_stride, Hq, scale, window, sinks, out, lse, &a);
     if (st != EP_OK || no_rows(s)) return st;
-    return from_cuda(launch_attn_prefill(a, reinterpret_cast<cudaStream_t>(stream)));
+    if (workspace &&
+        (!aligned(workspace, 16) ||
+         workspace_bytes < attn_prefill_workspace(s->num_tokens, s->num_seqs, Hq, c->num_kv_heads, c->head_dim)))
+        return EP_ERR_INVALID_ARG;
+    return from_cuda(launch_attn_prefill(a, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

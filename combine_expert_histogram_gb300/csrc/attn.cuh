@@ -91,6 +91,8 @@ cudaError_t launch_kv_append(const KvArgs &kv, const SeqArgs &seq, const uint16_
                              int64_t q_out_stride, cudaStream_t stream);
 cudaError_t launch_attn_decode(const AttnArgs &a, void *workspace, cudaStream_t stream);
 size_t attn_decode_workspace(int B, int Hq, int Hkv, int D);
-cudaError_t launch_attn_prefill(const AttnArgs &a, cudaStream_t stream);
+// workspace may be nullptr.
+cudaError_t launch_attn_prefill(const AttnArgs &a, void *workspace, cudaStream_t stream);
+size_t attn_prefill_workspace(int T, int B, int Hq, int Hkv, int D);
 
 }  // namespace ep

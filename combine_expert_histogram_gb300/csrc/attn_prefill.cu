@@ -2,21 +2,26 @@
 //
 //   S = Q K^T,  P = exp(scale S - m),  O = sum P V,  l = sum P,  out = O / l
 //
-// with the running maximum m of a row.  A block has 256 rows, the tokens of one sequence times
-// the query heads that share a key head, in two tiles of 128, and goes once over the 128-key
-// tiles that its rows see.  Roles:
+// with the running maximum m of a row.  A block has up to 256 rows, the tokens of one sequence
+// times the query heads that share a key head, and goes once over the 128-key tiles that its
+// rows see.  Roles:
 //   - a loader keeps a ring of key and value tiles in flight by tiled TMA loads, page by
 //     page;
 //   - one thread issues the products on tcgen05: S of a tile into tensor memory, and P V
-//     with P read from tensor memory, where it takes the place of S.  The two row tiles
-//     alternate, so that one tile's exponentials run under the other's products;
-//   - two warpgroups, a thread a row, take S out of tensor memory, and put P back as bf16.
+//     with P read from tensor memory, where it takes the place of S.  Two row tiles of 128
+//     alternate, so that one tile's exponentials run under the other's products; a block of
+//     at most 128 rows has the even key tiles in one and the odd ones in the other;
+//   - two warpgroups, a thread a row, take S out of tensor memory, and put P back in 16 bits,
+//     in two halves, so that the first one's products run under the second's exponentials.
 //     m is let lag behind the true maximum by up to 2^8 (P and l stay far inside fp32, and
 //     P's relative rounding is the same), so that O is rescaled only in the rare tiles where
 //     a row's maximum jumps;
-//   - 8-bit caches: a warpgroup turns the E4M3 tiles into bf16, row by row, which is exact
-//     (a power of two times three bits).  bf16 caches: two warps look for values that are
-//     not finite in tiles that not all rows see: 0 * NaN would reach the other rows.
+//   - 8-bit caches: a warpgroup turns the E4M3 tiles into fp16, which is exact.  The
+//     keys' scales go to the logits, and the values' to the probabilities (as summands in
+//     the exponent).  bf16 caches: two warps look for values that are not finite in tiles
+//     that not all rows see: 0 * NaN would reach the other rows.
+// Few blocks are multiplied by sharing their key tiles out among several, whose sums a second
+// kernel adds.
 #include "attn.cuh"
 #include "tcgen05.cuh"
 
@@ -24,40 +29,50 @@ namespace ep {
 namespace {
 
 constexpr int kTile = 128;   // rows of a tile, keys of a tile
+constexpr int kRows = 2 * kTile;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 8.0f;  // log2 of how far m may be behind
-
-template <int D, bool FP8>
-struct Cfg {
-    static constexpr int kThreads = FP8 ? 512 : 384;
-    // registers a thread: 128 or 168 at launch
-    static constexpr int kSoftRegs = FP8 ? 176 : 208, kOtherRegs = FP8 ? 80 : 88;
-    static constexpr int kPanels = D / 64;               // 128-byte columns of a tile
-    static constexpr int kPanel = kTile * 128;
-    static constexpr int kStage = kPanels * kPanel;      // a bf16 tile
-    static constexpr int kStages = FP8 ? 4 : 5;
-    static constexpr int kRaw = FP8 ? kTile * D : 0, kRaws = 2;
-    static constexpr int kSmem = 1024 + (2 + kStages) * kStage + kRaws * kRaw;
-};
-
-struct PrefillArgs {
-    AttnArgs a;
-    int G, box;  // query heads a key head; cache rows of a TMA box
-};
+constexpr float kBoost = 5.0f;  // fp16 probabilities: log2 of the largest that does not lag
 
 struct Shared {
     uint64_t full[5], empty[5], raw_full[2], raw_empty[2];
-    uint64_t q_full, s_full[2], p_ready[2], o_full[2], v_check, v_ok, drain;
+    uint64_t q_full, s_full[2], p_ready[2][2], o_full[2], v_check, v_ok, drain;
     int64_t sums[16];
-    int64_t before;
     uint32_t tmem;
     int fail, fix, issued;
     int b, block;
 };
 
-// bf16 x bf16 -> fp32; the second factor's rows may be along K (values) instead of N.
-constexpr uint32_t bf16_instr(int n, bool b_rows_k) {
-    return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)b_rows_k << 16 | (uint32_t)(n / 8) << 17 |
+template <int D, bool FP8>
+struct Cfg {
+    static constexpr int kThreads = FP8 ? 512 : 384;
+    // registers a thread: 128 or 168 at launch
+    static constexpr int kSoftRegs = FP8 ? 184 : 208, kOtherRegs = FP8 ? 72 : 88;
+    static constexpr int kPanels = D / 64;               // 128-byte columns of a tile
+    static constexpr int kPanel = kTile * 128;
+    static constexpr int kStage = kPanels * kPanel;      // a 16-bit tile
+    static constexpr int kStages = FP8 ? 4 : 5;
+    static constexpr int kRaw = FP8 ? kTile * D : 0, kRaws = 2;
+    // of two tiles: the keys' (fp32), log2 of the values' (fp32), 1 / the values' (bf16)
+    static constexpr int kScaleTile = kTile * 10, kScales = FP8 ? 2 * kScaleTile : 0;
+    static constexpr int kSmem = (2 + kStages) * kStage + kRaws * kRaw + kScales + (int)sizeof(Shared);
+};
+
+struct PrefillArgs {
+    AttnArgs a;
+    int G, box;  // query heads a key head; cache rows of a TMA box
+    int shares;  // blocks that may share one's key tiles
+    float *ws;   // [block][share][row]: m (log2), l; then [block][share][row][D]
+    int64_t blocks;
+};
+__host__ __device__ constexpr size_t ws_floats(int64_t blocks, int shares, int D) {
+    return (size_t)blocks * shares * kRows * (D + 2);
+}
+
+// bf16 x bf16 (or fp16 x fp16) -> fp32; the second factor's rows may be along K (values)
+// instead of N.
+constexpr uint32_t instr16(bool half, int n, bool b_rows_k) {
+    return 1u << 4 | (half ? 0u : 1u << 7 | 1u << 10) | (uint32_t)b_rows_k << 16 | (uint32_t)(n / 8) << 17 |
            (uint32_t)(kTile / 16) << 24;
 }
 // Descriptor of a value tile: 64 channels a 128-byte row, the rows along K, in 128-byte
@@ -66,7 +81,7 @@ __device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3ffffu) >> 4) | (uint64_t)(kTile * 128 >> 4) << 16 |
            (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool accumulate) {
+__device__ __forceinline__ void mma_16(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
@@ -74,7 +89,7 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 // The first factor in tensor memory.
-__device__ __forceinline__ void mma_bf16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, bool accumulate) {
+__device__ __forceinline__ void mma_16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
@@ -114,6 +129,35 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+// Bits 0 .. n-1, for any n.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+}
 __device__ __forceinline__ uint64_t pair(float x, float y) {
     uint64_t p;
     asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
@@ -133,12 +177,15 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// In the upper bit of each half: whether that bf16 is an infinity or NaN.
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+// In the upper bit of each half: whether that bf16 (fp16) is an infinity or NaN.
+template <bool HALF>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    return HALF ? ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u : ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
 // w with the halves that are not finite as 0.
+template <bool HALF>
 __device__ __forceinline__ uint32_t finite_part(uint32_t w) {
-    const uint32_t n = not_finite(w);
-    return w & ~((n >> 15) * 0xffffu);
+    return w & ~((not_finite<HALF>(w) >> 15) * 0xffffu);
 }
 
 // What a block works on, the same for all its threads.
@@ -148,9 +195,14 @@ struct Block {
     int first, pos0;     // token of q that is the sequence's first, its position
     int minpos, maxpos;  // of the block's rows
     int lo, S;           // keys [lo, maxpos] and [0, S), S <= lo, are seen by some row
-    int tile0, ns, nt;   // tiles 0 .. ns-1, then from tile0 on, nt in all
+    int tile0, ns;       // tiles 0 .. ns-1, then from tile0 on
+    int nt, i0;          // this share's tiles, of which the first
+    int shares;          // blocks that share the rows
     int window, sinks;
-    __device__ __forceinline__ int key(int i) const { return (i < ns ? i : tile0 + i - ns) * kTile; }
+    __device__ __forceinline__ int key(int i) const {
+        i += i0;
+        return (i < ns ? i : tile0 + i - ns) * kTile;
+    }
     // Not all rows see all of the tile's keys.
     __device__ __forceinline__ bool edge(int key) const {
         return !(key + kTile - 1 <= minpos &&
@@ -162,16 +214,77 @@ struct Block {
     }
 };
 
+// Block `index` of a key head: blocks of 256 rows, a sequence's last ones (with the most keys)
+// first.  False if there are not so many.  All threads of the block call it.
+template <int NT>
+__device__ __forceinline__ bool find_block(const PrefillArgs &d, int64_t index, int h, int share, Shared &sh, Block &k) {
+    const AttnArgs &a = d.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.seq.B; b0 += NT) {
+        const int b = b0 + threadIdx.x;
+        int64_t n = 0;
+        if (b < a.seq.B) n = ((int64_t)seq_span(a.seq, a.kv.page_size, b).n * d.G + kRows - 1) / kRows;
+        int64_t incl = n;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int64_t o = __shfl_up_sync(kFullMask, incl, s);
+            if (lane >= s) incl += o;
+        }
+        __syncthreads();
+        if (lane == 31) sh.sums[warp] = incl;
+        __syncthreads();
+        int64_t all = 0, below = 0;
+#pragma unroll
+        for (int i = 0; i < NT / 32; ++i) {
+            if (i == warp) below = all;
+            all += sh.sums[i];
+        }
+        incl += before + below;
+        if (index >= incl - n && index < incl) {
+            sh.b = b;
+            sh.block = (int)(incl - 1 - index);
+        }
+        before += all;
+        if (before > index) break;
+    }
+    __syncthreads();
+    if (before <= index) return false;
+    k.b = sh.b;
+    k.h = h;
+    const Span sp = seq_span(a.seq, a.kv.page_size, k.b);
+    k.first = sp.first;
+    k.pos0 = sp.len - sp.n;
+    k.row0 = sh.block * kRows;
+    k.rows = min(sp.n * d.G - k.row0, kRows);
+    k.minpos = k.pos0 + k.row0 / d.G;
+    k.maxpos = k.pos0 + (k.row0 + k.rows - 1) / d.G;
+    k.window = a.window;
+    k.sinks = k.S = a.sinks;
+    k.lo = a.window && k.minpos >= a.window ? k.minpos - a.window + 1 : 0;
+    if (k.S >= k.lo) k.lo = k.S = 0;
+    k.tile0 = k.lo / kTile;
+    k.ns = min((k.S + kTile - 1) / kTile, k.tile0);
+    const int nt = k.maxpos < 0 ? 0 : k.ns + k.maxpos / kTile + 1 - k.tile0;
+    // two tiles a share at least
+    k.shares = min(d.shares, max(nt / 2, 1));
+    k.i0 = (int)((int64_t)nt * share / k.shares);
+    k.nt = (int)((int64_t)nt * (share + 1) / k.shares) - k.i0;
+    return share < k.shares;
+}
+
 template <int D, bool FP8>
 __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ PrefillArgs d) {
     using C = Cfg<D, FP8>;
     constexpr int kStages = C::kStages;
-    extern __shared__ __align__(16) uint8_t raw_smem[];
-    uint8_t *smem = raw_smem + (1024 - (smem_addr(raw_smem) & 1023)) % 1024;
-    __shared__ Shared sh;
+    // all of the block's shared memory: queries, the ring (the swizzle wants 1024-byte
+    // alignment; static arrays would push it off), 8-bit tiles, scales
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem + 2 * C::kStage, *raws = ring + kStages * C::kStage;
+    uint8_t *scales = raws + C::kRaws * C::kRaw;
+    Shared &sh = *reinterpret_cast<Shared *>(scales + C::kScales);
     const AttnArgs &a = d.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const volatile int *fail = &sh.fail;
@@ -186,7 +299,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             mbar_init(&sh.raw_full[i], 1);
             mbar_init(&sh.raw_empty[i], 4);
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_ready[i], 4);
+            mbar_init(&sh.p_ready[i][0], 4);
+            mbar_init(&sh.p_ready[i][1], 4);
             mbar_init(&sh.o_full[i], 1);
         }
         mbar_init(&sh.q_full, 8);
@@ -194,66 +308,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         mbar_init(&sh.v_ok, 2);
         mbar_init(&sh.drain, 1);
         sh.fail = sh.fix = sh.issued = 0;
-        sh.b = -1;
         mbar_init_fence();
         tma_prefetch_map(&kmap);
         tma_prefetch_map(&vmap);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // ---- the block's rows: blocks of 256 rows, a sequence's last ones (with the most keys)
-    // first ----
     Block k;
-    k.h = blockIdx.x % a.kv.Hkv;
-    const int64_t index = blockIdx.x / a.kv.Hkv;
-    int64_t before = 0;
-    for (int b0 = 0; b0 < a.seq.B; b0 += C::kThreads) {
-        const int b = b0 + threadIdx.x;
-        int64_t n = 0;
-        if (b < a.seq.B) n = ((int64_t)seq_span(a.seq, a.kv.page_size, b).n * d.G + 2 * kTile - 1) / (2 * kTile);
-        int64_t incl = n;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const int64_t o = __shfl_up_sync(kFullMask, incl, s);
-            if (lane >= s) incl += o;
-        }
-        __syncthreads();
-        if (lane == 31) sh.sums[warp] = incl;
-        __syncthreads();
-        int64_t all = 0, below = 0;
-#pragma unroll
-        for (int i = 0; i < C::kThreads / 32; ++i) {
-            if (i == warp) below = all;
-            all += sh.sums[i];
-        }
-        incl += before + below;
-        if (index >= incl - n && index < incl) {
-            sh.b = b;
-            sh.block = (int)(incl - 1 - index);
-        }
-        before += all;
-        if (before > index) break;
-    }
-    __syncthreads();
-    if (sh.b < 0) return;
-    k.b = sh.b;
-    {
-        const Span sp = seq_span(a.seq, a.kv.page_size, k.b);
-        k.first = sp.first;
-        k.pos0 = sp.len - sp.n;
-        k.row0 = sh.block * 2 * kTile;
-        k.rows = min(sp.n * d.G - k.row0, 2 * kTile);
-        k.minpos = k.pos0 + k.row0 / d.G;
-        k.maxpos = k.pos0 + (k.row0 + k.rows - 1) / d.G;
-        k.window = a.window;
-        k.sinks = k.S = a.sinks;
-        k.lo = a.window && k.minpos >= a.window ? k.minpos - a.window + 1 : 0;
-        if (k.S >= k.lo) k.lo = k.S = 0;
-        k.tile0 = k.lo / kTile;
-        k.ns = min((k.S + kTile - 1) / kTile, k.tile0);
-        k.nt = k.maxpos < 0 ? 0 : k.ns + k.maxpos / kTile + 1 - k.tile0;
-    }
-    const int tiles = k.rows > kTile ? 2 : 1;  // row tiles
+    const int share = blockIdx.x % d.shares;
+    const int64_t block = blockIdx.x / d.shares;
+    if (!find_block<C::kThreads>(d, block / a.kv.Hkv, (int)(block % a.kv.Hkv), share, sh, k)) return;
+    // one row tile: its even key tiles here, its odd ones there
+    const bool halves = k.rows <= kTile;
+    const int stride = halves ? 2 : 1;
     if (warp == kMmaWarp) tmem_alloc<512>(&sh.tmem);
     tc_fence_before();
     __syncthreads();
@@ -263,7 +330,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
         // ---- a thread's row ----
-        const int t = warp >> 2, local = t * kTile + (warp & 3) * 32 + lane;
+        const int t = warp >> 2, local = (halves ? 0 : t * kTile) + (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + t * kTile + lanes, o_at = tmem + 2 * kTile + t * D + lanes;
         const bool valid = local < k.rows;
@@ -275,6 +342,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         constexpr int CH = D / 8, RP = 32 / CH;  // 16-byte chunks a row, rows an instruction
         const uint32_t mine = smem_addr(smem) + t * C::kStage;
         const int wrow = (warp & 3) * 32;
+        float sl2 = a.scale * kLog2e;  // FP8: of this row, whose queries are scaled
         {
             uint4 x[32 / RP];
 #pragma unroll
@@ -285,157 +353,278 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32 / RP; ++i) {
                 const int r = wrow + i * RP + lane / CH, ch = lane % CH;
+                if constexpr (FP8) {
+                    // as fp16 next to 2^8 at most, exact down to 2^-32 of the row's largest
+                    uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    float amax = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
+#pragma unroll
+                    for (int j = 1; j < CH; j <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, j));
+                    const int e = min(max((int)(__float_as_uint(amax) >> 23), 8), 254);
+                    const float up = __uint_as_float((uint32_t)(261 - e) << 23);
+                    const float down = __uint_as_float((uint32_t)max(e - 7, 0) << 23);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = pack_half(bf16_lo(w[j]) * up, bf16_hi(w[j]) * up);
+                    x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    const float f = __shfl_sync(kFullMask, down, (lane % RP) * CH);
+                    if (lane / RP == i) sl2 *= f;
+                }
                 sts16(mine + (ch >> 3) * C::kPanel + r * 128 + 16 * ((ch & 7) ^ (r & 7)), x[i]);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.q_full);
         }
-        const float sl2 = a.scale * kLog2e;
-        float m = -INFINITY, l = 0.0f;  // m in S's units
+        // bf16: m in S's units; FP8: in log2 units, of the logits with their values' scales
+        float m = -INFINITY, l = 0.0f;
         bool ok = true;
-        if (t < tiles) {
-            int wmin = pos, wmax = pos;  // of the warp's rows; rows that are none see nothing
+        int wmin = valid ? pos : 0x7fffffff, wmax = pos;  // of the warp's rows
 #pragma unroll
-            for (int x = 16; x; x >>= 1) {
-                wmin = min(wmin, __shfl_xor_sync(kFullMask, wmin, x));
-                wmax = max(wmax, __shfl_xor_sync(kFullMask, wmax, x));
-            }
-            for (int i = 0; i < k.nt; ++i) {
-                const int key = k.key(i);
-                ok = __all_sync(kFullMask, mbar_wait_fast(&sh.s_full[t], i & 1, fail));
-                if (!ok) break;
-                tc_fence_after();
-                uint32_t v[4][32];
+        for (int x = 16; x; x >>= 1) {
+            wmin = min(wmin, __shfl_xor_sync(kFullMask, wmin, x));
+            wmax = max(wmax, __shfl_xor_sync(kFullMask, wmax, x));
+        }
+        const int i_first = halves ? t : 0;
+        int n = 0;
+        for (int i = i_first; i < k.nt; i += stride, ++n) {
+            const int key = k.key(i);
+            ok = mbar_wait_fast(&sh.s_full[t], n & 1, fail);
+            // the scales are there when the values are
+            if (FP8) ok = ok && mbar_wait_fast(&sh.full[(2 * i + 1) % kStages], ((2 * i + 1) / kStages) & 1, fail);
+            ok = __all_sync(kFullMask, ok);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t v[4][32];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) tmem_ld(s_at + 32 * x, v[x]);
+            for (int x = 0; x < 4; ++x) tmem_ld(s_at + 32 * x, v[x]);
+            const uint32_t kf = smem_addr(scales) + (i & 1) * C::kScaleTile, vf = kf + kTile * 4, vi = vf + kTile * 4;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) tmem_ld_wait(v[x]);
-                if (!(key + kTile - 1 <= wmin && (!a.window || key > wmax - a.window || key + kTile <= a.sinks))) {
-                    const int hi = pos - key, lo = a.window && hi >= a.window ? hi - a.window + 1 : 0, s = a.sinks - key;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int n = 32 * x + j;
-                            if (!(n <= hi && (n >= lo || n < s))) v[x][j] = 0xff800000u;  // -infinity
-                        }
-                }
-                float top = m;
+            for (int x = 0; x < 4; ++x) tmem_ld_wait(v[x]);
+            if constexpr (FP8) {
+                const uint64_t sl = pair(sl2, sl2);
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(v[x][j]));
-                const bool grown = top > m && !((top - m) * sl2 <= kLag);
-                if (__any_sync(kFullMask, grown)) {
-                    const float next = grown ? top : m;
-                    const float f = grown ? exp2_fast((m - next) * sl2) : 1.0f;
-                    l *= f;
-                    m = next;
-                    if (i > 0) {
-#pragma unroll 1
-                        for (int x = 0; x < D / 32; ++x) {
-                            uint32_t o[32];
-                            tmem_ld(o_at + 32 * x, o);
-                            tmem_ld_wait(o);
+                    for (int j = 0; j < 32; j += 4) {
+                        const uint4 f = lds16(kf + (32 * x + j) * 4), e = lds16(vf + (32 * x + j) * 4);
+                        const uint64_t u = fma2(pair(__uint_as_float(v[x][j]), __uint_as_float(v[x][j + 1])),
+                                                mul2(pair(__uint_as_float(f.x), __uint_as_float(f.y)), sl),
+                                                pair(__uint_as_float(e.x), __uint_as_float(e.y)));
+                        const uint64_t w = fma2(pair(__uint_as_float(v[x][j + 2]), __uint_as_float(v[x][j + 3])),
+                                                mul2(pair(__uint_as_float(f.z), __uint_as_float(f.w)), sl),
+                                                pair(__uint_as_float(e.z), __uint_as_float(e.w)));
+                        float y0, y1;
+                        unpair(u, y0, y1);
+                        v[x][j] = __float_as_uint(y0), v[x][j + 1] = __float_as_uint(y1);
+                        unpair(w, y0, y1);
+                        v[x][j + 2] = __float_as_uint(y0), v[x][j + 3] = __float_as_uint(y1);
+                    }
+            }
+            if (!(key + kTile - 1 <= wmin && (!a.window || key > wmax - a.window || key + kTile <= a.sinks))) {
+                const int hi = pos - key, lo = a.window && hi >= a.window ? hi - a.window + 1 : 0, s = a.sinks - key;
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                            tmem_st(o_at + 32 * x, o);
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t seen = low_bits(hi + 1 - 32 * x) & (~low_bits(lo - 32 * x) | low_bits(s - 32 * x));
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[x][j] = seen >> j & 1 ? v[x][j] : 0xff800000u;  // -infinity
+                }
+            }
+            float top = m;
+            {
+                float part[4] = {m, m, m, m};
+#pragma unroll
+                for (int j = 0; j < 32; j += 2)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) part[x] = max3(part[x], __uint_as_float(v[x][j]), __uint_as_float(v[x][j + 1]));
+                top = fmaxf(max3(part[0], part[1], part[2]), part[3]);
+            }
+            const float unit = FP8 ? 1.0f : sl2;
+            const bool grown = top > m && !((top - m) * unit <= kLag);
+            if (__any_sync(kFullMask, grown)) {
+                const float next = grown ? top : m;
+                const float f = grown ? exp2_fast((m - next) * unit) : 1.0f;
+                l *= f;
+                m = next;
+                if (n > 0) {
+#pragma unroll 1
+                    for (int x = 0; x < D / 32; ++x) {
+                        uint32_t o[32];
+                        tmem_ld(o_at + 32 * x, o);
+                        tmem_ld_wait(o);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_st(o_at + 32 * x, o);
+                    }
+                }
+            }
+            // a row that has seen no key yet subtracts 0 from its -infinities
+            const float base = (m == -INFINITY ? 0.0f : -m * unit) + (FP8 ? kBoost : 0.0f);
+            const uint64_t sl = pair(sl2, sl2), bb = pair(base, base);
+            uint64_t acc0 = pair(l, 0.0f), acc1 = pair(0.0f, 0.0f);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t p[16];
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    uint4 e = make_uint4(0, 0, 0, 0);
+                    if (FP8) e = lds16(vi + (32 * x + 2 * j) * 2);
+                    const uint32_t inverse[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        uint64_t y = pair(__uint_as_float(v[x][2 * (j + z)]), __uint_as_float(v[x][2 * (j + z) + 1]));
+                        y = FP8 ? add2(y, bb) : fma2(y, sl, bb);
+                        float e0, e1;
+                        unpair(y, e0, e1);
+                        e0 = exp2_fast(e0);
+                        e1 = exp2_fast(e1);
+                        p[j + z] = FP8 ? pack_half(e0, e1) : pack_bf16(e0, e1);
+                        y = pair(e0, e1);
+                        uint64_t &acc = z & 1 ? acc1 : acc0;
+                        if constexpr (FP8) {
+                            // the probability itself: without the value's scale
+                            acc = fma2(y, pair(bf16_lo(inverse[z]), bf16_hi(inverse[z])), acc);
+                        } else {
+                            acc = add2(acc, y);
                         }
                     }
                 }
-                // a row that has seen no key yet subtracts 0 from its -infinities
-                const float base = m == -INFINITY ? 0.0f : -m * sl2;
-                const uint64_t sl = pair(sl2, sl2), bb = pair(base, base);
-                uint64_t acc0 = pair(l, 0.0f), acc1 = pair(0.0f, 0.0f);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        uint64_t e = pair(__uint_as_float(v[x][2 * j]), __uint_as_float(v[x][2 * j + 1]));
-                        asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(e) : "l"(sl), "l"(bb));
-                        float e0, e1;
-                        unpair(e, e0, e1);
-                        e0 = exp2_fast(e0);
-                        e1 = exp2_fast(e1);
-                        p[j] = pack_bf16(e0, e1);
-                        e = pair(e0, e1);
-                        if (j & 1)
-                            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc1) : "l"(e));
-                        else
-                            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc0) : "l"(e));
-                    }
-                    tmem_st(s_at + 16 * x, p);
+                tmem_st(s_at + 16 * x, p);
+                if (x & 1) {  // half of the keys
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.p_ready[t][x >> 1]);
                 }
-                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc0) : "l"(acc1));
-                float l0, l1;
-                unpair(acc0, l0, l1);
-                l = l0 + l1;
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_ready[t]);
             }
-            if (ok && k.nt > 0) ok = __all_sync(kFullMask, mbar_wait_fast(&sh.o_full[t], 0, fail));
+            acc0 = add2(acc0, acc1);
+            float l0, l1;
+            unpair(acc0, l0, l1);
+            l = l0 + l1;
+        }
+        if (ok && n > 0) ok = __all_sync(kFullMask, mbar_wait_fast(&sh.o_full[t], 0, fail));
+        // m in log2 units
+        float m2 = FP8 ? m - kBoost : m * sl2;
+        if (m == -INFINITY) m2 = -INFINITY;
+        float f0 = 1.0f, f1 = 0.0f;  // of this warpgroup's sums, of the other's
+        const uint32_t other = smem_addr(ring);  // [128][D] fp32, then [128] m2, l
+        if (halves) {
+            // the products of both are done, and nothing loads: the ring is free
+            if (ok && k.nt > 1) ok = __all_sync(kFullMask, mbar_wait_fast(&sh.o_full[t ^ 1], 0, fail));
             if (!ok) sh.fail = 1;
-            if (ok) {
-                tc_fence_after();
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                const bool fix = sh.fix != 0 && k.nt > 0;
-                const int64_t o_here = o_off;
+            if (t == 1) {
+                if (ok && n > 0) {
+                    tc_fence_after();
 #pragma unroll 1
-                for (int x = 0; x < D / 32; ++x) {
-                    uint32_t o[32];
-                    if (k.nt > 0) {
+                    for (int x = 0; x < D / 32; ++x) {
+                        uint32_t o[32];
                         tmem_ld(o_at + 32 * x, o);
                         tmem_ld_wait(o);
-                    } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0;
+                        for (int j = 0; j < 8; ++j)
+                            sts16(other + (wrow + lane) * D * 4 + 16 * ((8 * x + j) ^ (lane & 7)),
+                                  make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
                     }
-                    if (l == 0.0f) {
+                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(other + kTile * D * 4 + (wrow + lane) * 8), "f"(m2), "f"(l) : "memory");
+                }
+                __syncwarp();
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+            } else {
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (ok && k.nt > 1) {
+                    float om, ol;
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(om), "=f"(ol) : "r"(other + kTile * D * 4 + (wrow + lane) * 8) : "memory");
+                    const float both = fmaxf(m2, om), ref = both == -INFINITY ? 0.0f : both;
+                    f0 = exp2_fast(m2 - ref);
+                    f1 = exp2_fast(om - ref);
+                    l = l * f0 + ol * f1;
+                    m2 = both;
+                }
+            }
+        }
+        if (!ok) sh.fail = 1;
+        if (ok && !(halves && t == 1)) {
+            tc_fence_after();
+            const bool fix = sh.fix != 0 && k.nt > 0, direct = k.shares == 1;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const int64_t o_here = o_off;
+            const int64_t part = (int64_t)blockIdx.x * kRows + local;  // of the workspace
+            float *sums = d.ws + d.blocks * d.shares * kRows * 2 + part * D;
+#pragma unroll 1
+            for (int x = 0; x < D / 32; ++x) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld(o_at + 32 * x, o);
+                    tmem_ld_wait(o);
+                } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0;  // sees no key
+                    for (int j = 0; j < 32; ++j) o[j] = 0;
+                }
+                if (halves && k.nt > 1) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint4 w = lds16(other + (wrow + lane) * D * 4 + 16 * ((8 * x + j) ^ (lane & 7)));
+                        o[4 * j] = __float_as_uint(__uint_as_float(o[4 * j]) * f0 + __uint_as_float(w.x) * f1);
+                        o[4 * j + 1] = __float_as_uint(__uint_as_float(o[4 * j + 1]) * f0 + __uint_as_float(w.y) * f1);
+                        o[4 * j + 2] = __float_as_uint(__uint_as_float(o[4 * j + 2]) * f0 + __uint_as_float(w.z) * f1);
+                        o[4 * j + 3] = __float_as_uint(__uint_as_float(o[4 * j + 3]) * f0 + __uint_as_float(w.w) * f1);
                     }
+                }
+                if (l == 0.0f) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) o[j] = pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-                    if (fix) {
-                        // values that the products were spared, added where a row sees them
-                        for (int i = 0; i < k.nt; ++i) {
-                            const int key = k.key(i);
-                            if (!k.edge(key)) continue;
-                            for (int j = key; j <= min(pos, key + kTile - 1); ++j) {
-                                if (a.window && j <= pos - a.window && j >= a.sinks) continue;
-                                const int page = page_of(a.kv, a.seq, k.b, j / a.kv.page_size);
-                                if (page < 0) continue;
-                                const int r = j % a.kv.page_size;
-                                const uint8_t *src = a.kv.v + page * a.kv.page_stride + r * a.kv.row_stride + k.h * a.kv.head_stride;
-                                const bool none = FP8 && a.kv.v_scales[((int64_t)page * a.kv.Hkv + k.h) * a.kv.page_size + r] == 255;
+                    for (int j = 0; j < 32; ++j) o[j] = 0;  // sees no key
+                }
+                if (fix) {
+                    // values that the products were spared, added where a row sees them (an
+                    // infinity or NaN, so any probability will do)
+                    for (int i = 0; i < k.nt; ++i) {
+                        const int key = k.key(i);
+                        if (!k.edge(key)) continue;
+                        for (int j = key; j <= min(pos, key + kTile - 1); ++j) {
+                            if (a.window && j <= pos - a.window && j >= a.sinks) continue;
+                            const int page = page_of(a.kv, a.seq, k.b, j / a.kv.page_size);
+                            if (page < 0) continue;
+                            const int r = j % a.kv.page_size;
+                            const uint8_t *src = a.kv.v + page * a.kv.page_stride + r * a.kv.row_stride + k.h * a.kv.head_stride;
+                            const bool none = FP8 && a.kv.v_scales[((int64_t)page * a.kv.Hkv + k.h) * a.kv.page_size + r] == 255;
 #pragma unroll
-                                for (int n = 0; n < 16; ++n) {
-                                    uint32_t w;
-                                    if constexpr (FP8) {
-                                        const uint32_t e = reinterpret_cast<const uint16_t *>(src)[16 * x + n];
-                                        w = (none || (e & 0x7f) == 0x7f ? 0x7fffu : 0u) |
-                                            (none || (e & 0x7f00) == 0x7f00 ? 0x7fff0000u : 0u);
-                                    } else {
-                                        w = reinterpret_cast<const uint32_t *>(src)[16 * x + n];
-                                        w &= (not_finite(w) >> 15) * 0xffffu;
-                                    }
-                                    if (w) o[n] = pack_bf16(bf16_lo(o[n]) + bf16_lo(w), bf16_hi(o[n]) + bf16_hi(w));
+                            for (int w = 0; w < 16; ++w) {
+                                uint32_t y;
+                                if constexpr (FP8) {
+                                    const uint32_t e = reinterpret_cast<const uint16_t *>(src)[16 * x + w];
+                                    y = (none || (e & 0x7f) == 0x7f ? 0x7fffu : 0u) |
+                                        (none || (e & 0x7f00) == 0x7f00 ? 0x7fff0000u : 0u);
+                                } else {
+                                    y = reinterpret_cast<const uint32_t *>(src)[16 * x + w];
+                                    y &= (not_finite<false>(y) >> 15) * 0xffffu;
+                                }
+                                if (y) {
+                                    o[2 * w] = __float_as_uint(__uint_as_float(o[2 * w]) + bf16_lo(y));
+                                    o[2 * w + 1] = __float_as_uint(__uint_as_float(o[2 * w + 1]) + bf16_hi(y));
                                 }
                             }
                         }
                     }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int ch = 4 * x + j;
-                        sts16(mine + (ch >> 3) * C::kPanel + (wrow + lane) * 128 + 16 * ((ch & 7) ^ (lane & 7)),
-                              make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
-                    }
                 }
-                __syncwarp();
+                if (!direct) {
+                    if (valid) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            st_v4(sums + 32 * x + 4 * j, make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+                    }
+                    continue;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int ch = 4 * x + j;
+                    sts16(mine + (ch >> 3) * C::kPanel + (wrow + lane) * 128 + 16 * ((ch & 7) ^ (lane & 7)),
+                          make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+                }
+            }
+            __syncwarp();
+            if (direct) {
 #pragma unroll
                 for (int i = 0; i < 32 / RP; ++i) {
                     const int64_t off = __shfl_sync(kFullMask, o_here, i * RP + lane / CH);
@@ -443,8 +632,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     if (off >= 0)
                         st_v4(a.out + off + 8 * ch, lds16(mine + (ch >> 3) * C::kPanel + r * 128 + 16 * ((ch & 7) ^ (r & 7))));
                 }
-                if (a.lse && valid)
-                    a.lse[o_off / D] = l == 0.0f ? -INFINITY : (m * sl2 + log2f(l)) / kLog2e;
+                if (a.lse && valid) a.lse[o_off / D] = l == 0.0f ? -INFINITY : (m2 + log2f(l)) / kLog2e;
+            } else if (valid) {
+                *reinterpret_cast<float2 *>(d.ws + 2 * part) = make_float2(m2, l);
             }
         }
     } else {
@@ -475,11 +665,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                         sh.fail = 1;
                         break;
                     }
-                    if (elect_one()) expect_bytes(&fulls[s], bytes);
-                    __syncwarp();
+                    const bool leader = elect_one();
+                    if (leader) expect_bytes(&fulls[s], bytes);
                     for (int x = 0; x < boxes; ++x) {
                         const int px = __shfl_sync(kFullMask, page, x), rx = __shfl_sync(kFullMask, r, x);
-                        if (elect_one()) {
+                        if (leader) {
                             uint8_t *dst = to + s * bytes;
                             const CUtensorMap *map = v ? &vmap : &kmap;
                             if constexpr (FP8) {
@@ -490,16 +680,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                                     tma_load_4d(dst + n * C::kPanel + x * box * 128, map, 128 * n, k.h, rx, px, &fulls[s]);
                             }
                         }
-                        __syncwarp();
                     }
+                    __syncwarp();
                 }
             }
             if (lane == 0) sh.issued = it;
         } else if (warp == kMmaWarp) {
             // ---- products ----
-            constexpr uint32_t qk = bf16_instr(kTile, false), pv = bf16_instr(D, true);
+            constexpr uint32_t qk = instr16(FP8, kTile, false), pv = instr16(FP8, D, true);
             int edges = 0;
-            bool ok = k.nt == 0 || mbar_wait_fast(&sh.q_full, 0, fail);
             auto full = [&](int it) { return mbar_wait_fast(&sh.full[it % kStages], (it / kStages) & 1, fail); };
             auto logits = [&](int t, int it) {
                 const uint64_t da = tile_desc(smem_addr(smem + t * C::kStage));
@@ -507,46 +696,65 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
                     const uint32_t at = (x / 4) * (C::kPanel / 16) + 2 * (x % 4);
-                    mma_bf16(tmem + t * kTile, da + at, db + at, qk, x > 0);
+                    mma_16(tmem + t * kTile, da + at, db + at, qk, x > 0);
                 }
                 mma_commit(&sh.s_full[t]);
             };
-            ok = __all_sync(kFullMask, ok && (k.nt == 0 || full(0)));
-            if (ok && k.nt > 0) {
+            bool ok = k.nt == 0 || mbar_wait_fast(&sh.q_full, 0, fail);
+            // the first logits: of tile 0 for both, or of tiles 0 and 1
+            for (int t = 0; t < 2 && (halves ? t : 0) < k.nt; ++t) {
+                const int it = halves ? 2 * t : 0;
+                ok = __all_sync(kFullMask, ok && full(it));
+                if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    for (int t = 0; t < tiles; ++t) logits(t, 0);
-                    mma_commit(&sh.empty[0]);
+                    logits(t, it);
+                    if (halves || t) mma_commit(&sh.empty[it]);
                 }
                 __syncwarp();
             }
-            for (int i = 0; ok && i < k.nt; ++i) {
-                const int kt = 2 * i + 2, vt = 2 * i + 1;
-                const bool more = i + 1 < k.nt;
-                const bool check = !FP8 && k.edge(k.key(i));
-                ok = __all_sync(kFullMask, full(vt));
-                if (check && ok && elect_one()) mbar_arrive(&sh.v_check);
-                __syncwarp();
-                const uint64_t db = value_desc(smem_addr(ring + (vt % kStages) * C::kStage));
-                for (int t = 0; t < tiles; ++t) {
-                    ok = ok && mbar_wait_fast(&sh.p_ready[t], i & 1, fail);
-                    if (t == 0 && check) ok = ok && mbar_wait_fast(&sh.v_ok, edges++ & 1, fail);
-                    if (t == 0 && more) ok = ok && full(kt);
-                    ok = __all_sync(kFullMask, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
+            int n = 0;
+            for (int i0 = 0; ok && i0 < k.nt; i0 += stride, ++n) {
+                bool check = false;
+                for (int t = 0; t < 2; ++t) {
+                    const int i = halves ? i0 + t : i0;
+                    if (i >= k.nt) break;
+                    const int kt = 2 * (i + stride), vt = 2 * i + 1;
+                    const bool more = i + stride < k.nt, own = halves || t == 0, done = halves || t == 1;
+                    if (own) {
+                        check = !FP8 && k.edge(k.key(i));
+                        ok = __all_sync(kFullMask, full(vt));
+                        if (check && ok && elect_one()) mbar_arrive(&sh.v_check);
+                        __syncwarp();
+                    }
+                    const uint64_t db = value_desc(smem_addr(ring + (vt % kStages) * C::kStage));
 #pragma unroll
-                        for (int x = 0; x < kTile / 16; ++x)
-                            mma_bf16_tmem(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * x, db + x * (2048 / 16), pv, i > 0 || x > 0);
-                        if (more)
-                            logits(t, kt);
-                        else
-                            mma_commit(&sh.o_full[t]);
-                        if (t == tiles - 1) {
-                            mma_commit(&sh.empty[vt % kStages]);
-                            if (more) mma_commit(&sh.empty[kt % kStages]);
+                    for (int half = 0; half < 2; ++half) {
+                        ok = ok && mbar_wait_fast(&sh.p_ready[t][half], n & 1, fail);
+                        if (half == 0 && own && check) ok = ok && mbar_wait_fast(&sh.v_ok, edges++ & 1, fail);
+                        ok = __all_sync(kFullMask, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int x = 4 * half; x < 4 * half + 4; ++x)
+                                mma_16_tmem(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * x, db + x * (2048 / 16), pv, n > 0 || x > 0);
                         }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    if (done && elect_one()) mma_commit(&sh.empty[vt % kStages]);
+                    __syncwarp();
+                    if (more) {
+                        ok = __all_sync(kFullMask, !own || full(kt));
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            logits(t, kt);
+                            if (done) mma_commit(&sh.empty[kt % kStages]);
+                        }
+                    } else if (elect_one()) {
+                        mma_commit(&sh.o_full[t]);
                     }
                     __syncwarp();
                 }
@@ -571,10 +779,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 #pragma unroll 4
                 for (int x = (role - 2) * 32 + lane; x < C::kStage / 16; x += 64) {
                     uint4 w = lds16(st + 16 * x);
-                    if (not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w)) {
+                    if (not_finite<false>(w.x) | not_finite<false>(w.y) | not_finite<false>(w.z) | not_finite<false>(w.w)) {
                         const int j = key + (x * 16 % C::kPanel) / 128;
                         if (k.wanted(j, 1)) sh.fix = 1;
-                        sts16(st + 16 * x, make_uint4(finite_part(w.x), finite_part(w.y), finite_part(w.z), finite_part(w.w)));
+                        sts16(st + 16 * x, make_uint4(finite_part<false>(w.x), finite_part<false>(w.y),
+                                                      finite_part<false>(w.z), finite_part<false>(w.w)));
                     }
                 }
                 fence_proxy_async_smem();
@@ -583,12 +792,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             }
             if (!ok) sh.fail = 1;
         } else if (FP8 && role < 4) {
-            // ---- E4M3 rows to bf16, a thread a row ----
+            // ---- E4M3 rows to fp16, a thread a row ----
             const int r = role * 32 + lane;
             bool ok = true;
-            // scale bytes of the row's key and value; 0 where there are none
-            auto scales = [&](int i, uint32_t &sk, uint32_t &sv) {
-                sk = sv = 0;
+            // scale bytes of the row's key and value; 2^0 where there are none
+            auto bytes = [&](int i, uint32_t &sk, uint32_t &sv) {
+                sk = sv = 127;
                 const int j = k.key(i) + r;
                 if (i < k.nt && k.wanted(j, 1)) {
                     const int entry = j / a.kv.page_size;
@@ -601,12 +810,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 }
             };
             uint32_t sk, sv;
-            scales(0, sk, sv);
+            bytes(0, sk, sv);
             for (int i = 0; ok && i < k.nt; ++i) {
                 const int key = k.key(i);
                 const bool edge = k.edge(key), wanted = k.wanted(key + r, 1);
-                const uint32_t e[2] = {sk, sv};
-                scales(i + 1, sk, sv);
+                // a value whose scale is NaN is NaN itself, with the scale 1
+                const bool nan = sv == 255;
+                if (nan) sv = 127;
+                const float fk = scale_value(sk), ev = (float)((int)sv - 127);
+                const uint16_t inverse = (uint16_t)(sv == 254 ? 0x0040 : (254 - sv) << 7);  // 2^(127 - sv) as bf16
+                bytes(i + 1, sk, sv);
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                     const int it = 2 * i + v, rs = it % C::kRaws, s = it % kStages;
@@ -614,7 +827,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                          (it < kStages || mbar_wait_fast(&sh.empty[s], (it / kStages - 1) & 1, fail));
                     ok = __all_sync(kFullMask, ok);
                     if (!ok) break;
-                    const float f = scale_value(e[v]);
                     const uint32_t src = smem_addr(raws + rs * C::kRaw), dst = smem_addr(ring + s * C::kStage);
                     uint32_t bad = 0;
 #pragma unroll
@@ -625,21 +837,33 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                         uint32_t y[8];
 #pragma unroll
-                        for (int n = 0; n < 8; ++n) {
-                            uint32_t hp;
-                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hp) : "h"((uint16_t)(n & 1 ? w[n / 2] >> 16 : w[n / 2])));
-                            const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&hp));
-                            y[n] = wanted ? pack_bf16(g.x * f, g.y * f) : 0u;
-                            if (v && edge) {
-                                bad |= not_finite(y[n]);
-                                y[n] = finite_part(y[n]);
+                        for (int j = 0; j < 4; ++j)
+                            asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+                                "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+                                : "=r"(y[2 * j]), "=r"(y[2 * j + 1])
+                                : "r"(w[j]));
+                        if (v && nan) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) y[j] = 0x7fff7fffu;
+                        }
+                        if (v && edge) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                bad |= not_finite<true>(y[j]);
+                                y[j] = finite_part<true>(y[j]);
                             }
                         }
                         const uint32_t to = dst + (c >> 2) * C::kPanel + r * 128;
                         sts16(to + 16 * ((2 * c & 7) ^ (r & 7)), make_uint4(y[0], y[1], y[2], y[3]));
                         sts16(to + 16 * ((2 * c + 1 & 7) ^ (r & 7)), make_uint4(y[4], y[5], y[6], y[7]));
                     }
-                    if (bad) sh.fix = 1;
+                    if (bad && wanted) sh.fix = 1;
+                    if (v) {  // the products of the tile two before are done, so its scales are free
+                        uint8_t *to = scales + (i & 1) * C::kScaleTile;
+                        reinterpret_cast<float *>(to)[r] = fk;
+                        reinterpret_cast<float *>(to)[kTile + r] = wanted ? ev : 0.0f;
+                        reinterpret_cast<uint16_t *>(to + 8 * kTile)[r] = wanted ? inverse : 0x3f80;
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -670,6 +894,61 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     }
 }
 
+// The shares' sums of a block's rows, a warp a row.
+template <int D>
+__global__ void __launch_bounds__(kRows) join_kernel(const __grid_constant__ PrefillArgs d) {
+    constexpr int N = D / 32;
+    __shared__ Shared sh;
+    const AttnArgs &a = d.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t block = blockIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Block k;
+    if (!find_block<kRows>(d, block / a.kv.Hkv, (int)(block % a.kv.Hkv), 0, sh, k) || k.shares == 1) return;
+    const float *ml = d.ws + block * d.shares * kRows * 2;
+    const float *sums = d.ws + d.blocks * d.shares * kRows * 2 + block * d.shares * kRows * D + N * lane;
+    for (int r = warp; r < k.rows; r += kRows / 32) {
+        float m = -INFINITY, l = 0.0f;
+        if (lane < k.shares) {
+            m = ld_dep(ml + 2 * (lane * kRows + r));
+            l = ld_dep(ml + 2 * (lane * kRows + r) + 1);
+        }
+        float top = m;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
+        const float f = exp2_fast(m - (top == -INFINITY ? 0.0f : top));
+        float sum = l * f, acc[N];
+#pragma unroll
+        for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(kFullMask, sum, x);
+#pragma unroll
+        for (int x = 0; x < N; ++x) acc[x] = 0.0f;
+#pragma unroll 8
+        for (int i = 0; i < k.shares; ++i) {
+            const float g = __shfl_sync(kFullMask, f, i);
+            const float *src = sums + (int64_t)(i * kRows + r) * D;
+#pragma unroll
+            for (int x = 0; x < N; ++x) acc[x] += ld_dep(src + x) * g;
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int token = (k.row0 + r) / d.G;
+        const int64_t to = (int64_t)(k.first + token) * a.Hq + (int64_t)k.h * d.G + (k.row0 + r - token * d.G);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + to * D + N * lane);
+#pragma unroll
+        for (int x = 0; x < N; x += 2) dst[x / 2] = pack_bf16(acc[x] * inv, acc[x + 1] * inv);
+        if (a.lse && lane == 0) a.lse[to] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
+    }
+}
+
+// At most this many blocks of 256 rows, a sequence's last one not being full.
+int64_t most_blocks(int64_t T, int64_t B, int G, int Hkv) {
+    return ((T * G) / kRows + (T < B ? T : B)) * Hkv;
+}
+// Blocks that share one's keys: as many as two for each SM allow.
+int most_shares(int64_t blocks) {
+    const int64_t n = 2 * sm_count() / (blocks > 0 ? blocks : 1);
+    return n < 1 ? 1 : n > 32 ? 32 : (int)n;
+}
+
 template <int D, bool FP8>
 cudaError_t launch(const PrefillArgs &d, cudaStream_t stream) {
     const KvArgs &kv = d.a.kv;
@@ -682,20 +961,29 @@ cudaError_t launch(const PrefillArgs &d, cudaStream_t stream) {
     if (!encode_bytes(&kmap, kv.k, 4, dims, strides, box, swizzle) ||
         !encode_bytes(&vmap, kv.v, 4, dims, strides, box, swizzle))
         return cudaErrorInvalidValue;
-    // at most this many blocks of 256 rows, a sequence's last one not being full
-    const int64_t T = d.a.seq.T, blocks = (T * d.G) / (2 * kTile) + (T < d.a.seq.B ? T : d.a.seq.B);
-    return launch_large<prefill_kernel<D, FP8>>((int)(blocks * kv.Hkv), Cfg<D, FP8>::kThreads,
-                                                Cfg<D, FP8>::kSmem, stream, kmap, vmap, d);
+    const cudaError_t err = launch_large<prefill_kernel<D, FP8>>((int)(d.blocks * d.shares), Cfg<D, FP8>::kThreads,
+                                                                 Cfg<D, FP8>::kSmem, stream, kmap, vmap, d);
+    if (err != cudaSuccess || d.shares == 1) return err;
+    return launch_kernel(join_kernel<D>, (int)d.blocks, kRows, 0, stream, true, d);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_prefill(const AttnArgs &a, cudaStream_t stream) {
+size_t attn_prefill_workspace(int T, int B, int Hq, int Hkv, int D) {
+    const int64_t blocks = most_blocks(T, B, Hq / Hkv, Hkv);
+    const int shares = most_shares(blocks);
+    return shares == 1 ? 0 : ws_floats(blocks, shares, D) * 4;
+}
+
+cudaError_t launch_attn_prefill(const AttnArgs &a, void *workspace, cudaStream_t stream) {
     PrefillArgs d = {};
     d.a = a;
     d.G = a.Hq / a.kv.Hkv;
     d.box = a.kv.page_size & -a.kv.page_size;  // a box lies within a page
     if (d.box > kTile) d.box = kTile;
+    d.blocks = most_blocks(a.seq.T, a.seq.B, d.G, a.kv.Hkv);
+    d.shares = workspace ? most_shares(d.blocks) : 1;
+    d.ws = static_cast<float *>(workspace);
     const bool fp8 = a.kv.k_scales != nullptr;
     if (a.kv.D == 64) return fp8 ? launch<64, true>(d, stream) : launch<64, false>(d, stream);
     return fp8 ? launch<128, true>(d, stream) : launch<128, false>(d, stream);

@@ -706,11 +706,20 @@ ep_status_t ep_attn_decode(const ep_kv_cache_t *cache, const ep_kv_seqs_t *seqs,
  * which ep_kv_append has added the chunk: every token sees the keys up to its own
  * position, within the window and the first keys if one is given.  Arguments and
  * results as for ep_attn_decode with q_start given (or not: one token a sequence), and
- * no workspace.  lse is [T, num_q_heads].
+ * lse is [T, num_q_heads], but
+ *
+ *   workspace  device scratch, 16-byte aligned, of ep_attn_prefill_workspace_bytes()
+ *              with this device current (0 for many tokens), clobbered.  Holds nothing
+ *              between calls; calls (or replayed graphs) that share one must not overlap
+ *              on the GPU.  NULL: the keys of a few tokens are not shared out among blocks,
+ *              which takes longer.
  */
+size_t ep_attn_prefill_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                                       int32_t num_kv_heads, int32_t head_dim);
 ep_status_t ep_attn_prefill(const ep_kv_cache_t *cache, const ep_kv_seqs_t *seqs, const void *q,
                             int64_t q_stride, int32_t num_q_heads, float scale, int32_t window,
-                            int32_t sinks, void *out, float *lse, ep_stream_t stream);
+                            int32_t sinks, void *out, float *lse, void *workspace,
+                            size_t workspace_bytes, ep_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -55,9 +55,10 @@ def _entries(lib):  # noqa: F811
         return lib.ep_attn_decode(ctypes.byref(c or cache()), ctypes.byref(s or seqs()), q, qs, Hq,
                                   scale, window, sinks, out, lse, ws, n, None)
 
-    def prefill(c=None, s=None, q=A, qs=512, Hq=4, scale=0.1, window=0, sinks=0, out=A, lse=None):
+    def prefill(c=None, s=None, q=A, qs=512, Hq=4, scale=0.1, window=0, sinks=0, out=A, lse=None,
+                ws=None, n=0):
         return lib.ep_attn_prefill(ctypes.byref(c or cache()), ctypes.byref(s or seqs()), q, qs, Hq,
-                                   scale, window, sinks, out, lse, None)
+                                   scale, window, sinks, out, lse, ws, n, None)
 
     return append, decode, prefill
 
@@ -100,9 +101,10 @@ def test_attention_arguments(lib, which):  # noqa: F811
                dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(window=-1),
                dict(window=8, sinks=-1)):
         assert call(**kw) == INVALID, kw
-    if which == 1:
-        for kw in (dict(ws=None), dict(ws=P(4104)), dict(n=8), dict(s=seqs(q_start=256))):
-            assert call(**kw) == INVALID, kw
+    more = ((dict(ws=None), dict(ws=P(4104)), dict(n=8), dict(s=seqs(q_start=256))) if which == 1
+            else (dict(ws=P(4104), n=1 << 30), dict(ws=A, n=8)))
+    for kw in more:
+        assert call(**kw) == INVALID, kw
 
 
 def test_workspace_sizes(lib):  # noqa: F811
@@ -113,6 +115,14 @@ def test_workspace_sizes(lib):  # noqa: F811
         for heads in ((1, 1), (4, 2), (32, 4), (64, 1), (1024, 1024)):
             sizes = [size(B, *heads, D) for B in (0, 1, 2, 7, 64, 1000)]
             assert sizes == sorted(sizes) and 0 < sizes[0]
+
+
+def test_prefill_workspace_sizes(lib):  # noqa: F811
+    size = lib.ep_attn_prefill_workspace_bytes
+    assert size(-1, 1, 4, 2, 128) == size(1, -1, 4, 2, 128) == size(1, 1, 3, 2, 128) == 0
+    assert size(1, 1, 4, 2, 96) == size(1 << 28, 1, 64, 2, 128) == 0
+    assert size(1 << 20, 1, 64, 2, 128) == 0 and size(1, 1, 4, 2, 128) > 0  # many, few tokens
+    assert max(size(T, B, 32, 8, 128) for T in (1, 40, 700, 5000) for B in (1, 3, 40)) < 1 << 27
 
 
 def test_status_name(lib):  # noqa: F811

@@ -269,6 +269,38 @@ def test_prefill_window(window, sinks, quant):
     close(make(), out, lse, window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("quant", [BF, F8])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,new,Hq,Hkv,kw", [
+    ([4000], [3], 8, 1, {}), ([4000, 1, 2100], [2, 1, 40], 4, 2, {}), ([1500], [300], 8, 1, {}),
+    ([3000, 700], [130, 5], 2, 2, dict(window=900, sinks=200)), ([256], [1], 1, 1, {}),
+    ([257, 600, 0], [2, 0, 0], 6, 1, {}),
+])
+def test_prefill_few_tokens(lens, new, Hq, Hkv, kw, D, quant):
+    """Keys shared out among blocks, and not."""
+    s = Seqs(lens, new, Hq=Hq, Hkv=Hkv, D=D, quant=quant, page=64, tail=2)
+    out, lse = run(s, False, **kw)
+    close(s, out, lse, **kw)
+    cache, seqs, q = s.cuda()
+    n = ep.ep_attn_prefill_workspace_bytes(s.T, len(lens), Hq, Hkv, D)
+    assert n > 0
+    dirty = torch.full((n + 16,), 0xFF, dtype=torch.uint8, device="cuda")
+    own = s.owned()
+    again = ep.ep_attn_prefill(cache, seqs, q, scratch=dirty, **kw)
+    assert torch.equal(again.cpu()[own], out.cpu()[own])
+    lib = ep.load_library()
+    alone = poisoned(s.T, Hq, D)
+    import ctypes
+    code = lib.ep_attn_prefill(ctypes.byref(cache._c), ctypes.byref(seqs._struct(s.T)), q.data_ptr(),
+                               Hq * D, Hq, D ** -0.5, kw.get("window", 0), kw.get("sinks", 0),
+                               alone.data_ptr(), None, None, 0, None)
+    assert code == 0
+    torch.cuda.synchronize()
+    close(s, alone, **kw)
+    with pytest.raises(ep.EPError):
+        ep.ep_attn_prefill(cache, seqs, q, scratch=dirty[:n - 16].clone(), **kw)
+
+
 @pytest.mark.parametrize("decode", [True, False])
 def test_long_sequences(decode):
     """A cache of more than 2^32 bytes, with the sequence's pages at both of its ends."""
@@ -305,9 +337,11 @@ def test_prefill_not_finite_in_later_keys(what, quant):
             getattr(s, what)[p, r, 0, 5] = float("nan")
         else:
             getattr(s, what + "s")[p, 0, r] = 255
-    out, _ = run(s, False)
+    out, lse = run(s, False)
     clean = Seqs([300], [300], Hq=4, Hkv=2, quant=quant)
-    want, noise, _, _ = clean.attention()
+    want, noise, want_l, noise_l = clean.attention()
+    if what == "v":  # the sum of probabilities is without the values
+        assert ((lse.cpu().to(ref.F64) - want_l).abs() <= noise_l).all()
     ref.close_bf16(out[:130].cpu(), want[:130], noise[:130])
     ref.close_bf16(out[:, 2:].cpu(), want[:, 2:], noise[:, 2:])  # the other key head's queries
     hit = out[130:, :2].cpu()
