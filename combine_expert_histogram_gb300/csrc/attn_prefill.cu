@@ -7,19 +7,20 @@
 // rows see.  Roles:
 //   - a loader keeps a ring of key and value tiles in flight by tiled TMA loads, page by
 //     page;
-//   - one thread issues the products on tcgen05: S of a tile into tensor memory, and P V
-//     with P read from tensor memory, where it takes the place of S.  Two row tiles of 128
-//     alternate, so that one tile's exponentials run under the other's products; a block of
-//     at most 128 rows has the even key tiles in one and the odd ones in the other;
-//   - two warpgroups, a thread a row, take S out of tensor memory, and put P back in 16 bits,
-//     in two halves, so that the first one's products run under the second's exponentials.
+//   - one thread for each of two row tiles of 128 issues the products on tcgen05: S of a tile
+//     into tensor memory, and P V with P read from tensor memory, where it takes the place of
+//     S.  One tile's exponentials run under the other's products; a block of at most
+//     128 rows has the even key tiles in one and the odd ones in the other.  (With one thread
+//     for both, its waits for one tile left the other's products undone: 3700 clocks for two
+//     row tiles and 128 keys, where the products take 2270.);
+//   - two warpgroups, a thread a row, take S out of tensor memory, and put P back as bf16, in
+//     two halves, so that the first one's products run under the second's exponentials.
 //     m is let lag behind the true maximum by up to 2^8 (P and l stay far inside fp32, and
 //     P's relative rounding is the same), so that O is rescaled only in the rare tiles where
 //     a row's maximum jumps;
-//   - 8-bit caches: a warpgroup turns the E4M3 tiles into fp16, which is exact.  The
-//     keys' scales go to the logits, and the values' to the probabilities (as summands in
-//     the exponent).  bf16 caches: two warps look for values that are not finite in tiles
-//     that not all rows see: 0 * NaN would reach the other rows.
+//   - 8-bit caches: a warpgroup turns the E4M3 tiles into bf16, a thread a row, which is exact
+//     (a power of two times three bits).  bf16 caches: a warp looks for values that are not
+//     finite in tiles that not all rows see: 0 * NaN would reach the other rows.
 // Few blocks are multiplied by sharing their key tiles out among several, whose sums a second
 // kernel adds.
 #include "attn.cuh"
@@ -32,11 +33,10 @@ constexpr int kTile = 128;   // rows of a tile, keys of a tile
 constexpr int kRows = 2 * kTile;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 8.0f;  // log2 of how far m may be behind
-constexpr float kBoost = 5.0f;  // fp16 probabilities: log2 of the largest that does not lag
 
 struct Shared {
-    uint64_t full[5], empty[5], raw_full[2], raw_empty[2];
-    uint64_t q_full, s_full[2], p_ready[2][2], o_full[2], v_check, v_ok, drain;
+    uint64_t full[5], empty[5], raw_full[5], raw_empty[5];
+    uint64_t q_full[2], s_full[2], p_ready[2][2], o_full[2], turn[2], v_ok[4], drain;
     int64_t sums[16];
     uint32_t tmem;
     int fail, fix, issued;
@@ -50,12 +50,11 @@ struct Cfg {
     static constexpr int kSoftRegs = FP8 ? 184 : 208, kOtherRegs = FP8 ? 72 : 88;
     static constexpr int kPanels = D / 64;               // 128-byte columns of a tile
     static constexpr int kPanel = kTile * 128;
-    static constexpr int kStage = kPanels * kPanel;      // a 16-bit tile
-    static constexpr int kStages = FP8 ? 4 : 5;
-    static constexpr int kRaw = FP8 ? kTile * D : 0, kRaws = 2;
-    // of two tiles: the keys' (fp32), log2 of the values' (fp32), 1 / the values' (bf16)
-    static constexpr int kScaleTile = kTile * 10, kScales = FP8 ? 2 * kScaleTile : 0;
-    static constexpr int kSmem = (2 + kStages) * kStage + kRaws * kRaw + kScales + (int)sizeof(Shared);
+    static constexpr int kStage = kPanels * kPanel;      // a bf16 tile
+    static constexpr int kStages = FP8 && D == 128 ? 3 : 5;
+    // 8-bit tiles: memory answers after about 1.5 us, in which four are wanted
+    static constexpr int kRaw = FP8 ? kTile * D : 0, kRaws = D == 128 ? 4 : 5;
+    static constexpr int kSmem = (2 + kStages) * kStage + kRaws * kRaw + (int)sizeof(Shared);
 };
 
 struct PrefillArgs {
@@ -69,10 +68,9 @@ __host__ __device__ constexpr size_t ws_floats(int64_t blocks, int shares, int D
     return (size_t)blocks * shares * kRows * (D + 2);
 }
 
-// bf16 x bf16 (or fp16 x fp16) -> fp32; the second factor's rows may be along K (values)
-// instead of N.
-constexpr uint32_t instr16(bool half, int n, bool b_rows_k) {
-    return 1u << 4 | (half ? 0u : 1u << 7 | 1u << 10) | (uint32_t)b_rows_k << 16 | (uint32_t)(n / 8) << 17 |
+// bf16 x bf16 -> fp32; the second factor's rows may be along K (values) instead of N.
+constexpr uint32_t bf16_instr(int n, bool b_rows_k) {
+    return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)b_rows_k << 16 | (uint32_t)(n / 8) << 17 |
            (uint32_t)(kTile / 16) << 24;
 }
 // Descriptor of a value tile: 64 channels a 128-byte row, the rows along K, in 128-byte
@@ -81,7 +79,7 @@ __device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3ffffu) >> 4) | (uint64_t)(kTile * 128 >> 4) << 16 |
            (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-__device__ __forceinline__ void mma_16(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool accumulate) {
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
@@ -89,7 +87,7 @@ __device__ __forceinline__ void mma_16(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
 }
 // The first factor in tensor memory.
-__device__ __forceinline__ void mma_16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, bool accumulate) {
+__device__ __forceinline__ void mma_bf16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
@@ -134,19 +132,9 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
     return r;
 }
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 __device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
     return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
@@ -177,16 +165,10 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// In the upper bit of each half: whether that bf16 (fp16) is an infinity or NaN.
-template <bool HALF>
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-    return HALF ? ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u : ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-}
+// In the upper bit of each half: whether that bf16 is an infinity or NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 // w with the halves that are not finite as 0.
-template <bool HALF>
-__device__ __forceinline__ uint32_t finite_part(uint32_t w) {
-    return w & ~((not_finite<HALF>(w) >> 15) * 0xffffu);
-}
+__device__ __forceinline__ uint32_t finite_part(uint32_t w) { return w & ~((not_finite(w) >> 15) * 0xffffu); }
 
 // What a block works on, the same for all its threads.
 struct Block {
@@ -280,33 +262,34 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     using C = Cfg<D, FP8>;
     constexpr int kStages = C::kStages;
     // all of the block's shared memory: queries, the ring (the swizzle wants 1024-byte
-    // alignment; static arrays would push it off), 8-bit tiles, scales
+    // alignment; static arrays would push it off), 8-bit tiles
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem + 2 * C::kStage, *raws = ring + kStages * C::kStage;
-    uint8_t *scales = raws + C::kRaws * C::kRaw;
-    Shared &sh = *reinterpret_cast<Shared *>(scales + C::kScales);
+    Shared &sh = *reinterpret_cast<Shared *>(raws + C::kRaws * C::kRaw);
     const AttnArgs &a = d.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const volatile int *fail = &sh.fail;
-    constexpr int kMmaWarp = FP8 ? 12 : 9;
+    constexpr int kMmaWarp = FP8 ? 12 : 9;  // and the next one
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.full[i], FP8 ? 4 : 1);
-            mbar_init(&sh.empty[i], 1);
+            mbar_init(&sh.empty[i], FP8 ? 2 : 3);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kRaws; ++i) {
             mbar_init(&sh.raw_full[i], 1);
             mbar_init(&sh.raw_empty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.q_full[i], 4);
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_ready[i][0], 4);
             mbar_init(&sh.p_ready[i][1], 4);
             mbar_init(&sh.o_full[i], 1);
+            mbar_init(&sh.turn[i], 1);
         }
-        mbar_init(&sh.q_full, 8);
-        mbar_init(&sh.v_check, 1);
-        mbar_init(&sh.v_ok, 2);
-        mbar_init(&sh.drain, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&sh.v_ok[i], 1);
+        mbar_init(&sh.drain, 2);
         sh.fail = sh.fix = sh.issued = 0;
         mbar_init_fence();
         tma_prefetch_map(&kmap);
@@ -342,7 +325,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         constexpr int CH = D / 8, RP = 32 / CH;  // 16-byte chunks a row, rows an instruction
         const uint32_t mine = smem_addr(smem) + t * C::kStage;
         const int wrow = (warp & 3) * 32;
-        float sl2 = a.scale * kLog2e;  // FP8: of this row, whose queries are scaled
+        const float sl2 = a.scale * kLog2e;
         {
             uint4 x[32 / RP];
 #pragma unroll
@@ -353,31 +336,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32 / RP; ++i) {
                 const int r = wrow + i * RP + lane / CH, ch = lane % CH;
-                if constexpr (FP8) {
-                    // as fp16 next to 2^8 at most, exact down to 2^-32 of the row's largest
-                    uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                    float amax = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
-#pragma unroll
-                    for (int j = 1; j < CH; j <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, j));
-                    const int e = min(max((int)(__float_as_uint(amax) >> 23), 8), 254);
-                    const float up = __uint_as_float((uint32_t)(261 - e) << 23);
-                    const float down = __uint_as_float((uint32_t)max(e - 7, 0) << 23);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) w[j] = pack_half(bf16_lo(w[j]) * up, bf16_hi(w[j]) * up);
-                    x[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                    const float f = __shfl_sync(kFullMask, down, (lane % RP) * CH);
-                    if (lane / RP == i) sl2 *= f;
-                }
                 sts16(mine + (ch >> 3) * C::kPanel + r * 128 + 16 * ((ch & 7) ^ (r & 7)), x[i]);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.q_full);
+            if (lane == 0) mbar_arrive(&sh.q_full[t]);
         }
-        // bf16: m in S's units; FP8: in log2 units, of the logits with their values' scales
-        float m = -INFINITY, l = 0.0f;
+        float m = -INFINITY, l = 0.0f;  // m in S's units
         bool ok = true;
         int wmin = valid ? pos : 0x7fffffff, wmax = pos;  // of the warp's rows
 #pragma unroll
@@ -389,38 +354,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         int n = 0;
         for (int i = i_first; i < k.nt; i += stride, ++n) {
             const int key = k.key(i);
-            ok = mbar_wait_fast(&sh.s_full[t], n & 1, fail);
-            // the scales are there when the values are
-            if (FP8) ok = ok && mbar_wait_fast(&sh.full[(2 * i + 1) % kStages], ((2 * i + 1) / kStages) & 1, fail);
-            ok = __all_sync(kFullMask, ok);
+            ok = __all_sync(kFullMask, mbar_wait_fast(&sh.s_full[t], n & 1, fail));
             if (!ok) break;
             tc_fence_after();
             uint32_t v[4][32];
 #pragma unroll
             for (int x = 0; x < 4; ++x) tmem_ld(s_at + 32 * x, v[x]);
-            const uint32_t kf = smem_addr(scales) + (i & 1) * C::kScaleTile, vf = kf + kTile * 4, vi = vf + kTile * 4;
 #pragma unroll
             for (int x = 0; x < 4; ++x) tmem_ld_wait(v[x]);
-            if constexpr (FP8) {
-                const uint64_t sl = pair(sl2, sl2);
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const uint4 f = lds16(kf + (32 * x + j) * 4), e = lds16(vf + (32 * x + j) * 4);
-                        const uint64_t u = fma2(pair(__uint_as_float(v[x][j]), __uint_as_float(v[x][j + 1])),
-                                                mul2(pair(__uint_as_float(f.x), __uint_as_float(f.y)), sl),
-                                                pair(__uint_as_float(e.x), __uint_as_float(e.y)));
-                        const uint64_t w = fma2(pair(__uint_as_float(v[x][j + 2]), __uint_as_float(v[x][j + 3])),
-                                                mul2(pair(__uint_as_float(f.z), __uint_as_float(f.w)), sl),
-                                                pair(__uint_as_float(e.z), __uint_as_float(e.w)));
-                        float y0, y1;
-                        unpair(u, y0, y1);
-                        v[x][j] = __float_as_uint(y0), v[x][j + 1] = __float_as_uint(y1);
-                        unpair(w, y0, y1);
-                        v[x][j + 2] = __float_as_uint(y0), v[x][j + 3] = __float_as_uint(y1);
-                    }
-            }
             if (!(key + kTile - 1 <= wmin && (!a.window || key > wmax - a.window || key + kTile <= a.sinks))) {
                 const int hi = pos - key, lo = a.window && hi >= a.window ? hi - a.window + 1 : 0, s = a.sinks - key;
 #pragma unroll
@@ -439,11 +380,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     for (int x = 0; x < 4; ++x) part[x] = max3(part[x], __uint_as_float(v[x][j]), __uint_as_float(v[x][j + 1]));
                 top = fmaxf(max3(part[0], part[1], part[2]), part[3]);
             }
-            const float unit = FP8 ? 1.0f : sl2;
-            const bool grown = top > m && !((top - m) * unit <= kLag);
+            const bool grown = top > m && !((top - m) * sl2 <= kLag);
             if (__any_sync(kFullMask, grown)) {
                 const float next = grown ? top : m;
-                const float f = grown ? exp2_fast((m - next) * unit) : 1.0f;
+                const float f = grown ? exp2_fast((m - next) * sl2) : 1.0f;
                 l *= f;
                 m = next;
                 if (n > 0) {
@@ -459,35 +399,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 }
             }
             // a row that has seen no key yet subtracts 0 from its -infinities
-            const float base = (m == -INFINITY ? 0.0f : -m * unit) + (FP8 ? kBoost : 0.0f);
+            const float base = m == -INFINITY ? 0.0f : -m * sl2;
             const uint64_t sl = pair(sl2, sl2), bb = pair(base, base);
             uint64_t acc0 = pair(l, 0.0f), acc1 = pair(0.0f, 0.0f);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 uint32_t p[16];
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    uint4 e = make_uint4(0, 0, 0, 0);
-                    if (FP8) e = lds16(vi + (32 * x + 2 * j) * 2);
-                    const uint32_t inverse[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        uint64_t y = pair(__uint_as_float(v[x][2 * (j + z)]), __uint_as_float(v[x][2 * (j + z) + 1]));
-                        y = FP8 ? add2(y, bb) : fma2(y, sl, bb);
-                        float e0, e1;
-                        unpair(y, e0, e1);
-                        e0 = exp2_fast(e0);
-                        e1 = exp2_fast(e1);
-                        p[j + z] = FP8 ? pack_half(e0, e1) : pack_bf16(e0, e1);
-                        y = pair(e0, e1);
-                        uint64_t &acc = z & 1 ? acc1 : acc0;
-                        if constexpr (FP8) {
-                            // the probability itself: without the value's scale
-                            acc = fma2(y, pair(bf16_lo(inverse[z]), bf16_hi(inverse[z])), acc);
-                        } else {
-                            acc = add2(acc, y);
-                        }
-                    }
+                for (int j = 0; j < 16; ++j) {
+                    const uint64_t y = fma2(pair(__uint_as_float(v[x][2 * j]), __uint_as_float(v[x][2 * j + 1])), sl, bb);
+                    float e0, e1;
+                    unpair(y, e0, e1);
+                    e0 = exp2_fast(e0);
+                    e1 = exp2_fast(e1);
+                    p[j] = pack_bf16(e0, e1);
+                    if (j & 1)
+                        acc1 = add2(acc1, pair(e0, e1));
+                    else
+                        acc0 = add2(acc0, pair(e0, e1));
                 }
                 tmem_st(s_at + 16 * x, p);
                 if (x & 1) {  // half of the keys
@@ -503,9 +432,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             l = l0 + l1;
         }
         if (ok && n > 0) ok = __all_sync(kFullMask, mbar_wait_fast(&sh.o_full[t], 0, fail));
-        // m in log2 units
-        float m2 = FP8 ? m - kBoost : m * sl2;
-        if (m == -INFINITY) m2 = -INFINITY;
+        float m2 = m == -INFINITY ? m : m * sl2;  // in log2 units
         float f0 = 1.0f, f1 = 0.0f;  // of this warpgroup's sums, of the other's
         const uint32_t other = smem_addr(ring);  // [128][D] fp32, then [128] m2, l
         if (halves) {
@@ -596,7 +523,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                                         (none || (e & 0x7f00) == 0x7f00 ? 0x7fff0000u : 0u);
                                 } else {
                                     y = reinterpret_cast<const uint32_t *>(src)[16 * x + w];
-                                    y &= (not_finite<false>(y) >> 15) * 0xffffu;
+                                    y &= (not_finite(y) >> 15) * 0xffffu;
                                 }
                                 if (y) {
                                     o[2 * w] = __float_as_uint(__uint_as_float(o[2 * w]) + bf16_lo(y));
@@ -640,159 +567,151 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         const int role = warp - 8;
-        if (role == (FP8 ? 5 : 0)) {
-            // ---- loads: tile 0's keys, its values, tile 1's keys, ... ----
+        if (role == (FP8 ? 6 : 0)) {
+            // ---- loads: tile 0's keys, its values, tile 1's keys, ...; a lane a box ----
             const int box = d.box, boxes = kTile / box;
             constexpr int bytes = FP8 ? C::kRaw : C::kStage, slots = FP8 ? C::kRaws : kStages;
             uint64_t *fulls = FP8 ? sh.raw_full : sh.full, *empties = FP8 ? sh.raw_empty : sh.empty;
-            uint8_t *to = FP8 ? raws : ring;
-            int it = 0, page = 0, r = 0;
+            uint8_t *to = (FP8 ? raws : ring) + lane * box * (FP8 ? D : 128);
+            int it = 0;
             bool ok = true;
             for (int i = 0; ok && i < k.nt; ++i) {
                 const int key = k.key(i) + lane * box;
-                page = a.kv.pages;  // outside: zeros, and no reads
-                r = 0;
+                int page = a.kv.pages, r = 0;  // outside: zeros, and no reads
                 if (lane < boxes && k.wanted(key, box)) {
                     const int entry = key / a.kv.page_size;
                     const int p = page_of(a.kv, a.seq, k.b, entry);
                     if (p >= 0) page = p;
                     r = key - entry * a.kv.page_size;
                 }
-                for (int v = 0; ok && v < 2; ++v, ++it) {
+                for (int v = 0; v < 2; ++v, ++it) {
                     const int s = it % slots;
                     ok = __all_sync(kFullMask, it < slots || mbar_wait_fast(&empties[s], (it / slots - 1) & 1, fail));
                     if (!ok) {
                         sh.fail = 1;
                         break;
                     }
-                    const bool leader = elect_one();
-                    if (leader) expect_bytes(&fulls[s], bytes);
-                    for (int x = 0; x < boxes; ++x) {
-                        const int px = __shfl_sync(kFullMask, page, x), rx = __shfl_sync(kFullMask, r, x);
-                        if (leader) {
-                            uint8_t *dst = to + s * bytes;
-                            const CUtensorMap *map = v ? &vmap : &kmap;
-                            if constexpr (FP8) {
-                                tma_load_4d(dst + x * box * D, map, 0, k.h, rx, px, &fulls[s]);
-                            } else {
+                    if (elect_one()) expect_bytes(&fulls[s], bytes);
+                    __syncwarp();
+                    if (lane < boxes) {
+                        const CUtensorMap *map = v ? &vmap : &kmap;
 #pragma unroll
-                                for (int n = 0; n < C::kPanels; ++n)
-                                    tma_load_4d(dst + n * C::kPanel + x * box * 128, map, 128 * n, k.h, rx, px, &fulls[s]);
-                            }
-                        }
+                        for (int n = 0; n < (FP8 ? 1 : C::kPanels); ++n)
+                            tma_load_4d(to + s * bytes + n * C::kPanel, map, 128 * n, k.h, r, page, &fulls[s]);
                     }
                     __syncwarp();
                 }
             }
             if (lane == 0) sh.issued = it;
-        } else if (warp == kMmaWarp) {
-            // ---- products ----
-            constexpr uint32_t qk = instr16(FP8, kTile, false), pv = instr16(FP8, D, true);
-            int edges = 0;
+        } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+            // ---- products of row tile t ----
+            constexpr uint32_t qk = bf16_instr(kTile, false), pv = bf16_instr(D, true);
+            const int t = warp - kMmaWarp;
+            const uint64_t da = tile_desc(smem_addr(smem + t * C::kStage));
+            const uint32_t s_at = tmem + t * kTile, o_at = tmem + 2 * kTile + t * D;
             auto full = [&](int it) { return mbar_wait_fast(&sh.full[it % kStages], (it / kStages) & 1, fail); };
-            auto logits = [&](int t, int it) {
-                const uint64_t da = tile_desc(smem_addr(smem + t * C::kStage));
+            auto logits = [&](int it) {
                 const uint64_t db = tile_desc(smem_addr(ring + (it % kStages) * C::kStage));
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
                     const uint32_t at = (x / 4) * (C::kPanel / 16) + 2 * (x % 4);
-                    mma_16(tmem + t * kTile, da + at, db + at, qk, x > 0);
+                    mma_bf16(s_at, da + at, db + at, qk, x > 0);
                 }
                 mma_commit(&sh.s_full[t]);
             };
-            bool ok = k.nt == 0 || mbar_wait_fast(&sh.q_full, 0, fail);
-            // the first logits: of tile 0 for both, or of tiles 0 and 1
-            for (int t = 0; t < 2 && (halves ? t : 0) < k.nt; ++t) {
-                const int it = halves ? 2 * t : 0;
-                ok = __all_sync(kFullMask, ok && full(it));
+            // a tile is free when both rows' products have read it
+            auto release = [&](int it) {
+                mma_commit(&sh.empty[it % kStages]);
+                if (halves) mma_commit(&sh.empty[it % kStages]);
+            };
+            int i = halves ? t : 0, n = 0;
+            bool ok = true;
+            if (i < k.nt) {
+                ok = __all_sync(kFullMask, mbar_wait_fast(&sh.q_full[t], 0, fail) && full(2 * i));
+                if (ok) {
+                    tc_fence_after();
+                    if (elect_one()) {
+                        logits(2 * i);
+                        release(2 * i);
+                    }
+                    __syncwarp();
+                }
+            }
+            for (; ok && i < k.nt; i += stride, ++n) {
+                const int kt = 2 * (i + stride), vt = 2 * i + 1;
+                const bool more = i + stride < k.nt;
+                ok = full(vt) && (FP8 || !k.edge(k.key(i)) || mbar_wait_fast(&sh.v_ok[i & 3], (i >> 2) & 1, fail));
+                const uint64_t db = value_desc(smem_addr(ring + (vt % kStages) * C::kStage));
+                ok = __all_sync(kFullMask, ok && mbar_wait_fast(&sh.p_ready[t][0], n & 1, fail));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    logits(t, it);
-                    if (halves || t) mma_commit(&sh.empty[it]);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) mma_bf16_tmem(o_at, s_at + 8 * x, db + x * (2048 / 16), pv, n > 0 || x > 0);
                 }
                 __syncwarp();
-            }
-            int n = 0;
-            for (int i0 = 0; ok && i0 < k.nt; i0 += stride, ++n) {
-                bool check = false;
-                for (int t = 0; t < 2; ++t) {
-                    const int i = halves ? i0 + t : i0;
-                    if (i >= k.nt) break;
-                    const int kt = 2 * (i + stride), vt = 2 * i + 1;
-                    const bool more = i + stride < k.nt, own = halves || t == 0, done = halves || t == 1;
-                    if (own) {
-                        check = !FP8 && k.edge(k.key(i));
-                        ok = __all_sync(kFullMask, full(vt));
-                        if (check && ok && elect_one()) mbar_arrive(&sh.v_check);
-                        __syncwarp();
-                    }
-                    const uint64_t db = value_desc(smem_addr(ring + (vt % kStages) * C::kStage));
+                // The tiles take turns, so that one's exponentials run under the other's products:
+                // left alone they fall into step, and each waits for the other in both.
+                ok = mbar_wait_fast(&sh.p_ready[t][1], n & 1, fail);
+                ok = __all_sync(kFullMask, ok && (t + n == 0 || mbar_wait_fast(&sh.turn[t], (n + t - 1) & 1, fail)));
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        ok = ok && mbar_wait_fast(&sh.p_ready[t][half], n & 1, fail);
-                        if (half == 0 && own && check) ok = ok && mbar_wait_fast(&sh.v_ok, edges++ & 1, fail);
-                        ok = __all_sync(kFullMask, ok);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int x = 4 * half; x < 4 * half + 4; ++x)
-                                mma_16_tmem(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * x, db + x * (2048 / 16), pv, n > 0 || x > 0);
-                        }
-                        __syncwarp();
-                    }
-                    if (!ok) break;
-                    if (done && elect_one()) mma_commit(&sh.empty[vt % kStages]);
-                    __syncwarp();
-                    if (more) {
-                        ok = __all_sync(kFullMask, !own || full(kt));
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            logits(t, kt);
-                            if (done) mma_commit(&sh.empty[kt % kStages]);
-                        }
-                    } else if (elect_one()) {
+                    for (int x = 4; x < 8; ++x) mma_bf16_tmem(o_at, s_at + 8 * x, db + x * (2048 / 16), pv, true);
+                    release(vt);
+                    if (!more) {
                         mma_commit(&sh.o_full[t]);
+                        mbar_arrive(&sh.turn[t ^ 1]);
                     }
-                    __syncwarp();
                 }
+                __syncwarp();
+                if (!more) break;
+                // only now: these keys may be waiting for the values' place
+                ok = __all_sync(kFullMask, full(kt));
+                if (!ok) break;
+                if (elect_one()) {
+                    logits(kt);
+                    mbar_arrive(&sh.turn[t ^ 1]);
+                    release(kt);
+                }
+                __syncwarp();
             }
             if (!ok) sh.fail = 1;
             // tensor memory and the barriers outlive the last product
             if (elect_one()) mma_commit(&sh.drain);
             __syncwarp();
             if (!mbar_wait(&sh.drain, 0, nullptr)) sh.fail = 1;
-        } else if (!FP8 && role >= 2) {
-            // ---- values that are not finite, in tiles that not all rows see ----
+        } else if (!FP8 && role == 3) {
+            // ---- values that are not finite, in tiles that not all rows see.  It passes every
+            // tile, so that the barriers' phases are never two ahead of it. ----
             bool ok = true;
-            int edges = 0;
-            for (int i = 0; ok && i < k.nt; ++i) {
-                const int key = k.key(i), vt = 2 * i + 1;
-                if (!k.edge(key)) continue;
-                ok = mbar_wait_fast(&sh.v_check, edges++ & 1, fail) &&
-                     mbar_wait_fast(&sh.full[vt % kStages], (vt / kStages) & 1, fail);
-                ok = __all_sync(kFullMask, ok);
+            for (int it = 0; ok && it < 2 * k.nt; ++it) {
+                const int s = it % kStages, i = it >> 1, key = k.key(i);
+                ok = __all_sync(kFullMask, mbar_wait_fast(&sh.full[s], (it / kStages) & 1, fail));
                 if (!ok) break;
-                const uint32_t st = smem_addr(ring + (vt % kStages) * C::kStage);
-#pragma unroll 4
-                for (int x = (role - 2) * 32 + lane; x < C::kStage / 16; x += 64) {
-                    uint4 w = lds16(st + 16 * x);
-                    if (not_finite<false>(w.x) | not_finite<false>(w.y) | not_finite<false>(w.z) | not_finite<false>(w.w)) {
-                        const int j = key + (x * 16 % C::kPanel) / 128;
-                        if (k.wanted(j, 1)) sh.fix = 1;
-                        sts16(st + 16 * x, make_uint4(finite_part<false>(w.x), finite_part<false>(w.y),
-                                                      finite_part<false>(w.z), finite_part<false>(w.w)));
+                if ((it & 1) && k.edge(key)) {
+                    const uint32_t st = smem_addr(ring + s * C::kStage);
+#pragma unroll 8
+                    for (int x = lane; x < C::kStage / 16; x += 32) {
+                        uint4 w = lds16(st + 16 * x);
+                        if (not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w)) {
+                            const int j = key + (x * 16 % C::kPanel) / 128;
+                            if (k.wanted(j, 1)) sh.fix = 1;
+                            sts16(st + 16 * x, make_uint4(finite_part(w.x), finite_part(w.y), finite_part(w.z), finite_part(w.w)));
+                        }
                     }
+                    fence_proxy_async_smem();
                 }
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.v_ok);
+                if (lane == 0) {
+                    if (it & 1) mbar_arrive(&sh.v_ok[i & 3]);
+                    mbar_arrive(&sh.empty[s]);
+                }
             }
             if (!ok) sh.fail = 1;
         } else if (FP8 && role < 4) {
-            // ---- E4M3 rows to fp16, a thread a row ----
+            // ---- E4M3 rows to bf16, a thread a row ----
             const int r = role * 32 + lane;
             bool ok = true;
             // scale bytes of the row's key and value; 2^0 where there are none
@@ -814,11 +733,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             for (int i = 0; ok && i < k.nt; ++i) {
                 const int key = k.key(i);
                 const bool edge = k.edge(key), wanted = k.wanted(key + r, 1);
-                // a value whose scale is NaN is NaN itself, with the scale 1
-                const bool nan = sv == 255;
-                if (nan) sv = 127;
-                const float fk = scale_value(sk), ev = (float)((int)sv - 127);
-                const uint16_t inverse = (uint16_t)(sv == 254 ? 0x0040 : (254 - sv) << 7);  // 2^(127 - sv) as bf16
+                const float f[2] = {scale_value(sk), scale_value(sv)};
                 bytes(i + 1, sk, sv);
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
@@ -827,43 +742,40 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                          (it < kStages || mbar_wait_fast(&sh.empty[s], (it / kStages - 1) & 1, fail));
                     ok = __all_sync(kFullMask, ok);
                     if (!ok) break;
-                    const uint32_t src = smem_addr(raws + rs * C::kRaw), dst = smem_addr(ring + s * C::kStage);
+                    const uint32_t src = smem_addr(raws + rs * C::kRaw) + r * D, dst = smem_addr(ring + s * C::kStage) + r * 128;
                     uint32_t bad = 0;
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c) {
-                        uint32_t at = src + r * D + 16 * c;
+                        uint32_t at = src + 16 * c;
                         at ^= (at >> 3) & (D == 128 ? 0x70 : 0x30);  // the TMA's swizzle, by the address
                         const uint4 x = lds16(at);
                         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                         uint32_t y[8];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t p[2];
                             asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
                                 "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
-                                : "=r"(y[2 * j]), "=r"(y[2 * j + 1])
+                                : "=r"(p[0]), "=r"(p[1])
                                 : "r"(w[j]));
-                        if (v && nan) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) y[j] = 0x7fff7fffu;
+                            for (int z = 0; z < 2; ++z) {
+                                const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&p[z]));
+                                y[2 * j + z] = pack_bf16(g.x * f[v], g.y * f[v]);
+                            }
                         }
                         if (v && edge) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
-                                bad |= not_finite<true>(y[j]);
-                                y[j] = finite_part<true>(y[j]);
+                                bad |= not_finite(y[j]);
+                                y[j] = finite_part(y[j]);
                             }
                         }
-                        const uint32_t to = dst + (c >> 2) * C::kPanel + r * 128;
+                        const uint32_t to = dst + (c >> 2) * C::kPanel;
                         sts16(to + 16 * ((2 * c & 7) ^ (r & 7)), make_uint4(y[0], y[1], y[2], y[3]));
                         sts16(to + 16 * ((2 * c + 1 & 7) ^ (r & 7)), make_uint4(y[4], y[5], y[6], y[7]));
                     }
                     if (bad && wanted) sh.fix = 1;
-                    if (v) {  // the products of the tile two before are done, so its scales are free
-                        uint8_t *to = scales + (i & 1) * C::kScaleTile;
-                        reinterpret_cast<float *>(to)[r] = fk;
-                        reinterpret_cast<float *>(to)[kTile + r] = wanted ? ev : 0.0f;
-                        reinterpret_cast<uint16_t *>(to + 8 * kTile)[r] = wanted ? inverse : 0x3f80;
-                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
