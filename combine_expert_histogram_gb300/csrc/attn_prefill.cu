@@ -18,8 +18,8 @@
 //     m is let lag behind the true maximum by up to 2^8 (P and l stay far inside fp32, and
 //     P's relative rounding is the same), so that O is rescaled only in the rare tiles where
 //     a row's maximum jumps;
-//   - 8-bit caches: a warpgroup turns the E4M3 tiles into bf16, a thread a row, which is exact
-//     (a power of two times three bits).  bf16 caches: a warp looks for values that are not
+//   - 8-bit caches: two warpgroups turn the E4M3 tiles into bf16, a thread half a row, which is
+//     exact (a power of two times three bits).  bf16 caches: a warp looks for values that are not
 //     finite in tiles that not all rows see: 0 * NaN would reach the other rows.
 // Few blocks are multiplied by sharing their key tiles out among several, whose sums a second
 // kernel adds.
@@ -37,7 +37,7 @@ constexpr float kLag = 8.0f;  // log2 of how far m may be behind
 struct Shared {
     uint64_t full[5], empty[5], raw_full[5], raw_empty[5];
     uint64_t q_full[2], s_full[2], p_ready[2][2], o_full[2], turn[2], v_ok[4], drain;
-    int64_t sums[16];
+    int64_t sums[20];
     uint32_t tmem;
     int fail, fix, issued;
     int b, block;
@@ -45,9 +45,9 @@ struct Shared {
 
 template <int D, bool FP8>
 struct Cfg {
-    static constexpr int kThreads = FP8 ? 512 : 384;
-    // registers a thread: 128 or 168 at launch
-    static constexpr int kSoftRegs = FP8 ? 184 : 208, kOtherRegs = FP8 ? 72 : 88;
+    static constexpr int kThreads = FP8 ? 640 : 384;
+    // registers a thread: 96 or 168 at launch
+    static constexpr int kSoftRegs = FP8 ? 168 : 208, kOtherRegs = FP8 ? 48 : 88;
     static constexpr int kPanels = D / 64;               // 128-byte columns of a tile
     static constexpr int kPanel = kTile * 128;
     static constexpr int kStage = kPanels * kPanel;      // a bf16 tile
@@ -273,12 +273,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], FP8 ? 4 : 1);
+            mbar_init(&sh.full[i], FP8 ? 8 : 1);
             mbar_init(&sh.empty[i], FP8 ? 2 : 3);
         }
         for (int i = 0; i < C::kRaws; ++i) {
             mbar_init(&sh.raw_full[i], 1);
-            mbar_init(&sh.raw_empty[i], 4);
+            mbar_init(&sh.raw_empty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.q_full[i], 4);
@@ -710,9 +710,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 }
             }
             if (!ok) sh.fail = 1;
-        } else if (FP8 && role < 4) {
-            // ---- E4M3 rows to bf16, a thread a row ----
-            const int r = role * 32 + lane;
+        } else if (FP8 && (role < 4 || role >= 8)) {
+            // ---- E4M3 rows to bf16, a thread half a row ----
+            const int r = (role & 3) * 32 + lane, c0 = role < 4 ? 0 : D / 32;
             bool ok = true;
             // scale bytes of the row's key and value; 2^0 where there are none
             auto bytes = [&](int i, uint32_t &sk, uint32_t &sv) {
@@ -744,12 +744,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     if (!ok) break;
                     const uint32_t src = smem_addr(raws + rs * C::kRaw) + r * D, dst = smem_addr(ring + s * C::kStage) + r * 128;
                     uint32_t bad = 0;
+                    uint4 x[D / 32];  // all of it first: it takes its time
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t at = src + 16 * c;
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t at = src + 16 * (c0 + c);
                         at ^= (at >> 3) & (D == 128 ? 0x70 : 0x30);  // the TMA's swizzle, by the address
-                        const uint4 x = lds16(at);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        x[c] = lds16(at);
+                    }
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
                         uint32_t y[8];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -771,9 +775,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                                 y[j] = finite_part(y[j]);
                             }
                         }
-                        const uint32_t to = dst + (c >> 2) * C::kPanel;
-                        sts16(to + 16 * ((2 * c & 7) ^ (r & 7)), make_uint4(y[0], y[1], y[2], y[3]));
-                        sts16(to + 16 * ((2 * c + 1 & 7) ^ (r & 7)), make_uint4(y[4], y[5], y[6], y[7]));
+                        const int ch = 2 * (c0 + c);
+                        const uint32_t to = dst + (ch >> 3) * C::kPanel;
+                        sts16(to + 16 * ((ch & 7) ^ (r & 7)), make_uint4(y[0], y[1], y[2], y[3]));
+                        sts16(to + 16 * ((ch + 1 & 7) ^ (r & 7)), make_uint4(y[4], y[5], y[6], y[7]));
                     }
                     if (bad && wanted) sh.fix = 1;
                     fence_proxy_async_smem();
