@@ -166,7 +166,7 @@ size_t ep_attn_prefill_workspace_bytes(int32_t T, int32_t B, int32_t Hq, int32_t
     if (T < 0 || B < 0 || check_heads(Hq, Hkv) != EP_OK || check_head_dim(D) != EP_OK ||
         (int64_t)T * Hq > EP_ATTN_MAX_ROWS)
         return 0;
-    return attn_prefill_workspace(T, B, Hq, Hkv, D);
+    return attn_prefill_workspace(D);
 }
 
 ep_status_t ep_attn_prefill(const ep_kv_cache_t *c, const ep_kv_seqs_t *s, const void *q,
@@ -179,7 +179,7 @@ ep_status_t ep_attn_prefill(const ep_kv_cache_t *c, const ep_kv_seqs_t *s, const
     if (st != EP_OK || no_rows(s)) return st;
     if (workspace &&
         (!aligned(workspace, 16) ||
-         workspace_bytes < attn_prefill_workspace(s->num_tokens, s->num_seqs, Hq, c->num_kv_heads, c->head_dim)))
+         workspace_bytes < attn_prefill_workspace(c->head_dim)))
         return EP_ERR_INVALID_ARG;
     return from_cuda(launch_attn_prefill(a, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }

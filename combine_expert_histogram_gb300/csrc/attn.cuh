@@ -79,6 +79,29 @@ __device__ __forceinline__ int page_of(const KvArgs &kv, const SeqArgs &s, int b
     return -1;
 }
 
+// ld_dep_v4 where `there`, else zeros, without a branch: one would wait for each load where
+// its two ways meet.
+__device__ __forceinline__ uint4 ld_dep_v4_if(bool there, const void *p) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@p ld.global.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((uint32_t)there)
+        : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_dep_if(bool there, const void *p) {
+    uint32_t v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, 0;\n\t@p ld.global.u32 %0, [%1];\n\t}"
+        : "=&r"(v)
+        : "l"(p), "r"((uint32_t)there)
+        : "memory");
+    return v;
+}
+
 // The value of an E8M0 scale (255: NaN).
 __device__ __forceinline__ float scale_value(uint32_t e) {
     return e == 255 ? __uint_as_float(0x7fffffffu) : ue8m0_value(e);
@@ -93,6 +116,6 @@ cudaError_t launch_attn_decode(const AttnArgs &a, void *workspace, cudaStream_t 
 size_t attn_decode_workspace(int B, int Hq, int Hkv, int D);
 // workspace may be nullptr.
 cudaError_t launch_attn_prefill(const AttnArgs &a, void *workspace, cudaStream_t stream);
-size_t attn_prefill_workspace(int T, int B, int Hq, int Hkv, int D);
+size_t attn_prefill_workspace(int D);
 
 }  // namespace ep

@@ -512,11 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (!FP8) {
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i)
-                    word[n][i] = r < heads ? (uint32_t)ld_dep(reinterpret_cast<const int32_t *>(src + 8 * i + 2 * c)) : 0u;
+                    word[n][i] = ld_dep_if(r < heads, src + 8 * i + 2 * c);
             } else {
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
-                    const uint4 v = r < heads ? ld_dep_v4(src + D / 4 * c + 8 * i) : make_uint4(0, 0, 0, 0);
+                    const uint4 v = ld_dep_v4_if(r < heads, src + D / 4 * c + 8 * i);
                     word[n][4 * i] = v.x;
                     word[n][4 * i + 1] = v.y;
                     word[n][4 * i + 2] = v.z;

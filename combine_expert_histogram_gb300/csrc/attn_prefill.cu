@@ -21,8 +21,10 @@
 //   - 8-bit caches: two warpgroups turn the E4M3 tiles into bf16, a thread half a row, which is
 //     exact (a power of two times three bits).  bf16 caches: a warp looks for values that are not
 //     finite in tiles that not all rows see: 0 * NaN would reach the other rows.
-// Few blocks are multiplied by sharing their key tiles out among several, whose sums a second
-// kernel adds.
+// The work, a step being one tile of keys (two, for a block of at most 128 rows), is one list
+// over sequences, key heads and row blocks, of which every SM takes an equal run, wherever row
+// blocks begin and end; a row block that several SMs share leaves its sums in the workspace, and
+// a second kernel adds them.  The loader walks the run and tells the other roles its pieces.
 #include "attn.cuh"
 #include "tcgen05.cuh"
 
@@ -34,38 +36,76 @@ constexpr int kRows = 2 * kTile;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 8.0f;  // log2 of how far m may be behind
 
+constexpr int kItem = 4;    // steps of time that a row block costs beside its own
+constexpr int kLeast = 3;   // steps an SM takes at least
+constexpr int kPieces = 4;  // pieces ahead
+
+// A piece of the list: some of a row block's tiles.
+struct Piece {
+    int b, h;            // sequence, key head
+    int row0, rows;      // first row (token * G + head) in the sequence, rows of the block
+    int first, pos0;     // token of q that is the sequence's first, its position
+    int minpos, maxpos;  // of the block's rows
+    int lo, S;           // keys [lo, maxpos] and [0, S), S <= lo, are seen by some row
+    int tile0, ns;       // tiles 0 .. ns-1, then from tile0 on
+    int i0, nt;          // the piece's tiles, the first of them; nt < 0: there is no piece more
+    int part;            // where its sums go in the workspace, -1: it is a whole block
+    __device__ __forceinline__ int key(int i) const {
+        i += i0;
+        return (i < ns ? i : tile0 + i - ns) * kTile;
+    }
+    // Not all rows see all of the tile's keys.
+    __device__ __forceinline__ bool edge(int key, int window, int sinks) const {
+        return !(key + kTile - 1 <= minpos &&
+                 (!window || key > maxpos - window || key + kTile <= sinks));
+    }
+    // Some row may see one of the keys [key, key + n).
+    __device__ __forceinline__ bool wanted(int key, int n) const {
+        return key <= maxpos && (key + n > lo || key < S);
+    }
+    // One row tile: its even key tiles are in one half, its odd ones in the other.
+    __device__ __forceinline__ bool halves() const { return rows <= kTile; }
+    __device__ __forceinline__ int steps() const { return halves() ? (nt + 1) / 2 : nt; }
+    // Of row tile t, or half t.
+    __device__ __forceinline__ int tiles(int t) const { return halves() ? (nt + 1 - t) / 2 : nt; }
+};
+
 struct Shared {
-    uint64_t full[5], empty[5], raw_full[5], raw_empty[5];
-    uint64_t q_full[2], s_full[2], p_ready[2][2], o_full[2], turn[2], v_ok[4], drain;
-    int64_t sums[20];
+    uint64_t full[5], empty[5], raw_full[4], raw_empty[4];
+    uint64_t q_full[2], s_full[2], p_ready[2][2], o_full[2], turn[2], v_ok[4], ml_ready, o_read, drain;
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
+    int64_t sums[20], found_at;
+    float2 ml[kTile];  // of the odd tiles' half
+    Piece pieces[kPieces];
     uint32_t tmem;
-    int fail, fix, issued;
-    int b, block;
+    int fail, fix, issued, found_b;
 };
 
 template <int D, bool FP8>
 struct Cfg {
     static constexpr int kThreads = FP8 ? 640 : 384;
     // registers a thread: 96 or 168 at launch
-    static constexpr int kSoftRegs = FP8 ? 168 : 208, kOtherRegs = FP8 ? 48 : 88;
+    static constexpr int kSoftRegs = FP8 ? 144 : 208, kOtherRegs = FP8 ? 64 : 88;
     static constexpr int kPanels = D / 64;               // 128-byte columns of a tile
     static constexpr int kPanel = kTile * 128;
     static constexpr int kStage = kPanels * kPanel;      // a bf16 tile
     static constexpr int kStages = FP8 && D == 128 ? 3 : 5;
     // 8-bit tiles: memory answers after about 1.5 us, in which four are wanted
-    static constexpr int kRaw = FP8 ? kTile * D : 0, kRaws = D == 128 ? 4 : 5;
+    static constexpr int kRaw = FP8 ? kTile * D : 0, kRaws = 4;
     static constexpr int kSmem = (2 + kStages) * kStage + kRaws * kRaw + (int)sizeof(Shared);
 };
 
 struct PrefillArgs {
     AttnArgs a;
-    int G, box;  // query heads a key head; cache rows of a TMA box
-    int shares;  // blocks that may share one's key tiles
-    float *ws;   // [block][share][row]: m (log2), l; then [block][share][row][D]
-    int64_t blocks;
+    int G, box;   // query heads a key head; cache rows of a TMA box
+    uint8_t *ws;  // nullptr: row blocks stay whole
 };
-__host__ __device__ constexpr size_t ws_floats(int64_t blocks, int shares, int D) {
-    return (size_t)blocks * shares * kRows * (D + 2);
+// The workspace: for each SM the shared row block that begins in its run (sequence, head, block,
+// SMs after it); m (log2) and l of its first and last piece's rows; their sums.
+__host__ __device__ constexpr size_t ws_ml(int blocks) { return (size_t)blocks * 16; }
+__host__ __device__ constexpr size_t ws_sums(int blocks) { return ws_ml(blocks) + (size_t)blocks * 2 * kRows * 8; }
+__host__ __device__ constexpr size_t ws_bytes(int blocks, int D) {
+    return ws_sums(blocks) + (size_t)blocks * 2 * kRows * D * 4;
 }
 
 // bf16 x bf16 -> fp32; the second factor's rows may be along K (values) instead of N.
@@ -100,6 +140,12 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
         "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
         : "memory");
+}
+__device__ __forceinline__ void st_v8(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                      uint32_t g, uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e),
+                 "r"(f), "r"(g), "r"(h)
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
@@ -170,89 +216,36 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7f80
 // w with the halves that are not finite as 0.
 __device__ __forceinline__ uint32_t finite_part(uint32_t w) { return w & ~((not_finite(w) >> 15) * 0xffffu); }
 
-// What a block works on, the same for all its threads.
-struct Block {
-    int b, h;            // sequence, key head
-    int row0, rows;      // first row (token * G + head) in the sequence, rows of the block
-    int first, pos0;     // token of q that is the sequence's first, its position
-    int minpos, maxpos;  // of the block's rows
-    int lo, S;           // keys [lo, maxpos] and [0, S), S <= lo, are seen by some row
-    int tile0, ns;       // tiles 0 .. ns-1, then from tile0 on
-    int nt, i0;          // this share's tiles, of which the first
-    int shares;          // blocks that share the rows
-    int window, sinks;
-    __device__ __forceinline__ int key(int i) const {
-        i += i0;
-        return (i < ns ? i : tile0 + i - ns) * kTile;
-    }
-    // Not all rows see all of the tile's keys.
-    __device__ __forceinline__ bool edge(int key) const {
-        return !(key + kTile - 1 <= minpos &&
-                 (!window || key > maxpos - window || key + kTile <= sinks));
-    }
-    // Some row may see one of the keys [key, key + n).
-    __device__ __forceinline__ bool wanted(int key, int n) const {
-        return key <= maxpos && (key + n > lo || key < S);
-    }
-};
+__device__ __forceinline__ int row_blocks(const PrefillArgs &d, const Span &sp) { return (sp.n * d.G + kRows - 1) / kRows; }
 
-// Block `index` of a key head: blocks of 256 rows, a sequence's last ones (with the most keys)
-// first.  False if there are not so many.  All threads of the block call it.
-template <int NT>
-__device__ __forceinline__ bool find_block(const PrefillArgs &d, int64_t index, int h, int share, Shared &sh, Block &k) {
-    const AttnArgs &a = d.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int64_t before = 0;
-    for (int b0 = 0; b0 < a.seq.B; b0 += NT) {
-        const int b = b0 + threadIdx.x;
-        int64_t n = 0;
-        if (b < a.seq.B) n = ((int64_t)seq_span(a.seq, a.kv.page_size, b).n * d.G + kRows - 1) / kRows;
-        int64_t incl = n;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const int64_t o = __shfl_up_sync(kFullMask, incl, s);
-            if (lane >= s) incl += o;
-        }
-        __syncthreads();
-        if (lane == 31) sh.sums[warp] = incl;
-        __syncthreads();
-        int64_t all = 0, below = 0;
-#pragma unroll
-        for (int i = 0; i < NT / 32; ++i) {
-            if (i == warp) below = all;
-            all += sh.sums[i];
-        }
-        incl += before + below;
-        if (index >= incl - n && index < incl) {
-            sh.b = b;
-            sh.block = (int)(incl - 1 - index);
-        }
-        before += all;
-        if (before > index) break;
-    }
-    __syncthreads();
-    if (before <= index) return false;
-    k.b = sh.b;
-    k.h = h;
-    const Span sp = seq_span(a.seq, a.kv.page_size, k.b);
+// Row block j of a sequence and any head, whole: those with the last rows come first.
+__device__ __forceinline__ Piece row_block(const PrefillArgs &d, const Span &sp, int j) {
+    Piece k;
     k.first = sp.first;
     k.pos0 = sp.len - sp.n;
-    k.row0 = sh.block * kRows;
+    k.row0 = (row_blocks(d, sp) - 1 - j) * kRows;
     k.rows = min(sp.n * d.G - k.row0, kRows);
     k.minpos = k.pos0 + k.row0 / d.G;
     k.maxpos = k.pos0 + (k.row0 + k.rows - 1) / d.G;
-    k.window = a.window;
-    k.sinks = k.S = a.sinks;
-    k.lo = a.window && k.minpos >= a.window ? k.minpos - a.window + 1 : 0;
+    k.S = d.a.sinks;
+    k.lo = d.a.window && k.minpos >= d.a.window ? k.minpos - d.a.window + 1 : 0;
     if (k.S >= k.lo) k.lo = k.S = 0;
     k.tile0 = k.lo / kTile;
     k.ns = min((k.S + kTile - 1) / kTile, k.tile0);
-    const int nt = k.maxpos < 0 ? 0 : k.ns + k.maxpos / kTile + 1 - k.tile0;
-    // two tiles a share at least
-    k.shares = min(d.shares, max(nt / 2, 1));
-    k.i0 = (int)((int64_t)nt * share / k.shares);
-    k.nt = (int)((int64_t)nt * (share + 1) / k.shares) - k.i0;
-    return share < k.shares;
+    k.i0 = 0;
+    k.nt = k.maxpos < 0 ? 0 : k.ns + k.maxpos / kTile + 1 - k.tile0;
+    k.part = -1;
+    return k;
+}
+// Its places in the list.
+__device__ __forceinline__ int places(const PrefillArgs &d, const Piece &k) { return d.ws ? k.steps() + kItem : 1; }
+// The places of all of a sequence's blocks of one head, by one warp.
+__device__ __forceinline__ int64_t all_places(const PrefillArgs &d, const Span &sp, int lane) {
+    int64_t n = 0;
+    for (int j = lane; j < row_blocks(d, sp); j += 32) n += places(d, row_block(d, sp, j));
+#pragma unroll
+    for (int x = 16; x; x >>= 1) n += __shfl_xor_sync(kFullMask, n, x);
+    return n;
 }
 
 template <int D, bool FP8>
@@ -289,6 +282,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             mbar_init(&sh.turn[i], 1);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&sh.v_ok[i], 1);
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&sh.piece_full[i], 1);
+            mbar_init(&sh.piece_empty[i], FP8 ? 18 : 11);  // warps that read it
+        }
+        mbar_init(&sh.ml_ready, 4);
+        mbar_init(&sh.o_read, 4);
         mbar_init(&sh.drain, 2);
         sh.fail = sh.fix = sh.issued = 0;
         mbar_init_fence();
@@ -297,51 +296,123 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    Block k;
-    const int share = blockIdx.x % d.shares;
-    const int64_t block = blockIdx.x / d.shares;
-    if (!find_block<C::kThreads>(d, block / a.kv.Hkv, (int)(block % a.kv.Hkv), share, sh, k)) return;
-    // one row tile: its even key tiles here, its odd ones there
-    const bool halves = k.rows <= kTile;
-    const int stride = halves ? 2 : 1;
+    // ---- the block's run of the list, and its first sequence ----
+    int64_t total = 0, n0 = 0, excl0 = 0;
+    auto scan = [&](int b0, int64_t &n, int64_t &excl) {
+        const int b = b0 + threadIdx.x;
+        Span sp = {0, 0, 0};
+        if (b < a.seq.B) sp = seq_span(a.seq, a.kv.page_size, b);
+        const int nb = row_blocks(d, sp);
+        n = 0;
+        if (nb <= 4)
+            for (int j = 0; j < nb; ++j) n += places(d, row_block(d, sp, j));
+        for (uint32_t many = __ballot_sync(kFullMask, nb > 4); many; many &= many - 1) {
+            const int src = __ffs(many) - 1;
+            const Span one = {__shfl_sync(kFullMask, sp.first, src), __shfl_sync(kFullMask, sp.n, src),
+                              __shfl_sync(kFullMask, sp.len, src)};
+            const int64_t m = all_places(d, one, lane);
+            if (lane == src) n = m;
+        }
+        n *= a.kv.Hkv;
+        int64_t incl = n;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int64_t o = __shfl_up_sync(kFullMask, incl, s);
+            if (lane >= s) incl += o;
+        }
+        __syncthreads();
+        if (lane == 31) sh.sums[warp] = incl;
+        __syncthreads();
+        int64_t all = 0, below = 0;
+#pragma unroll
+        for (int i = 0; i < C::kThreads / 32; ++i) {
+            if (i == warp) below = all;
+            all += sh.sums[i];
+        }
+        excl = incl - n + below;
+        return all;
+    };
+    for (int b0 = 0; b0 < a.seq.B; b0 += C::kThreads) {
+        int64_t n, excl;
+        total += scan(b0, n, excl);
+        if (b0 == 0) n0 = n, excl0 = excl;
+    }
+    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(d.ws ? kLeast : 1));
+    const int64_t x0 = blockIdx.x * per, x1 = min(x0 + per, total);
+    if (d.ws && threadIdx.x == 0) reinterpret_cast<int4 *>(d.ws)[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (x0 >= x1) return;
+    int64_t before = 0;
+    for (int b0 = 0;; b0 += C::kThreads) {
+        int64_t n = n0, excl = excl0, all = total;
+        if (a.seq.B > C::kThreads) all = scan(b0, n, excl);
+        if (x0 >= before + excl && x0 < before + excl + n) {
+            sh.found_b = b0 + threadIdx.x;
+            sh.found_at = before + excl;
+        }
+        before += all;
+        if (before > x0 || b0 + C::kThreads >= a.seq.B) break;
+    }
     if (warp == kMmaWarp) tmem_alloc<512>(&sh.tmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;  // S (and P) of both tiles, then O of both
+    // The next piece of the run, for a warp that goes through them.
+    auto next_piece = [&](int p, Piece &k) {
+        const bool ok = __all_sync(kFullMask, mbar_wait_fast(&sh.piece_full[p % kPieces], (p / kPieces) & 1, fail));
+        if (!ok) {
+            sh.fail = 1;
+            return false;
+        }
+        k = sh.pieces[p % kPieces];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.piece_empty[p % kPieces]);
+        return k.nt >= 0;
+    };
 
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
-        // ---- a thread's row ----
-        const int t = warp >> 2, local = (halves ? 0 : t * kTile) + (warp & 3) * 32 + lane;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int t = warp >> 2, wrow = (warp & 3) * 32;
+        const uint32_t lanes = (uint32_t)wrow << 16;
         const uint32_t s_at = tmem + t * kTile + lanes, o_at = tmem + 2 * kTile + t * D + lanes;
-        const bool valid = local < k.rows;
-        const int row = k.row0 + local, token = row / d.G;
-        const int pos = valid ? k.pos0 + token : -1;
-        const int64_t head = (int64_t)k.h * d.G + (row - token * d.G);
-        const int64_t q_off = valid ? (k.first + token) * a.q_stride + head * D : -1;
-        const int64_t o_off = valid ? ((int64_t)(k.first + token) * a.Hq + head) * D : -1;
         constexpr int CH = D / 8, RP = 32 / CH;  // 16-byte chunks a row, rows an instruction
         const uint32_t mine = smem_addr(smem) + t * C::kStage;
-        const int wrow = (warp & 3) * 32;
         const float sl2 = a.scale * kLog2e;
-        {
-            uint4 x[32 / RP];
-#pragma unroll
+        int done = 0, o_done = 0, merged = 0;  // tiles, pieces with tiles, pieces in halves so far
+        // The queries of a piece, asynchronously into their tile; zeros where there is no row.
+        auto copy_queries = [&](const Piece &k) {
+            const int local = (k.halves() ? 0 : t * kTile) + wrow + lane, row = k.row0 + local, token = row / d.G;
+            const int64_t off = local < k.rows ? (k.first + token) * a.q_stride + ((int64_t)k.h * d.G + (row - token * d.G)) * D : -1;
+#pragma unroll 4
             for (int i = 0; i < 32 / RP; ++i) {
-                const int64_t off = __shfl_sync(kFullMask, q_off, i * RP + lane / CH);
-                x[i] = off >= 0 ? ld_dep_v4(a.q + off + 8 * (lane % CH)) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < 32 / RP; ++i) {
+                const int64_t o = __shfl_sync(kFullMask, off, i * RP + lane / CH);
                 const int r = wrow + i * RP + lane / CH, ch = lane % CH;
-                sts16(mine + (ch >> 3) * C::kPanel + r * 128 + 16 * ((ch & 7) ^ (r & 7)), x[i]);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 mine + (ch >> 3) * C::kPanel + r * 128 + 16 * ((ch & 7) ^ (r & 7))),
+                             "l"(a.q + (o >= 0 ? o + 8 * ch : 0)), "r"(o >= 0 ? 16 : 0)
+                             : "memory");
             }
+        };
+        auto queries_there = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.q_full[t]);
+        };
+        Piece k;
+        bool have = next_piece(0, k);
+        if (have && k.tiles(t) > 0) {
+            copy_queries(k);
+            queries_there();
         }
+        for (int p = 1; have; ++p) {
+        // ---- a thread's row ----
+        const bool halves = k.halves();
+        const int local = (halves ? 0 : t * kTile) + wrow + lane;
+        const bool valid = local < k.rows;
+        const int row = k.row0 + local, token = row / d.G;
+        const int pos = valid ? k.pos0 + token : -1;
+        const int mine_of = k.tiles(t);
         float m = -INFINITY, l = 0.0f;  // m in S's units
         bool ok = true;
         int wmin = valid ? pos : 0x7fffffff, wmax = pos;  // of the warp's rows
@@ -350,36 +421,53 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             wmin = min(wmin, __shfl_xor_sync(kFullMask, wmin, x));
             wmax = max(wmax, __shfl_xor_sync(kFullMask, wmax, x));
         }
-        const int i_first = halves ? t : 0;
-        int n = 0;
-        for (int i = i_first; i < k.nt; i += stride, ++n) {
-            const int key = k.key(i);
-            ok = __all_sync(kFullMask, mbar_wait_fast(&sh.s_full[t], n & 1, fail));
+        for (int n = 0; n < mine_of; ++n, ++done) {
+            const int key = k.key(halves ? 2 * n + t : n);
+            ok = __all_sync(kFullMask, mbar_wait_fast(&sh.s_full[t], done & 1, fail));
             if (!ok) break;
             tc_fence_after();
-            uint32_t v[4][32];
+            // All of the row's S in registers; 8-bit caches, whose other roles leave fewer, take it
+            // twice, for the maximum and for the exponentials (a tenth longer with bf16, and
+            // as much shorter than with the registers spilled).
+            uint32_t u[FP8 ? 2 : 4][32];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) tmem_ld(s_at + 32 * x, v[x]);
+            for (int x = 0; x < (FP8 ? 1 : 4); ++x) tmem_ld(s_at + 32 * x, u[x]);
+            const bool masked = !(key + kTile - 1 <= wmin && (!a.window || key > wmax - a.window || key + kTile <= a.sinks));
+            const int hi = pos - key + 1, lo = a.window && hi > a.window ? hi - a.window : 0, first = a.sinks - key;
+            auto mask = [&](uint32_t (&v)[32], int at) {
+                if (!masked) return;
+                const uint32_t seen = low_bits(hi - at) & (~low_bits(lo - at) | low_bits(first - at));
 #pragma unroll
-            for (int x = 0; x < 4; ++x) tmem_ld_wait(v[x]);
-            if (!(key + kTile - 1 <= wmin && (!a.window || key > wmax - a.window || key + kTile <= a.sinks))) {
-                const int hi = pos - key, lo = a.window && hi >= a.window ? hi - a.window + 1 : 0, s = a.sinks - key;
+                for (int j = 0; j < 32; ++j) v[j] = seen >> j & 1 ? v[j] : 0xff800000u;  // -infinity
+            };
+            float part[4] = {m, m, m, m};
+            auto largest = [&](const uint32_t (&v)[32]) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const uint32_t seen = low_bits(hi + 1 - 32 * x) & (~low_bits(lo - 32 * x) | low_bits(s - 32 * x));
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[x][j] = seen >> j & 1 ? v[x][j] : 0xff800000u;  // -infinity
+                for (int j = 0; j < 32; j += 2) part[j / 2 & 3] = max3(part[j / 2 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+            };
+            if constexpr (FP8) {
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    tmem_ld_wait(u[0]);
+                    tmem_ld(s_at + 64 * h + 32, u[1]);
+                    mask(u[0], 64 * h);
+                    largest(u[0]);
+                    tmem_ld_wait(u[1]);
+                    tmem_ld(s_at + 64 * (h ^ 1), u[0]);  // the last time: the first columns again
+                    mask(u[1], 64 * h + 32);
+                    largest(u[1]);
                 }
-            }
-            float top = m;
-            {
-                float part[4] = {m, m, m, m};
+            } else {
 #pragma unroll
-                for (int j = 0; j < 32; j += 2)
+                for (int x = 0; x < 4; ++x) tmem_ld_wait(u[x]);
+                if (masked) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) part[x] = max3(part[x], __uint_as_float(v[x][j]), __uint_as_float(v[x][j + 1]));
-                top = fmaxf(max3(part[0], part[1], part[2]), part[3]);
+                    for (int x = 0; x < 4; ++x) mask(u[x], 32 * x);
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) largest(u[x]);
             }
+            const float top = fmaxf(max3(part[0], part[1], part[2]), part[3]);
             const bool grown = top > m && !((top - m) * sl2 <= kLag);
             if (__any_sync(kFullMask, grown)) {
                 const float next = grown ? top : m;
@@ -402,12 +490,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             const float base = m == -INFINITY ? 0.0f : -m * sl2;
             const uint64_t sl = pair(sl2, sl2), bb = pair(base, base);
             uint64_t acc0 = pair(l, 0.0f), acc1 = pair(0.0f, 0.0f);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            auto exponentials = [&](const uint32_t (&v)[32], uint32_t to) {
                 uint32_t p[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const uint64_t y = fma2(pair(__uint_as_float(v[x][2 * j]), __uint_as_float(v[x][2 * j + 1])), sl, bb);
+                    const uint64_t y = fma2(pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), sl, bb);
                     float e0, e1;
                     unpair(y, e0, e1);
                     e0 = exp2_fast(e0);
@@ -418,12 +505,33 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     else
                         acc0 = add2(acc0, pair(e0, e1));
                 }
-                tmem_st(s_at + 16 * x, p);
-                if (x & 1) {  // half of the keys
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.p_ready[t][x >> 1]);
+                tmem_st(to, p);  // over columns that are in registers by now
+            };
+            auto half_done = [&](int h) {
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_ready[t][h]);
+            };
+            if constexpr (FP8) {
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    tmem_ld_wait(u[0]);
+                    tmem_ld(s_at + 64 * h + 32, u[1]);
+                    mask(u[0], 64 * h);
+                    exponentials(u[0], s_at + 32 * h);
+                    tmem_ld_wait(u[1]);
+                    if (h == 0) tmem_ld(s_at + 64, u[0]);
+                    mask(u[1], 64 * h + 32);
+                    exponentials(u[1], s_at + 32 * h + 16);
+                    half_done(h);
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    exponentials(u[2 * h], s_at + 32 * h);
+                    exponentials(u[2 * h + 1], s_at + 32 * h + 16);
+                    half_done(h);
                 }
             }
             acc0 = add2(acc0, acc1);
@@ -431,177 +539,249 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             unpair(acc0, l0, l1);
             l = l0 + l1;
         }
-        if (ok && n > 0) ok = __all_sync(kFullMask, mbar_wait_fast(&sh.o_full[t], 0, fail));
+        Piece next;
+        have = ok && next_piece(p, next);
+        if (ok && mine_of > 0) ok = __all_sync(kFullMask, mbar_wait_fast(&sh.o_full[t], o_done++ & 1, fail));
+        // The next piece's queries come while this one's results go (and not for a half without a
+        // tile, which would run ahead of its barriers' readers).
+        bool pending = ok && have && next.tiles(t) > 0;
+        if (pending) copy_queries(next);
         float m2 = m == -INFINITY ? m : m * sl2;  // in log2 units
-        float f0 = 1.0f, f1 = 0.0f;  // of this warpgroup's sums, of the other's
-        const uint32_t other = smem_addr(ring);  // [128][D] fp32, then [128] m2, l
-        if (halves) {
-            // the products of both are done, and nothing loads: the ring is free
-            if (ok && k.nt > 1) ok = __all_sync(kFullMask, mbar_wait_fast(&sh.o_full[t ^ 1], 0, fail));
-            if (!ok) sh.fail = 1;
-            if (t == 1) {
-                if (ok && n > 0) {
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int x = 0; x < D / 32; ++x) {
-                        uint32_t o[32];
-                        tmem_ld(o_at + 32 * x, o);
-                        tmem_ld_wait(o);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            sts16(other + (wrow + lane) * D * 4 + 16 * ((8 * x + j) ^ (lane & 7)),
-                                  make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
-                    }
-                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(other + kTile * D * 4 + (wrow + lane) * 8), "f"(m2), "f"(l) : "memory");
-                }
+        float f0 = 1.0f, f1 = 0.0f;  // of this half's sums, of the other's
+        const bool both = halves && k.nt > 1;
+        if (both && t == 1) {
+            // the even tiles' half takes these sums out of tensor memory with its own
+            if (ok) {
+                sh.ml[wrow + lane] = make_float2(m2, l);
+                tc_fence_before();
                 __syncwarp();
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-            } else {
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                if (ok && k.nt > 1) {
-                    float om, ol;
-                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(om), "=f"(ol) : "r"(other + kTile * D * 4 + (wrow + lane) * 8) : "memory");
-                    const float both = fmaxf(m2, om), ref = both == -INFINITY ? 0.0f : both;
-                    f0 = exp2_fast(m2 - ref);
-                    f1 = exp2_fast(om - ref);
-                    l = l * f0 + ol * f1;
-                    m2 = both;
-                }
+                if (lane == 0) mbar_arrive(&sh.ml_ready);
+                if (pending) queries_there();
+                pending = false;
+                ok = __all_sync(kFullMask, mbar_wait_fast(&sh.o_read, merged++ & 1, fail));
+            }
+        } else if (both) {
+            ok = ok && __all_sync(kFullMask, mbar_wait_fast(&sh.ml_ready, merged++ & 1, fail));
+            if (ok) {
+                const float2 other = sh.ml[wrow + lane];
+                const float top = fmaxf(m2, other.x), ref = top == -INFINITY ? 0.0f : top;
+                f0 = exp2_fast(m2 - ref);
+                f1 = exp2_fast(other.x - ref);
+                l = l * f0 + other.y * f1;
+                m2 = top;
             }
         }
-        if (!ok) sh.fail = 1;
-        if (ok && !(halves && t == 1)) {
+        if (!ok) {
+            sh.fail = 1;
+            break;
+        }
+        if (!(halves && t == 1)) {
             tc_fence_after();
-            const bool fix = sh.fix != 0 && k.nt > 0, direct = k.shares == 1;
+            const bool direct = k.part < 0;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            const int64_t o_here = o_off;
-            const int64_t part = (int64_t)blockIdx.x * kRows + local;  // of the workspace
-            float *sums = d.ws + d.blocks * d.shares * kRows * 2 + part * D;
+            const int64_t part = (int64_t)k.part * kRows + local;  // of the workspace
+            float *sums = reinterpret_cast<float *>(d.ws + ws_sums(gridDim.x)) + part * D;
+            const int64_t to = (int64_t)(k.first + token) * a.Hq + (int64_t)k.h * d.G + (row - token * d.G);
+            uint16_t *out = a.out + to * D;
+            // Straight from the registers: shared memory is busy with the products' operands.
 #pragma unroll 1
             for (int x = 0; x < D / 32; ++x) {
                 uint32_t o[32];
-                if (n > 0) {
+                if (mine_of > 0) {
                     tmem_ld(o_at + 32 * x, o);
                     tmem_ld_wait(o);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = 0;
                 }
-                if (halves && k.nt > 1) {
+                if (both) {
+                    uint32_t w[32];
+                    tmem_ld(o_at + D + 32 * x, w);
+                    tmem_ld_wait(w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint4 w = lds16(other + (wrow + lane) * D * 4 + 16 * ((8 * x + j) ^ (lane & 7)));
-                        o[4 * j] = __float_as_uint(__uint_as_float(o[4 * j]) * f0 + __uint_as_float(w.x) * f1);
-                        o[4 * j + 1] = __float_as_uint(__uint_as_float(o[4 * j + 1]) * f0 + __uint_as_float(w.y) * f1);
-                        o[4 * j + 2] = __float_as_uint(__uint_as_float(o[4 * j + 2]) * f0 + __uint_as_float(w.z) * f1);
-                        o[4 * j + 3] = __float_as_uint(__uint_as_float(o[4 * j + 3]) * f0 + __uint_as_float(w.w) * f1);
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        o[j] = __float_as_uint(__uint_as_float(o[j]) * f0 + __uint_as_float(w[j]) * f1);
                 }
-                if (l == 0.0f) {
+                if (direct) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0;  // sees no key
+                    for (int j = 0; j < 16; ++j) o[j] = pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
                 }
-                if (fix) {
-                    // values that the products were spared, added where a row sees them (an
-                    // infinity or NaN, so any probability will do)
-                    for (int i = 0; i < k.nt; ++i) {
-                        const int key = k.key(i);
-                        if (!k.edge(key)) continue;
-                        for (int j = key; j <= min(pos, key + kTile - 1); ++j) {
-                            if (a.window && j <= pos - a.window && j >= a.sinks) continue;
-                            const int page = page_of(a.kv, a.seq, k.b, j / a.kv.page_size);
-                            if (page < 0) continue;
-                            const int r = j % a.kv.page_size;
-                            const uint8_t *src = a.kv.v + page * a.kv.page_stride + r * a.kv.row_stride + k.h * a.kv.head_stride;
-                            const bool none = FP8 && a.kv.v_scales[((int64_t)page * a.kv.Hkv + k.h) * a.kv.page_size + r] == 255;
+                if (valid) {
 #pragma unroll
-                            for (int w = 0; w < 16; ++w) {
-                                uint32_t y;
-                                if constexpr (FP8) {
-                                    const uint32_t e = reinterpret_cast<const uint16_t *>(src)[16 * x + w];
-                                    y = (none || (e & 0x7f) == 0x7f ? 0x7fffu : 0u) |
-                                        (none || (e & 0x7f00) == 0x7f00 ? 0x7fff0000u : 0u);
-                                } else {
-                                    y = reinterpret_cast<const uint32_t *>(src)[16 * x + w];
-                                    y &= (not_finite(y) >> 15) * 0xffffu;
-                                }
-                                if (y) {
-                                    o[2 * w] = __float_as_uint(__uint_as_float(o[2 * w]) + bf16_lo(y));
-                                    o[2 * w + 1] = __float_as_uint(__uint_as_float(o[2 * w + 1]) + bf16_hi(y));
-                                }
+                    for (int j = 0; j < 32; j += 8)
+                        if (j < 16 || !direct)
+                            st_v8(direct ? (void *)(out + 32 * x + 2 * j) : (void *)(sums + 32 * x + j), o[j], o[j + 1],
+                                  o[j + 2], o[j + 3], o[j + 4], o[j + 5], o[j + 6], o[j + 7]);
+                }
+                if (x == 0 && pending) {
+                    queries_there();
+                    pending = false;
+                }
+            }
+            if (both) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.o_read);
+            }
+            if (sh.fix && valid) {
+                // values that the products were spared, added where a row sees them (an infinity
+                // or NaN, so any probability will do)
+                for (int i = 0; i < k.nt; ++i) {
+                    const int key = k.key(i);
+                    if (!k.edge(key, a.window, a.sinks)) continue;
+                    for (int j = key; j <= min(pos, key + kTile - 1); ++j) {
+                        if (a.window && j <= pos - a.window && j >= a.sinks) continue;
+                        const int page = page_of(a.kv, a.seq, k.b, j / a.kv.page_size);
+                        if (page < 0) continue;
+                        const int r = j % a.kv.page_size;
+                        const uint8_t *src = a.kv.v + page * a.kv.page_stride + r * a.kv.row_stride + k.h * a.kv.head_stride;
+                        const bool none = FP8 && a.kv.v_scales[((int64_t)page * a.kv.Hkv + k.h) * a.kv.page_size + r] == 255;
+#pragma unroll 1
+                        for (int w = 0; w < D / 2; ++w) {
+                            uint32_t y;
+                            if constexpr (FP8) {
+                                const uint32_t e = reinterpret_cast<const uint16_t *>(src)[w];
+                                y = (none || (e & 0x7f) == 0x7f ? 0x7fffu : 0u) | (none || (e & 0x7f00) == 0x7f00 ? 0x7fff0000u : 0u);
+                            } else {
+                                y = reinterpret_cast<const uint32_t *>(src)[w];
+                                y &= (not_finite(y) >> 15) * 0xffffu;
+                            }
+                            if (!y) continue;
+                            if (direct) {
+                                uint32_t *at = reinterpret_cast<uint32_t *>(out) + w;
+                                *at = pack_bf16(bf16_lo(*at) + bf16_lo(y), bf16_hi(*at) + bf16_hi(y));
+                            } else {
+                                sums[2 * w] += bf16_lo(y);
+                                sums[2 * w + 1] += bf16_hi(y);
                             }
                         }
                     }
                 }
-                if (!direct) {
-                    if (valid) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            st_v4(sums + 32 * x + 4 * j, make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
-                    }
-                    continue;
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int ch = 4 * x + j;
-                    sts16(mine + (ch >> 3) * C::kPanel + (wrow + lane) * 128 + 16 * ((ch & 7) ^ (lane & 7)),
-                          make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
-                }
             }
-            __syncwarp();
-            if (direct) {
-#pragma unroll
-                for (int i = 0; i < 32 / RP; ++i) {
-                    const int64_t off = __shfl_sync(kFullMask, o_here, i * RP + lane / CH);
-                    const int r = wrow + i * RP + lane / CH, ch = lane % CH;
-                    if (off >= 0)
-                        st_v4(a.out + off + 8 * ch, lds16(mine + (ch >> 3) * C::kPanel + r * 128 + 16 * ((ch & 7) ^ (r & 7))));
-                }
-                if (a.lse && valid) a.lse[o_off / D] = l == 0.0f ? -INFINITY : (m2 + log2f(l)) / kLog2e;
+            if (valid && direct) {
+                if (a.lse) a.lse[to] = l == 0.0f ? -INFINITY : (m2 + log2f(l)) / kLog2e;
             } else if (valid) {
-                *reinterpret_cast<float2 *>(d.ws + 2 * part) = make_float2(m2, l);
+                *reinterpret_cast<float2 *>(d.ws + ws_ml(gridDim.x) + part * 8) = make_float2(m2, l);
             }
+        }
+        if (pending) queries_there();
+        k = next;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         const int role = warp - 8;
         if (role == (FP8 ? 6 : 0)) {
-            // ---- loads: tile 0's keys, its values, tile 1's keys, ...; a lane a box ----
+            // ---- the run's pieces, and their loads: tile 0's keys, its values, tile 1's keys, ...;
+            // a lane a box ----
             const int box = d.box, boxes = kTile / box;
             constexpr int bytes = FP8 ? C::kRaw : C::kStage, slots = FP8 ? C::kRaws : kStages;
             uint64_t *fulls = FP8 ? sh.raw_full : sh.full, *empties = FP8 ? sh.raw_empty : sh.empty;
             uint8_t *to = (FP8 ? raws : ring) + lane * box * (FP8 ? D : 128);
-            int it = 0;
-            bool ok = true;
-            for (int i = 0; ok && i < k.nt; ++i) {
-                const int key = k.key(i) + lane * box;
-                int page = a.kv.pages, r = 0;  // outside: zeros, and no reads
-                if (lane < boxes && k.wanted(key, box)) {
-                    const int entry = key / a.kv.page_size;
-                    const int p = page_of(a.kv, a.seq, k.b, entry);
-                    if (p >= 0) page = p;
-                    r = key - entry * a.kv.page_size;
-                }
-                for (int v = 0; v < 2; ++v, ++it) {
-                    const int s = it % slots;
-                    ok = __all_sync(kFullMask, it < slots || mbar_wait_fast(&empties[s], (it / slots - 1) & 1, fail));
-                    if (!ok) {
-                        sh.fail = 1;
+            int b = sh.found_b, h, j = 0, it = 0, p = 0;
+            int64_t at = sh.found_at;
+            Span sp = seq_span(a.seq, a.kv.page_size, b);
+            {
+                const int64_t one = all_places(d, sp, lane);  // of a head
+                h = (int)((x0 - at) / one);
+                at += h * one;
+                for (;; j += 32) {  // the block where the run begins
+                    int64_t n = j + lane < row_blocks(d, sp) ? places(d, row_block(d, sp, j + lane)) : 0, incl = n;
+#pragma unroll
+                    for (int s = 1; s < 32; s <<= 1) {
+                        const int64_t o = __shfl_up_sync(kFullMask, incl, s);
+                        if (lane >= s) incl += o;
+                    }
+                    const uint32_t past = __ballot_sync(kFullMask, at + incl > x0);
+                    if (past || j + 32 >= row_blocks(d, sp)) {
+                        const int src = past ? __ffs(past) - 1 : 31;
+                        at += __shfl_sync(kFullMask, incl - n, src);
+                        j += src;
                         break;
                     }
-                    if (elect_one()) expect_bytes(&fulls[s], bytes);
-                    __syncwarp();
-                    if (lane < boxes) {
-                        const CUtensorMap *map = v ? &vmap : &kmap;
-#pragma unroll
-                        for (int n = 0; n < (FP8 ? 1 : C::kPanels); ++n)
-                            tma_load_4d(to + s * bytes + n * C::kPanel, map, 128 * n, k.h, r, page, &fulls[s]);
-                    }
-                    __syncwarp();
+                    at += __shfl_sync(kFullMask, incl, 31);
                 }
             }
+            bool ok = true;
+            while (ok) {
+                Piece k;
+                bool some = false;
+                while (!some && at < x1) {
+                    k = row_block(d, sp, j);
+                    k.b = b;
+                    k.h = h;
+                    const int steps = k.steps();
+                    if (d.ws) {
+                        // steps [s0, s1) of the block
+                        const int s0 = (int)max(x0 - at, (int64_t)0), s1 = (int)min((int64_t)steps, x1 - at);
+                        const bool starts = at >= x0, ends = at + steps <= x1;
+                        some = steps == 0 ? starts : s0 < s1;
+                        if (some && !(starts && ends)) {
+                            const int scale = k.halves() ? 2 : 1;
+                            k.part = 2 * blockIdx.x + starts;
+                            k.i0 = s0 * scale;
+                            k.nt = min(s1 * scale, k.nt) - k.i0;
+                            if (starts && lane == 0)
+                                reinterpret_cast<int4 *>(d.ws)[blockIdx.x] =
+                                    make_int4(b, h, j, (int)((at + steps - 1) / per) - (int)blockIdx.x);
+                        }
+                        at += steps + kItem;
+                    } else {
+                        some = true;
+                        ++at;
+                    }
+                    if (++j == row_blocks(d, sp)) {
+                        j = 0;
+                        if (++h == a.kv.Hkv) {
+                            h = 0;
+                            do {
+                                if (++b < a.seq.B) sp = seq_span(a.seq, a.kv.page_size, b);
+                            } while (b < a.seq.B && sp.n == 0);
+                            if (b >= a.seq.B) at = x1;  // the list's end
+                        }
+                    }
+                }
+                if (!some) k.nt = -1;
+                for (int r = lane; some && r < k.rows; r += 32) {  // its queries, into L2
+                    const int row = k.row0 + r, token = row / d.G;
+                    const uint16_t *src = a.q + (k.first + token) * a.q_stride + ((int64_t)k.h * d.G + (row - token * d.G)) * D;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(src) : "memory");
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(src + D - 1) : "memory");
+                }
+                ok = __all_sync(kFullMask, p < kPieces || mbar_wait_fast(&sh.piece_empty[p % kPieces], (p / kPieces - 1) & 1, fail));
+                if (!ok) break;
+                if (lane == 0) {
+                    sh.pieces[p % kPieces] = k;
+                    mbar_arrive(&sh.piece_full[p % kPieces]);
+                }
+                __syncwarp();
+                ++p;
+                if (!some) break;
+                for (int i = 0; ok && i < k.nt; ++i) {
+                    const int key = k.key(i) + lane * box;
+                    int page = a.kv.pages, r = 0;  // outside: zeros, and no reads
+                    if (lane < boxes && k.wanted(key, box)) {
+                        const int entry = key / a.kv.page_size;
+                        const int q = page_of(a.kv, a.seq, k.b, entry);
+                        if (q >= 0) page = q;
+                        r = key - entry * a.kv.page_size;
+                    }
+                    for (int v = 0; v < 2; ++v, ++it) {
+                        const int s = it % slots;
+                        ok = __all_sync(kFullMask, it < slots || mbar_wait_fast(&empties[s], (it / slots - 1) & 1, fail));
+                        if (!ok) break;
+                        if (elect_one()) expect_bytes(&fulls[s], bytes);
+                        __syncwarp();
+                        if (lane < boxes) {
+                            const CUtensorMap *map = v ? &vmap : &kmap;
+#pragma unroll
+                            for (int n = 0; n < (FP8 ? 1 : C::kPanels); ++n)
+                                tma_load_4d(to + s * bytes + n * C::kPanel, map, 128 * n, k.h, r, page, &fulls[s]);
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (!ok) sh.fail = 1;
             if (lane == 0) sh.issued = it;
         } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
             // ---- products of row tile t ----
@@ -609,9 +789,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             const int t = warp - kMmaWarp;
             const uint64_t da = tile_desc(smem_addr(smem + t * C::kStage));
             const uint32_t s_at = tmem + t * kTile, o_at = tmem + 2 * kTile + t * D;
-            auto full = [&](int it) { return mbar_wait_fast(&sh.full[it % kStages], (it / kStages) & 1, fail); };
-            auto logits = [&](int it) {
-                const uint64_t db = tile_desc(smem_addr(ring + (it % kStages) * C::kStage));
+            auto logits = [&](int stage) {
+                const uint64_t db = tile_desc(smem_addr(ring + stage * C::kStage));
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
                     const uint32_t at = (x / 4) * (C::kPanel / 16) + 2 * (x % 4);
@@ -619,63 +798,96 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 }
                 mma_commit(&sh.s_full[t]);
             };
-            // a tile is free when both rows' products have read it
-            auto release = [&](int it) {
-                mma_commit(&sh.empty[it % kStages]);
-                if (halves) mma_commit(&sh.empty[it % kStages]);
+            // The place in the ring of this row tile's next keys and values, and the parity of its phase.
+            struct Place {
+                int it, s, parity;
+                __device__ __forceinline__ void set(int n) {
+                    it = n;
+                    s = n % kStages;
+                    parity = n / kStages & 1;
+                }
+                __device__ __forceinline__ void add(int n) {  // n < kStages, or twice that
+                    it += n;
+                    s += n;
+                    while (s >= kStages) s -= kStages, parity ^= 1;
+                }
             };
-            int i = halves ? t : 0, n = 0;
+            auto full = [&](const Place &at) { return mbar_wait_fast(&sh.full[at.s], at.parity, fail); };
+            int base = 0, done = 0, blocks = 0, queries = 0;  // ring index, tiles, turns, pieces with tiles so far
             bool ok = true;
-            if (i < k.nt) {
-                ok = __all_sync(kFullMask, mbar_wait_fast(&sh.q_full[t], 0, fail) && full(2 * i));
-                if (ok) {
-                    tc_fence_after();
-                    if (elect_one()) {
-                        logits(2 * i);
-                        release(2 * i);
-                    }
-                    __syncwarp();
-                }
-            }
-            for (; ok && i < k.nt; i += stride, ++n) {
-                const int kt = 2 * (i + stride), vt = 2 * i + 1;
-                const bool more = i + stride < k.nt;
-                ok = full(vt) && (FP8 || !k.edge(k.key(i)) || mbar_wait_fast(&sh.v_ok[i & 3], (i >> 2) & 1, fail));
-                const uint64_t db = value_desc(smem_addr(ring + (vt % kStages) * C::kStage));
-                ok = __all_sync(kFullMask, ok && mbar_wait_fast(&sh.p_ready[t][0], n & 1, fail));
+            Piece k;
+            for (int p = 0; ok && next_piece(p, k); ++p, base += 2 * k.nt) {
+                if (k.nt == 0) continue;
+                const bool halves = k.halves();
+                const int mine = k.tiles(t), step = halves ? 4 : 2;
+                // a tile is free when both row tiles' products have read it
+                auto release = [&](const Place &at) {
+                    mma_commit(&sh.empty[at.s]);
+                    if (halves) mma_commit(&sh.empty[at.s]);
+                };
+                Place kt, vt;
+                kt.set(base + (halves ? 2 * t : 0));
+                vt = kt;
+                vt.add(1);
+                ok = mine == 0 || (mbar_wait_fast(&sh.q_full[t], queries++ & 1, fail) && full(kt));
+                ok = __all_sync(kFullMask, ok);
                 if (!ok) break;
                 tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) mma_bf16_tmem(o_at, s_at + 8 * x, db + x * (2048 / 16), pv, n > 0 || x > 0);
-                }
-                __syncwarp();
-                // The tiles take turns, so that one's exponentials run under the other's products:
-                // left alone they fall into step, and each waits for the other in both.
-                ok = mbar_wait_fast(&sh.p_ready[t][1], n & 1, fail);
-                ok = __all_sync(kFullMask, ok && (t + n == 0 || mbar_wait_fast(&sh.turn[t], (n + t - 1) & 1, fail)));
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int x = 4; x < 8; ++x) mma_bf16_tmem(o_at, s_at + 8 * x, db + x * (2048 / 16), pv, true);
-                    release(vt);
-                    if (!more) {
-                        mma_commit(&sh.o_full[t]);
-                        mbar_arrive(&sh.turn[t ^ 1]);
-                    }
-                }
-                __syncwarp();
-                if (!more) break;
-                // only now: these keys may be waiting for the values' place
-                ok = __all_sync(kFullMask, full(kt));
-                if (!ok) break;
-                if (elect_one()) {
-                    logits(kt);
-                    mbar_arrive(&sh.turn[t ^ 1]);
+                if (mine > 0 && elect_one()) {
+                    logits(kt.s);
                     release(kt);
                 }
                 __syncwarp();
+                for (int n = 0; n < mine; ++n, ++done, ++blocks) {
+                    const bool more = n + 1 < mine;
+                    const int key = k.key(halves ? 2 * n + t : n);
+                    ok = full(vt) && (FP8 || !k.edge(key, a.window, a.sinks) ||
+                                      mbar_wait_fast(&sh.v_ok[(vt.it >> 1) & 3], (vt.it >> 3) & 1, fail));
+                    const uint64_t db = value_desc(smem_addr(ring + vt.s * C::kStage));
+                    kt.add(step);
+                    ok = __all_sync(kFullMask, ok && mbar_wait_fast(&sh.p_ready[t][0], done & 1, fail));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) mma_bf16_tmem(o_at, s_at + 8 * x, db + x * (2048 / 16), pv, n > 0 || x > 0);
+                    }
+                    __syncwarp();
+                    // The tiles take turns, so that one's exponentials run under the other's products:
+                    // left alone they fall into step, and each waits for the other in both.
+                    ok = t + blocks == 0 || mbar_wait_fast(&sh.turn[t], (blocks + t - 1) & 1, fail);
+                    ok = __all_sync(kFullMask, ok && mbar_wait_fast(&sh.p_ready[t][1], done & 1, fail));
+                    if (!ok) break;
+                    tc_fence_after();
+                    // these keys may be waiting for the values' place: with few stages only then
+                    const bool ready = more && kStages >= 5 && __all_sync(kFullMask, full(kt));
+                    if (elect_one()) {
+#pragma unroll
+                        for (int x = 4; x < 8; ++x) mma_bf16_tmem(o_at, s_at + 8 * x, db + x * (2048 / 16), pv, true);
+                        if (ready) logits(kt.s);
+                        release(vt);
+                        if (ready) release(kt);
+                        if (!more) mma_commit(&sh.o_full[t]);
+                        if (ready || !more) mbar_arrive(&sh.turn[t ^ 1]);
+                    }
+                    __syncwarp();
+                    vt.add(step);
+                    if (ready || !more) continue;
+                    ok = __all_sync(kFullMask, full(kt));
+                    if (!ok) break;
+                    if (elect_one()) {
+                        logits(kt.s);
+                        release(kt);
+                        mbar_arrive(&sh.turn[t ^ 1]);
+                    }
+                    __syncwarp();
+                }
+                if (ok && mine < k.tiles(0)) {  // an odd number in halves: a turn without a tile
+                    ok = __all_sync(kFullMask, mbar_wait_fast(&sh.turn[t], (blocks + t - 1) & 1, fail));
+                    ++blocks;
+                    if (ok && elect_one()) mbar_arrive(&sh.turn[t ^ 1]);
+                    __syncwarp();
+                }
             }
             if (!ok) sh.fail = 1;
             // tensor memory and the barriers outlive the last product
@@ -686,27 +898,31 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             // ---- values that are not finite, in tiles that not all rows see.  It passes every
             // tile, so that the barriers' phases are never two ahead of it. ----
             bool ok = true;
-            for (int it = 0; ok && it < 2 * k.nt; ++it) {
-                const int s = it % kStages, i = it >> 1, key = k.key(i);
-                ok = __all_sync(kFullMask, mbar_wait_fast(&sh.full[s], (it / kStages) & 1, fail));
-                if (!ok) break;
-                if ((it & 1) && k.edge(key)) {
-                    const uint32_t st = smem_addr(ring + s * C::kStage);
+            int it = 0;
+            Piece k;
+            for (int p = 0; ok && next_piece(p, k); ++p) {
+                for (int n = 0; ok && n < 2 * k.nt; ++n, ++it) {
+                    const int s = it % kStages, key = k.key(n >> 1);
+                    ok = __all_sync(kFullMask, mbar_wait_fast(&sh.full[s], (it / kStages) & 1, fail));
+                    if (!ok) break;
+                    if ((n & 1) && k.edge(key, a.window, a.sinks)) {
+                        const uint32_t st = smem_addr(ring + s * C::kStage);
 #pragma unroll 8
-                    for (int x = lane; x < C::kStage / 16; x += 32) {
-                        uint4 w = lds16(st + 16 * x);
-                        if (not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w)) {
-                            const int j = key + (x * 16 % C::kPanel) / 128;
-                            if (k.wanted(j, 1)) sh.fix = 1;
-                            sts16(st + 16 * x, make_uint4(finite_part(w.x), finite_part(w.y), finite_part(w.z), finite_part(w.w)));
+                        for (int x = lane; x < C::kStage / 16; x += 32) {
+                            uint4 w = lds16(st + 16 * x);
+                            if (not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w)) {
+                                const int j = key + (x * 16 % C::kPanel) / 128;
+                                if (k.wanted(j, 1)) sh.fix = 1;
+                                sts16(st + 16 * x, make_uint4(finite_part(w.x), finite_part(w.y), finite_part(w.z), finite_part(w.w)));
+                            }
                         }
+                        fence_proxy_async_smem();
                     }
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    if (it & 1) mbar_arrive(&sh.v_ok[i & 3]);
-                    mbar_arrive(&sh.empty[s]);
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (n & 1) mbar_arrive(&sh.v_ok[(it >> 1) & 3]);
+                        mbar_arrive(&sh.empty[s]);
+                    }
                 }
             }
             if (!ok) sh.fail = 1;
@@ -714,6 +930,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             // ---- E4M3 rows to bf16, a thread half a row ----
             const int r = (role & 3) * 32 + lane, c0 = role < 4 ? 0 : D / 32;
             bool ok = true;
+            Piece k;
             // scale bytes of the row's key and value; 2^0 where there are none
             auto bytes = [&](int i, uint32_t &sk, uint32_t &sv) {
                 sk = sv = 127;
@@ -728,16 +945,18 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     }
                 }
             };
+            int base = 0;
+            for (int p = 0; ok && next_piece(p, k); ++p, base += 2 * k.nt) {
             uint32_t sk, sv;
             bytes(0, sk, sv);
             for (int i = 0; ok && i < k.nt; ++i) {
                 const int key = k.key(i);
-                const bool edge = k.edge(key), wanted = k.wanted(key + r, 1);
+                const bool edge = k.edge(key, a.window, a.sinks), wanted = k.wanted(key + r, 1);
                 const float f[2] = {scale_value(sk), scale_value(sv)};
                 bytes(i + 1, sk, sv);
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
-                    const int it = 2 * i + v, rs = it % C::kRaws, s = it % kStages;
+                    const int it = base + 2 * i + v, rs = it % C::kRaws, s = it % kStages;
                     ok = ok && mbar_wait_fast(&sh.raw_full[rs], (it / C::kRaws) & 1, fail) &&
                          (it < kStages || mbar_wait_fast(&sh.empty[s], (it / kStages - 1) & 1, fail));
                     ok = __all_sync(kFullMask, ok);
@@ -789,6 +1008,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     }
                 }
             }
+            }
             if (!ok) sh.fail = 1;
         }
     }
@@ -811,59 +1031,69 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     }
 }
 
-// The shares' sums of a block's rows, a warp a row.
+// The sums of the row blocks that several SMs share, a warp two rows; 16 blocks for each that may
+// begin one.
 template <int D>
-__global__ void __launch_bounds__(kRows) join_kernel(const __grid_constant__ PrefillArgs d) {
-    constexpr int N = D / 32;
-    __shared__ Shared sh;
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ PrefillArgs d, int blocks) {
+    constexpr int N = D / 32, kAhead = 8;  // channels a lane, sums in flight
     const AttnArgs &a = d.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t block = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = blockIdx.x >> 4;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    Block k;
-    if (!find_block<kRows>(d, block / a.kv.Hkv, (int)(block % a.kv.Hkv), 0, sh, k) || k.shares == 1) return;
-    const float *ml = d.ws + block * d.shares * kRows * 2;
-    const float *sums = d.ws + d.blocks * d.shares * kRows * 2 + block * d.shares * kRows * D + N * lane;
-    for (int r = warp; r < k.rows; r += kRows / 32) {
-        float m = -INFINITY, l = 0.0f;
-        if (lane < k.shares) {
-            m = ld_dep(ml + 2 * (lane * kRows + r));
-            l = ld_dep(ml + 2 * (lane * kRows + r) + 1);
-        }
-        float top = m;
-#pragma unroll
-        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
-        const float f = exp2_fast(m - (top == -INFINITY ? 0.0f : top));
-        float sum = l * f, acc[N];
-#pragma unroll
-        for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(kFullMask, sum, x);
+    const uint4 rec = ld_dep_v4(d.ws + 16 * c0);
+    const int n = (int)rec.w;  // SMs after the first
+    if (n == 0) return;
+    const Piece k = row_block(d, seq_span(a.seq, a.kv.page_size, (int)rec.x), (int)rec.z);
+    const float *ml = reinterpret_cast<const float *>(d.ws + ws_ml(blocks));
+    const float *sums = reinterpret_cast<const float *>(d.ws + ws_sums(blocks)) + N * lane;
+    for (int r = (blockIdx.x & 15) * 8 + warp; r < k.rows; r += 128) {
+        auto at = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0)) * kRows + r; };
+        float m = -INFINITY, l = 0.0f, top = -INFINITY, base = 0.0f, sum = 0.0f, acc[N];
 #pragma unroll
         for (int x = 0; x < N; ++x) acc[x] = 0.0f;
-#pragma unroll 8
-        for (int i = 0; i < k.shares; ++i) {
-            const float g = __shfl_sync(kFullMask, f, i);
-            const float *src = sums + (int64_t)(i * kRows + r) * D;
+        for (int w0 = 0; w0 <= n; w0 += 32) {  // the SMs of whose m and l the lanes hold
+            m = w0 + lane <= n ? ld_dep(ml + 2 * at(w0 + lane)) : -INFINITY;
+            l = w0 + lane <= n ? ld_dep(ml + 2 * at(w0 + lane) + 1) : 0.0f;
+            const int end = min(n + 1 - w0, 32);
+            for (int i0 = 0; i0 < end; i0 += kAhead) {
+                float v[kAhead][N];
 #pragma unroll
-            for (int x = 0; x < N; ++x) acc[x] += ld_dep(src + x) * g;
+                for (int i = 0; i < kAhead; ++i) {
+                    const float *src = sums + at(min(w0 + i0 + i, n)) * D;
+                    if constexpr (N == 4) {
+                        const uint4 q = ld_dep_v4(src);
+                        v[i][0] = __uint_as_float(q.x), v[i][1] = __uint_as_float(q.y);
+                        v[i][2] = __uint_as_float(q.z), v[i][3] = __uint_as_float(q.w);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < N; ++x) v[i][x] = ld_dep(src + x);
+                    }
+                }
+                if (w0 + i0 == 0) {  // after the first loads are on their way
+                    top = m;
+                    for (int i = lane + 32; i <= n; i += 32) top = fmaxf(top, ld_dep(ml + 2 * at(i)));
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
+                    base = top == -INFINITY ? 0.0f : top;
+                }
+                const float f = exp2_fast(m - base), fl = l * f;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const float g = __shfl_sync(kFullMask, f, i0 + i), gl = __shfl_sync(kFullMask, fl, i0 + i);
+                    if (i0 + i >= end) break;
+                    sum += gl;
+#pragma unroll
+                    for (int x = 0; x < N; ++x) acc[x] += v[i][x] * g;
+                }
+            }
         }
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         const int token = (k.row0 + r) / d.G;
-        const int64_t to = (int64_t)(k.first + token) * a.Hq + (int64_t)k.h * d.G + (k.row0 + r - token * d.G);
+        const int64_t to = (int64_t)(k.first + token) * a.Hq + (int64_t)rec.y * d.G + (k.row0 + r - token * d.G);
         uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + to * D + N * lane);
 #pragma unroll
         for (int x = 0; x < N; x += 2) dst[x / 2] = pack_bf16(acc[x] * inv, acc[x + 1] * inv);
         if (a.lse && lane == 0) a.lse[to] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
     }
-}
-
-// At most this many blocks of 256 rows, a sequence's last one not being full.
-int64_t most_blocks(int64_t T, int64_t B, int G, int Hkv) {
-    return ((T * G) / kRows + (T < B ? T : B)) * Hkv;
-}
-// Blocks that share one's keys: as many as two for each SM allow.
-int most_shares(int64_t blocks) {
-    const int64_t n = 2 * sm_count() / (blocks > 0 ? blocks : 1);
-    return n < 1 ? 1 : n > 32 ? 32 : (int)n;
 }
 
 template <int D, bool FP8>
@@ -878,19 +1108,16 @@ cudaError_t launch(const PrefillArgs &d, cudaStream_t stream) {
     if (!encode_bytes(&kmap, kv.k, 4, dims, strides, box, swizzle) ||
         !encode_bytes(&vmap, kv.v, 4, dims, strides, box, swizzle))
         return cudaErrorInvalidValue;
-    const cudaError_t err = launch_large<prefill_kernel<D, FP8>>((int)(d.blocks * d.shares), Cfg<D, FP8>::kThreads,
-                                                                 Cfg<D, FP8>::kSmem, stream, kmap, vmap, d);
-    if (err != cudaSuccess || d.shares == 1) return err;
-    return launch_kernel(join_kernel<D>, (int)d.blocks, kRows, 0, stream, true, d);
+    const int blocks = sm_count();
+    const cudaError_t err = launch_large<prefill_kernel<D, FP8>>(blocks, Cfg<D, FP8>::kThreads, Cfg<D, FP8>::kSmem,
+                                                                 stream, kmap, vmap, d);
+    if (err != cudaSuccess || !d.ws) return err;
+    return launch_kernel(join_kernel<D>, 16 * blocks, 256, 0, stream, true, d, blocks);
 }
 
 }  // namespace
 
-size_t attn_prefill_workspace(int T, int B, int Hq, int Hkv, int D) {
-    const int64_t blocks = most_blocks(T, B, Hq / Hkv, Hkv);
-    const int shares = most_shares(blocks);
-    return shares == 1 ? 0 : ws_floats(blocks, shares, D) * 4;
-}
+size_t attn_prefill_workspace(int D) { return ws_bytes(sm_count(), D); }
 
 cudaError_t launch_attn_prefill(const AttnArgs &a, void *workspace, cudaStream_t stream) {
     PrefillArgs d = {};
@@ -898,9 +1125,7 @@ cudaError_t launch_attn_prefill(const AttnArgs &a, void *workspace, cudaStream_t
     d.G = a.Hq / a.kv.Hkv;
     d.box = a.kv.page_size & -a.kv.page_size;  // a box lies within a page
     if (d.box > kTile) d.box = kTile;
-    d.blocks = most_blocks(a.seq.T, a.seq.B, d.G, a.kv.Hkv);
-    d.shares = workspace ? most_shares(d.blocks) : 1;
-    d.ws = static_cast<float *>(workspace);
+    d.ws = static_cast<uint8_t *>(workspace);
     const bool fp8 = a.kv.k_scales != nullptr;
     if (a.kv.D == 64) return fp8 ? launch<64, true>(d, stream) : launch<64, false>(d, stream);
     return fp8 ? launch<128, true>(d, stream) : launch<128, false>(d, stream);

@@ -709,10 +709,10 @@ ep_status_t ep_attn_decode(const ep_kv_cache_t *cache, const ep_kv_seqs_t *seqs,
  * lse is [T, num_q_heads], but
  *
  *   workspace  device scratch, 16-byte aligned, of ep_attn_prefill_workspace_bytes()
- *              with this device current (0 for many tokens), clobbered.  Holds nothing
- *              between calls; calls (or replayed graphs) that share one must not overlap
- *              on the GPU.  NULL: the keys of a few tokens are not shared out among blocks,
- *              which takes longer.
+ *              with this device current, which depends on head_dim alone; clobbered.
+ *              Holds nothing between calls; calls (or replayed graphs) that share one must
+ *              not overlap on the GPU.  NULL: no row block of 256 tokens times heads is shared out
+ *              among SMs, which takes longer, for few tokens many times longer.
  */
 size_t ep_attn_prefill_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
                                        int32_t num_kv_heads, int32_t head_dim);

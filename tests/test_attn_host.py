@@ -121,8 +121,8 @@ def test_prefill_workspace_sizes(lib):  # noqa: F811
     size = lib.ep_attn_prefill_workspace_bytes
     assert size(-1, 1, 4, 2, 128) == size(1, -1, 4, 2, 128) == size(1, 1, 3, 2, 128) == 0
     assert size(1, 1, 4, 2, 96) == size(1 << 28, 1, 64, 2, 128) == 0
-    assert size(1 << 20, 1, 64, 2, 128) == 0 and size(1, 1, 4, 2, 128) > 0  # many, few tokens
-    assert max(size(T, B, 32, 8, 128) for T in (1, 40, 700, 5000) for B in (1, 3, 40)) < 1 << 27
+    assert size(1, 1, 4, 2, 128) > size(1, 1, 4, 2, 64) > 0
+    assert len({size(T, B, 32, 8, 128) for T in (0, 1, 700, 5000) for B in (0, 1, 40)}) == 1
 
 
 def test_status_name(lib):  # noqa: F811
