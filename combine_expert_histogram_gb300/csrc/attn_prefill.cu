@@ -72,7 +72,7 @@ struct Piece {
 
 struct Shared {
     uint64_t full[5], empty[5], raw_full[4], raw_empty[4];
-    uint64_t q_full[2], s_full[2], p_ready[2][2], o_full[2], turn[2], v_ok[4], ml_ready, o_read, drain;
+    uint64_t q_full[2], s_full[2], s_free[2], p_ready[2][2], o_full[2], turn[2], v_ok[4], ml_ready, o_read, drain;
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     int64_t sums[20], found_at;
     float2 ml[kTile];  // of the odd tiles' half
@@ -87,6 +87,11 @@ struct Cfg {
     // registers a thread: 96 or 168 at launch
     static constexpr int kSoftRegs = FP8 ? 144 : 208, kOtherRegs = FP8 ? 64 : 88;
     static constexpr int kPanels = D / 64;               // 128-byte columns of a tile
+    // Tensor memory (512 columns): S of both tiles, then O.  Heads of 64 leave room for P apart from S, so
+    // that the next tile's S is there when its exponentials begin.
+    static constexpr bool kApart = D == 64;
+    static constexpr int kP = kApart ? 2 * kTile : 0, kPStep = kApart ? kTile / 2 : kTile;
+    static constexpr int kO = kApart ? 3 * kTile : 2 * kTile;
     static constexpr int kPanel = kTile * 128;
     static constexpr int kStage = kPanels * kPanel;      // a bf16 tile
     static constexpr int kStages = FP8 && D == 128 ? 3 : 5;
@@ -276,6 +281,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.q_full[i], 4);
             mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.s_free[i], 4);
             mbar_init(&sh.p_ready[i][0], 4);
             mbar_init(&sh.p_ready[i][1], 4);
             mbar_init(&sh.o_full[i], 1);
@@ -356,7 +362,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;  // S (and P) of both tiles, then O of both
+    const uint32_t tmem = sh.tmem;
     // The next piece of the run, for a warp that goes through them.
     auto next_piece = [&](int p, Piece &k) {
         const bool ok = __all_sync(kFullMask, mbar_wait_fast(&sh.piece_full[p % kPieces], (p / kPieces) & 1, fail));
@@ -374,7 +380,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
         const int t = warp >> 2, wrow = (warp & 3) * 32;
         const uint32_t lanes = (uint32_t)wrow << 16;
-        const uint32_t s_at = tmem + t * kTile + lanes, o_at = tmem + 2 * kTile + t * D + lanes;
+        const uint32_t s_at = tmem + t * kTile + lanes, p_at = tmem + C::kP + t * C::kPStep + lanes;
+        const uint32_t o_at = tmem + C::kO + t * D + lanes;
         constexpr int CH = D / 8, RP = 32 / CH;  // 16-byte chunks a row, rows an instruction
         const uint32_t mine = smem_addr(smem) + t * C::kStage;
         const float sl2 = a.scale * kLog2e;
@@ -434,6 +441,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             for (int x = 0; x < (FP8 ? 1 : 4); ++x) tmem_ld(s_at + 32 * x, u[x]);
             const bool masked = !(key + kTile - 1 <= wmin && (!a.window || key > wmax - a.window || key + kTile <= a.sinks));
             const int hi = pos - key + 1, lo = a.window && hi > a.window ? hi - a.window : 0, first = a.sinks - key;
+            auto s_read = [&]() {  // S is in registers
+                if (!C::kApart) return;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.s_free[t]);
+            };
             auto mask = [&](uint32_t (&v)[32], int at) {
                 if (!masked) return;
                 const uint32_t seen = low_bits(hi - at) & (~low_bits(lo - at) | low_bits(first - at));
@@ -460,6 +473,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             } else {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) tmem_ld_wait(u[x]);
+                s_read();
                 if (masked) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x) mask(u[x], 32 * x);
@@ -468,6 +482,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 for (int x = 0; x < 4; ++x) largest(u[x]);
             }
             const float top = fmaxf(max3(part[0], part[1], part[2]), part[3]);
+            // the products of the tile before read P and write O
+            if (C::kApart && n > 0) {
+                ok = __all_sync(kFullMask, mbar_wait_fast(&sh.o_full[t], (done - 1) & 1, fail));
+                if (!ok) break;
+                tc_fence_after();
+            }
             const bool grown = top > m && !((top - m) * sl2 <= kLag);
             if (__any_sync(kFullMask, grown)) {
                 const float next = grown ? top : m;
@@ -519,18 +539,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     tmem_ld_wait(u[0]);
                     tmem_ld(s_at + 64 * h + 32, u[1]);
                     mask(u[0], 64 * h);
-                    exponentials(u[0], s_at + 32 * h);
+                    exponentials(u[0], p_at + 32 * h);
                     tmem_ld_wait(u[1]);
                     if (h == 0) tmem_ld(s_at + 64, u[0]);
+                    else s_read();
                     mask(u[1], 64 * h + 32);
-                    exponentials(u[1], s_at + 32 * h + 16);
+                    exponentials(u[1], p_at + 32 * h + 16);
                     half_done(h);
                 }
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    exponentials(u[2 * h], s_at + 32 * h);
-                    exponentials(u[2 * h + 1], s_at + 32 * h + 16);
+                    exponentials(u[2 * h], p_at + 32 * h);
+                    exponentials(u[2 * h + 1], p_at + 32 * h + 16);
                     half_done(h);
                 }
             }
@@ -541,7 +562,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         }
         Piece next;
         have = ok && next_piece(p, next);
-        if (ok && mine_of > 0) ok = __all_sync(kFullMask, mbar_wait_fast(&sh.o_full[t], o_done++ & 1, fail));
+        if (ok && mine_of > 0) ok = __all_sync(kFullMask, mbar_wait_fast(&sh.o_full[t], (C::kApart ? done - 1 : o_done++) & 1, fail));
         // The next piece's queries come while this one's results go (and not for a half without a
         // tile, which would run ahead of its barriers' readers).
         bool pending = ok && have && next.tiles(t) > 0;
@@ -788,7 +809,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             constexpr uint32_t qk = bf16_instr(kTile, false), pv = bf16_instr(D, true);
             const int t = warp - kMmaWarp;
             const uint64_t da = tile_desc(smem_addr(smem + t * C::kStage));
-            const uint32_t s_at = tmem + t * kTile, o_at = tmem + 2 * kTile + t * D;
+            const uint32_t s_at = tmem + t * kTile, p_at = tmem + C::kP + t * C::kPStep, o_at = tmem + C::kO + t * D;
             auto logits = [&](int stage) {
                 const uint64_t db = tile_desc(smem_addr(ring + stage * C::kStage));
 #pragma unroll
@@ -845,14 +866,38 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                                       mbar_wait_fast(&sh.v_ok[(vt.it >> 1) & 3], (vt.it >> 3) & 1, fail));
                     const uint64_t db = value_desc(smem_addr(ring + vt.s * C::kStage));
                     kt.add(step);
+                    if (C::kApart && more) {
+                        ok = __all_sync(kFullMask, ok && mbar_wait_fast(&sh.s_free[t], done & 1, fail) && full(kt));
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            logits(kt.s);
+                            release(kt);
+                        }
+                        __syncwarp();
+                    }
                     ok = __all_sync(kFullMask, ok && mbar_wait_fast(&sh.p_ready[t][0], done & 1, fail));
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) mma_bf16_tmem(o_at, s_at + 8 * x, db + x * (2048 / 16), pv, n > 0 || x > 0);
+                        for (int x = 0; x < 4; ++x) mma_bf16_tmem(o_at, p_at + 8 * x, db + x * (2048 / 16), pv, n > 0 || x > 0);
                     }
                     __syncwarp();
+                    if constexpr (C::kApart) {
+                        ok = __all_sync(kFullMask, mbar_wait_fast(&sh.p_ready[t][1], done & 1, fail));
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int x = 4; x < 8; ++x) mma_bf16_tmem(o_at, p_at + 8 * x, db + x * (2048 / 16), pv, true);
+                            mma_commit(&sh.o_full[t]);
+                            release(vt);
+                        }
+                        __syncwarp();
+                        vt.add(step);
+                        continue;
+                    }
                     // The tiles take turns, so that one's exponentials run under the other's products:
                     // left alone they fall into step, and each waits for the other in both.
                     ok = t + blocks == 0 || mbar_wait_fast(&sh.turn[t], (blocks + t - 1) & 1, fail);
@@ -863,7 +908,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     const bool ready = more && kStages >= 5 && __all_sync(kFullMask, full(kt));
                     if (elect_one()) {
 #pragma unroll
-                        for (int x = 4; x < 8; ++x) mma_bf16_tmem(o_at, s_at + 8 * x, db + x * (2048 / 16), pv, true);
+                        for (int x = 4; x < 8; ++x) mma_bf16_tmem(o_at, p_at + 8 * x, db + x * (2048 / 16), pv, true);
                         if (ready) logits(kt.s);
                         release(vt);
                         if (ready) release(kt);
@@ -882,7 +927,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (ok && mine < k.tiles(0)) {  // an odd number in halves: a turn without a tile
+                if (!C::kApart && ok && mine < k.tiles(0)) {  // an odd number in halves: a turn without a tile
                     ok = __all_sync(kFullMask, mbar_wait_fast(&sh.turn[t], (blocks + t - 1) & 1, fail));
                     ++blocks;
                     if (ok && elect_one()) mbar_arrive(&sh.turn[t ^ 1]);
