@@ -25,6 +25,9 @@ constexpr int kHeads = 16;           // query heads of an item at most
 constexpr int kLeast = 2 * kWarps;   // units a block takes at least
 constexpr int kItem = 8;             // units of time that an item costs beside its own
 constexpr float kLog2e = 1.4426950408889634f;
+// log2 of how far m may be behind the largest logit (so that most units need no maximum over the
+// lanes), and what FP8 weights are raised by: fp16 from 2^15 down to 2^-32 of the largest
+constexpr float kLag = 8.0f, kBoost = 7.0f;
 
 // What a block leaves of a head that others share: [block][first or last][row].
 struct Part {
@@ -65,7 +68,7 @@ __host__ __device__ constexpr size_t ws_bytes(int blocks, int D) {
 struct DecodeArgs {
     AttnArgs a;
     int G, groups, heads, items;  // query heads a key head, in `groups` of up to `heads`; items a sequence
-    int box;                      // cache rows of a TMA box
+    int box, boxes;               // cache rows of a TMA box, boxes a unit
     uint8_t *ws;
 };
 
@@ -276,14 +279,15 @@ struct Loader {
     using C = Cfg<D, FP8>;
     Place<C::kUnit> p;
     int64_t x0, x1;       // the block's run
-    int u, end;           // the warp's next unit in the item, the piece's end in it
+    int u, end, h;        // the warp's next unit in the item, the piece's end in it; key head
     int left, held;       // units of which the lanes (still) hold the pages
     int page, row;        // lane: of box lane % (boxes a unit); the page past the last: none
     int slot, scale_slot, behind;  // behind: whose scales are not yet in shared memory, or -1
     uint2 scales;         // lane: eight of those
     bool more;
 
-    __device__ __forceinline__ void piece(int warp) {
+    __device__ __forceinline__ void piece(const DecodeArgs &d, int warp) {
+        h = d.groups == 1 ? p.item : p.item / d.groups;
         u = (int)(max(x0, p.at) - p.at) + warp;
         end = (int)min((int64_t)p.k.n, x1 - p.at);
         left = 0;
@@ -321,12 +325,12 @@ struct Loader {
         while (more && u >= end) {
             p.next(d);
             more = p.at < x1;
-            if (more) piece(warp);
+            if (more) piece(d, warp);
         }
         if (!more) return;
-        const int boxes = C::kUnit / d.box;
+        const int boxes = d.boxes;
         if (left == 0) pages(d, boxes, lane);
-        const int h = p.item / d.groups, from = boxes * (held - left);
+        const int from = boxes * (held - left);
         const uint32_t st = ring + slot * 2 * C::kTile;
         const bool leader = elect_one();
         if (leader) expect_bytes(full + slot, 2 * C::kTile);
@@ -488,11 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     load.p = p;
     load.x0 = x0;
     load.x1 = x1;
-    load.held = 32 / (C::kUnit / d.box);
+    load.held = 32 / d.boxes;
     load.slot = load.scale_slot = 0;
     load.behind = -1;
     load.more = true;
-    load.piece(warp);
+    load.piece(d, warp);
 #pragma unroll 1
     for (int i = 0; i < C::kStages - 1; ++i) load.issue(d, &kmap, &vmap, ring, scale_ring, full, warp, lane);
 
@@ -644,13 +648,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t ek, e;
                         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(ek) : "r"(sc + 16 * t + 8 * i + row) : "memory");
                         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(sc + C::kUnit + 16 * t + 8 * i + row) : "memory");
-                        const float f = scale_value(ek);
+                        // 2^(ek - 127), NaN for 255; 0 for ek = 0, which is off by less than the logits'
+                        // last bit: 2^-127 of a sum below 2^17 |q|
+                        const float f = __uint_as_float(ek == 255 ? 0x7fffffffu : ek << 23);
 #pragma unroll
                         for (int n = 0; n < NH; ++n) {
                             s[t][n][2 * i] *= f;
                             s[t][n][2 * i + 1] *= f;
                         }
-                        ev[t][i] = e == 255 ? __uint_as_float(0x7fffffffu) : (float)((int)e - 127);
+                        // e - 127, by a number whose last bits are e
+                        ev[t][i] = e == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | e) - 8388735.0f;
                     }
             }
 #pragma unroll
@@ -670,52 +677,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int n = 0; n < NH; ++n) s[t][n][2 * i] = s[t][n][2 * i + 1] = -INFINITY;
                         }
             }
-            float base[NH][2], basev[NH][2];
+            float top[NH][2], topv[NH][2];
             bool grown = false;
 #pragma unroll
             for (int n = 0; n < NH; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float top = m[n][i], topv = mv[n][i];
+                    top[n][i] = topv[n][i] = -INFINITY;
 #pragma unroll
                     for (int t = 0; t < KT; ++t) {
-                        top = fmaxf(top, fmaxf(s[t][n][i], s[t][n][2 + i]));
-                        if constexpr (FP8) topv = fmaxf(topv, fmaxf(s[t][n][i] + ev[t][0], s[t][n][2 + i] + ev[t][1]));
+                        top[n][i] = fmaxf(top[n][i], fmaxf(s[t][n][i], s[t][n][2 + i]));
+                        if constexpr (FP8)
+                            topv[n][i] = fmaxf(topv[n][i], fmaxf(s[t][n][i] + ev[t][0], s[t][n][2 + i] + ev[t][1]));
                     }
-#pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) {
-                        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
-                        if constexpr (FP8) topv = fmaxf(topv, __shfl_xor_sync(kFullMask, topv, x));
-                    }
-                    grown |= top > m[n][i] || (FP8 && topv > mv[n][i]);
-                    base[n][i] = top;
-                    basev[n][i] = topv;
+                    grown |= top[n][i] > m[n][i] + kLag || (FP8 && topv[n][i] > mv[n][i] + kLag);
                 }
             if (__any_sync(kFullMask, grown)) {
 #pragma unroll
                 for (int n = 0; n < NH; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        // a head that has seen no key yet subtracts 0 from its -infinities
-                        const float f = base[n][i] == -INFINITY ? 1.0f : exp2_fast(m[n][i] - base[n][i]);
-                        const float fo = !FP8 ? f : basev[n][i] == -INFINITY ? 1.0f : exp2_fast(mv[n][i] - basev[n][i]);
+                        float a1 = fmaxf(m[n][i], top[n][i]), a2 = fmaxf(mv[n][i], topv[n][i]);
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) {
+                            a1 = fmaxf(a1, __shfl_xor_sync(kFullMask, a1, x));
+                            if constexpr (FP8) a2 = fmaxf(a2, __shfl_xor_sync(kFullMask, a2, x));
+                        }
+                        // a head that has seen no key yet has nothing to scale down
+                        const float f = a1 == -INFINITY ? 1.0f : exp2_fast(m[n][i] - a1);
+                        const float fo = !FP8 ? f : a2 == -INFINITY ? 1.0f : exp2_fast(mv[n][i] - a2);
                         l[n][i] *= f;
 #pragma unroll
                         for (int t = 0; t < D / 16; ++t) {
                             o[n][t][i] *= fo;
                             o[n][t][2 + i] *= fo;
                         }
-                        m[n][i] = base[n][i];
-                        mv[n][i] = basev[n][i];
+                        m[n][i] = a1;
+                        mv[n][i] = a2;
                     }
             }
+            float base[NH][2], basev[NH][2];
 #pragma unroll
             for (int n = 0; n < NH; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (base[n][i] == -INFINITY) base[n][i] = 0.0f;
-                    // the value's scale belongs to the weight: next to 2^10 at most, fp16
-                    basev[n][i] = 10.0f - (basev[n][i] == -INFINITY ? 0.0f : basev[n][i]);
+                    // a head that has seen no key yet subtracts 0 from its -infinities
+                    base[n][i] = m[n][i] == -INFINITY ? 0.0f : m[n][i];
+                    // the value's scale belongs to the weight
+                    basev[n][i] = kBoost - (mv[n][i] == -INFINITY ? 0.0f : mv[n][i]);
                 }
             // ---- probabilities, and o += v p, sixteen keys at a time ----
 #pragma unroll
@@ -807,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r = 2 * c + i;
                 if (row == 0) sh.part[warp][r] = {m[n][i], l[n][i]};
                 // FP8: from the scaled weights' unit to the probabilities'
-                const float f = !FP8 ? 1.0f : m[n][i] == -INFINITY ? 0.0f : exp2_fast(mv[n][i] - m[n][i] - 10.0f);
+                const float f = !FP8 ? 1.0f : m[n][i] == -INFINITY ? 0.0f : exp2_fast(mv[n][i] - m[n][i] - kBoost);
                 float *to = merge + (warp * 8 + r) * D;
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t)
@@ -908,6 +917,7 @@ cudaError_t launch(DecodeArgs d, cudaStream_t stream) {
     const KvArgs &kv = d.a.kv;
     d.box = kv.page_size & -kv.page_size;  // a box lies within a page
     if (d.box > C::kUnit) d.box = C::kUnit;
+    d.boxes = C::kUnit / d.box;
     CUtensorMap kmap, vmap;
     const int64_t dims[4] = {C::kRow, kv.Hkv, kv.page_size, kv.pages};
     const int64_t strides[3] = {kv.head_stride, kv.row_stride, kv.page_stride};

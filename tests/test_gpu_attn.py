@@ -372,6 +372,34 @@ def test_prefill_not_finite_outside_the_window(quant):
     assert torch.isnan(out.cpu()[seen]).any(-1).all()
 
 
+@pytest.mark.parametrize("quant", [BF, F8])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_decode_not_finite_in_seen_keys(what, quant):
+    """A key or value that is not a number makes every query head that sees it NaN, whatever the
+    sign of its product with the query."""
+    s = Seqs([300, 40, 5], None, Hq=32, Hkv=2, quant=quant, page=64)
+    for j in (3, 250):  # behind the second sequence's last key lies what its page holds
+        p, r = s.table[0, j // s.page].long(), j % s.page
+        if quant == BF:
+            getattr(s, what)[p, r, 0, 5] = float("nan")
+        else:
+            getattr(s, what + "s")[p, 0, r] = 255
+    out, lse = run(s, True)
+    clean = Seqs([300, 40, 5], None, Hq=32, Hkv=2, quant=quant, page=64)
+    want, noise, want_l, noise_l = clean.attention()
+    ref.close_bf16(out[1:].cpu(), want[1:], noise[1:])
+    ref.close_bf16(out[:1, 16:].cpu(), want[:1, 16:], noise[:1, 16:])
+    hit = out[0, :16].cpu()
+    if what == "v" and quant == BF:
+        assert torch.isnan(hit[:, 5]).all()
+        rest = [d for d in range(128) if d != 5]
+        ref.close_bf16(hit[:, rest], want[0, :16][:, rest], noise[0, :16][:, rest])
+    else:
+        assert torch.isnan(hit).all()
+    if what == "v":
+        assert ((lse.cpu().to(ref.F64) - want_l).abs() <= noise_l).all()
+
+
 def test_infinite_value_that_is_seen():
     """An infinite value channel is infinite in every row that sees it, the others are not."""
     s = Seqs([200], [200], Hq=2, Hkv=1)
