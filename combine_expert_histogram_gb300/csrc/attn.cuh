@@ -101,6 +101,15 @@ __device__ __forceinline__ uint32_t ld_dep_if(bool there, const void *p) {
         : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t ld_byte_if(bool there, const void *p, uint32_t otherwise) {
+    uint32_t v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, %3;\n\t@p ld.global.u8 %0, [%1];\n\t}"
+        : "=&r"(v)
+        : "l"(p), "r"((uint32_t)there), "r"(otherwise)
+        : "memory");
+    return v;
+}
 
 // The value of an E8M0 scale (255: NaN).
 __device__ __forceinline__ float scale_value(uint32_t e) {

@@ -18,8 +18,11 @@
 //     m is let lag behind the true maximum by up to 2^8 (P and l stay far inside fp32, and
 //     P's relative rounding is the same), so that O is rescaled only in the rare tiles where
 //     a row's maximum jumps;
-//   - 8-bit caches: two warpgroups turn the E4M3 tiles into bf16, a thread half a row, which is
-//     exact (a power of two times three bits).  bf16 caches: a warp looks for values that are not
+//   - 8-bit caches: a warpgroup turns the E4M3 tiles into bf16, a thread a row, which is exact (a
+//     power of two times four bits), in loops of few instructions: beside the other roles' code long
+//     unrolled ones wait for their instructions (570 us for the prompts that take 470 now).  Two
+//     such warpgroups would leave the exponentials too few registers for a row of S (540 us,
+//     with S taken twice).  bf16 caches: a warp looks for values that are not
 //     finite in tiles that not all rows see: 0 * NaN would reach the other rows.
 // The work, a step being one tile of keys (two, for a block of at most 128 rows), is one list
 // over sequences, key heads and row blocks, of which every SM takes an equal run, wherever row
@@ -71,7 +74,7 @@ struct Piece {
 };
 
 struct Shared {
-    uint64_t full[5], empty[5], raw_full[4], raw_empty[4];
+    uint64_t full[5], empty[5], raw_full[5], raw_empty[5];
     uint64_t q_full[2], s_full[2], s_free[2], p_ready[2][2], o_full[2], turn[2], v_ok[4], ml_ready, o_read, drain;
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     int64_t sums[20], found_at;
@@ -83,9 +86,9 @@ struct Shared {
 
 template <int D, bool FP8>
 struct Cfg {
-    static constexpr int kThreads = FP8 ? 640 : 384;
-    // registers a thread: 96 or 168 at launch
-    static constexpr int kSoftRegs = FP8 ? 144 : 208, kOtherRegs = FP8 ? 64 : 88;
+    static constexpr int kThreads = FP8 ? 512 : 384;
+    // registers a thread: 128 or 168 at launch
+    static constexpr int kSoftRegs = FP8 ? 192 : 208, kOtherRegs = FP8 ? 64 : 88;
     static constexpr int kPanels = D / 64;               // 128-byte columns of a tile
     // Tensor memory (512 columns): S of both tiles, then O.  Heads of 64 leave room for P apart from S, so
     // that the next tile's S is there when its exponentials begin.
@@ -94,10 +97,14 @@ struct Cfg {
     static constexpr int kO = kApart ? 3 * kTile : 2 * kTile;
     static constexpr int kPanel = kTile * 128;
     static constexpr int kStage = kPanels * kPanel;      // a bf16 tile
-    static constexpr int kStages = FP8 && D == 128 ? 3 : 5;
-    // 8-bit tiles: memory answers after about 1.5 us, in which four are wanted
-    static constexpr int kRaw = FP8 ? kTile * D : 0, kRaws = 4;
-    static constexpr int kSmem = (2 + kStages) * kStage + kRaws * kRaw + (int)sizeof(Shared);
+    static constexpr int kStages = 5;
+    // 8-bit tiles: of heads of 128, where there is no room beside the stages, in their stage's second panel,
+    // whose rows are as long as theirs
+    static constexpr bool kInside = FP8 && D == 128;
+    static constexpr int kRawPitch = kInside ? kStage : kTile * D;
+    static constexpr int kRawAt = 2 * kStage + (kInside ? kPanel : kStages * kStage);
+    static constexpr int kBarriers = (2 + kStages) * kStage + (FP8 && !kInside ? kStages * kRawPitch : 0);
+    static constexpr int kSmem = kBarriers + (int)sizeof(Shared);
 };
 
 struct PrefillArgs {
@@ -216,6 +223,15 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+// 2^(e - 127), NaN for 255, twice in bf16.
+__device__ __forceinline__ uint32_t scale_bf16(uint32_t e) {
+    return (e == 255 ? 0x7fffu : e == 0 ? 0x40u : e << 7) * 0x10001u;
+}
+__device__ __forceinline__ uint32_t mul_bf16(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
 // In the upper bit of each half: whether that bf16 is an infinity or NaN.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 // w with the halves that are not finite as 0.
@@ -262,8 +278,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     // all of the block's shared memory: queries, the ring (the swizzle wants 1024-byte
     // alignment; static arrays would push it off), 8-bit tiles
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *ring = smem + 2 * C::kStage, *raws = ring + kStages * C::kStage;
-    Shared &sh = *reinterpret_cast<Shared *>(raws + C::kRaws * C::kRaw);
+    uint8_t *ring = smem + 2 * C::kStage;
+    Shared &sh = *reinterpret_cast<Shared *>(smem + C::kBarriers);
     const AttnArgs &a = d.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const volatile int *fail = &sh.fail;
@@ -271,12 +287,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], FP8 ? 8 : 1);
+            mbar_init(&sh.full[i], FP8 ? 4 : 1);
             mbar_init(&sh.empty[i], FP8 ? 2 : 3);
         }
-        for (int i = 0; i < C::kRaws; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.raw_full[i], 1);
-            mbar_init(&sh.raw_empty[i], 8);
+            mbar_init(&sh.raw_empty[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.q_full[i], 4);
@@ -290,7 +306,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         for (int i = 0; i < 4; ++i) mbar_init(&sh.v_ok[i], 1);
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&sh.piece_full[i], 1);
-            mbar_init(&sh.piece_empty[i], FP8 ? 18 : 11);  // warps that read it
+            mbar_init(&sh.piece_empty[i], FP8 ? 14 : 11);  // warps that read it
         }
         mbar_init(&sh.ml_ready, 4);
         mbar_init(&sh.o_read, 4);
@@ -433,12 +449,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             ok = __all_sync(kFullMask, mbar_wait_fast(&sh.s_full[t], done & 1, fail));
             if (!ok) break;
             tc_fence_after();
-            // All of the row's S in registers; 8-bit caches, whose other roles leave fewer, take it
-            // twice, for the maximum and for the exponentials (a tenth longer with bf16, and
-            // as much shorter than with the registers spilled).
-            uint32_t u[FP8 ? 2 : 4][32];
+            uint32_t u[4][32];  // the row's S
 #pragma unroll
-            for (int x = 0; x < (FP8 ? 1 : 4); ++x) tmem_ld(s_at + 32 * x, u[x]);
+            for (int x = 0; x < 4; ++x) tmem_ld(s_at + 32 * x, u[x]);
             const bool masked = !(key + kTile - 1 <= wmin && (!a.window || key > wmax - a.window || key + kTile <= a.sinks));
             const int hi = pos - key + 1, lo = a.window && hi > a.window ? hi - a.window : 0, first = a.sinks - key;
             auto s_read = [&]() {  // S is in registers
@@ -448,7 +461,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 if (lane == 0) mbar_arrive(&sh.s_free[t]);
             };
             auto mask = [&](uint32_t (&v)[32], int at) {
-                if (!masked) return;
                 const uint32_t seen = low_bits(hi - at) & (~low_bits(lo - at) | low_bits(first - at));
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = seen >> j & 1 ? v[j] : 0xff800000u;  // -infinity
@@ -458,29 +470,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) part[j / 2 & 3] = max3(part[j / 2 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
             };
-            if constexpr (FP8) {
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    tmem_ld_wait(u[0]);
-                    tmem_ld(s_at + 64 * h + 32, u[1]);
-                    mask(u[0], 64 * h);
-                    largest(u[0]);
-                    tmem_ld_wait(u[1]);
-                    tmem_ld(s_at + 64 * (h ^ 1), u[0]);  // the last time: the first columns again
-                    mask(u[1], 64 * h + 32);
-                    largest(u[1]);
-                }
-            } else {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) tmem_ld_wait(u[x]);
-                s_read();
-                if (masked) {
+            for (int x = 0; x < 4; ++x) tmem_ld_wait(u[x]);
+            s_read();
+            if (masked) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) mask(u[x], 32 * x);
-                }
-#pragma unroll
-                for (int x = 0; x < 4; ++x) largest(u[x]);
+                for (int x = 0; x < 4; ++x) mask(u[x], 32 * x);
             }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) largest(u[x]);
             const float top = fmaxf(max3(part[0], part[1], part[2]), part[3]);
             // the products of the tile before read P and write O
             if (C::kApart && n > 0) {
@@ -533,27 +531,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.p_ready[t][h]);
             };
-            if constexpr (FP8) {
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    tmem_ld_wait(u[0]);
-                    tmem_ld(s_at + 64 * h + 32, u[1]);
-                    mask(u[0], 64 * h);
-                    exponentials(u[0], p_at + 32 * h);
-                    tmem_ld_wait(u[1]);
-                    if (h == 0) tmem_ld(s_at + 64, u[0]);
-                    else s_read();
-                    mask(u[1], 64 * h + 32);
-                    exponentials(u[1], p_at + 32 * h + 16);
-                    half_done(h);
-                }
-            } else {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    exponentials(u[2 * h], p_at + 32 * h);
-                    exponentials(u[2 * h + 1], p_at + 32 * h + 16);
-                    half_done(h);
-                }
+            for (int h = 0; h < 2; ++h) {
+                exponentials(u[2 * h], p_at + 32 * h);
+                exponentials(u[2 * h + 1], p_at + 32 * h + 16);
+                half_done(h);
             }
             acc0 = add2(acc0, acc1);
             float l0, l1;
@@ -695,9 +677,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             // ---- the run's pieces, and their loads: tile 0's keys, its values, tile 1's keys, ...;
             // a lane a box ----
             const int box = d.box, boxes = kTile / box;
-            constexpr int bytes = FP8 ? C::kRaw : C::kStage, slots = FP8 ? C::kRaws : kStages;
-            uint64_t *fulls = FP8 ? sh.raw_full : sh.full, *empties = FP8 ? sh.raw_empty : sh.empty;
-            uint8_t *to = (FP8 ? raws : ring) + lane * box * (FP8 ? D : 128);
+            constexpr int bytes = FP8 ? kTile * D : C::kStage, pitch = FP8 ? C::kRawPitch : C::kStage;
+            uint64_t *fulls = FP8 ? sh.raw_full : sh.full, *empties = FP8 && !C::kInside ? sh.raw_empty : sh.empty;
+            uint8_t *to = (FP8 ? smem + C::kRawAt : ring) + lane * box * (FP8 ? D : 128);
             int b = sh.found_b, h, j = 0, it = 0, p = 0;
             int64_t at = sh.found_at;
             Span sp = seq_span(a.seq, a.kv.page_size, b);
@@ -787,8 +769,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                         r = key - entry * a.kv.page_size;
                     }
                     for (int v = 0; v < 2; ++v, ++it) {
-                        const int s = it % slots;
-                        ok = __all_sync(kFullMask, it < slots || mbar_wait_fast(&empties[s], (it / slots - 1) & 1, fail));
+                        const int s = it % kStages;
+                        ok = __all_sync(kFullMask, it < kStages || mbar_wait_fast(&empties[s], (it / kStages - 1) & 1, fail));
                         if (!ok) break;
                         if (elect_one()) expect_bytes(&fulls[s], bytes);
                         __syncwarp();
@@ -796,7 +778,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                             const CUtensorMap *map = v ? &vmap : &kmap;
 #pragma unroll
                             for (int n = 0; n < (FP8 ? 1 : C::kPanels); ++n)
-                                tma_load_4d(to + s * bytes + n * C::kPanel, map, 128 * n, k.h, r, page, &fulls[s]);
+                                tma_load_4d(to + s * pitch + n * C::kPanel, map, 128 * n, k.h, r, page, &fulls[s]);
                         }
                         __syncwarp();
                     }
@@ -898,34 +880,36 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                         vt.add(step);
                         continue;
                     }
+                    // 8-bit keys may come late, converted: these products do not wait for them
+                    constexpr bool late = FP8;
                     // The tiles take turns, so that one's exponentials run under the other's products:
                     // left alone they fall into step, and each waits for the other in both.
                     ok = t + blocks == 0 || mbar_wait_fast(&sh.turn[t], (blocks + t - 1) & 1, fail);
-                    ok = __all_sync(kFullMask, ok && mbar_wait_fast(&sh.p_ready[t][1], done & 1, fail));
+                    ok = ok && mbar_wait_fast(&sh.p_ready[t][1], done & 1, fail) && (late || !more || full(kt));
+                    ok = __all_sync(kFullMask, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    // these keys may be waiting for the values' place: with few stages only then
-                    const bool ready = more && kStages >= 5 && __all_sync(kFullMask, full(kt));
                     if (elect_one()) {
 #pragma unroll
                         for (int x = 4; x < 8; ++x) mma_bf16_tmem(o_at, p_at + 8 * x, db + x * (2048 / 16), pv, true);
-                        if (ready) logits(kt.s);
+                        if (!late && more) logits(kt.s);
                         release(vt);
-                        if (ready) release(kt);
+                        if (!late && more) release(kt);
                         if (!more) mma_commit(&sh.o_full[t]);
-                        if (ready || !more) mbar_arrive(&sh.turn[t ^ 1]);
+                        if (!late || !more) mbar_arrive(&sh.turn[t ^ 1]);
+                    }
+                    if (late && more) {
+                        ok = __all_sync(kFullMask, full(kt));
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            logits(kt.s);
+                            release(kt);
+                            mbar_arrive(&sh.turn[t ^ 1]);
+                        }
                     }
                     __syncwarp();
                     vt.add(step);
-                    if (ready || !more) continue;
-                    ok = __all_sync(kFullMask, full(kt));
-                    if (!ok) break;
-                    if (elect_one()) {
-                        logits(kt.s);
-                        release(kt);
-                        mbar_arrive(&sh.turn[t ^ 1]);
-                    }
-                    __syncwarp();
                 }
                 if (!C::kApart && ok && mine < k.tiles(0)) {  // an odd number in halves: a turn without a tile
                     ok = __all_sync(kFullMask, mbar_wait_fast(&sh.turn[t], (blocks + t - 1) & 1, fail));
@@ -952,7 +936,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     if (!ok) break;
                     if ((n & 1) && k.edge(key, a.window, a.sinks)) {
                         const uint32_t st = smem_addr(ring + s * C::kStage);
-#pragma unroll 8
+#pragma unroll 2
                         for (int x = lane; x < C::kStage / 16; x += 32) {
                             uint4 w = lds16(st + 16 * x);
                             if (not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w)) {
@@ -971,88 +955,114 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 }
             }
             if (!ok) sh.fail = 1;
-        } else if (FP8 && (role < 4 || role >= 8)) {
-            // ---- E4M3 rows to bf16, a thread half a row ----
-            const int r = (role & 3) * 32 + lane, c0 = role < 4 ? 0 : D / 32;
+        } else if (FP8 && role < 4) {
+            // ---- E4M3 rows to bf16, a thread a row ----
+            const int r = role * 32 + lane;
             bool ok = true;
             Piece k;
-            // scale bytes of the row's key and value; 2^0 where there are none
-            auto bytes = [&](int i, uint32_t &sk, uint32_t &sv) {
-                sk = sv = 127;
-                const int j = k.key(i) + r;
-                if (i < k.nt && k.wanted(j, 1)) {
-                    const int entry = j / a.kv.page_size;
-                    const int page = page_of(a.kv, a.seq, k.b, entry);
-                    if (page >= 0) {
-                        const int64_t at = ((int64_t)page * a.kv.Hkv + k.h) * a.kv.page_size + (j - entry * a.kv.page_size);
-                        sk = a.kv.k_scales[at];
-                        sv = a.kv.v_scales[at];
-                    }
-                }
+            // A row's place in the cache: its entry in the block table is read a tile ahead of its
+            // scales, which are a tile ahead of their use, so that nothing waits for a load that has
+            // just been issued.
+            struct Row {
+                int entry, off;
+                bool there;
             };
-            int base = 0;
-            for (int p = 0; ok && next_piece(p, k); ++p, base += 2 * k.nt) {
-            uint32_t sk, sv;
-            bytes(0, sk, sv);
-            for (int i = 0; ok && i < k.nt; ++i) {
-                const int key = k.key(i);
-                const bool edge = k.edge(key, a.window, a.sinks), wanted = k.wanted(key + r, 1);
-                const float f[2] = {scale_value(sk), scale_value(sv)};
-                bytes(i + 1, sk, sv);
+            const int psize = a.kv.page_size, step_entries = kTile / psize, step_off = kTile % psize;
+            auto next_row = [&](int i, Row &x) {
+                const int j = k.key(i) + r;
+                if (i == 0 || k.i0 + i == k.ns) {
+                    x.entry = j / psize;
+                    x.off = j - x.entry * psize;
+                } else {  // a tile further
+                    x.entry += step_entries;
+                    x.off += step_off;
+                    if (x.off >= psize) x.off -= psize, ++x.entry;
+                }
+                x.there = i < k.nt && k.wanted(j, 1);
+            };
+            auto page = [&](const Row &x) {
+                return ld_dep_if(x.there, a.seq.table + (int64_t)k.b * a.seq.max_pages + (x.there ? x.entry : 0));
+            };
+            // scale bytes of the row's key and value; 2^0 where there are none
+            auto scales = [&](const Row &x, uint32_t page, uint32_t &sk, uint32_t &sv) {
+                const bool there = x.there && page < (uint32_t)a.kv.pages;
+                const int64_t at = there ? (int64_t)page * (a.kv.Hkv * psize) + (k.h * psize + x.off) : 0;
+                sk = ld_byte_if(there, a.kv.k_scales + at, 127);
+                sv = ld_byte_if(there, a.kv.v_scales + at, 127);
+            };
+            int s = 0, parity = 0, it = 0;  // stage, the parity of its phase, tiles so far
+            for (int p = 0; ok && next_piece(p, k); ++p) {
+                uint32_t sk, sv, then;
+                Row at;
+                next_row(0, at);
+                scales(at, page(at), sk, sv);
+                next_row(1, at);
+                then = page(at);
+                for (int i = 0; ok && i < k.nt; ++i) {
+                    const uint32_t fk = scale_bf16(sk), fv = scale_bf16(sv);
+                    scales(at, then, sk, sv);
+                    next_row(i + 2, at);
+                    then = page(at);
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v) {
+                        ok = ok && mbar_wait_fast(&sh.raw_full[s], parity, fail) &&
+                             (C::kInside || it < kStages || mbar_wait_fast(&sh.empty[s], parity ^ 1, fail));
+                        ok = __all_sync(kFullMask, ok);
+                        if (!ok) break;
+                        const uint32_t src = smem_addr(smem + C::kRawAt + s * C::kRawPitch) + r * D;
+                        const uint32_t dst = smem_addr(ring + s * C::kStage) + r * 128;
+                        auto chunk = [&](int ch) { return dst + (ch >> 3) * C::kPanel + 16 * ((ch & 7) ^ (r & 7)); };
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D / 16; c0 += 2) {
+                            uint4 x[2];
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const int it = base + 2 * i + v, rs = it % C::kRaws, s = it % kStages;
-                    ok = ok && mbar_wait_fast(&sh.raw_full[rs], (it / C::kRaws) & 1, fail) &&
-                         (it < kStages || mbar_wait_fast(&sh.empty[s], (it / kStages - 1) & 1, fail));
-                    ok = __all_sync(kFullMask, ok);
-                    if (!ok) break;
-                    const uint32_t src = smem_addr(raws + rs * C::kRaw) + r * D, dst = smem_addr(ring + s * C::kStage) + r * 128;
-                    uint32_t bad = 0;
-                    uint4 x[D / 32];  // all of it first: it takes its time
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t from = src + 16 * (c0 + c);
+                                from ^= (from >> 3) & (D == 128 ? 0x70 : 0x30);  // the TMA's swizzle, by the address
+                                x[c] = lds16(from);
+                            }
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t at = src + 16 * (c0 + c);
-                        at ^= (at >> 3) & (D == 128 ? 0x70 : 0x30);  // the TMA's swizzle, by the address
-                        x[c] = lds16(at);
-                    }
+                            for (int c = 0; c < 2; ++c) {
+                                const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+                                uint32_t y[8];
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-                        uint32_t y[8];
+                                for (int j = 0; j < 4; ++j) {
+                                    uint32_t h[2];
+                                    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+                                        "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+                                        : "=r"(h[0]), "=r"(h[1])
+                                        : "r"(w[j]));
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t p[2];
-                            asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
-                                "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
-                                : "=r"(p[0]), "=r"(p[1])
-                                : "r"(w[j]));
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&p[z]));
-                                y[2 * j + z] = pack_bf16(g.x * f[v], g.y * f[v]);
+                                    for (int z = 0; z < 2; ++z) {
+                                        const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&h[z]));
+                                        y[2 * j + z] = mul_bf16(pack_bf16(g.x, g.y), v ? fv : fk);
+                                    }
+                                }
+                                sts16(chunk(2 * (c0 + c)), make_uint4(y[0], y[1], y[2], y[3]));
+                                sts16(chunk(2 * (c0 + c) + 1), make_uint4(y[4], y[5], y[6], y[7]));
                             }
                         }
-                        if (v && edge) {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                bad |= not_finite(y[j]);
-                                y[j] = finite_part(y[j]);
+                        if (v && k.edge(k.key(i), a.window, a.sinks)) {
+                            uint32_t bad = 0;
+#pragma unroll 1
+                            for (int ch = 0; ch < D / 8; ++ch) {
+                                const uint4 y = lds16(chunk(ch));
+                                const uint32_t some = not_finite(y.x) | not_finite(y.y) | not_finite(y.z) | not_finite(y.w);
+                                if (some) sts16(chunk(ch), make_uint4(finite_part(y.x), finite_part(y.y), finite_part(y.z), finite_part(y.w)));
+                                bad |= some;
                             }
+                            if (bad && k.wanted(k.key(i) + r, 1)) sh.fix = 1;
                         }
-                        const int ch = 2 * (c0 + c);
-                        const uint32_t to = dst + (ch >> 3) * C::kPanel;
-                        sts16(to + 16 * ((ch & 7) ^ (r & 7)), make_uint4(y[0], y[1], y[2], y[3]));
-                        sts16(to + 16 * ((ch + 1 & 7) ^ (r & 7)), make_uint4(y[4], y[5], y[6], y[7]));
-                    }
-                    if (bad && wanted) sh.fix = 1;
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sh.full[s]);
-                        mbar_arrive(&sh.raw_empty[rs]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&sh.full[s]);
+                            if (!C::kInside) mbar_arrive(&sh.raw_empty[s]);
+                        }
+                        ++it;
+                        if (++s == kStages) s = 0, parity ^= 1;
                     }
                 }
-            }
             }
             if (!ok) sh.fail = 1;
         }
@@ -1063,10 +1073,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     if (sh.fail) {
         if (threadIdx.x == 0) raise_status(a.seq.status, EP_ERR_TIMEOUT);
         // let the loads in flight land before the shared memory goes
-        constexpr int slots = FP8 ? C::kRaws : kStages;
-        if ((int)threadIdx.x < slots) {
+        if ((int)threadIdx.x < kStages) {
             const int last = sh.issued - 1 - (int)threadIdx.x;
-            if (last >= 0) mbar_wait(FP8 ? &sh.raw_full[last % slots] : &sh.full[last % slots], (last / slots) & 1, nullptr);
+            if (last >= 0) mbar_wait(FP8 ? &sh.raw_full[last % kStages] : &sh.full[last % kStages], (last / kStages) & 1, nullptr);
         }
         __syncthreads();
     }
