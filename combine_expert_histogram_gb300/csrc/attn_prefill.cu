@@ -88,7 +88,7 @@ template <int D, bool FP8>
 struct Cfg {
     static constexpr int kThreads = FP8 ? 512 : 384;
     // registers a thread: 128 or 168 at launch
-    static constexpr int kSoftRegs = FP8 ? 192 : 208, kOtherRegs = FP8 ? 64 : 88;
+    static constexpr int kSoftRegs = FP8 ? 184 : 200, kOtherRegs = FP8 ? 72 : 104;
     static constexpr int kPanels = D / 64;               // 128-byte columns of a tile
     // Tensor memory (512 columns): S of both tiles, then O.  Heads of 64 leave room for P apart from S, so
     // that the next tile's S is there when its exponentials begin.
@@ -422,13 +422,20 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.q_full[t]);
         };
-        Piece k;
-        bool have = next_piece(0, k);
-        if (have && k.tiles(t) > 0) {
-            copy_queries(k);
+        // Pieces stay in shared memory: registers are short here.
+        auto piece = [&](int p) -> const Piece & { return sh.pieces[p % kPieces]; };
+        auto piece_there = [&](int p) {
+            const bool ok = __all_sync(kFullMask, mbar_wait_fast(&sh.piece_full[p % kPieces], (p / kPieces) & 1, fail));
+            if (!ok) sh.fail = 1;
+            return ok && piece(p).nt >= 0;
+        };
+        bool have = piece_there(0);
+        if (have && piece(0).tiles(t) > 0) {
+            copy_queries(piece(0));
             queries_there();
         }
         for (int p = 1; have; ++p) {
+        const Piece &k = piece(p - 1), &next = piece(p);
         // ---- a thread's row ----
         const bool halves = k.halves();
         const int local = (halves ? 0 : t * kTile) + wrow + lane;
@@ -542,8 +549,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             unpair(acc0, l0, l1);
             l = l0 + l1;
         }
-        Piece next;
-        have = ok && next_piece(p, next);
+        have = ok && piece_there(p);
         if (ok && mine_of > 0) ok = __all_sync(kFullMask, mbar_wait_fast(&sh.o_full[t], (C::kApart ? done - 1 : o_done++) & 1, fail));
         // The next piece's queries come while this one's results go (and not for a half without a
         // tile, which would run ahead of its barriers' readers).
@@ -668,7 +674,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             }
         }
         if (pending) queries_there();
-        k = next;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.piece_empty[(p - 1) % kPieces]);
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
