@@ -766,15 +766,26 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 __syncwarp();
                 ++p;
                 if (!some) break;
+                // the block table's entry and the row of a box, looked up a tile ahead
+                uint32_t entry = 0;
+                int row = 0;
+                bool there = false;
+                auto look = [&](int i) {
+                    const int key = k.key(i) + lane * box, e = key / a.kv.page_size;
+                    there = i < k.nt && lane < boxes && k.wanted(key, box);
+                    row = key - e * a.kv.page_size;
+                    entry = ld_dep_if(there, a.seq.table + (int64_t)k.b * a.seq.max_pages + (there ? e : 0));
+                };
+                look(0);
                 for (int i = 0; ok && i < k.nt; ++i) {
-                    const int key = k.key(i) + lane * box;
                     int page = a.kv.pages, r = 0;  // outside: zeros, and no reads
-                    if (lane < boxes && k.wanted(key, box)) {
-                        const int entry = key / a.kv.page_size;
-                        const int q = page_of(a.kv, a.seq, k.b, entry);
-                        if (q >= 0) page = q;
-                        r = key - entry * a.kv.page_size;
+                    if (there && entry < (uint32_t)a.kv.pages) {
+                        page = entry;
+                        r = row;
+                    } else if (there) {
+                        raise_status(a.seq.status, EP_ERR_BAD_PAGE);
                     }
+                    look(i + 1);
                     for (int v = 0; v < 2; ++v, ++it) {
                         const int s = it % kStages;
                         ok = __all_sync(kFullMask, it < kStages || mbar_wait_fast(&empties[s], (it / kStages - 1) & 1, fail));
