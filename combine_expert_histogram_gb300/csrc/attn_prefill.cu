@@ -834,6 +834,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 }
             };
             auto full = [&](const Place &at) { return mbar_wait_fast(&sh.full[at.s], at.parity, fail); };
+            // A wait for a phase must not come before the phase before it is over: a half's keys take
+            // the stage that the other half's values had, which this warp has not waited for.  Where
+            // the row tiles take turns, or converters fill the stages in order, they are there; else
+            // it waits for the values before these keys to be looked through, which goes in order.
+            auto keys = [&](const Place &at, bool alone) {
+                const int last = (at.it >> 1) - 1;
+                return (!C::kApart || FP8 || !alone || last < 0 ||
+                        mbar_wait_fast(&sh.v_ok[last & 3], last >> 2 & 1, fail)) && full(at);
+            };
             int base = 0, done = 0, blocks = 0, queries = 0;  // ring index, tiles, turns, pieces with tiles so far
             bool ok = true;
             Piece k;
@@ -850,7 +859,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 kt.set(base + (halves ? 2 * t : 0));
                 vt = kt;
                 vt.add(1);
-                ok = mine == 0 || (mbar_wait_fast(&sh.q_full[t], queries++ & 1, fail) && full(kt));
+                ok = mine == 0 || (mbar_wait_fast(&sh.q_full[t], queries++ & 1, fail) && keys(kt, true));
                 ok = __all_sync(kFullMask, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -867,7 +876,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     const uint64_t db = value_desc(smem_addr(ring + vt.s * C::kStage));
                     kt.add(step);
                     if (C::kApart && more) {
-                        ok = __all_sync(kFullMask, ok && mbar_wait_fast(&sh.s_free[t], done & 1, fail) && full(kt));
+                        ok = __all_sync(kFullMask, ok && mbar_wait_fast(&sh.s_free[t], done & 1, fail) && keys(kt, halves));
                         if (!ok) break;
                         tc_fence_after();
                         if (elect_one()) {
