@@ -5,8 +5,8 @@
 // with the running maximum m of a row.  A block has up to 256 rows, the tokens of one sequence
 // times the query heads that share a key head, and goes once over the 128-key tiles that its
 // rows see.  Roles:
-//   - a loader keeps a ring of key and value tiles in flight by tiled TMA loads, page by
-//     page;
+//   - a loader (two, where pages are short) keeps a ring of key and value tiles in flight by
+//     tiled TMA loads, page by page;
 //   - one thread for each of two row tiles of 128 issues the products on tcgen05: S of a tile
 //     into tensor memory, and P V with P read from tensor memory, where it takes the place of
 //     S.  One tile's exponentials run under the other's products; a block of at most
@@ -81,14 +81,15 @@ struct Shared {
     float2 ml[kTile];  // of the odd tiles' half
     Piece pieces[kPieces];
     uint32_t tmem;
-    int fail, fix, issued, found_b;
+    int fail, fix, issued[2], found_b;
 };
 
-template <int D, bool FP8>
+// TWO: a warp loads the keys, another the values.
+template <int D, bool FP8, bool TWO>
 struct Cfg {
-    static constexpr int kThreads = FP8 ? 512 : 384;
+    static constexpr int kThreads = FP8 || TWO ? 512 : 384, kMmaWarp = FP8 || TWO ? 12 : 9;  // and the next warp
     // registers a thread: 128 or 168 at launch
-    static constexpr int kSoftRegs = FP8 ? 184 : 200, kOtherRegs = FP8 ? 72 : 104;
+    static constexpr int kSoftRegs = FP8 ? 184 : TWO ? 176 : 200, kOtherRegs = FP8 ? 72 : TWO ? 80 : 104;
     static constexpr int kPanels = D / 64;               // 128-byte columns of a tile
     // Tensor memory (512 columns): S of both tiles, then O.  Heads of 64 leave room for P apart from S, so
     // that the next tile's S is there when its exponentials begin.
@@ -269,11 +270,11 @@ __device__ __forceinline__ int64_t all_places(const PrefillArgs &d, const Span &
     return n;
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
+template <int D, bool FP8, bool TWO>
+__global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ PrefillArgs d) {
-    using C = Cfg<D, FP8>;
+    using C = Cfg<D, FP8, TWO>;
     constexpr int kStages = C::kStages;
     // all of the block's shared memory: queries, the ring (the swizzle wants 1024-byte
     // alignment; static arrays would push it off), 8-bit tiles
@@ -283,11 +284,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     const AttnArgs &a = d.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const volatile int *fail = &sh.fail;
-    constexpr int kMmaWarp = FP8 ? 12 : 9;  // and the next one
+    constexpr int kMmaWarp = C::kMmaWarp;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], FP8 ? 4 : 1);
+            mbar_init(&sh.full[i], FP8 ? 4 : 1 + TWO);
             mbar_init(&sh.empty[i], FP8 ? 2 : 3);
         }
         for (int i = 0; i < kStages; ++i) {
@@ -306,12 +307,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         for (int i = 0; i < 4; ++i) mbar_init(&sh.v_ok[i], 1);
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&sh.piece_full[i], 1);
-            mbar_init(&sh.piece_empty[i], FP8 ? 14 : 11);  // warps that read it
+            mbar_init(&sh.piece_empty[i], FP8 ? 14 : 11 + TWO);  // warps that read it
         }
         mbar_init(&sh.ml_ready, 4);
         mbar_init(&sh.o_read, 4);
         mbar_init(&sh.drain, 2);
-        sh.fail = sh.fix = sh.issued = 0;
+        sh.fail = sh.fix = sh.issued[0] = sh.issued[1] = 0;
         mbar_init_fence();
         tma_prefetch_map(&kmap);
         tma_prefetch_map(&vmap);
@@ -680,14 +681,55 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         const int role = warp - 8;
-        if (role == (FP8 ? 6 : 0)) {
-            // ---- the run's pieces, and their loads: tile 0's keys, its values, tile 1's keys, ...;
-            // a lane a box ----
+        // The loads of a piece, the run's tiles n, n + 1, ...: keys, values, keys, ...; with two loaders
+        // the `mine` ones (0: keys).  A lane a box, whose entry in the block table is looked up a
+        // tile ahead.
+        auto load = [&](const Piece &k, int mine, int &n) {
             const int box = d.box, boxes = kTile / box;
             constexpr int bytes = FP8 ? kTile * D : C::kStage, pitch = FP8 ? C::kRawPitch : C::kStage;
             uint64_t *fulls = FP8 ? sh.raw_full : sh.full, *empties = FP8 && !C::kInside ? sh.raw_empty : sh.empty;
             uint8_t *to = (FP8 ? smem + C::kRawAt : ring) + lane * box * (FP8 ? D : 128);
-            int b = sh.found_b, h, j = 0, it = 0, p = 0;
+            uint32_t entry = 0;
+            int row = 0;
+            bool there = false;
+            auto look = [&](int i) {
+                const int key = k.key(i) + lane * box, e = key / a.kv.page_size;
+                there = i < k.nt && lane < boxes && k.wanted(key, box);
+                row = key - e * a.kv.page_size;
+                entry = ld_dep_if(there, a.seq.table + (int64_t)k.b * a.seq.max_pages + (there ? e : 0));
+            };
+            look(0);
+            for (int i = 0; i < k.nt; ++i) {
+                const bool ok = there && entry < (uint32_t)a.kv.pages;
+                if (there && !ok) raise_status(a.seq.status, EP_ERR_BAD_PAGE);
+                const int page = ok ? entry : a.kv.pages, r = ok ? row : 0;  // outside: zeros, and no reads
+                look(i + 1);
+                for (int v = 0; v < 2; ++v, ++n) {
+                    const int s = n % kStages;
+                    const bool empty = n < kStages || mbar_wait_fast(&empties[s], (n / kStages - 1) & 1, fail);
+                    if (!__all_sync(kFullMask, empty)) return false;
+                    // Both loaders see every phase of every stage, and none goes on without them: a
+                    // wait that comes a phase late or early would take one for another.
+                    if (TWO && v != mine) {
+                        if (lane == 0) mbar_arrive(&fulls[s]);
+                        continue;
+                    }
+                    if (elect_one()) expect_bytes(&fulls[s], bytes);
+                    __syncwarp();
+                    if (lane < boxes) {
+                        const CUtensorMap *map = v ? &vmap : &kmap;
+#pragma unroll
+                        for (int x = 0; x < (FP8 ? 1 : C::kPanels); ++x)
+                            tma_load_4d(to + s * pitch + x * C::kPanel, map, 128 * x, k.h, r, page, &fulls[s]);
+                    }
+                    __syncwarp();
+                }
+            }
+            return true;
+        };
+        if (role == (FP8 || TWO ? 6 : 0)) {
+            // ---- the run's pieces, and their loads ----
+            int b = sh.found_b, h, j = 0, n = 0, p = 0;
             int64_t at = sh.found_at;
             Span sp = seq_span(a.seq, a.kv.page_size, b);
             {
@@ -766,44 +808,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 __syncwarp();
                 ++p;
                 if (!some) break;
-                // the block table's entry and the row of a box, looked up a tile ahead
-                uint32_t entry = 0;
-                int row = 0;
-                bool there = false;
-                auto look = [&](int i) {
-                    const int key = k.key(i) + lane * box, e = key / a.kv.page_size;
-                    there = i < k.nt && lane < boxes && k.wanted(key, box);
-                    row = key - e * a.kv.page_size;
-                    entry = ld_dep_if(there, a.seq.table + (int64_t)k.b * a.seq.max_pages + (there ? e : 0));
-                };
-                look(0);
-                for (int i = 0; ok && i < k.nt; ++i) {
-                    int page = a.kv.pages, r = 0;  // outside: zeros, and no reads
-                    if (there && entry < (uint32_t)a.kv.pages) {
-                        page = entry;
-                        r = row;
-                    } else if (there) {
-                        raise_status(a.seq.status, EP_ERR_BAD_PAGE);
-                    }
-                    look(i + 1);
-                    for (int v = 0; v < 2; ++v, ++it) {
-                        const int s = it % kStages;
-                        ok = __all_sync(kFullMask, it < kStages || mbar_wait_fast(&empties[s], (it / kStages - 1) & 1, fail));
-                        if (!ok) break;
-                        if (elect_one()) expect_bytes(&fulls[s], bytes);
-                        __syncwarp();
-                        if (lane < boxes) {
-                            const CUtensorMap *map = v ? &vmap : &kmap;
-#pragma unroll
-                            for (int n = 0; n < (FP8 ? 1 : C::kPanels); ++n)
-                                tma_load_4d(to + s * pitch + n * C::kPanel, map, 128 * n, k.h, r, page, &fulls[s]);
-                        }
-                        __syncwarp();
-                    }
-                }
+                ok = load(k, 0, n);
             }
             if (!ok) sh.fail = 1;
-            if (lane == 0) sh.issued = it;
+            if (lane == 0) sh.issued[0] = n;
+            if (!TWO && lane == 0) sh.issued[1] = n;
+        } else if (TWO && role == 7) {
+            // ---- the loads of values ----
+            bool ok = true;
+            int n = 0;
+            Piece k;
+            for (int p = 0; ok && next_piece(p, k); ++p) ok = load(k, 1, n);
+            if (!ok) sh.fail = 1;
+            if (lane == 0) sh.issued[1] = n;
         } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
             // ---- products of row tile t ----
             constexpr uint32_t qk = bf16_instr(kTile, false), pv = bf16_instr(D, true);
@@ -950,7 +967,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             if (elect_one()) mma_commit(&sh.drain);
             __syncwarp();
             if (!mbar_wait(&sh.drain, 0, nullptr)) sh.fail = 1;
-        } else if (!FP8 && role == 3) {
+        } else if (!FP8 && role == (TWO ? 0 : 3)) {
             // ---- values that are not finite, in tiles that not all rows see.  It passes every
             // tile, so that the barriers' phases are never two ahead of it. ----
             bool ok = true;
@@ -1101,7 +1118,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         if (threadIdx.x == 0) raise_status(a.seq.status, EP_ERR_TIMEOUT);
         // let the loads in flight land before the shared memory goes
         if ((int)threadIdx.x < kStages) {
-            const int last = sh.issued - 1 - (int)threadIdx.x;
+            int last = max(sh.issued[0], sh.issued[1]) - 1 - (int)threadIdx.x;
+            if (last >= sh.issued[last & 1]) last -= kStages;
             if (last >= 0) mbar_wait(FP8 ? &sh.raw_full[last % kStages] : &sh.full[last % kStages], (last / kStages) & 1, nullptr);
         }
         __syncthreads();
@@ -1177,7 +1195,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Prefi
     }
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool TWO = false>
 cudaError_t launch(const PrefillArgs &d, cudaStream_t stream) {
     const KvArgs &kv = d.a.kv;
     CUtensorMap kmap, vmap;
@@ -1190,8 +1208,8 @@ cudaError_t launch(const PrefillArgs &d, cudaStream_t stream) {
         !encode_bytes(&vmap, kv.v, 4, dims, strides, box, swizzle))
         return cudaErrorInvalidValue;
     const int blocks = sm_count();
-    const cudaError_t err = launch_large<prefill_kernel<D, FP8>>(blocks, Cfg<D, FP8>::kThreads, Cfg<D, FP8>::kSmem,
-                                                                 stream, kmap, vmap, d);
+    const cudaError_t err = launch_large<prefill_kernel<D, FP8, TWO>>(
+        blocks, Cfg<D, FP8, TWO>::kThreads, Cfg<D, FP8, TWO>::kSmem, stream, kmap, vmap, d);
     if (err != cudaSuccess || !d.ws) return err;
     return launch_kernel(join_kernel<D>, 16 * blocks, 256, 0, stream, true, d, blocks);
 }
@@ -1209,7 +1227,12 @@ cudaError_t launch_attn_prefill(const AttnArgs &a, void *workspace, cudaStream_t
     d.ws = static_cast<uint8_t *>(workspace);
     const bool fp8 = a.kv.k_scales != nullptr;
     if (a.kv.D == 64) return fp8 ? launch<64, true>(d, stream) : launch<64, false>(d, stream);
-    return fp8 ? launch<128, true>(d, stream) : launch<128, false>(d, stream);
+    if (fp8) return launch<128, true>(d, stream);
+    // One warp issues a request of TMA in about 110 clocks: 64 of 8 rows a step of 128 keys take
+    // longer than the step.  Two loaders, for requests of 8 / 16 / 64 rows: chunks of 700 tokens
+    // after 6000, 64 heads, 412 / 378 / 367 us, with one 659 / 403 / 357; 5 tokens after 3000 73 / 66
+    // / 65, with one 82 / 64 / 62.  Rows of 128 bytes are half the requests.
+    return d.box <= 16 ? launch<128, false, true>(d, stream) : launch<128, false>(d, stream);
 }
 
 }  // namespace ep

@@ -326,6 +326,19 @@ def test_long_sequences(decode):
     assert torch.equal(k[to[-1], (n - 1) % page, 0], new[-1, 0])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("quant", [BF, F8])
+@pytest.mark.parametrize("page", [8, 16, 24, 40, 64, 256])
+def test_prefill_page_sizes(page, quant, D):
+    """Whole row blocks and row blocks of few rows, one after another, over pages of every kind."""
+    lens = [1500, 200, 1300, 3, 900]
+    s = Seqs(lens, [700, 3, 1, 3, 33], Hq=16, Hkv=2, D=D, page=page, quant=quant)
+    check(s, False)
+    out, _ = run(s, False)
+    again, _ = run(s, False)
+    assert torch.equal(out, again)
+
+
 @pytest.mark.parametrize("quant", [BF, F8])
 @pytest.mark.parametrize("what", ["k", "v"])
 def test_prefill_not_finite_in_later_keys(what, quant):
