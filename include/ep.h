@@ -47,9 +47,9 @@
  *       - the SM count of each device (read once with cudaDeviceGetAttribute);
  *       - for ep_layout and ep_layout_dispatch, the cluster size that each device
  *         can place, and its cap (EP_MAX_CLUSTER_CTAS, read once);
- *       - for ep_expert_gemm, ep_expert_swiglu and ep_moe_decode, the address of
- *         the driver's tensor-map encoder, and on which devices their kernels'
- *         shared-memory limits have been raised;
+ *       - for ep_expert_gemm, ep_expert_swiglu, ep_moe_decode, ep_attn_decode and
+ *         ep_attn_prefill, the address of the driver's tensor-map encoder, and on
+ *         which devices their kernels' shared-memory limits have been raised;
  *       - for ep_layout_noalloc alone, the fixed device array that call uses as
  *         scratch, with its looked-up address.
  *   - Tracing: with the environment variable EP_NVTX=1 (read once per

@@ -603,6 +603,57 @@ def test_replayed_graph_follows_the_arrays(quant):
 
 
 @pytest.mark.parametrize("quant", [BF, F8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_replayed_prompts_follow_the_arrays(quant, D):
+    """Prompts' attention captured twice over one scratch; lengths and rows' owners change between
+    replays, down to nothing."""
+    s = Seqs([700, 90, 400], [300, 90, 7], Hq=8, Hkv=2, D=D, quant=quant)
+    cache, seqs, q = s.cuda()
+    n = ep.ep_attn_prefill_workspace_bytes(s.T, 3, 8, 2, D)
+    scratch = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse = poisoned(s.T, 8, D), torch.empty((s.T, 8), device="cuda")
+
+    def step():
+        ep.ep_attn_prefill(cache, seqs, q, out=out, lse=lse, scratch=scratch, window=150, sinks=20)
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        graphs.append(graph)
+    for x, (lens, new) in enumerate([([700, 90, 400], [300, 90, 7]), ([650, 40, 0], [1, 40, 0]),
+                                     ([0, 0, 0], [0, 0, 0]), ([300, 90, 399], [300, 1, 96])]):
+        s.lens, s.new, s.starts = lens, new, [0]
+        for m in new:
+            s.starts.append(s.starts[-1] + m)
+        seqs.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        seqs.q_start.copy_(torch.tensor(s.starts, dtype=torch.int32))
+        out.fill_(float("nan"))
+        graphs[x % 2].replay()
+        torch.cuda.synchronize()
+        seqs.check_status()
+        own = s.owned()
+        assert torch.isnan(out.cpu()[~own]).all()
+        close(s, out, lse, window=150, sinks=20)
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("quant", [BF, F8])
+def test_largest_heads_and_pages(quant, decode):
+    """The most query heads on one key head; the largest pages, the last one hardly used."""
+    lens = [130, 3]
+    check(Seqs(lens, None if decode else [5, 3], Hq=1024, Hkv=1, quant=quant, D=64), decode)
+    lens = [4097, 4000]
+    check(Seqs(lens, None if decode else [300, 1], Hq=4, Hkv=2, quant=quant, page=4096), decode)
+
+
+@pytest.mark.parametrize("quant", [BF, F8])
 @pytest.mark.parametrize("layout", ["heads", "rows"])
 def test_a_prompt_its_next_chunk_and_single_tokens(quant, layout):
     """The run of a model's layer: append and attend a prompt in two chunks, then token by token."""
