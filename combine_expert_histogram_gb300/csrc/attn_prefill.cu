@@ -28,6 +28,15 @@
 // over sequences, key heads and row blocks, of which every SM takes an equal run, wherever row
 // blocks begin and end; a row block that several SMs share leaves its sums in the workspace, and
 // a second kernel adds them.  The loader walks the run and tells the other roles its pieces.
+//
+// Bound by the chain S -> exponentials -> P V of a row tile, which takes 3300 clocks for the 2270
+// of both tiles' products (tensor pipe 63 % active): S and P share their tensor memory, which
+// O fills otherwise, so that a tile's next S waits for its P V.  A prompt of 8192, 32 heads on 4,
+// takes 385 us (1.43 PFLOP/s); 5 prompts' chunks of 350 - 700 tokens after 3000 - 6000, 64 heads on
+// 8, 357 us in bf16 (1.34 PFLOP/s) and 460 in 8 bits, where the conversion competes for issue slots and
+// shared memory; heads of 64 are bound by the exponentials' instructions.  Two threads a row of S
+// would halve its part of the chain, but their 64 columns and 104 registers spill (452 us then
+// for 392).
 #include "attn.cuh"
 #include "tcgen05.cuh"
 
