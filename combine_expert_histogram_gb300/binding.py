@@ -934,6 +934,7 @@ class KvSeqs:
         if self.q_start is not None:
             start = _want(self.q_start, "q_start", (_I32,), (B + 1,), dev)
         status = _want(self.status, "status", (_I32,), (1,), dev)
+        # the struct of the last call's number of rows: replaced by another, never changed
         object.__setattr__(self, "_c", _KvSeqs(B, B, P, table, lens, start, status))
 
     def check_status(self) -> None:
@@ -945,7 +946,10 @@ class KvSeqs:
     def _struct(self, tokens: int) -> _KvSeqs:
         """The C struct of a call of `tokens` rows."""
         c = self._c
-        return _KvSeqs(c.num_seqs, tokens, c.max_pages, c.block_table, c.kv_len, c.q_start, c.status)
+        if c.num_tokens != tokens:
+            c = _KvSeqs(c.num_seqs, tokens, c.max_pages, c.block_table, c.kv_len, c.q_start, c.status)
+            object.__setattr__(self, "_c", c)
+        return c
 
 
 def new_kv_seqs(block_table: torch.Tensor, kv_len: torch.Tensor,
@@ -1079,6 +1083,9 @@ def ep_attn_decode(cache: KvCache, seqs: KvSeqs, q: torch.Tensor, scale: Optiona
     return out
 
 
+_prefill_bytes = {}  # bytes of ep_attn_prefill's scratch by (device, head_dim)
+
+
 def ep_attn_prefill_workspace_bytes(num_tokens: int, num_seqs: int, num_q_heads: int,
                                     num_kv_heads: int, head_dim: int) -> int:
     return int(load_library().ep_attn_prefill_workspace_bytes(num_tokens, num_seqs, num_q_heads,
@@ -1095,13 +1102,14 @@ def ep_attn_prefill(cache: KvCache, seqs: KvSeqs, q: torch.Tensor, scale: Option
     the call's own by default).  Rows of the result that belong to no sequence are not written."""
     lib = load_library()
     dev, c, s, pq, sq, Hq, scale, out, po, pl = _attn_args(cache, seqs, q, scale, out, lse, stream)
-    shape = s.num_tokens, s.num_seqs, Hq, c.num_kv_heads, c.head_dim
     if scratch is None:
-        if dev == torch.cuda.current_device():
-            n = lib.ep_attn_prefill_workspace_bytes(*shape)
-        else:
+        n = _prefill_bytes.get((dev, c.head_dim))
+        if n is None:  # depends on the device and head_dim alone
             with torch.cuda.device(dev):
-                n = lib.ep_attn_prefill_workspace_bytes(*shape)
+                n = lib.ep_attn_prefill_workspace_bytes(s.num_tokens, s.num_seqs, Hq, c.num_kv_heads,
+                                                        c.head_dim)
+            if n:
+                _prefill_bytes[dev, c.head_dim] = n
         if n:
             scratch = _empty(n, torch.uint8, dev, stream)
     nbytes = scratch.numel() if scratch is not None else 0
