@@ -714,6 +714,51 @@ def test_streams_at_once():
         close(p, b)
 
 
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("quant", [BF, F8])
+def test_queries_that_are_not_finite(quant, decode):
+    """A query with a NaN or an infinity is NaN, and only that one."""
+    def make():
+        return Seqs([300, 77], None if decode else [200, 77], Hq=8, Hkv=2, quant=quant)
+    s, clean = make(), make()
+    s.q[0, 1, 5], s.q[1, 3, 0], s.q[1, 7, 100] = float("nan"), float("inf"), float("-inf")
+    out, _ = run(s, decode)
+    want, noise, _, _ = clean.attention()
+    hit = torch.zeros((s.T, s.Hq), dtype=torch.bool)
+    hit[0, 1] = hit[1, 3] = hit[1, 7] = True
+    assert torch.isnan(out.cpu()[hit]).all()
+    ref.close_bf16(out.cpu()[~hit], want[~hit], noise[~hit])
+
+
+def test_two_threads():
+    """Calls from two host threads, each with handles, a stream and a workspace of its own."""
+    import threading
+    made, wrong = [], []
+    for i in range(2):
+        s = Seqs([400 + i, 60], Hq=8, Hkv=2, seed=i, quant=(BF, F8)[i])
+        p = Seqs([300 + i, 60], [100 + i, 60], Hq=8, Hkv=2, seed=i, quant=(F8, BF)[i])
+        made.append((s, p, s.cuda(), p.cuda(), ep.new_attn_workspace(2, 8, 2, 128), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(s, p, a, b, ws, stream):
+        try:
+            for _ in range(20):
+                x = ep.ep_attn_decode(*a, workspace=ws, stream=stream)
+                y = ep.ep_attn_prefill(*b, stream=stream)
+            stream.synchronize()
+            close(s, x)
+            close(p, y)
+        except BaseException as e:  # noqa: BLE001 - a thread's failure is the test's
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=m) for m in made]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+
+
 def test_attention_beside_the_experts():
     """One layer: norm, append, attention, norm, the few-token experts; programmatic launches all."""
     T, H, Hq, Hkv, D = 3, 512, 4, 2, 128
