@@ -32,7 +32,7 @@
 // Bound by the chain S -> exponentials -> P V of a row tile, which takes 3300 clocks for the 2270
 // of both tiles' products (tensor pipe 63 % active): S and P share their tensor memory, which
 // O fills otherwise, so that a tile's next S waits for its P V.  A prompt of 8192, 32 heads on 4,
-// takes 385 us (1.43 PFLOP/s); 5 prompts' chunks of 350 - 700 tokens after 3000 - 6000, 64 heads on
+// takes 379 us (1.45 PFLOP/s); 5 prompts' chunks of 350 - 700 tokens after 3000 - 6000, 64 heads on
 // 8, 357 us in bf16 (1.34 PFLOP/s) and 460 in 8 bits, where the conversion competes for issue slots and
 // shared memory; heads of 64 are bound by the exponentials' instructions.  Two threads a row of S
 // would halve its part of the chain, but their 64 columns and 104 registers spill (452 us then
@@ -48,7 +48,9 @@ constexpr int kRows = 2 * kTile;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 8.0f;  // log2 of how far m may be behind
 
-constexpr int kItem = 4;    // steps of time that a row block costs beside its own
+// Steps of time that a row block costs beside its own, and one of at most 128 rows (a prompt of
+// 8192: 448 / 402 / 384 / 378 / 388 us with 2 to 6; few tokens a sequence: 68 / 68 / 72 with 2 to 4).
+constexpr int kItem = 5, kItemFew = 3;
 constexpr int kLeast = 3;   // steps an SM takes at least
 constexpr int kPieces = 4;  // pieces ahead
 
@@ -78,6 +80,7 @@ struct Piece {
     // One row tile: its even key tiles are in one half, its odd ones in the other.
     __device__ __forceinline__ bool halves() const { return rows <= kTile; }
     __device__ __forceinline__ int steps() const { return halves() ? (nt + 1) / 2 : nt; }
+    __device__ __forceinline__ int beside() const { return halves() ? kItemFew : kItem; }
     // Of row tile t, or half t.
     __device__ __forceinline__ int tiles(int t) const { return halves() ? (nt + 1 - t) / 2 : nt; }
 };
@@ -269,7 +272,7 @@ __device__ __forceinline__ Piece row_block(const PrefillArgs &d, const Span &sp,
     return k;
 }
 // Its places in the list.
-__device__ __forceinline__ int places(const PrefillArgs &d, const Piece &k) { return d.ws ? k.steps() + kItem : 1; }
+__device__ __forceinline__ int places(const PrefillArgs &d, const Piece &k) { return d.ws ? k.steps() + k.beside() : 1; }
 // The places of all of a sequence's blocks of one head, by one warp.
 __device__ __forceinline__ int64_t all_places(const PrefillArgs &d, const Span &sp, int lane) {
     int64_t n = 0;
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
                                 reinterpret_cast<int4 *>(d.ws)[blockIdx.x] =
                                     make_int4(b, h, j, (int)((at + steps - 1) / per) - (int)blockIdx.x);
                         }
-                        at += steps + kItem;
+                        at += steps + k.beside();
                     } else {
                         some = true;
                         ++at;
