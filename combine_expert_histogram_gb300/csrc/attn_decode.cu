@@ -15,7 +15,7 @@
 // leaves its sums in the workspace, and the block that arrives last adds them (a second kernel
 // for that took 5 us more: 3 from the last block's end to its first instruction).
 //
-// What it takes: 128 sequences of 800 - 8000 keys, 32 heads on 4, 1.16 GB, 178 us (6.5 TB/s); 3
+// What it takes: 128 sequences of 800 - 8000 keys, 32 heads on 4, 1.16 GB, 175 us (6.6 TB/s); 3
 // sequences of 210000 - 300000, 64 heads on 8, in 8 bits, 1.67 GB, 251 us (6.7 TB/s); one of 4096
 // keys 10.9 us, of which 4 are the launch and the last join, 2 the first load's answer.
 //
@@ -30,7 +30,9 @@ namespace {
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kHeads = 16;           // query heads of an item at most
 constexpr int kLeast = 2 * kWarps;   // units a block takes at least
-constexpr int kItem = 8;             // units of time that an item costs beside its own
+// units of time that an item costs beside its own (128 sequences of up to 500 keys: 33.0 / 28.3 /
+// 27.9 / 27.5 us with 8 / 12 / 16 / 24; of up to 8000, in 8 bits, 105 / 101 / 99 / 100)
+constexpr int kItem = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 // log2 of how far m may be behind the largest logit (so that most units need no maximum over the
 // lanes), and what FP8 weights are raised by: fp16 from 2^15 down to 2^-32 of the largest
