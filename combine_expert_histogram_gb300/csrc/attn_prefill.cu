@@ -38,6 +38,7 @@
 // would halve its part of the chain, but their 64 columns and 104 registers spill (452 us then
 // for 392).
 #include "attn.cuh"
+#include "attn_ring.h"
 #include "tcgen05.cuh"
 
 namespace ep {
@@ -82,7 +83,7 @@ struct Piece {
     __device__ __forceinline__ int steps() const { return halves() ? (nt + 1) / 2 : nt; }
     __device__ __forceinline__ int beside() const { return halves() ? kItemFew : kItem; }
     // Of row tile t, or half t.
-    __device__ __forceinline__ int tiles(int t) const { return halves() ? (nt + 1 - t) / 2 : nt; }
+    __device__ __forceinline__ int tiles(int t) const { return ring_tiles(halves(), t, nt); }
 };
 
 struct Shared {
@@ -863,14 +864,22 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
                 }
             };
             auto full = [&](const Place &at) { return mbar_wait_fast(&sh.full[at.s], at.parity, fail); };
-            // A wait for a phase must not come before the phase before it is over: a half's keys take
-            // the stage that the other half's values had, which this warp has not waited for.  Where
-            // the row tiles take turns, or converters fill the stages in order, they are there; else
-            // it waits for the values before these keys to be looked through, which goes in order.
-            auto keys = [&](const Place &at, bool alone) {
-                const int last = (at.it >> 1) - 1;
-                return (!C::kApart || FP8 || !alone || last < 0 ||
-                        mbar_wait_fast(&sh.v_ok[last & 3], last >> 2 & 1, fail)) && full(at);
+            // The next n places are the other half's.  A wait for a phase is sound only if the phase
+            // before it is over.  Where the row tiles take turns, a turn says that the other warp has
+            // waited for its places before it, and they are skipped; else this warp waits for them too,
+            // in order, and hands them back.  (Doing so everywhere, 8-bit prompts of heads of 128 took
+            // 563 us for 460: more code beside the conversion's.)
+            auto pass = [&](Place &at, int n) {
+                if constexpr (C::kApart) {
+                    for (; n > 0; --n, at.add(1)) {
+                        if (!__all_sync(kFullMask, full(at))) return false;
+                        if (elect_one()) mbar_arrive(&sh.empty[at.s]);
+                        __syncwarp();
+                    }
+                } else {
+                    at.add(n);
+                }
+                return true;
             };
             int base = 0, done = 0, blocks = 0, queries = 0;  // ring index, tiles, turns, pieces with tiles so far
             bool ok = true;
@@ -879,17 +888,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
                 if (k.nt == 0) continue;
                 const bool halves = k.halves();
                 const int mine = k.tiles(t), step = halves ? 4 : 2;
-                // a tile is free when both row tiles' products have read it
+                // a tile is free when both warps' products have read it, or one's have and the other has
+                // passed it (with turns: or one's have, which then arrives twice)
                 auto release = [&](const Place &at) {
                     mma_commit(&sh.empty[at.s]);
-                    if (halves) mma_commit(&sh.empty[at.s]);
+                    if (!C::kApart && halves) mma_commit(&sh.empty[at.s]);
                 };
                 Place kt, vt;
-                kt.set(base + (halves ? 2 * t : 0));
+                kt.set(base);
+                ok = mine == 0 || (pass(kt, ring_others_before(halves, t, 0)) &&
+                                   mbar_wait_fast(&sh.q_full[t], queries++ & 1, fail) && full(kt));
+                ok = __all_sync(kFullMask, ok);
                 vt = kt;
                 vt.add(1);
-                ok = mine == 0 || (mbar_wait_fast(&sh.q_full[t], queries++ & 1, fail) && keys(kt, true));
-                ok = __all_sync(kFullMask, ok);
                 if (!ok) break;
                 tc_fence_after();
                 if (mine > 0 && elect_one()) {
@@ -903,9 +914,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
                     ok = full(vt) && (FP8 || !k.edge(key, a.window, a.sinks) ||
                                       mbar_wait_fast(&sh.v_ok[(vt.it >> 1) & 3], (vt.it >> 3) & 1, fail));
                     const uint64_t db = value_desc(smem_addr(ring + vt.s * C::kStage));
-                    kt.add(step);
+                    kt.add(2);
                     if (C::kApart && more) {
-                        ok = __all_sync(kFullMask, ok && mbar_wait_fast(&sh.s_free[t], done & 1, fail) && keys(kt, halves));
+                        ok = __all_sync(kFullMask, ok && mbar_wait_fast(&sh.s_free[t], done & 1, fail)) &&
+                             pass(kt, ring_others_before(halves, t, n + 1));
+                        ok = __all_sync(kFullMask, ok && full(kt));
                         if (!ok) break;
                         tc_fence_after();
                         if (elect_one()) {
@@ -941,6 +954,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
                     // The tiles take turns, so that one's exponentials run under the other's products:
                     // left alone they fall into step, and each waits for the other in both.
                     ok = t + blocks == 0 || mbar_wait_fast(&sh.turn[t], (blocks + t - 1) & 1, fail);
+                    if (more) pass(kt, ring_others_before(halves, t, n + 1));
                     ok = ok && mbar_wait_fast(&sh.p_ready[t][1], done & 1, fail) && (late || !more || full(kt));
                     ok = __all_sync(kFullMask, ok);
                     if (!ok) break;
@@ -967,6 +981,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
                     __syncwarp();
                     vt.add(step);
                 }
+                ok = ok && pass(kt, ring_others_after(halves, t, k.nt));
                 if (!C::kApart && ok && mine < k.tiles(0)) {  // an odd number in halves: a turn without a tile
                     ok = __all_sync(kFullMask, mbar_wait_fast(&sh.turn[t], (blocks + t - 1) & 1, fail));
                     ++blocks;
