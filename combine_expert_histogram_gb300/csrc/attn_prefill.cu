@@ -869,15 +869,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
             // waited for its places before it, and they are skipped; else this warp waits for them too,
             // in order, and hands them back.  (Doing so everywhere, 8-bit prompts of heads of 128 took
             // 563 us for 460: more code beside the conversion's.)
+            constexpr bool walk = C::kApart;
             auto pass = [&](Place &at, int n) {
-                if constexpr (C::kApart) {
-                    for (; n > 0; --n, at.add(1)) {
-                        if (!__all_sync(kFullMask, full(at))) return false;
-                        if (elect_one()) mbar_arrive(&sh.empty[at.s]);
-                        __syncwarp();
-                    }
-                } else {
-                    at.add(n);
+                for (; n > 0; --n, at.add(1)) {
+                    if (!__all_sync(kFullMask, full(at))) return false;
+                    if (elect_one()) mbar_arrive(&sh.empty[at.s]);
+                    __syncwarp();
                 }
                 return true;
             };
@@ -892,15 +889,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
                 // passed it (with turns: or one's have, which then arrives twice)
                 auto release = [&](const Place &at) {
                     mma_commit(&sh.empty[at.s]);
-                    if (!C::kApart && halves) mma_commit(&sh.empty[at.s]);
+                    if (!walk && halves) mma_commit(&sh.empty[at.s]);
                 };
                 Place kt, vt;
-                kt.set(base);
-                ok = mine == 0 || (pass(kt, ring_others_before(halves, t, 0)) &&
-                                   mbar_wait_fast(&sh.q_full[t], queries++ & 1, fail) && full(kt));
-                ok = __all_sync(kFullMask, ok);
+                kt.set(base + (!walk && halves ? 2 * t : 0));
+                ok = mine == 0 || !walk || pass(kt, ring_others_before(halves, t, 0));
                 vt = kt;
                 vt.add(1);
+                ok = ok && (mine == 0 || (mbar_wait_fast(&sh.q_full[t], queries++ & 1, fail) && full(kt)));
+                ok = __all_sync(kFullMask, ok);
                 if (!ok) break;
                 tc_fence_after();
                 if (mine > 0 && elect_one()) {
@@ -914,7 +911,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
                     ok = full(vt) && (FP8 || !k.edge(key, a.window, a.sinks) ||
                                       mbar_wait_fast(&sh.v_ok[(vt.it >> 1) & 3], (vt.it >> 3) & 1, fail));
                     const uint64_t db = value_desc(smem_addr(ring + vt.s * C::kStage));
-                    kt.add(2);
+                    kt.add(walk ? 2 : step);
                     if (C::kApart && more) {
                         ok = __all_sync(kFullMask, ok && mbar_wait_fast(&sh.s_free[t], done & 1, fail)) &&
                              pass(kt, ring_others_before(halves, t, n + 1));
@@ -954,7 +951,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
                     // The tiles take turns, so that one's exponentials run under the other's products:
                     // left alone they fall into step, and each waits for the other in both.
                     ok = t + blocks == 0 || mbar_wait_fast(&sh.turn[t], (blocks + t - 1) & 1, fail);
-                    if (more) pass(kt, ring_others_before(halves, t, n + 1));
                     ok = ok && mbar_wait_fast(&sh.p_ready[t][1], done & 1, fail) && (late || !more || full(kt));
                     ok = __all_sync(kFullMask, ok);
                     if (!ok) break;
@@ -981,7 +977,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
                     __syncwarp();
                     vt.add(step);
                 }
-                ok = ok && pass(kt, ring_others_after(halves, t, k.nt));
+                if (walk) ok = ok && pass(kt, ring_others_after(halves, t, k.nt));
                 if (!C::kApart && ok && mine < k.tiles(0)) {  // an odd number in halves: a turn without a tile
                     ok = __all_sync(kFullMask, mbar_wait_fast(&sh.turn[t], (blocks + t - 1) & 1, fail));
                     ++blocks;
