@@ -33,3 +33,45 @@ def test_prefill_of_many_short_sequences(B, n, window, D, quant):
             big.fill_(i)
         assert torch.equal(ep.ep_attn_prefill(cache, seqs, q, window=window), out)
     seqs.check_status()
+
+
+def offset(t, nbytes):
+    """A contiguous copy of t that begins nbytes behind an aligned address."""
+    raw = torch.empty(t.numel() * t.element_size() + nbytes, dtype=torch.uint8, device="cuda")
+    part = raw[nbytes:].view(t.dtype).view(t.shape)
+    part.copy_(t)
+    assert part.data_ptr() % 512 == nbytes
+    return part
+
+
+@pytest.mark.parametrize("quant", [BF, F8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_addresses_of_sixteen_bytes(D, quant):
+    """Rows, results and scratch that begin at a multiple of 16 bytes and of no more: the same
+    bits; of 8 bytes: refused."""
+    s = Seqs([700, 300, 9], [300, 5, 9], Hq=8, Hkv=2, D=D, quant=quant, page=24)
+    cache, seqs, q = s.cuda()
+    want = ep.ep_attn_prefill(cache, seqs, q)
+    n = ep.ep_attn_prefill_workspace_bytes(s.T, 3, 8, 2, D)
+    for at in (16, 48):
+        out, lse = offset(torch.zeros_like(q), at), offset(torch.zeros((s.T, 8), device="cuda"), 4)
+        scratch = offset(torch.zeros(n, dtype=torch.uint8, device="cuda"), at)
+        ep.ep_attn_prefill(cache, seqs, offset(q, at), out=out, lse=lse, scratch=scratch)
+        assert torch.equal(out, want)
+    close(s, out, lse)
+    one = Seqs([700, 300, 9], Hq=8, Hkv=2, D=D, quant=quant, page=24)
+    c1, s1, q1 = one.cuda()
+    ws = ep.AttnWorkspace(offset(torch.zeros(ep.ep_attn_decode_workspace_bytes(3, 8, 2, D), dtype=torch.uint8,
+                                             device="cuda"), 16))
+    got = ep.ep_attn_decode(c1, s1, offset(q1, 16), workspace=ws, out=offset(torch.zeros_like(q1), 16))
+    assert torch.equal(got, ep.ep_attn_decode(c1, s1, q1))
+    k = torch.randn((s.T, 2, D), generator=s.g).bfloat16().cuda()
+    tables = torch.cat([torch.ones((700, D // 2)), torch.zeros((700, D // 2))], 1).cuda()
+    rot = ep.ep_kv_append(cache, seqs, offset(k, 16), offset(k, 48), cos_sin=offset(tables, 16), q=offset(q, 16),
+                          q_out=offset(torch.zeros_like(q), 48))
+    assert torch.equal(rot, q)
+    seqs.check_status()
+    for kw in (dict(out=offset(torch.zeros_like(q), 8)),
+               dict(scratch=offset(torch.zeros(n, dtype=torch.uint8, device="cuda"), 8))):
+        with pytest.raises(ep.EPError):
+            ep.ep_attn_prefill(cache, seqs, q, **kw)
