@@ -36,26 +36,30 @@ struct AttnArgs {
     float *lse;         // [T, Hq] or nullptr
 };
 
-// Tokens of sequence b among the call's rows, and its length; both are whatever the
-// device arrays hold, brought into range (a length past the table raises
-// EP_ERR_BAD_PAGE).
+// Tokens of sequence b among the call's rows, and its length, which may be past the table; both
+// are whatever the device arrays hold, brought into range.
 struct Span {
     int first, n, len;
 };
-__device__ __forceinline__ Span seq_span(const SeqArgs &s, int page_size, int b) {
+__device__ __forceinline__ Span seq_rows(const SeqArgs &s, int b) {
     Span r;
     r.len = max(ld_dep(s.kv_len + b), 0);
-    const int most = s.max_pages * page_size;
-    if (r.len > most) {
-        raise_status(s.status, EP_ERR_BAD_PAGE);
-        r.len = most;
-    }
     if (s.q_start) {
         r.first = min(max(ld_dep(s.q_start + b), 0), s.T);
         r.n = min(max(ld_dep(s.q_start + b + 1), r.first), s.T) - r.first;
     } else {
         r.first = b;
         r.n = 1;
+    }
+    return r;
+}
+// The same for the attention: a length past the table raises EP_ERR_BAD_PAGE and counts as the table's.
+__device__ __forceinline__ Span seq_span(const SeqArgs &s, int page_size, int b) {
+    Span r = seq_rows(s, b);
+    const int most = s.max_pages * page_size;
+    if (r.len > most) {
+        raise_status(s.status, EP_ERR_BAD_PAGE);
+        r.len = most;
     }
     return r;
 }

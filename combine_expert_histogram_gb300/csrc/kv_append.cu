@@ -77,10 +77,11 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a)
 
     const int b = seq_of(a.seq, t);
     if (b < 0) return;
-    const Span sp = seq_span(a.seq, a.kv.page_size, b);
+    const Span sp = seq_rows(a.seq, b);
     const int pos = sp.len - sp.n + (t - sp.first);
     if (pos < 0) return;
-    if (a.R && pos >= a.positions) {
+    // past a table there is no place for the token, and none that it may take
+    if (pos >= a.seq.max_pages * a.kv.page_size || (a.R && pos >= a.positions)) {
         raise_status(a.seq.status, EP_ERR_BAD_PAGE);
         return;
     }

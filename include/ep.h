@@ -628,7 +628,8 @@ typedef struct ep_kv_seqs {
                               call needs (past a sequence's end, before its window)
                               are not read                                         */
     const int32_t *kv_len;   /* device [B]; more than max_pages * page_size raises
-                                EP_ERR_BAD_PAGE and counts as that                   */
+                                EP_ERR_BAD_PAGE and counts as that in the attention;
+                                ep_kv_append skips the tokens past it               */
     const int32_t *q_start;  /* device [B+1], rising, or NULL                       */
     int32_t *status;         /* device [1], see above                               */
 } ep_kv_seqs_t;

@@ -4,7 +4,8 @@ import pytest
 import torch
 
 from combine_expert_histogram_gb300 import binding as ep
-from tests.attn_ref import Seqs, close
+from tests import layer_ref as ref
+from tests.attn_ref import Seqs, close, in_8_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +76,46 @@ def test_addresses_of_sixteen_bytes(D, quant):
                dict(scratch=offset(torch.zeros(n, dtype=torch.uint8, device="cuda"), 8))):
         with pytest.raises(ep.EPError):
             ep.ep_attn_prefill(cache, seqs, q, **kw)
+
+
+@pytest.mark.parametrize("quant", [BF, F8])
+def test_append_past_the_block_table(quant):
+    """Tokens past a block table are skipped, whatever the length says; those before its end are
+    stored where they belong, and what the cache held stays."""
+    for length, n in ((41, 4), (42, 4), (43, 4), (44, 4), (48, 4), (1000, 4), ((1 << 31) - 1, 4), (40, 4), (45, 40)):
+        s = Seqs([40, 20], [n, 2], Hq=2, Hkv=2, D=64, page=8, quant=quant, extra_cols=0)
+        cache, seqs, _ = s.cuda()
+        seqs.kv_len[0] = length
+        k = torch.randn((s.T, 2, 64), generator=s.g).bfloat16()
+        q = torch.randn((s.T, 2, 64), generator=s.g).bfloat16().cuda()
+        nan = torch.full((s.T, 2, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+        cos, sin = torch.ones((2000, 32)), torch.zeros((2000, 32))  # no turn: rows as they are
+        kept = [t.clone() for t in (cache.k, cache.v)]
+        scales = [] if quant == BF else [t.clone() for t in (cache.k_scales, cache.v_scales)]
+        out = ep.ep_kv_append(cache, seqs, k.cuda(), k.cuda(), cos_sin=torch.cat([cos, sin], 1).cuda(), q=q, q_out=nan)
+        torch.cuda.synchronize()
+        if length > 40:
+            with pytest.raises(ep.EPError) as e:
+                seqs.check_status()
+            assert e.value.code == ep.EP_ERR_BAD_PAGE
+        else:
+            seqs.check_status()
+        stored = [(t, 0, length - n + t) for t in range(n) if 0 <= length - n + t < 40]
+        stored += [(n, 1, 18), (n + 1, 1, 19)]
+        at = [x for x, _, _ in stored]
+        page = torch.tensor([int(s.table[b, i // 8]) for _, b, i in stored])
+        row = torch.tensor([i % 8 for _, _, i in stored])
+        rest = [t for t in range(s.T) if t not in at]
+        assert torch.equal(out[at], q[at]) and torch.isnan(out[rest]).all()
+        rows, e8 = (k[at], None) if quant == BF else in_8_bits(k[at].to(ref.F64))
+        if quant == F8:
+            rows = rows.float().to(torch.float8_e4m3fn).view(torch.uint8)
+        bits = torch.int16 if quant == BF else torch.uint8
+        for was, now in zip(kept, (cache.k, cache.v)):
+            want = was.cpu()
+            want[page, row] = rows
+            assert torch.equal(now.cpu().view(bits), want.view(bits))
+        for was, now in zip(scales, (cache.k_scales, cache.v_scales)):
+            want = was.cpu()
+            want[page, :, row] = e8
+            assert torch.equal(now.cpu(), want)
