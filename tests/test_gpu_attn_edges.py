@@ -1,5 +1,8 @@
 """The paged cache and its attention where their numbers and lists end: short pieces of many
 sequences, addresses, tables and values at the edges of what include/ep.h allows."""
+import ctypes
+import math
+
 import pytest
 import torch
 
@@ -119,3 +122,40 @@ def test_append_past_the_block_table(quant):
             want = was.cpu()
             want[page, :, row] = e8
             assert torch.equal(now.cpu(), want)
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("drop", [0.75, 3.0, 4.0])
+def test_a_million_equal_logits(drop, decode):
+    """The sum of a long row's probabilities: a tile's are added by themselves, then to the row's.  All
+    values are 1, so that the result is 1; shared out among blocks, and by one (prompts)."""
+    L, page, D = 1 << 20, 128, 64
+    k, v = torch.zeros((L // page, 1, page, D)), torch.ones((L // page, 1, page, D))
+    k[0, 0, 0, 0] = k[1, 0, 0, 0] = drop  # in a tile of each half
+    cache = ep.KvCache(k.bfloat16().cuda().transpose(1, 2), v.bfloat16().cuda().transpose(1, 2))
+    table = torch.arange(L // page, dtype=torch.int32)[None].cuda()
+    seqs = ep.new_kv_seqs(table, torch.tensor([L], dtype=torch.int32).cuda())
+    q = torch.zeros((1, 1, D), dtype=torch.bfloat16, device="cuda")
+    q[0, 0, 0] = 1.0
+    out, lse = torch.zeros_like(q), torch.zeros((1, 1), device="cuda")
+    want = math.log(2 * math.exp(drop) + L - 2)
+    # logits are exact.  Of the sum, relative: an exponential's 2^-22 and four roundings of its
+    # argument, one rounding for each of half the tiles' sums, and 64 for a tile's own chain and the joins
+    # (single tokens: a chain of 2^20 / 64 at most); the logarithm's 2^-22, four roundings of the result
+    rel = 2.0 ** -22 + 4 * ref.U * 2 * drop + ref.U * ((L // 64 if decode else L // 256) + 64)
+    off = rel + 2.0 ** -22 + 4 * ref.U * (drop + want)
+
+    def check():
+        assert abs(float(lse) - want) <= off, (float(lse), want, off)
+        assert ((out.double() - 1).abs() <= ref.BF16 + 2 * ref.BF16).all()  # P's rounding, and the result's
+
+    if decode:
+        ep.ep_attn_decode(cache, seqs, q, scale=1.0, out=out, lse=lse)
+        return check()
+    ep.ep_attn_prefill(cache, seqs, q, scale=1.0, out=out, lse=lse)
+    check()
+    code = ep.load_library().ep_attn_prefill(ctypes.byref(cache._c), ctypes.byref(seqs._struct(1)), q.data_ptr(), D, 1,
+                                             1.0, 0, 0, out.data_ptr(), lse.data_ptr(), None, 0, None)
+    assert code == 0
+    torch.cuda.synchronize()
+    check()
