@@ -115,6 +115,14 @@ __device__ __forceinline__ uint32_t ld_byte_if(bool there, const void *p, uint32
     return v;
 }
 
+// Four E4M3 values -> two pairs of fp16, exactly.
+__device__ __forceinline__ void half_pairs(uint32_t four, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
+}
+
 // The value of an E8M0 scale (255: NaN).
 __device__ __forceinline__ float scale_value(uint32_t e) {
     return e == 255 ? __uint_as_float(0x7fffffffu) : ue8m0_value(e);

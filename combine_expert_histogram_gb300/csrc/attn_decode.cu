@@ -194,13 +194,6 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Four E4M3 values -> two pairs of fp16, exactly.
-__device__ __forceinline__ void half_pairs(uint32_t four, uint32_t &lo, uint32_t &hi) {
-    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(four));
-}
 
 // A load that does not look into L1: another block's words.
 template <int N>

@@ -19,7 +19,7 @@
 //     P's relative rounding is the same), so that O is rescaled only in the rare tiles where
 //     a row's maximum jumps;
 //   - 8-bit caches: a warpgroup turns the E4M3 tiles into bf16, a thread a row, which is exact (a
-//     power of two times four bits), in loops of few instructions: beside the other roles' code long
+//     power of two times four bits; 2^128 and more, which a scale of 2^120 can make, is an infinity), in loops of few instructions: beside the other roles' code long
 //     unrolled ones wait for their instructions (570 us for the prompts that take 470 now).  Two
 //     such warpgroups would leave the exponentials too few registers for a row of S (540 us,
 //     with S taken twice).  bf16 caches: a warp looks for values that are not
@@ -252,6 +252,11 @@ __device__ __forceinline__ uint32_t mul_bf16(uint32_t x, uint32_t y) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
     return r;
+}
+// A pair of E4M3 values as fp16 -> bf16, exactly.
+__device__ __forceinline__ uint32_t bf16_pair(uint32_t h) {
+    const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return pack_bf16(g.x, g.y);
 }
 // In the upper bit of each half: whether that bf16 is an infinity or NaN.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
@@ -664,17 +669,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
                         if (page < 0) continue;
                         const int r = j % a.kv.page_size;
                         const uint8_t *src = a.kv.v + page * a.kv.page_stride + r * a.kv.row_stride + k.h * a.kv.head_stride;
-                        const bool none = FP8 && a.kv.v_scales[((int64_t)page * a.kv.Hkv + k.h) * a.kv.page_size + r] == 255;
+                        const uint32_t scale =
+                            FP8 ? scale_bf16(a.kv.v_scales[((int64_t)page * a.kv.Hkv + k.h) * a.kv.page_size + r]) : 0;
 #pragma unroll 1
                         for (int w = 0; w < D / 2; ++w) {
                             uint32_t y;
                             if constexpr (FP8) {
-                                const uint32_t e = reinterpret_cast<const uint16_t *>(src)[w];
-                                y = (none || (e & 0x7f) == 0x7f ? 0x7fffu : 0u) | (none || (e & 0x7f00) == 0x7f00 ? 0x7fff0000u : 0u);
+                                uint32_t lo, hi;
+                                half_pairs(reinterpret_cast<const uint16_t *>(src)[w], lo, hi);
+                                y = mul_bf16(bf16_pair(lo), scale);
                             } else {
                                 y = reinterpret_cast<const uint32_t *>(src)[w];
-                                y &= (not_finite(y) >> 15) * 0xffffu;
                             }
+                            y &= (not_finite(y) >> 15) * 0xffffu;
                             if (!y) continue;
                             if (direct) {
                                 uint32_t *at = reinterpret_cast<uint32_t *>(out) + w;
@@ -1101,15 +1108,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) {
                                     uint32_t h[2];
-                                    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
-                                        "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
-                                        : "=r"(h[0]), "=r"(h[1])
-                                        : "r"(w[j]));
+                                    half_pairs(w[j], h[0], h[1]);
 #pragma unroll
-                                    for (int z = 0; z < 2; ++z) {
-                                        const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&h[z]));
-                                        y[2 * j + z] = mul_bf16(pack_bf16(g.x, g.y), v ? fv : fk);
-                                    }
+                                    for (int z = 0; z < 2; ++z) y[2 * j + z] = mul_bf16(bf16_pair(h[z]), v ? fv : fk);
                                 }
                                 sts16(chunk(2 * (c0 + c)), make_uint4(y[0], y[1], y[2], y[3]));
                                 sts16(chunk(2 * (c0 + c) + 1), make_uint4(y[4], y[5], y[6], y[7]));

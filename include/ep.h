@@ -714,6 +714,9 @@ ep_status_t ep_attn_decode(const ep_kv_cache_t *cache, const ep_kv_seqs_t *seqs,
  *              Holds nothing between calls; calls (or replayed graphs) that share one must
  *              not overlap on the GPU.  NULL: no row block of 256 tokens times heads is shared out
  *              among SMs, which takes longer, for few tokens many times longer.
+ *
+ * 8-bit rows are multiplied as bf16, which holds their values exactly below 2^128; larger ones
+ * (a scale byte of 247 and more) are infinities here.
  */
 size_t ep_attn_prefill_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
                                        int32_t num_kv_heads, int32_t head_dim);

@@ -159,3 +159,33 @@ def test_a_million_equal_logits(drop, decode):
     assert code == 0
     torch.cuda.synchronize()
     check()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_values_past_bf16(D):
+    """An 8-bit value that bf16 does not hold (the largest bf16, appended, is 2^128) is an infinity in every
+    row that sees it, in tiles that all rows see and in others."""
+    def make():
+        return Seqs([400], [400], Hq=2, Hkv=1, D=D, quant=F8)
+    s = make()
+    for j in (20, 150, 300):
+        p, r = s.table[0, j // s.page].long(), j % s.page
+        s.v[p, r, 0], s.vs[p, 0, r] = 0, 247
+        s.v[p, r, 0, 5], s.v[p, r, 0, 6] = 0x78, 0xF8  # 256 * 2^120
+    big = torch.full((1, 1, D), 3.3895e38).bfloat16()  # what ep_kv_append makes of such a row
+    q8, e = in_8_bits(big.to(ref.F64))
+    assert int(e) == 247 and float(q8.max()) == 256
+    for window, sees in ((0, lambda i: i >= 20), (30, lambda i: any(j <= i < j + 30 for j in (20, 150, 300)))):
+        cache, seqs, q = s.cuda()
+        out = ep.ep_attn_prefill(cache, seqs, q, window=window).cpu()
+        seqs.check_status()
+        seen = torch.tensor([sees(i) for i in range(400)])
+        assert (out[seen][..., 5] == float("inf")).all() and (out[seen][..., 6] == float("-inf")).all()
+        assert torch.isfinite(out[~seen]).all()
+        # the others' channels: the row's values there are zeros
+        clean = make()
+        for j in (20, 150, 300):
+            clean.vval[clean.table[0, j // s.page].long(), j % s.page] = 0
+        want, noise, _, _ = clean.attention(window=window)
+        rest = [d for d in range(D) if d not in (5, 6)]
+        ref.close_bf16(out[..., rest], want[..., rest], noise[..., rest])
