@@ -744,12 +744,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             hi[n][i] = transposed(pack_half(exp2_fast(x + (ev[t][i] + basev[n][0])),
                                                             exp2_fast(y + (ev[t][i] + basev[n][1]))));
                         } else {
-                            // p as two bf16, its own and what that leaves: one would be off by
-                            // 2^-9 in every probability, and the products are not what bounds
-                            // the kernel
-                            const uint32_t w = pack_bf16(ex, ey);
+                            // p as two bf16, its upper bits and what they leave, off by 2^-16 of it
+                            // (one would be off by 2^-8, and the products are not what bounds the
+                            // kernel).  p's last bit is set, so that neither is below 0, and the second
+                            // is 0 only where the first is: an infinite value times both stays infinite.
+                            const uint32_t bx = __float_as_uint(ex) | 1, by = __float_as_uint(ey) | 1;
+                            const uint32_t w = __byte_perm(bx, by, 0x7632);
                             hi[n][i] = transposed(w);
-                            lo[n][i] = transposed(pack_bf16(ex - bf16_lo(w), ey - bf16_hi(w)));
+                            lo[n][i] = transposed(
+                                pack_bf16(__uint_as_float(bx) - bf16_lo(w), __uint_as_float(by) - bf16_hi(w)));
                         }
                     }
                 if constexpr (!FP8) {

@@ -189,3 +189,43 @@ def test_prefill_values_past_bf16(D):
         want, noise, _, _ = clean.attention(window=window)
         rest = [d for d in range(D) if d not in (5, 6)]
         ref.close_bf16(out[..., rest], want[..., rest], noise[..., rest])
+
+
+@pytest.mark.parametrize("Hq", [4, 32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_infinite_value_that_is_seen(D, Hq):
+    """An infinite value channel is infinite in every head that sees it, the others are not."""
+    lens = [200, 1, 5000, 40]
+    s, clean = (Seqs(lens, Hq=Hq, Hkv=2, D=D) for _ in range(2))
+    at = ((0, 150), (1, 0), (2, 77), (2, 4001))
+    for b, j in at:
+        p, r = s.table[b, j // s.page].long(), j % s.page
+        s.v[p, r, 0, 9], s.v[p, r, 0, 30] = float("-inf"), float("inf")
+    cache, seqs, q = s.cuda()
+    out = ep.ep_attn_decode(cache, seqs, q).cpu()
+    G = Hq // 2
+    assert (out[:3, :G, 9] == float("-inf")).all() and (out[:3, :G, 30] == float("inf")).all()
+    want, noise, _, _ = clean.attention()
+    rest = [d for d in range(D) if d not in (9, 30)]
+    ref.close_bf16(out[..., rest], want[..., rest], noise[..., rest])
+    ref.close_bf16(out[:, G:], want[:, G:], noise[:, G:])
+    ref.close_bf16(out[3], want[3], noise[3])
+
+
+def test_decode_probabilities_keep_sixteen_bits():
+    """One key of value 0 and one of value v: the result p v / (1 + p) has no rounding of p to 8 bits
+    (2^-16 is what two bf16 leave of it), only the result's own."""
+    D, B = 128, 64
+    s = Seqs([2] * B, Hq=8, Hkv=2, D=D, page=8)
+    p = s.table[:, 0].long()
+    s.v[p, 0] = 0
+    s.vval = s.v.to(ref.F64)
+    cache, seqs, q = s.cuda()
+    out = ep.ep_attn_decode(cache, seqs, q).cpu().to(ref.F64)
+    want, _, _, _ = s.attention()
+    k = s.kval[p, :2]  # [B, 2, Hkv, D]
+    mag = torch.einsum("bhgd,bjhd->bhgj", s.q.to(ref.F64).abs().view(B, 2, 4, D), k.abs()).amax(-1).reshape(B, 8, 1)
+    # two logits and exponentials, p and the sums
+    off = 2 * (2 * (D + 4) * ref.U * D ** -0.5 * mag + 2.0 ** -20) + 2.0 ** -16 + 2.0 ** -20
+    half = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=2.0 ** -100)))) * ref.BF16
+    assert ((out - want).abs() <= half + want.abs() * off).all()
