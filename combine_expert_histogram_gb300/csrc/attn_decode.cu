@@ -211,11 +211,12 @@ __device__ __forceinline__ auto ld_l2(const void *p) {
         return v;
     }
 }
-// A query head's result, by one warp; `top` in log2 units.
+// A query head's result, by one warp; `top` in log2 units.  A head that sees no key is 0; one
+// that does, and whose logits are all -infinity, 0 / 0.
 template <int D>
-__device__ __forceinline__ void store_head(const AttnArgs &a, int64_t to, int lane, float top, float sum,
-                                           const float (&acc)[D / 32]) {
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+__device__ __forceinline__ void store_head(const AttnArgs &a, int64_t to, int lane, bool keys, float top,
+                                           float sum, const float (&acc)[D / 32]) {
+    const float inv = keys ? 1.0f / sum : 0.0f;
     uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + to * D + D / 32 * lane);
 #pragma unroll
     for (int x = 0; x < D / 32; x += 2) dst[x / 2] = pack_bf16(acc[x] * inv, acc[x + 1] * inv);
@@ -272,7 +273,7 @@ __device__ __forceinline__ void join_head(const AttnArgs &a, const Share &t, int
             }
         }
     }
-    store_head<D>(a, t.row0 + r, lane, top, sum, acc);
+    store_head<D>(a, t.row0 + r, lane, true, top, sum, acc);
 }
 
 // A warp's stream of units: what is to be loaded next.
@@ -856,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (starts && ends) {
-                    store_head<D>(a, (int64_t)p.b * a.Hq + q0 + r, lane, top, sum, acc);
+                    store_head<D>(a, (int64_t)p.b * a.Hq + q0 + r, lane, p.k.L > 0, top, sum, acc);
                 } else {
                     const size_t to = (size_t)(2 * blockIdx.x + starts) * kHeads + r;
                     float *dst = out_sums + to * D + N * lane;

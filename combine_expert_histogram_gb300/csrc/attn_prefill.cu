@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TWO>::kThreads, 1)
         if (!(halves && t == 1)) {
             tc_fence_after();
             const bool direct = k.part < 0;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float inv = pos < 0 ? 0.0f : 1.0f / l;  // 0 / 0 where all logits are -infinity
             const int64_t part = (int64_t)k.part * kRows + local;  // of the workspace
             float *sums = reinterpret_cast<float *>(d.ws + ws_sums(gridDim.x)) + part * D;
             const int64_t to = (int64_t)(k.first + token) * a.Hq + (int64_t)k.h * d.G + (row - token * d.G);
@@ -1215,8 +1215,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Prefi
                 }
             }
         }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         const int token = (k.row0 + r) / d.G;
+        const float inv = k.pos0 + token < 0 ? 0.0f : 1.0f / sum;
         const int64_t to = (int64_t)(k.first + token) * a.Hq + (int64_t)rec.y * d.G + (k.row0 + r - token * d.G);
         uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + to * D + N * lane);
 #pragma unroll

@@ -692,7 +692,7 @@ ep_status_t ep_kv_append(const ep_kv_cache_t *cache, const ep_kv_seqs_t *seqs, c
  *   out = bf16_rn( sum over visible j of p_j v_j / sum of p_j ),  p_j = exp(scale * q.k_j)
  *   lse = log( sum of p_j )
  * with the sums in fp32.  A query that sees no key (kv_len[b] = 0) gets +0, and -infinity
- * in lse.  Cache rows that a query does not see, whatever they hold, do not matter to it.  A
+ * in lse; one whose logits are all -infinity gets NaN, which is 0 / 0, and -infinity in lse.  Cache rows that a query does not see, whatever they hold, do not matter to it.  A
  * page that is needed and not the cache's raises EP_ERR_BAD_PAGE; its rows count as zeros.
  */
 size_t ep_attn_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,

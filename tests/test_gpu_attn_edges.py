@@ -229,3 +229,27 @@ def test_decode_probabilities_keep_sixteen_bits():
     off = 2 * (2 * (D + 4) * ref.U * D ** -0.5 * mag + 2.0 ** -20) + 2.0 ** -16 + 2.0 ** -20
     half = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=2.0 ** -100)))) * ref.BF16
     assert ((out - want).abs() <= half + want.abs() * off).all()
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("quant", [BF, F8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_logits_of_minus_infinity(D, quant, decode):
+    """A row that sees keys, whose logits are all -infinity, is 0 / 0, not a row without keys."""
+    lens = [1, 0, 300, 5000]
+    new = None if decode else [1, 0, 2, 1]
+    s = Seqs(lens, new, Hq=4, Hkv=1, D=D, quant=quant)
+    if quant == BF:
+        s.k[..., 3] = s.k[..., 3].abs() + 1
+    else:
+        s.k[..., 3] = 0x38  # 1
+    s.q[..., 3] = 1.0
+    s.q[:, 1, 3] = float("-inf")
+    cache, seqs, q = s.cuda()
+    lse = torch.zeros((s.T, 4), device="cuda")
+    out = (ep.ep_attn_decode if decode else ep.ep_attn_prefill)(cache, seqs, q, lse=lse).cpu()
+    rows = [t for t in range(s.T) if not (decode and t == 1)]
+    assert torch.isnan(out[rows, 1]).all() and torch.isfinite(out[:, [0, 2, 3]]).all()
+    assert (lse.cpu()[rows, 1] == float("-inf")).all()
+    if decode:
+        assert (out[1] == 0).all() and (lse[1] == float("-inf")).all()
