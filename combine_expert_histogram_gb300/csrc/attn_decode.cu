@@ -652,23 +652,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(ek) : "r"(sc + 16 * t + 8 * i + row) : "memory");
                         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(sc + C::kUnit + 16 * t + 8 * i + row) : "memory");
                         // 2^(ek - 127), NaN for 255; 0 for ek = 0, which is off by less than the logits'
-                        // last bit: 2^-127 of a sum below 2^17 |q|
+                        // last bit: 2^-127 of a sum below 2^17 |q|.  The product of the scales first: the
+                        // queries were raised, and a sum times the key's scale alone may be past fp32.
                         const float f = __uint_as_float(ek == 255 ? 0x7fffffffu : ek << 23);
 #pragma unroll
                         for (int n = 0; n < NH; ++n) {
-                            s[t][n][2 * i] *= f;
-                            s[t][n][2 * i + 1] *= f;
+                            s[t][n][2 * i] *= f * to_log2[n][0];
+                            s[t][n][2 * i + 1] *= f * to_log2[n][1];
                         }
                         // e - 127, by a number whose last bits are e
                         ev[t][i] = e == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | e) - 8388735.0f;
                     }
             }
+            if constexpr (!FP8) {
 #pragma unroll
-            for (int t = 0; t < KT; ++t)
+                for (int t = 0; t < KT; ++t)
 #pragma unroll
-                for (int n = 0; n < NH; ++n)
+                    for (int n = 0; n < NH; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[t][n][i] *= to_log2[n][i & 1];
+                        for (int i = 0; i < 4; ++i) s[t][n][i] *= to_log2[n][i & 1];
+            }
             if (!whole) {
 #pragma unroll
                 for (int t = 0; t < KT; ++t)

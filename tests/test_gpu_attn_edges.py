@@ -253,3 +253,27 @@ def test_logits_of_minus_infinity(D, quant, decode):
     assert (lse.cpu()[rows, 1] == float("-inf")).all()
     if decode:
         assert (out[1] == 0).all() and (lse[1] == float("-inf")).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_large_logits_of_8_bit_keys(D):
+    """Products that fp32 holds, although 2^8 times as large ones would not be: one key takes it all."""
+    s = Seqs([50, 900], Hq=4, Hkv=1, D=D, quant=F8)
+    s.k[..., 1:] = 0
+    s.k[..., 0] = torch.randint(1, 0x70, s.k[..., 0].shape, generator=s.g).to(torch.uint8)
+    s.ks[:] = 245  # 2^118
+    s.q[:] = 0
+    s.q[..., 0] = 0.5
+    best = []
+    for b, L in enumerate(s.lens):
+        j = L // 3
+        p, r = s.table[b, j // s.page].long(), j % s.page
+        s.k[p, r, 0, 0] = 0x7E  # 448
+        best.append(s.vval[p, r, 0])
+    cache, seqs, q = s.cuda()
+    lse = torch.zeros((2, 4), device="cuda")
+    out = ep.ep_attn_decode(cache, seqs, q, lse=lse).cpu()
+    for b in range(2):
+        assert torch.equal(out[b].float(), best[b].float().expand(4, D))
+    want = 448 * 2.0 ** 117 * D ** -0.5
+    assert (abs(lse.cpu().double() / want - 1) <= 8 * ref.U).all()
