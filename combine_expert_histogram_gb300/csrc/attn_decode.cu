@@ -824,8 +824,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int x = 4; x < 32; x <<= 1) l[n][i] += __shfl_xor_sync(kFullMask, l[n][i], x);
                 const int r = 2 * c + i;
                 if (row == 0) sh.part[warp][r] = {m[n][i], l[n][i]};
-                // FP8: from the scaled weights' unit to the probabilities'
-                const float f = !FP8 ? 1.0f : m[n][i] == -INFINITY ? 0.0f : exp2_fast(mv[n][i] - m[n][i] - kBoost);
+                // FP8: from the scaled weights' unit to the probabilities', in two steps, as one of 2^-134
+                // (a value's scale of 2^-127) would be 0
+                const float f = !FP8 ? 1.0f : m[n][i] == -INFINITY ? 0.0f : exp2_fast(0.5f * (mv[n][i] - m[n][i] - kBoost));
                 float *to = merge + (warp * 8 + r) * D;
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t)
@@ -834,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // channel 16 t + row + 8 x, FP8: D/8 row + 2 t + x, whose place is
                         // 8 (2 t + x) + row there
                         const int at = 16 * t + row + 8 * x;
-                        to[at ^ (8 * c)] = FP8 ? o[n][t][2 * x + i] * f : o[n][t][2 * x + i];
+                        to[at ^ (8 * c)] = FP8 ? o[n][t][2 * x + i] * f * f : o[n][t][2 * x + i];
                     }
             }
             __syncthreads();

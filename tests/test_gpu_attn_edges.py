@@ -277,3 +277,26 @@ def test_decode_large_logits_of_8_bit_keys(D):
         assert torch.equal(out[b].float(), best[b].float().expand(4, D))
     want = 448 * 2.0 ** 117 * D ** -0.5
     assert (abs(lse.cpu().double() / want - 1) <= 8 * ref.U).all()
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_of_the_smallest_and_largest_scales(D, decode):
+    """Results down to bf16's smallest normal numbers and up to its largest; zeros beside the largest stay
+    zeros."""
+    for byte in (0, 1, 3, 120, 240, 246, 254):
+        s = Seqs([300, 40, 1], None if decode else [3, 1, 1], Hq=12, Hkv=1, D=D, quant=F8)
+        s.vs[:] = byte
+        s.v[:] = torch.randint(0x38, 0x3C, s.v.shape, generator=s.g).to(torch.uint8)  # 1 to 1.375
+        if byte == 254:
+            s.v[..., 1::2] = 0
+        s.vval = torch.ldexp(ref.decode(s.v), torch.tensor(byte - 127))
+        cache, seqs, q = s.cuda()
+        out = (ep.ep_attn_decode if decode else ep.ep_attn_prefill)(cache, seqs, q).cpu()
+        want, noise, _, _ = s.attention()
+        if byte == 254:
+            # sums are in fp32 before the division: of 2^127 and more, times probabilities that sum up to
+            # more than 2, they are past 2^128.  The one key of the last row has the probability 1.
+            assert (out[..., 1::2] == 0).all() and (out[..., ::2] > 0).all()
+            out, want, noise = out[-1:], want[-1:], noise[-1:]
+        ref.close_bf16(out, want, noise)
