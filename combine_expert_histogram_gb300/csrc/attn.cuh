@@ -123,11 +123,6 @@ __device__ __forceinline__ void half_pairs(uint32_t four, uint32_t &lo, uint32_t
         : "r"(four));
 }
 
-// The value of an E8M0 scale (255: NaN).
-__device__ __forceinline__ float scale_value(uint32_t e) {
-    return e == 255 ? __uint_as_float(0x7fffffffu) : ue8m0_value(e);
-}
-
 cudaError_t launch_kv_append(const KvArgs &kv, const SeqArgs &seq, const uint16_t *q,
                              int64_t q_stride, int Hq, const uint16_t *k, int64_t k_stride,
                              const uint16_t *v, int64_t v_stride, const float *cos_sin, int R,

@@ -15,7 +15,7 @@
 // leaves its sums in the workspace, and the block that arrives last adds them (a second kernel
 // for that took 5 us more: 3 from the last block's end to its first instruction).
 //
-// What it takes: 128 sequences of 800 - 8000 keys, 32 heads on 4, 1.16 GB, 175 us (6.6 TB/s); 3
+// What it takes: 128 sequences of 800 - 8000 keys, 32 heads on 4, 1.16 GB, 178 us (6.5 TB/s); 3
 // sequences of 210000 - 300000, 64 heads on 8, in 8 bits, 1.67 GB, 251 us (6.7 TB/s); one of 4096
 // keys 10.9 us, of which 4 are the launch and the last join, 2 the first load's answer.
 //
@@ -29,7 +29,9 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kHeads = 16;           // query heads of an item at most
-constexpr int kLeast = 2 * kWarps;   // units a block takes at least
+// units a block takes at least (one sequence of 4096 keys, 32 heads on 4: 12.7 / 12.0 / 11.0 / 11.6 us with
+// 8 / 12 / 16 / 24; of 1000 10.1 / 10.3 / 10.3 / 11.1)
+constexpr int kLeast = 2 * kWarps;
 // units of time that an item costs beside its own (128 sequences of up to 500 keys: 33.0 / 28.3 /
 // 27.9 / 27.5 us with 8 / 12 / 16 / 24; of up to 8000, in 8 bits, 105 / 101 / 99 / 100)
 constexpr int kItem = 16;
@@ -419,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         total = __shfl_sync(kFullMask, incl, 31);
         per = max(divided(total + blocks - 1, blocks), (int64_t)kLeast);
         // Runs that end with their item, where that makes them at most 12 units (2 us)
-        // longer: a block with two items' parts comes 3 us later than the others.
+        // longer: a block with two items' parts comes 3 us later than the others (one sequence of 16000
+        // keys: 14.7 us, 15.7 with runs that may not be longer).
         const int64_t spare = blocks - (int64_t)a.seq.B * d.items;
         if (spare > 0) {
             const int64_t units = total - (int64_t)a.seq.B * d.items * kItem;
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) q[n][i / 2][i & 1] = word[n][i];
             } else {
-                // as fp16 next to 2^8 at most, exact down to 2^-32 of the head's largest
+                // as fp16 next to 2^8 at most, off by less than 2^-32 of the head's largest
                 float amax = 0.0f;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i)

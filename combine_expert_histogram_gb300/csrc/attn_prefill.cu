@@ -19,8 +19,8 @@
 //     P's relative rounding is the same), so that O is rescaled only in the rare tiles where
 //     a row's maximum jumps;
 //   - 8-bit caches: a warpgroup turns the E4M3 tiles into bf16, a thread a row, which is exact (a
-//     power of two times four bits; 2^128 and more, which a scale of 2^120 can make, is an infinity), in loops of few instructions: beside the other roles' code long
-//     unrolled ones wait for their instructions (570 us for the prompts that take 470 now).  Two
+//     power of two times four bits; 2^128 and more, which a scale of 2^120 can make, is an infinity), in
+//     loops of few instructions: beside the other roles' code long unrolled ones wait for their instructions (570 us for the prompts that take 470 now).  Two
 //     such warpgroups would leave the exponentials too few registers for a row of S (540 us,
 //     with S taken twice).  bf16 caches: a warp looks for values that are not
 //     finite in tiles that not all rows see: 0 * NaN would reach the other rows.
@@ -30,12 +30,13 @@
 // a second kernel adds them.  The loader walks the run and tells the other roles its pieces.
 //
 // Bound by the chain S -> exponentials -> P V of a row tile, which takes 3300 clocks for the 2270
-// of both tiles' products (tensor pipe 63 % active): S and P share their tensor memory, which
+// of both tiles' products (tensor pipe 65 % active): S and P share their tensor memory, which
 // O fills otherwise, so that a tile's next S waits for its P V.  A prompt of 8192, 32 heads on 4,
-// takes 379 us (1.45 PFLOP/s); 5 prompts' chunks of 350 - 700 tokens after 3000 - 6000, 64 heads on
-// 8, 357 us in bf16 (1.34 PFLOP/s) and 460 in 8 bits, where the conversion competes for issue slots and
-// shared memory; heads of 64 are bound by the exponentials' instructions.  Two threads a row of S
-// would halve its part of the chain, but their 64 columns and 104 registers spill (452 us then
+// takes 386 us (1.42 PFLOP/s; in long runs about 405); 5 prompts' chunks of 350 - 700 tokens after 3000 -
+// 6000, 64 heads on 8, 370 us in bf16 (1.30 PFLOP/s) and 460 in 8 bits, where the conversion competes for
+// issue slots and shared memory.  Heads of 64 wait in the same chain, whose products are half as long: no
+// unit is over 40 % busy there (a prompt of 8192: 318 us, exponentials 39 %, tensor pipe 38 %).  Two
+// threads a row of S would halve its part of the chain, but their 64 columns and 104 registers spill (452 us then
 // for 392).
 #include "attn.cuh"
 #include "attn_ring.h"
@@ -52,7 +53,7 @@ constexpr float kLag = 8.0f;  // log2 of how far m may be behind
 // Steps of time that a row block costs beside its own, and one of at most 128 rows (a prompt of
 // 8192: 448 / 402 / 384 / 378 / 388 us with 2 to 6; few tokens a sequence: 68 / 68 / 72 with 2 to 4).
 constexpr int kItem = 5, kItemFew = 3;
-constexpr int kLeast = 3;   // steps an SM takes at least
+constexpr int kLeast = 3;   // steps an SM takes at least (few tokens a sequence: the same with 1 to 6)
 constexpr int kPieces = 4;  // pieces ahead
 
 // A piece of the list: some of a row block's tiles.

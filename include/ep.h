@@ -611,7 +611,7 @@ typedef struct ep_kv_cache {
  * kv_len[b] - 1.  Their rows in the call's q, k, v and outputs are
  * q_start[b] .. q_start[b+1] - 1; without q_start sequence b has the one row b.
  * Rows that no sequence owns (before q_start[0], from q_start[num_seqs] on) are
- * neither read nor written.  All of it is read on the device when the kernels run,
+ * not written, and what they hold does not matter.  All of it is read on the device when the kernels run,
  * so a captured call follows the arrays.  Arrays that are no such lists (negative or
  * falling numbers) give results without meaning, but no access outside the arrays;
  * negative lengths count as 0, rows at negative positions (n_b > kv_len[b]) are skipped by
@@ -674,7 +674,8 @@ ep_status_t ep_kv_append(const ep_kv_cache_t *cache, const ep_kv_seqs_t *seqs, c
  *   q          device bf16 [B, num_q_heads, head_dim], 16-byte aligned, tokens q_stride
  *              elements apart (a multiple of 8).
  *   num_q_heads  a multiple of num_kv_heads, at most EP_ATTN_MAX_HEADS; heads
- *              [g*G, (g+1)*G), G = num_q_heads / num_kv_heads, share key head g.
+ *              [g*G, (g+1)*G), G = num_q_heads / num_kv_heads, share key head g.  Its rows
+ *              are read once for every 16 of them.
  *   scale      of the products q.k, finite and > 0.
  *   window     > 0: a query at position i sees the keys i - window < j <= i and the
  *              first `sinks` keys; 0: all keys j <= i (sinks is then ignored).
@@ -682,8 +683,8 @@ ep_status_t ep_kv_append(const ep_kv_cache_t *cache, const ep_kv_seqs_t *seqs, c
  *   out        device bf16 [B, num_q_heads, head_dim], 16-byte aligned.
  *   lse        device fp32 [B, num_q_heads] or NULL.
  *   workspace  device scratch, 16-byte aligned, of at least
- *              ep_attn_decode_workspace_bytes() with this device current; enough for
- *              that many sequences and for fewer.  All zeros before the first call; its
+ *              ep_attn_decode_workspace_bytes() with this device current, which depends on
+ *              head_dim alone.  All zeros before the first call; its
  *              counters are zero again after each call, the rest is clobbered.  Calls (or
  *              replayed graphs) that share one must not overlap on the GPU, and nothing
  *              else may write it between them (counters that are not zero raise
@@ -691,7 +692,8 @@ ep_status_t ep_kv_append(const ep_kv_cache_t *cache, const ep_kv_seqs_t *seqs, c
  *
  *   out = bf16_rn( sum over visible j of p_j v_j / sum of p_j ),  p_j = exp(scale * q.k_j)
  *   lse = log( sum of p_j )
- * with the sums in fp32.  A query that sees no key (kv_len[b] = 0) gets +0, and -infinity
+ * with the sums in fp32, and the numerator's p_j, in units of about the row's largest, as
+ * two bf16 (off by 2^-16 of each), or as one fp16 over an 8-bit cache (2^-11).  A query that sees no key (kv_len[b] = 0) gets +0, and -infinity
  * in lse; one whose logits are all -infinity gets NaN, which is 0 / 0, and -infinity in lse.  Cache rows that a query does not see, whatever they hold, do not matter to it.  A
  * page that is needed and not the cache's raises EP_ERR_BAD_PAGE; its rows count as zeros.
  */
@@ -714,6 +716,10 @@ ep_status_t ep_attn_decode(const ep_kv_cache_t *cache, const ep_kv_seqs_t *seqs,
  *              Holds nothing between calls; calls (or replayed graphs) that share one must
  *              not overlap on the GPU.  NULL: no row block of 256 tokens times heads is shared out
  *              among SMs, which takes longer, for few tokens many times longer.
+ *
+ * The numerator's p_j are rounded to bf16 (off by at most 2^-8 of each), the denominator's are
+ * not: that is what a result may be off by where one key carries it.  Logits are below 2^29 in
+ * size (larger ones differ from one another by less than fp32 holds).
  *
  * 8-bit rows are multiplied as bf16, which holds their values exactly below 2^128; larger ones
  * (a scale byte of 247 and more) are infinities here.
