@@ -20,10 +20,11 @@
 //     a row's maximum jumps;
 //   - 8-bit caches: a warpgroup turns the E4M3 tiles into bf16, a thread a row, which is exact (a
 //     power of two times four bits; 2^128 and more, which a scale of 2^120 can make, is an infinity), in
-//     loops of few instructions: beside the other roles' code long unrolled ones wait for their instructions (570 us for the prompts that take 470 now).  Two
-//     such warpgroups would leave the exponentials too few registers for a row of S (540 us,
-//     with S taken twice).  bf16 caches: a warp looks for values that are not
-//     finite in tiles that not all rows see: 0 * NaN would reach the other rows.
+//     loops of few instructions: beside the other roles' code long unrolled ones wait for their
+//     instructions (570 us for the prompts that take 460 now).  Two such warpgroups would leave the
+//     exponentials too few registers for a row of S (540 us, with S taken twice).  bf16 caches: a warp
+//     looks for values that are not finite in tiles that not all rows see: 0 * NaN would reach the
+//     other rows.
 // The work, a step being one tile of keys (two, for a block of at most 128 rows), is one list
 // over sequences, key heads and row blocks, of which every SM takes an equal run, wherever row
 // blocks begin and end; a row block that several SMs share leaves its sums in the workspace, and

@@ -50,16 +50,17 @@ class Early(Exception):
 
 
 class Model:
-    """pieces: (halves, tiles) each.  apart: heads of 64 (no turns, S apart from P); fp8: converters.
+    """pieces: (halves, tiles) each.  apart: heads of 64 (no turns, S apart from P); fp8: converters;
+    two: a loader of keys and one of values.
     skip: a product warp does not wait for the other half's places (as the kernel with turns)."""
 
-    def __init__(self, ring, pieces, apart, fp8, rng, skip=None):
+    def __init__(self, ring, pieces, apart, fp8, rng, skip=None, two=False):
         self.ring, self.pieces, self.apart, self.fp8, self.rng = ring, pieces, apart, fp8, rng
-        self.skip = not apart if skip is None else skip
+        self.two, self.skip = two, not apart if skip is None else skip
         self.inside = fp8 and not apart
         n = STAGES
         self.raw_full, self.raw_empty = [Bar(1) for _ in range(n)], [Bar(1) for _ in range(n)]
-        self.full, self.empty = [Bar(1) for _ in range(n)], [Bar(2 if fp8 else 3) for _ in range(n)]
+        self.full, self.empty = [Bar(1 + two) for _ in range(n)], [Bar(2 if fp8 else 3) for _ in range(n)]
         self.q_full, self.s_full, self.s_free, self.o_full, self.turn = ([Bar(1) for _ in range(2)] for _ in range(5))
         self.p_ready = [[Bar(1), Bar(1)] for _ in range(2)]
         self.v_ok = [Bar(1) for _ in range(4)]
@@ -67,16 +68,23 @@ class Model:
         self.read = []  # ring places in the order of the products
 
     # what an actor yields: None (a step of its own), or (barrier, phase): wait until that phase is over
-    def loader(self):
+    def loader(self, mine=0):
         n = 0
         empties = self.raw_empty if self.fp8 and not self.inside else self.empty
-        for halves, nt in self.pieces:
-            self.published += 1
+        for p, (_, nt) in enumerate(self.pieces):
+            if mine == 0:
+                self.published += 1
+            while self.published <= p:
+                yield None
             yield None
             for _ in range(2 * nt):
                 if n >= STAGES:
                     yield empties[n % STAGES], n // STAGES - 1
-                self.landing.append((self.raw_full if self.fp8 else self.full)[n % STAGES])
+                bar = (self.raw_full if self.fp8 else self.full)[n % STAGES]
+                if self.two and n % 2 != mine:
+                    bar.arrive()
+                else:
+                    self.landing.append(bar)
                 n += 1
                 yield None
 
@@ -209,6 +217,8 @@ class Model:
 
     def run(self):
         actors = [self.loader(), self.passer(), self.product(0), self.product(1), self.softmax(0), self.softmax(1)]
+        if self.two:
+            actors.append(self.loader(1))
         state = [next(a, "end") for a in actors]
         slow = self.rng.choice([None, 1, 1, 2, 3, 4, 5])  # an actor that moves late
         idle = 0
@@ -248,15 +258,16 @@ def lists(rng):
     return pieces
 
 
-FORMS = [(apart, fp8) for apart in (False, True) for fp8 in (False, True)]
+FORMS = [(False, False, False), (False, False, True), (False, True, False), (True, False, False),
+         (True, True, False)]
 
 
-@pytest.mark.parametrize("apart,fp8", FORMS)
-def test_every_wait_is_for_its_phase(ring, apart, fp8):
+@pytest.mark.parametrize("apart,fp8,two", FORMS)
+def test_every_wait_is_for_its_phase(ring, apart, fp8, two):
     rng = random.Random(11)
     for _ in range(400):
         pieces = lists(rng)
-        m = Model(ring, pieces, apart, fp8, rng).run()
+        m = Model(ring, pieces, apart, fp8, rng, two=two).run()
         total, base = 0, 0
         for halves, nt in pieces:  # every place read, by one warp or by both
             total += 2 * nt * (1 if halves else 2)
